@@ -42,7 +42,27 @@ SYMBOLS = (
     "dspark_schedule_async",
     "dspark_draft_sample_rnn",
     "dspark_verify_rnn",
+    "dspark_cache_init",
+    "dspark_cache_workspace_bytes",
+    "dspark_cache_append",
+    "dspark_cache_read",
+    "dspark_attend",
 )
+
+
+DSPARK_CACHE_BF16 = 0
+DSPARK_CACHE_E4M3 = 1
+
+DEVFLAG_NONFINITE = 0x2
+DEVFLAG_ROW_RANGE = 0x4
+DEVFLAG_TIMEOUT = 0x10
+DEVFLAG_PAGE_RANGE = 0x20
+
+
+class KVCache(ctypes.Structure):
+    """dspark_cache: the host description of a layer's key/value pools."""
+
+    _fields_ = [("opaque", ctypes.c_uint64 * 64)]
 
 
 class DSparkError(RuntimeError):
@@ -101,6 +121,20 @@ def lib() -> ctypes.CDLL:
         L.dspark_verify_rnn.argtypes = [c_int, c_int, c_int, c_int, c_float, vp, vp, vp, c_int,
                                         vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp, vp, vp, vp,
                                         vp, vp, c_size, vp]
+        c_i64, cache = ctypes.c_int64, ctypes.POINTER(KVCache)
+        L.dspark_cache_init.restype = c_int
+        L.dspark_cache_init.argtypes = [cache, c_int, c_i64, c_int, c_int, c_int, vp, vp, vp, vp]
+        L.dspark_cache_workspace_bytes.restype = c_size
+        L.dspark_cache_workspace_bytes.argtypes = [cache, c_int, c_int, c_int]
+        L.dspark_cache_append.restype = c_int
+        L.dspark_cache_append.argtypes = [cache, c_int, c_int, vp, c_i64, vp, c_i64, vp, vp, vp,
+                                          c_int, vp, c_size, vp]
+        L.dspark_cache_read.restype = c_int
+        L.dspark_cache_read.argtypes = [cache, c_int, c_int, vp, vp, vp, c_int, vp, vp, vp,
+                                        c_size, vp]
+        L.dspark_attend.restype = c_int
+        L.dspark_attend.argtypes = [cache, c_int, c_int, c_int, c_int, c_float, c_int, c_int, vp,
+                                    c_i64, vp, vp, vp, c_int, vp, vp, vp, c_size, vp]
         L.dspark_check_wait_timeout.restype = c_int
         L.dspark_check_wait_timeout.argtypes = [c_int, vp, c_size, vp]
         L.dspark_launch_count.restype = ctypes.c_longlong
@@ -162,6 +196,13 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _raw_stream(stream):
+    """The stream's handle; the current device's current stream when None."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _dt(t) -> int:
@@ -297,3 +338,82 @@ def dspark_check_wait_timeout(limit_us, ws, stream=None):
     (diagnostic); afterwards the workspace's status word has the timeout bit."""
     _check("dspark_check_wait_timeout",
            lib().dspark_check_wait_timeout(int(limit_us), _p(ws), ws.numel(), _stream(stream)))
+
+
+def _rows(t, Hx, D):
+    """Pointer and row stride of a [T, Hx, D] bf16 tensor whose rows are packed
+    heads and may lie apart (a slice of one projection's output)."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != Hx or t.shape[2] != D:
+        raise ValueError(f"expected a bf16 tensor [T, {Hx}, {D}], got {t.dtype} {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and Hx > 1):
+        raise ValueError("the heads of a row must be contiguous")
+    return t.data_ptr(), (s0 if t.shape[0] > 1 else Hx * D)
+
+
+def _i32(t, n, what):
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.shape[0] != n:
+        raise ValueError(f"{what} must be a contiguous int32 tensor with {n} entries")
+    return t.data_ptr()
+
+
+def cache_init(k, v, k_exp=None, v_exp=None) -> KVCache:
+    """The host description of pools k, v [n_pages, Hkv, page, D]: bf16, or e4m3
+    codes (uint8 or float8_e4m3fn) with exponent bytes k_exp, v_exp
+    [n_pages, Hkv, page].  The caller keeps the tensors alive."""
+    e4m3 = k_exp is not None or v_exp is not None
+    types = (torch.uint8, torch.float8_e4m3fn) if e4m3 else (torch.bfloat16,)
+    if k.dim() != 4 or k.shape != v.shape or k.dtype not in types or v.dtype not in types:
+        raise ValueError(f"k and v must be {types} pools [n_pages, Hkv, page, D] of one shape")
+    if e4m3:
+        for t in (k_exp, v_exp):
+            if t is None or t.dtype != torch.uint8 or t.shape != k.shape[:3]:
+                raise ValueError("k_exp and v_exp must be uint8 [n_pages, Hkv, page]")
+    n_pages, Hkv, page, D = k.shape
+    c = KVCache()
+    _check("dspark_cache_init", lib().dspark_cache_init(
+        ctypes.byref(c), DSPARK_CACHE_E4M3 if e4m3 else DSPARK_CACHE_BF16, n_pages, Hkv, page, D,
+        _p(k), _p(v), _p(k_exp), _p(v_exp)))
+    return c
+
+
+def cache_workspace_bytes(cache, R, T, Hq) -> int:
+    return int(lib().dspark_cache_workspace_bytes(ctypes.byref(cache), R, T, Hq))
+
+
+def dspark_cache_append(cache, Hkv, D, k, v, row_off, ctx, pages, ws, stream=None):
+    R, T = ctx.shape[0], k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same rows")
+    kp, ks = _rows(k, Hkv, D)
+    vp, vs = _rows(v, Hkv, D)
+    _check("dspark_cache_append", lib().dspark_cache_append(
+        cache, R, T, kp, ks, vp, vs, _i32(row_off, R + 1, "row_off"), _i32(ctx, R, "ctx"),
+        _i32(pages, R, "pages"), pages.shape[1], ws.data_ptr(), ws.numel(), _raw_stream(stream)))
+
+
+def dspark_cache_read(cache, Hkv, D, row_off, start, pages, k_out, v_out, ws, stream=None):
+    R, T = start.shape[0], k_out.shape[0]
+    for t in (k_out, v_out):
+        if t.dtype != torch.bfloat16 or t.shape != (T, Hkv, D) or not t.is_contiguous():
+            raise ValueError(f"k_out and v_out must be contiguous bf16 tensors [T, {Hkv}, {D}]")
+    _check("dspark_cache_read", lib().dspark_cache_read(
+        cache, R, T, _i32(row_off, R + 1, "row_off"), _i32(start, R, "start"),
+        _i32(pages, R, "pages"), pages.shape[1], k_out.data_ptr(), v_out.data_ptr(),
+        ws.data_ptr(), ws.numel(), _raw_stream(stream)))
+
+
+def dspark_attend(cache, D, q, row_off, ctx, pages, out, lse, scale, causal, window, max_rows, ws,
+                  stream=None):
+    R = ctx.shape[0]
+    T, Hq = q.shape[0], q.shape[1]
+    qp, qs = _rows(q, Hq, D)
+    if out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 tensor of q's shape")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq)
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 tensor [T, Hq]")
+    _check("dspark_attend", lib().dspark_attend(
+        cache, R, T, Hq, max_rows, scale, causal, window, qp, qs, _i32(row_off, R + 1, "row_off"),
+        _i32(ctx, R, "ctx"), _i32(pages, R, "pages"), pages.shape[1], out.data_ptr(),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream)))

@@ -26,6 +26,7 @@ constexpr uint32_t kFlagNonFinite = 0x2u;
 constexpr uint32_t kFlagRowRange = 0x4u;
 constexpr uint32_t kFlagSpsRange = 0x8u;
 constexpr uint32_t kFlagWaitTimeout = 0x10u;  // a bounded on-chip wait gave up
+constexpr uint32_t kFlagPageRange = 0x20u;    // a page id or position outside the paged cache
 
 // log2(e) as a double-float pair (hi = fp32 rounding, lo = remainder) so that
 // y * log2(e) / T carries no shared fp32 rounding of the constant.
@@ -204,6 +205,9 @@ enum KernelKind {
   kKindFinalTc,
   kKindWaitCheck,
   kKindRnnState,
+  kKindCacheAppend,
+  kKindCacheRead,
+  kKindAttend,
   kKindCount
 };
 

@@ -15,6 +15,13 @@
  *   dspark_draft_sample_rnn, dspark_verify_rnn
  *                        the same two stages with the RNN sequential head
  *
+ * The target's attention over the scheduled rows, between dspark_schedule and
+ * dspark_verify, runs on a paged key/value cache:
+ *
+ *   dspark_cache_append  the rows' keys and values written into their pages
+ *   dspark_attend        the rows' attention over each request's pages
+ *   dspark_cache_read    a range of cached positions read back
+ *
  * Conventions shared by every call
  * --------------------------------
  * - Every array argument is a DEVICE pointer owned by the caller, row-major,
@@ -76,6 +83,7 @@ typedef enum { DSPARK_BF16 = 0, DSPARK_F32 = 1 } dspark_dtype;
 #define DSPARK_DEVFLAG_ROW_RANGE 0x4u   /* a target row index outside [0, n_target_rows) */
 #define DSPARK_DEVFLAG_SPS_RANGE 0x8u   /* the scheduler needed SPS[B] beyond the table */
 #define DSPARK_DEVFLAG_TIMEOUT 0x10u    /* a bounded on-chip wait gave up (results invalid) */
+#define DSPARK_DEVFLAG_PAGE_RANGE 0x20u /* a page id outside [0, n_pages), or a position past the page table */
 
 /* Human-readable name of a status code.  Never NULL. */
 const char* dspark_status_string(int status);
@@ -391,6 +399,130 @@ int dspark_schedule_noalloc(int R, int gamma, const float* a, const float* sps, 
  * ws), DSPARK_ERR_WORKSPACE, DSPARK_ERR_CUDA.
  */
 int dspark_check_wait_timeout(int limit_us, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Paged key/value cache.
+ *
+ * The target model's forward pass over the scheduled rows (news article,
+ * figure 1: the target verifies the scheduled prefix of every request in one
+ * batch) needs, in every layer, the rows' keys and values stored and their
+ * attention over everything cached before them.  The pages give no layout;
+ * this library's is:
+ *
+ *   Two pools, k and v, [n_pages][Hkv][page][D], either bf16
+ *   (DSPARK_CACHE_BF16) or e4m3 codes (DSPARK_CACHE_E4M3) with one exponent
+ *   byte for each (page, head, slot) in k_exp, v_exp [n_pages][Hkv][page].
+ *   A code c stands for c * 2^(byte - 127).
+ *   Request n's position p is in slot p % page of page pages[n][p / page]
+ *   (pages [R][max_pages] int32, any page ids; entries past the last used
+ *   position are not read).
+ *   Rows come packed as the scheduler lays them out: request n's rows are
+ *   row_off[n] .. row_off[n+1]-1 (row_off [R+1] int32, row_off[0] >= 0), its row j at
+ *   position ctx[n] + j, ctx[n] (int32) the number of positions cached before
+ *   the call.  A request may have no rows.  A row at a negative position
+ *   (ctx[n] < 0) is padding: it is not stored and sees nothing.  Rows of the
+ *   batch past row_off[R] are left as they are.
+ *
+ * Rejected rows need no undoing: the next step's ctx[n] is this step's plus
+ * n_acc[n] + 1, and what is written there replaces them.
+ *
+ * Limits: D a multiple of 16, 16 <= D <= 128; page a power of two, 16 <= page
+ * <= 1024; n_pages * Hkv * page < 2^31; 1 <= R <= 2^20; 0 <= T <= 2^24 rows (T
+ * = 0 does nothing); max_pages * page < 2^30.
+ *
+ * dspark_cache (host memory, the caller's) describes the pools: fill it once
+ * with dspark_cache_init and pass it to every call; it may be copied.  It
+ * holds the pools' addresses and their tensor maps, nothing else, and needs no
+ * release.  The pools are 16-byte aligned.  A layer has a cache of its own;
+ * layers may share pages and row_off.
+ */
+typedef enum { DSPARK_CACHE_BF16 = 0, DSPARK_CACHE_E4M3 = 1 } dspark_cache_format;
+
+typedef struct dspark_cache {
+  uint64_t opaque[64];
+} dspark_cache;
+
+/* k_exp, v_exp: NULL iff format is DSPARK_CACHE_BF16.  DSPARK_ERR_INVALID_ARG,
+ * or DSPARK_ERR_CUDA where the driver's tensor-map encoder is missing or refuses. */
+int dspark_cache_init(dspark_cache* cache, int format, int64_t n_pages, int Hkv, int page, int D,
+                      void* k, void* v, uint8_t* k_exp, uint8_t* v_exp);
+
+/* Workspace bytes that cover dspark_cache_append, dspark_cache_read and
+ * dspark_attend with up to T rows and Hq query heads.  Returns 0 if the sizes
+ * are out of range.  The rules of every workspace hold (256-byte aligned,
+ * zeroed once, the status word first). */
+size_t dspark_cache_workspace_bytes(const dspark_cache* cache, int R, int T, int Hq);
+
+/*
+ * dspark_cache_append -- writes the rows' keys and values into their pages.
+ *
+ * DSPARK_CACHE_E4M3: for each (row, head), over its D values x,
+ *   e    = the smallest integer >= -100 with max |x| <= 448 * 2^e
+ *   code = x * 2^-e rounded to e4m3 (to nearest, ties to even)
+ * and the exponent byte is e + 127.  The scale is a power of two, so the only
+ * rounding is the code's own.  Non-finite values set DSPARK_DEVFLAG_NONFINITE;
+ * the maximum is over the finite ones, an infinity is stored as +-448 * 2^e
+ * and a NaN as NaN.
+ *
+ *   k, v      [T][Hkv][D] bf16, consecutive rows k_stride, v_stride elements
+ *             apart (multiples of 8, at least Hkv * D; slices of one
+ *             projection's output), 16-byte aligned
+ *   row_off, ctx, pages   as above
+ * A page id outside [0, n_pages), or a position past the table, sets
+ * DSPARK_DEVFLAG_PAGE_RANGE; that row is not written.
+ */
+int dspark_cache_append(const dspark_cache* cache, int R, int T, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, const int32_t* row_off,
+                        const int32_t* ctx, const int32_t* pages, int max_pages, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/*
+ * dspark_cache_read -- reads cached positions as bf16 rows.
+ *
+ *   row_off   [R+1]  request n's output rows
+ *   start     [R]    its row j is position start[n] + j; negative: zeros
+ *   k_out, v_out  [T][Hkv][D] bf16, 16-byte aligned, densely packed
+ * e4m3 entries convert exactly (below 2^-126 to bf16's subnormals).  A bad
+ * page sets DSPARK_DEVFLAG_PAGE_RANGE and reads as zeros.
+ */
+int dspark_cache_read(const dspark_cache* cache, int R, int T, const int32_t* row_off,
+                      const int32_t* start, const int32_t* pages, int max_pages, void* k_out,
+                      void* v_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * dspark_attend -- attention of each request's rows over its cached positions.
+ *
+ * For row t = row_off[n] + j at position p = ctx[n] + j, query head hq and
+ * key/value head h = hq / (Hq / Hkv):
+ *   s_c   = scale * sum_d q[t][hq][d] * k[c][h][d]
+ *   lse   = ln sum_c exp(s_c),  out[t][hq] = sum_c exp(s_c - lse) * v[c][h]
+ * over the visible positions c: 0 <= c < ctx[n] + m_n, m_n the request's
+ * rows (they are stored first: append, then attend); causal != 0: c <= p;
+ * window > 0 (causal only): c > p - window.  causal == 0 is a block whose
+ * positions see each other both ways (the drafter's).  A row that sees
+ * nothing has out = 0 and lse = -inf.
+ *
+ *   q     [T][Hq][D] bf16, rows q_stride elements apart (a multiple of 8, at
+ *         least Hq * D), 16-byte aligned; Hq a multiple of Hkv, Hq / Hkv <= 128
+ *   out   [T][Hq][D] bf16, 16-byte aligned, densely packed
+ *   lse   [T][Hq] f32 or NULL
+ *   max_rows  an upper bound of every m_n, known to the host (gamma + 1 in a
+ *         verification step); 0 = T.  It decides how the work is tiled.  A
+ *         request with more rows has the rest left out and sets
+ *         DSPARK_DEVFLAG_ROW_RANGE.
+ *   scale finite and > 0
+ * Products are exact, sums and softmax statistics fp32; a probability is
+ * rounded to 16 bits for the product with v, the result once to bf16.
+ * Positions that no row of the request sees are never part of a sum, whatever
+ * is stored there.  A NaN or infinity stored at a visible position may also
+ * reach those rows of the same request that do not see it yet.  Results are
+ * bit-reproducible.  A bad page sets DSPARK_DEVFLAG_PAGE_RANGE and reads as
+ * zeros.
+ */
+int dspark_attend(const dspark_cache* cache, int R, int T, int Hq, int max_rows, float scale,
+                  int causal, int window, const void* q, int64_t q_stride,
+                  const int32_t* row_off, const int32_t* ctx, const int32_t* pages, int max_pages,
+                  void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Launch counting and kernel tracing (measurement support; no counterpart on
