@@ -112,14 +112,8 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const Params p) {
 
 }  // namespace
 
-size_t attend_workspace_bytes(int T, int group, int D) {
-  (void)T;
-  (void)group;
-  (void)D;
-  return 256;
-}
-
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
+  if (a.c.k_exp == nullptr) return launch_attend_tc(a, st);
   Params p;
   p.c = a.c;
   p.Hq = a.Hq;
@@ -133,7 +127,7 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
   const int64_t jobs = (int64_t)a.c.T * a.Hq;
-  auto kernel = a.c.k_exp != nullptr ? attend_kernel<true> : attend_kernel<false>;
+  auto kernel = attend_kernel<true>;
   DSPARK_LAUNCH(kKindAttend, st,
                 kernel<<<(unsigned)((jobs + kWarps - 1) / kWarps), kThreads, 0, st>>>(p));
   return cudaGetLastError();

@@ -82,5 +82,6 @@ struct AttendArgs {
 };
 size_t attend_workspace_bytes(int T, int group, int D);
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st);
+cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t st);
 
 }  // namespace dspark

@@ -222,6 +222,8 @@ int dspark_attend(const dspark_cache* cache, int R, int T, int Hq, int max_rows,
   if (Hq < 1 || Hq % d.Hkv != 0 || Hq / d.Hkv > 128)
     return fail(DSPARK_ERR_INVALID_ARG,
                 "Hq must be a multiple of Hkv, at most 128 times it (Hq=%d Hkv=%d)", Hq, d.Hkv);
+  if ((int64_t)T * (Hq / d.Hkv) > (1 << 30))
+    return fail(DSPARK_ERR_INVALID_ARG, "T * Hq / Hkv must be at most 2^30");
   if (max_rows < 0) return fail(DSPARK_ERR_INVALID_ARG, "max_rows must be >= 0 (got %d)", max_rows);
   if (!isfinite(scale) || !(scale > 0.0f))
     return fail(DSPARK_ERR_INVALID_ARG, "scale must be finite and > 0");
