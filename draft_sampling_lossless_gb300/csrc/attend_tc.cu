@@ -33,9 +33,10 @@
 // the device: every block finds its own range with a scan over the requests.
 //
 // Roles: warps 0-7 the two softmax warpgroups (they also load Q and store), warp 8
-// issues the MMAs, warp 9 the TMA loads (10 and 11 only complete its warpgroup).  Every wait is bounded; a timeout sets
-// DSPARK_DEVFLAG_TIMEOUT and ends the kernel.
+// issues the MMAs, warp 9 the TMA loads (10 and 11 complete its warpgroup).  Every
+// wait is bounded; a timeout sets DSPARK_DEVFLAG_TIMEOUT and ends the kernel.
 #include "cache.cuh"
+#include "f32x2.cuh"
 #include "sm100.cuh"
 
 namespace dspark {
@@ -54,7 +55,6 @@ constexpr int kMaxCtas = 160;
 constexpr uint32_t kHalf = kBN * 128;        // bytes of 128 rows of 64 values
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;              // S at 0 and 128, O at 256 and 256 + DP
-constexpr uint32_t kColRest = 64;            // in S's columns: P, then what its rounding left
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.0f;                // log2 growth of a maximum that moves the reference
@@ -163,7 +163,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   }
 }
 
-// Registers a thread after the roles part: 256 x 224 + 128 x 56 = 384 x 168.
+// Registers a thread after the roles part: 256 x 200 + 128 x 104 = 384 x 168.
 template <int N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -282,36 +282,69 @@ __device__ __forceinline__ Range plan(const Params& p, int64_t* s_sum, volatile 
   return r;
 }
 
+__device__ __forceinline__ void mask_chunk(uint32_t (&v)[32], int col, int lo, int hi) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (col + i < lo || col + i >= hi) v[i] = 0xff800000u;
+}
+
+__device__ __forceinline__ float max_chunk(const uint32_t (&v)[32], float top) {
+  float m[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      m[k] = fmaxf(m[k], fmaxf(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1])));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// P of 32 positions in place of their scores: its bf16 rounding in the first 16
+// columns, the bf16 rounding of the rest in the other 16.
+__device__ __forceinline__ void exp_chunk(const uint32_t (&v)[32], uint32_t t_at, float c2,
+                                          float mc, unsigned long long (&sum)[2]) {
+  uint32_t out[32];
+  const unsigned long long cc = pack2(c2, c2), mm = pack2(-mc, -mc);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float a, b;
+    unpack2(fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), cc, mm), a, b);
+    a = ex2_approx(a);
+    b = ex2_approx(b);
+    const unsigned long long e = pack2(a, b);
+    sum[i & 1] = add2(sum[i & 1], e);
+    out[i] = pack_bf16(a, b);
+    unpack2(sub2(e, pack2(__uint_as_float(out[i] << 16), __uint_as_float(out[i] & 0xffff0000u))),
+            a, b);
+    out[16 + i] = pack_bf16(a, b);
+  }
+  tmem_st_32x32b_x32(t_at, out);
+}
+
 // One tile's P for a warp: its rows' scores of NC * 32 positions from column col0
-// of S on, the running reference and sum, and P as packed bf16 over S's columns
-// (zero outside the warp's own positions).
+// of S on, the running reference and sum, and P over S's columns (zero outside
+// the warp's own positions).  128 positions are read twice, for the maximum and
+// for the exponentials: tensor memory has the bandwidth, registers would spill.
 template <int NC, int DP>
 __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, int col0, bool mask,
                                              int rel_lo, int rel_hi, float c2, bool first,
                                              float& m_ref, float& l) {
-  uint32_t v[NC][32];
+  constexpr int kHeld = NC < 2 ? 1 : 2;
+  uint32_t v[kHeld][32];
+  float top = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < NC; ++k) tmem_ld_32x32b_x32(t_s + col0 + 32 * k, v[k]);
-  tmem_wait_ld();
+  for (int k0 = 0; k0 < NC; k0 += kHeld) {
 #pragma unroll
-  for (int k = 0; k < NC; ++k)
+    for (int k = 0; k < kHeld; ++k) tmem_ld_32x32b_x32(t_s + col0 + 32 * (k0 + k), v[k]);
+    tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[k][i]));
-  if (mask) {
+    for (int k = 0; k < kHeld; ++k) {
 #pragma unroll
-    for (int k = 0; k < NC; ++k)
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int col = col0 + 32 * k + i;
-        if (col < rel_lo || col >= rel_hi) v[k][i] = 0xff800000u;
-      }
+      for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[k][i]));
+      if (mask) mask_chunk(v[k], col0 + 32 * (k0 + k), rel_lo, rel_hi);
+      top = max_chunk(v[k], top);
+    }
   }
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int k = 0; k < NC; ++k)
-#pragma unroll
-    for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(v[k][i]));
-  const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  if (NC > kHeld) tmem_ld_32x32b_x32(t_s + col0, v[0]);
   if (first) {
     m_ref = top;
   } else if (__any_sync(0xffffffffu, (top - m_ref) * c2 > kGrow)) {
@@ -321,7 +354,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, int col
       m_ref = top;
     }
     l *= f;
-#pragma unroll
+    if (NC > kHeld) tmem_wait_ld_regs(v[0]);
+#pragma unroll 1
     for (int ch = 0; ch < DP; ch += 32) {
       uint32_t o[32];
       tmem_ld_32x32b_x32(t_o + ch, o);
@@ -332,35 +366,28 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, int col
     }
   }
   const float mc = m_ref == -INFINITY ? 0.f : m_ref * c2;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  unsigned long long sum[2] = {0, 0};  // two packed zeros each
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
-    uint32_t pk[16], rest[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float a = ex2_approx(fmaf(__uint_as_float(v[k][2 * i]), c2, -mc));
-      const float b = ex2_approx(fmaf(__uint_as_float(v[k][2 * i + 1]), c2, -mc));
-      sum[(2 * i) & 3] += a;
-      sum[(2 * i + 1) & 3] += b;
-      pk[i] = pack_bf16(a, b);
-      rest[i] = pack_bf16(a - __uint_as_float(pk[i] << 16),
-                          b - __uint_as_float(pk[i] & 0xffff0000u));
+    if (NC > kHeld) {
+      // the next chunk's load is in flight under this one's exponentials
+      tmem_wait_ld_regs(v[k & 1]);
+      if (k + 1 < NC) tmem_ld_32x32b_x32(t_s + col0 + 32 * (k + 1), v[(k + 1) & 1]);
+      if (mask) mask_chunk(v[k & 1], col0 + 32 * k, rel_lo, rel_hi);
     }
-    tmem_st_32x32b_x16(t_s + col0 / 2 + 16 * k, pk);
-    tmem_st_32x32b_x16(t_s + kColRest + col0 / 2 + 16 * k, rest);
+    exp_chunk(v[k & (kHeld - 1)], t_s + col0 + 32 * k, c2, mc, sum);
   }
   if (NC < 4) {
-    uint32_t z[16];
+    uint32_t z[32];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = 0;
+    for (int i = 0; i < 32; ++i) z[i] = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (k < col0 / 32 || k >= col0 / 32 + NC) {
-        tmem_st_32x32b_x16(t_s + 16 * k, z);
-        tmem_st_32x32b_x16(t_s + kColRest + 16 * k, z);
-      }
+      if (k < col0 / 32 || k >= col0 / 32 + NC) tmem_st_32x32b_x32(t_s + 32 * k, z);
   }
-  l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  float a, b;
+  unpack2(add2(sum[0], sum[1]), a, b);
+  l += a + b;
 }
 
 // Zeroes the rows of a V tile that no row of the item sees: whatever is stored
@@ -476,15 +503,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *s_tmem;
 
   if (warp >= 8) {
-    reg_dec<56>();
+    reg_dec<104>();
     if (warp == kWarpTma) {
       // ------------------------------------------------------------ loads
       const int log_page = p.c.log_page, page = 1 << log_page;
       const int box_rows = min(page, kBN);
-      const int n_boxes = (kBN / box_rows) * NH;  // lane: one box of one half
-      const int my_box = lane / NH, my_half = lane % NH;
+      const int n_boxes = kBN / box_rows;  // of each half; lane b looks box b up
       const int none = (int)(p.c.n_pages * p.c.Hkv) << log_page;  // past the pool: zeros
-      const uint32_t box_at = my_half * kHalf + my_box * box_rows * 128;
       if (lane == 0) {
         tma_prefetch(&tm_k);
         tma_prefetch(&tm_v);
@@ -500,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t mine =
               qt + lane < qts ? (int64_t)item_of<kRows>(p, q, qt + lane).ntiles * p.c.Hkv : 0;
           int64_t incl = mine;
-  #pragma unroll
+#pragma unroll
           for (int d = 1; d < 32; d <<= 1) {
             const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
             if (lane >= d) incl += o;
@@ -552,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this lane's box of a tile: its row of the pool, or `none`
         auto lookup = [&](int tile) {
           if (lane >= n_boxes) return none;
-          const int pos = tile * kBN + my_box * box_rows;
+          const int pos = tile * kBN + lane * box_rows;
           if (pos >= sg.hi || pos + box_rows <= sg.lo) return none;
           const int64_t id = page_of(p.c, n, pos);
           if (id < 0) return none;
@@ -560,21 +585,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int next = lookup(sg.tile0);
         for (int i = 0; i < sg.ntiles; ++i, ++seq) {
-          const int y = next;
+          int y[8];
+#pragma unroll
+          for (int b = 0; b < 8; ++b) y[b] = __shfl_sync(0xffffffffu, next, b);
           if (i + 1 < sg.ntiles) next = lookup(sg.tile0 + i + 1);
-  #pragma unroll
+#pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const int64_t e = 2 * seq + kv;
             const int slot = (int)(e % NS);
             ok = wait_bar(b_empty + 8 * slot, (uint32_t)((e / NS) & 1) ^ 1, s_abort, status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const uint32_t full = b_full + 8 * slot;
-            if (lane == 0) mbar_arrive_expect_tx(full, S::kTile);
+            if (elect_one()) {
+              const uint32_t full = b_full + 8 * slot;
+              const uint32_t dst = smem_u32(s_kv) + slot * S::kTile;
+              mbar_arrive_expect_tx(full, S::kTile);
+#pragma unroll
+              for (int b = 0; b < 8; ++b)
+                if (b < n_boxes)
+#pragma unroll
+                  for (int half = 0; half < NH; ++half)
+                    tma_load_2d(dst + half * kHalf + b * box_rows * 128, kv ? &tm_v : &tm_k, full,
+                                half * 64, y[b]);
+            }
             __syncwarp();
-            if (lane < n_boxes)
-              tma_load_2d(smem_u32(s_kv) + slot * S::kTile + box_at, kv ? &tm_v : &tm_k, full,
-                          my_half * 64, y);
           }
           if (!ok) break;
         }
@@ -600,21 +634,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------ products
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr uint32_t kIdS = idesc_bf16_f32(128, kBN);
         constexpr uint32_t kIdO = idesc_bf16_f32(128, DP) | kIdescTransposeB;
         const int ksteps = (p.c.D + 15) / 16;
         const uint32_t q_at = smem_u32(s_q), kv_at = smem_u32(s_kv);
         int64_t base = 0;  // tiles of the segments before
-        uint32_t ph_q = 0, ph_p[2] = {0, 0};
+        uint32_t ph_q = 0, ph_p = 0;
         bool ok = true;
         auto need = [&](int64_t e) {
           ok = ok && wait_bar(b_full + 8 * (int)(e % NS), (uint32_t)((e / NS) & 1), s_abort, status);
           tc_fence_after();
         };
         auto need_p = [&](int s) {
-          ok = ok && wait_bar(b_p + 8 * s, ph_p[s], s_abort, status);
-          ph_p[s] ^= 1;
+          ok = ok && wait_bar(b_p + 8 * s, (ph_p >> s) & 1, s_abort, status);
+          ph_p ^= 1u << s;
           tc_fence_after();
         };
         auto scores = [&](int s, int qtile, int64_t e) {
@@ -627,12 +661,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(b_s + 8 * s);
         };
         auto values = [&](int s, int64_t e, bool acc) {
-          const uint32_t b = kv_at + (uint32_t)(e % NS) * S::kTile;
-  #pragma unroll
+          // 16 positions a step: 2048 bytes on (the sum stays within the 14 address bits)
+          const uint64_t v = desc_mnmajor_sw128(kv_at + (uint32_t)(e % NS) * S::kTile, kHalf);
+#pragma unroll 1
           for (int k = 0; k < kBN / 16; ++k) {
-            const uint64_t v = desc_mnmajor_sw128(b + k * 2048, kHalf);
-            mma_bf16_ts(tmem + kColO + s * DP, tmem + s * kBN + k * 8, v, kIdO, acc || k > 0);
-            mma_bf16_ts(tmem + kColO + s * DP, tmem + s * kBN + kColRest + k * 8, v, kIdO, 1);
+            const uint32_t a = tmem + s * kBN + (k >> 1) * 32 + (k & 1) * 8;
+            mma_bf16_ts(tmem + kColO + s * DP, a, v + k * (2048 >> 4), kIdO, acc || k > 0);
+            mma_bf16_ts(tmem + kColO + s * DP, a + 16, v + k * (2048 >> 4), kIdO, 1);
           }
         };
         auto release = [&](int64_t e) { mma_commit(b_empty + 8 * (int)(e % NS)); };
@@ -711,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else {
-    reg_inc<224>();
+    reg_inc<200>();
     // ------------------------------------------------------------ softmax
     const int s = warp >> 2;  // the stream
     const int lrow = tid & 127;
