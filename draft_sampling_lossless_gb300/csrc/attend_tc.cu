@@ -61,10 +61,29 @@ constexpr float kGrow = 8.0f;                // log2 growth of a maximum that mo
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint32_t kCounterOffset = 256;     // workspace: status word, counters, partials
 constexpr uint32_t kPartOffset = 4096;
+constexpr int kMinTiles = 2;
+
+// n / d for 0 <= n < 2^31 by a multiplication (d fixed for the launch): with
+// 2^(s-1) < d <= 2^s and mul = floor(2^32 (2^s - d) / d) + 1, n / d is
+// (mulhi(n, mul) + n) >> s (Granlund and Montgomery 1994).
+struct Divider {
+  uint32_t mul, shift;
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+  }
+};
+Divider divider(int d) {
+  Divider v;
+  v.shift = 0;
+  while ((1ll << v.shift) < d) ++v.shift;
+  v.mul = (uint32_t)(((1ull << 32) * ((1ull << v.shift) - d)) / d + 1);
+  return v;
+}
 
 struct Params {
   CacheView c;
   int Hq, G, max_rows, causal, window;
+  Divider by_G;
   float scale;
   const __nv_bfloat16* q;
   int64_t q_stride;
@@ -90,7 +109,7 @@ struct Smem {
   static constexpr uint32_t kSegOffset = kXchOffset + kSoftThreads * 8;
   static constexpr uint32_t kBarOffset = kSegOffset + kSegDepth * 64;
   static constexpr int kBars = 2 * kSlots + 2 * kSegDepth + 1 + 2 + 2 + 2 + 1;
-  static constexpr uint32_t kTotal = kBarOffset + kBars * 8 + 32;
+  static constexpr uint32_t kTotal = kBarOffset + kBars * 8 + 16 + 32;
   static_assert(kTotal <= 232448, "shared memory");
 };
 template <int DP>
@@ -126,7 +145,7 @@ __device__ __forceinline__ Item item_of(const Params& p, const Req& q, int qt) {
   const int M = q.m * p.G;
   it.r0 = qt * ROWS;
   it.nrows = min(ROWS, M - it.r0);
-  const int j0 = it.r0 / p.G, j1 = (it.r0 + it.nrows - 1) / p.G;
+  const int j0 = p.by_G(it.r0), j1 = p.by_G(it.r0 + it.nrows - 1);
   it.hi = max(p.causal ? q.ctx + j1 + 1 : q.ctx + q.m, 0);
   it.lo = p.window > 0 ? min(max(q.ctx + j0 - p.window + 1, 0), it.hi) : 0;
   it.tile0 = it.lo / kBN;
@@ -197,11 +216,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return d;
 }
 
+// Blocks 0 .. ctas-1 take `each` tiles, the first `extra` of them one more.
 struct Range {
-  int64_t total, u0, u1;  // tiles in all; this block's
-  int ctas;               // blocks that take part
-  int n;                  // the request of tile u0
-  int64_t before;         // tiles of the requests before n
+  int64_t each, u0, u1;  // u0 .. u1 - 1: this block's tiles
+  int ctas, extra;
+  int n;                 // the request of tile u0
+  int64_t before;        // tiles of the requests before n
+  Req q;                 // request n
+
+  __device__ __forceinline__ int block_of(int64_t u) const {
+    const int64_t wide = extra * (each + 1);
+    return u < wide ? (int)(u / (each + 1)) : extra + (int)((u - wide) / each);
+  }
+};
+
+struct Found {  // the request of a block's first tile, from the thread that finds it
+  int64_t before;
+  int n;
+  Req q;
 };
 
 // Tiles of request n over all row tiles and heads.
@@ -215,14 +247,14 @@ __device__ __forceinline__ int64_t req_tiles(const Params& p, const Req& q, int 
 
 // Every block's range of tiles, from a scan over the requests (all threads).
 template <int ROWS>
-__device__ __forceinline__ Range plan(const Params& p, int64_t* s_sum, volatile int* s_n,
-                                      volatile int64_t* s_before) {
+__device__ __forceinline__ Range plan(const Params& p, int64_t* s_sum, Found* s_found) {
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
   const int per = (p.c.R + kThreads - 1) / kThreads;
   int64_t local = 0;
+  Req q = {0, 0, 0};
   for (int i = 0; i < per; ++i) {
     const int n = tid * per + i;
-    Req q = {0, 0, 0};
+    q = {0, 0, 0};
     if (n < p.c.R) q = load_req(p, n);
     const bool many = row_tiles<ROWS>(p, q.m) > 4;
     if (!many) local += req_tiles<ROWS>(p, q, 0, 1);
@@ -254,31 +286,34 @@ __device__ __forceinline__ Range plan(const Params& p, int64_t* s_sum, volatile 
     total += s_sum[w];
   }
   Range r;
-  r.total = total;
-  // a block takes two tiles at least (one for each stream) while there are few
-  r.ctas = (int)min((int64_t)gridDim.x, (total + 1) / 2);
+  // few tiles: fewer blocks, kMinTiles each, rather than more partial results
+  r.ctas = (int)min((int64_t)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
   r.u0 = r.u1 = 0;
-  if ((int)blockIdx.x < r.ctas) {
-    r.u0 = total * blockIdx.x / r.ctas;
-    r.u1 = total * (blockIdx.x + 1) / r.ctas;
-    int64_t at = base + incl - local;
-    if (at <= r.u0 && r.u0 < at + local) {
-      for (int i = 0; i < per; ++i) {
-        const int n = tid * per + i;
-        if (n >= p.c.R) break;
-        const int64_t u = per == 1 ? local : req_tiles<ROWS>(p, load_req(p, n), 0, 1);
-        if (r.u0 < at + u) {
-          *s_n = n;
-          *s_before = at;
-          break;
-        }
-        at += u;
+  if ((int)blockIdx.x >= r.ctas) return r;
+  r.each = total < (1ll << 31) ? (int64_t)((uint32_t)total / (uint32_t)r.ctas) : total / r.ctas;
+  r.extra = (int)(total - r.each * r.ctas);
+  r.u0 = r.each * blockIdx.x + min((int)blockIdx.x, r.extra);
+  r.u1 = r.u0 + r.each + ((int)blockIdx.x < r.extra);
+  int64_t at = base + incl - local;
+  if (at <= r.u0 && r.u0 < at + local) {
+    for (int i = 0; i < per; ++i) {
+      const int n = tid * per + i;
+      if (n >= p.c.R) break;
+      if (per > 1) q = load_req(p, n);
+      const int64_t u = per == 1 ? local : req_tiles<ROWS>(p, q, 0, 1);
+      if (r.u0 < at + u) {
+        s_found->n = n;
+        s_found->before = at;
+        s_found->q = q;
+        break;
       }
+      at += u;
     }
   }
   __syncthreads();
-  r.n = *s_n;
-  r.before = *s_before;
+  r.n = s_found->n;
+  r.before = s_found->before;
+  r.q = s_found->q;
   return r;
 }
 
@@ -402,41 +437,73 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int to, int t
 }
 
 // Joins the partial results of an item's blocks (all softmax threads of the last
-// one to finish): rows of 4 values a thread, lanes along the rows.
+// one to finish).  `buf`, 32 KB of shared memory: the blocks' (m, l) of a
+// group of rows, then their weights 2^(m - M) / L; the sums run over the blocks in
+// order, eight values a thread with lanes along the rows.
 template <int DP, int ROWS>
-__device__ void join(const Params& p, const Segment& sg) {
+__device__ __forceinline__ void join(const Params& p, const Segment& sg, float2* buf) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int np = sg.last - sg.first + 1;
   const size_t rec = record_floats<DP>(ROWS);
-  const int rows = (sg.nrows + 31) & ~31;
-  for (int task = threadIdx.x; task < rows * (DP / 4); task += kSoftThreads) {
-    const int row = task % rows, d4 = task / rows;
-    if (row >= sg.nrows) continue;
-    float M = -INFINITY;
-    for (int i = 0; i < np; ++i) {
-      const float* r = p.part + ((size_t)(sg.first + i) * 2 + (i == 0 ? 1 : 0)) * rec;
-      M = fmaxf(M, __ldcg(r + (size_t)ROWS * DP + row * 2));
+  const float* rec0 = p.part + ((size_t)sg.first * 2 + 1) * rec;  // the first block's, then
+  const float* recs = p.part + ((size_t)sg.first * 2 + 2) * rec;  // two records a block on
+  auto part = [&](int i) { return i == 0 ? rec0 : recs + (size_t)(i - 1) * 2 * rec; };
+  const int group = min(sg.nrows, 4096 / np);
+  for (int r0 = 0; r0 < sg.nrows; r0 += group) {
+    const int g = min(group, sg.nrows - r0);
+    for (int i = tid; i < np * g; i += kSoftThreads) {
+      const int b = i / g, row = i - b * g;
+      buf[i] = __ldcg(reinterpret_cast<const float2*>(part(b) + (size_t)ROWS * DP) + r0 + row);
     }
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < np; ++i) {
-      const float* r = p.part + ((size_t)(sg.first + i) * 2 + (i == 0 ? 1 : 0)) * rec;
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(r + (size_t)ROWS * DP) + row);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(r) + (size_t)d4 * ROWS + row);
-      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-      L = fmaf(ml.y, f, L);
-      acc.x = fmaf(o.x, f, acc.x);
-      acc.y = fmaf(o.y, f, acc.y);
-      acc.z = fmaf(o.z, f, acc.z);
-      acc.w = fmaf(o.w, f, acc.w);
+    soft_sync();
+    for (int row = warp; row < g; row += kSoftThreads / 32) {
+      float M = -INFINITY, L = 0.f;
+      for (int b = lane; b < np; b += 32) M = fmaxf(M, buf[b * g + row].x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      for (int b = lane; b < np; b += 32) {
+        const float2 ml = buf[b * g + row];
+        L = fmaf(ml.y, ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M), L);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      for (int b = lane; b < np; b += 32) {
+        const float m = buf[b * g + row].x;
+        buf[b * g + row].x = m == -INFINITY ? 0.f : ex2_approx(m - M) * inv;
+      }
+      if (lane == 0 && p.lse != nullptr) {
+        const int r = sg.r0 + r0 + row, j = p.by_G(r);
+        p.lse[(int64_t)(sg.row0 + j) * p.Hq + (int64_t)sg.h * p.G + (r - j * p.G)] =
+            L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+      }
     }
-    const int r = sg.r0 + row, j = r / p.G;
-    const int64_t at = (int64_t)(sg.row0 + j) * p.Hq + (int64_t)sg.h * p.G + (r - j * p.G);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    if (d4 * 4 < p.c.D)
-      *reinterpret_cast<uint2*>(p.out + at * p.c.D + d4 * 4) =
-          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (d4 == 0 && p.lse != nullptr)
-      p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    soft_sync();
+    for (int task = tid; task < g * (DP / 8); task += kSoftThreads) {
+      const int d8 = task / g, row = task - d8 * g;
+      if (d8 * 8 >= p.c.D) break;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 4
+      for (int b = 0; b < np; ++b) {
+        const float4* r = reinterpret_cast<const float4*>(part(b)) + (size_t)d8 * 2 * ROWS + r0 + row;
+        const float4 u = __ldcg(r), v = __ldcg(r + ROWS);
+        const float f = buf[b * g + row].x;
+        x.x = fmaf(u.x, f, x.x);
+        x.y = fmaf(u.y, f, x.y);
+        x.z = fmaf(u.z, f, x.z);
+        x.w = fmaf(u.w, f, x.w);
+        y.x = fmaf(v.x, f, y.x);
+        y.y = fmaf(v.y, f, y.y);
+        y.z = fmaf(v.z, f, y.z);
+        y.w = fmaf(v.w, f, y.w);
+      }
+      const int r = sg.r0 + r0 + row, j = p.by_G(r);
+      const int64_t at = (int64_t)(sg.row0 + j) * p.Hq + (int64_t)sg.h * p.G + (r - j * p.G);
+      *reinterpret_cast<uint4*>(p.out + at * p.c.D + d8 * 8) =
+          make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y),
+                     pack_bf16(y.z, y.w));
+    }
+    soft_sync();
   }
 }
 
@@ -459,17 +526,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t b_q = b_segEmpty + 8 * kSegDepth;
   const uint32_t b_s = b_q + 8, b_p = b_s + 16, b_o = b_p + 16, b_drain = b_o + 16;
   volatile int* s_abort = reinterpret_cast<volatile int*>(bars + S::kBars);
-  volatile int* s_n = s_abort + 1;
-  volatile int* s_last = s_abort + 2;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + S::kBars) + 3;
-  volatile int64_t* s_before = reinterpret_cast<volatile int64_t*>(s_abort + 4);
+  volatile int* s_last = s_abort + 1;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + S::kBars) + 2;
+  Found* s_found = reinterpret_cast<Found*>(bars + S::kBars + 2);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t* status = p.c.status;
 
   if (tid == 0) {
     *s_abort = 0;
-    *s_n = 0;
-    *s_before = 0;
     for (int i = 0; i < NS; ++i) {
       mbar_init(b_full + 8 * i, 1);
       mbar_init(b_empty + 8 * i, 1);
@@ -487,12 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(b_drain, 1);
     fence_mbar_init();
   }
-  const Range rg = plan<kRows>(p, reinterpret_cast<int64_t*>(s_xch), s_n, s_before);
-  if (rg.u0 >= rg.u1) return;  // no tiles for this block
-  if (smem_u32(smem) & 1023) {  // the swizzled tiles need it
-    set_flag(status, kFlagWaitTimeout);
-    return;
-  }
+  const Range rg = plan<kRows>(p, reinterpret_cast<int64_t*>(s_xch), s_found);
+  if (rg.u0 >= rg.u1) return;       // no tiles for this block
+  if (smem_u32(smem) & 1023) return;  // never: the declared alignment, which the swizzle needs
   if (warp == kWarpMma) {
     tmem_alloc(smem_u32(s_tmem), kTmemCols);
     tmem_relinquish();
@@ -515,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch(&tm_v);
       }
       int n = rg.n;
-      Req q = load_req(p, n);
+      Req q = rg.q;
       int64_t u = rg.u0;
       int qts = row_tiles<kRows>(p, q.m), qt = 0, h, off;
       {
@@ -541,8 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           qt += 32;
         }
         const int nt = item_of<kRows>(p, q, qt).ntiles;
-        h = (int)(v / nt);
-        off = (int)(v % nt);
+        h = v < (1ll << 31) ? (int)((uint32_t)v / (uint32_t)nt) : (int)(v / nt);
+        off = (int)(v - (int64_t)h * nt);
       }
       int64_t seq = 0;  // tiles loaded; K is ring entry 2 seq, V 2 seq + 1
       bool ok = true;
@@ -563,10 +624,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         sg.hi = it.hi;
         sg.tile0 = it.tile0 + off;
         sg.ntiles = end ? 0 : (int)min((int64_t)(it.ntiles - off), rg.u1 - u);
-        const int64_t a = u - off, b = a + it.ntiles - 1;
-        sg.first = (int)(((a + 1) * rg.ctas - 1) / rg.total);
-        sg.last = (int)(((b + 1) * rg.ctas - 1) / rg.total);
-        sg.split = sg.first == sg.last ? 0 : (int)blockIdx.x == sg.first ? 2 : 1;
+        sg.split = sg.first = sg.last = 0;
+        if (off != 0 || sg.ntiles != it.ntiles) {
+          sg.first = rg.block_of(u - off);
+          sg.last = rg.block_of(u - off + it.ntiles - 1);
+          sg.split = (int)blockIdx.x == sg.first ? 2 : 1;
+        }
         if (lane == 0) {
           s_seg[ss] = sg;
           mbar_arrive(b_segFull + 8 * ss);
@@ -778,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = r_first + row % rp;
           uint4 x = make_uint4(0, 0, 0, 0);
           if (r < sg.r0 + sg.nrows && ch * 8 < p.c.D) {
-            const int j = r / p.G;
+            const int j = p.by_G(r);
             x = __ldg(reinterpret_cast<const uint4*>(
                 p.q + (int64_t)(sg.row0 + j) * p.q_stride +
                 ((int64_t)sg.h * p.G + (r - j * p.G)) * p.c.D + ch * 8));
@@ -793,13 +856,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this thread's row and the positions it sees
       const int my = (two ? s * 128 : 0) + lrow % rp;
       const bool live = my < sg.nrows;
-      const int pos = sg.ctx + (sg.r0 + my) / p.G;
+      const int pos = sg.ctx + p.by_G(sg.r0 + my);
       const int row_hi = !live ? 0x7fffffff : p.causal ? pos + 1 : sg.ctx + sg.m;
       const int row_lo = !live || p.window == 0 ? 0 : pos - p.window + 1;
       const int first_r = sg.r0 + (two ? s * 128 : 0);
       const int last_r = sg.r0 + min(sg.nrows, first_r - sg.r0 + 128) - 1;
-      const int min_hi = p.causal ? sg.ctx + first_r / p.G + 1 : sg.ctx + sg.m;
-      const int max_lo = p.window == 0 ? 0 : sg.ctx + last_r / p.G - p.window + 1;
+      const int min_hi = p.causal ? sg.ctx + p.by_G(first_r) + 1 : sg.ctx + sg.m;
+      const int max_lo = p.window == 0 ? 0 : sg.ctx + p.by_G(last_r) - p.window + 1;
       const int nc = 4 / rep, col0 = two ? 0 : (lrow / rp) * (kBN / rep);
 
       float m_ref = -INFINITY, l = 0.f;
@@ -846,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    ((size_t)blockIdx.x * 2 + (sg.split == 2 ? 1 : 0)) * record_floats<DP>(kRows);
       const float mine = m_ref == -INFINITY ? -INFINITY : m_ref * c2;
       if (two) {
-        const int r = sg.r0 + my, j = r / p.G;
+        const int r = sg.r0 + my, j = p.by_G(r);
         const int64_t at = (int64_t)(sg.row0 + j) * p.Hq + (int64_t)sg.h * p.G + (r - j * p.G);
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -881,57 +944,72 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.lse[at] = l == 0.f ? -INFINITY : (mine + log2f(l)) * kLn2;
         }
       } else {
-        // the copies of a row in the two streams: a common reference first
-        s_xch[tid] = make_float2(has ? mine : -INFINITY, has ? l : 0.f);
+        // the copies of a row in the streams: a common reference first
+        const int parts = sg.ntiles > 1 ? 2 * rep : rep;
+        s_xch[tid] = make_float2(mine, l);
         soft_sync();
         const int rr = lrow % rp;
         float M = -INFINITY, L = 0.f;
-        for (int a = 0; a < 2 * rep; ++a) M = fmaxf(M, s_xch[a * rp + rr].x);
-        for (int a = 0; a < 2 * rep; ++a) {
-          const float2 ml = s_xch[a * rp + rr];
-          L = fmaf(ml.y, ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M), L);
-        }
-        const float w = !has || mine == -INFINITY ? 0.f : ex2_approx(mine - M);
+#pragma unroll
+        for (int a = 0; a < 8; ++a)
+          if (a < parts) M = fmaxf(M, s_xch[a * rp + rr].x);
+#pragma unroll
+        for (int a = 0; a < 8; ++a)
+          if (a < parts) {
+            const float2 ml = s_xch[a * rp + rr];
+            L = fmaf(ml.y, ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M), L);
+          }
+        const float w = mine == -INFINITY ? 0.f : ex2_approx(mine - M);
         soft_sync();
         if (tid < rp) s_xch[tid] = make_float2(M, L);
-        float* buf = reinterpret_cast<float*>(s_q);  // Q is no longer read
+        // then their sums through shared memory (Q is no longer read): as many
+        // columns a round as 32 KB hold for the rows there are
+        float* buf = reinterpret_cast<float*>(s_q);
+        const int brows = sg.nrows <= 8 ? 8 : sg.nrows <= 16 ? 16 : rp;
+        const int cw = min(DP, 8192 / (2 * rep * brows)), log_c4 = 31 - __clz(cw >> 2);
+        const int brow = (tid / rp) * brows + rr;
 #pragma unroll 1
-        for (int ch = 0; ch < DP; ch += 32) {
-          uint32_t o[32];
+        for (int ch = 0; ch < DP; ch += cw) {
           __syncwarp();
           if (has) {
-            tmem_ld_32x32b_x32(t_o + ch, o);
-            tmem_wait_ld_regs(o);
-          }
+#pragma unroll 1
+            for (int c = 0; c < cw; c += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(t_o + ch + c, o);
+              tmem_wait_ld_regs(o);
+              if (rr < brows) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (has)
-              x = make_float4(__uint_as_float(o[4 * i]) * w, __uint_as_float(o[4 * i + 1]) * w,
-                              __uint_as_float(o[4 * i + 2]) * w,
-                              __uint_as_float(o[4 * i + 3]) * w);
-            *reinterpret_cast<float4*>(buf + tid * 32 + ((i ^ (tid & 7)) << 2)) = x;
+                for (int i = 0; i < 8; ++i)
+                  *reinterpret_cast<float4*>(buf + brow * cw + c + ((i ^ (brow & 7)) << 2)) =
+                      make_float4(__uint_as_float(o[4 * i]) * w, __uint_as_float(o[4 * i + 1]) * w,
+                                  __uint_as_float(o[4 * i + 2]) * w,
+                                  __uint_as_float(o[4 * i + 3]) * w);
+              }
+              __syncwarp();
+            }
           }
           soft_sync();
-          for (int task = tid; task < rp * 8; task += kSoftThreads) {
-            const int row = task >> 3, d4 = task & 7;
+          for (int task = tid; task < brows << log_c4; task += kSoftThreads) {
+            const int row = task >> log_c4, d4 = task & ((1 << log_c4) - 1);
             if (row >= sg.nrows) break;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int a = 0; a < 2 * rep; ++a) {
-              const int src = a * rp + row;
-              const float4 y =
-                  *reinterpret_cast<const float4*>(buf + src * 32 + ((d4 ^ (src & 7)) << 2));
-              x.x += y.x;
-              x.y += y.y;
-              x.z += y.z;
-              x.w += y.w;
-            }
+#pragma unroll
+            for (int a = 0; a < 8; ++a)
+              if (a < parts) {
+                const int src = a * brows + row;
+                const float4 y =
+                    *reinterpret_cast<const float4*>(buf + src * cw + ((d4 ^ (src & 7)) << 2));
+                x.x += y.x;
+                x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
+              }
             if (sg.split != 0) {
               __stcg(reinterpret_cast<float4*>(rec) + (size_t)(ch / 4 + d4) * kRows + row, x);
             } else if (ch + d4 * 4 < p.c.D) {
               const float Lr = s_xch[row].y;
               const float inv = Lr == 0.f ? 0.f : 1.f / Lr;
-              const int r = sg.r0 + row, j = r / p.G;
+              const int r = sg.r0 + row, j = p.by_G(r);
               const int64_t at =
                   (int64_t)(sg.row0 + j) * p.Hq + (int64_t)sg.h * p.G + (r - j * p.G);
               *reinterpret_cast<uint2*>(p.out + at * p.c.D + ch + d4 * 4) =
@@ -944,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (sg.split != 0) {
             __stcg(reinterpret_cast<float2*>(rec + (size_t)kRows * DP) + tid, make_float2(M, L));
           } else if (p.lse != nullptr) {
-            const int r = sg.r0 + tid, j = r / p.G;
+            const int r = sg.r0 + tid, j = p.by_G(r);
             p.lse[(int64_t)(sg.row0 + j) * p.Hq + (int64_t)sg.h * p.G + (r - j * p.G)] =
                 L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
           }
@@ -962,7 +1040,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         soft_sync();
         if (*s_last) {
           __threadfence();
-          join<DP, kRows>(p, sg);
+          join<DP, kRows>(p, sg, reinterpret_cast<float2*>(s_q));
         }
       }
       tc_fence_before();
@@ -1004,6 +1082,7 @@ cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t st) {
   p.c = a.c;
   p.Hq = a.Hq;
   p.G = a.Hq / a.c.Hkv;
+  p.by_G = divider(p.G);
   p.max_rows = a.max_rows;
   p.causal = a.causal;
   p.window = a.window;
