@@ -1,0 +1,513 @@
+// What the attention kernels share (attend_few.cu, attend_many.cu): the split of
+// the work over the blocks, the load of the pages, and the join of partial results.
+//
+// For each request and key/value head h, the rows of all G = Hq / Hkv query heads
+// that share h are packed, r = j * G + g, and cut into row tiles; an item is one row
+// tile of one head of one request, its work the tiles of 128 positions that its
+// rows see.  All items' tiles, in the order (request, row tile, head, position),
+// are split evenly over the blocks: a block that gets part of an item leaves
+// its O, m, l in the workspace, and the last of the item's blocks to finish joins
+// them in block order (results do not depend on which one that is).  The lengths are
+// read on the device: every block finds its own range with a scan over the
+// requests.  The TMA warp walks the range and hands the others their parts of items
+// through a short queue of segments.
+#pragma once
+
+#include "cache.cuh"
+#include "f32x2.cuh"
+#include "sm100.cuh"
+
+namespace dspark {
+namespace attend {
+
+using namespace sm100;
+
+constexpr int kBN = 128;               // positions a tile
+constexpr int kSoftThreads = 256;      // the two softmax warpgroups, warps 0-7
+constexpr int kWarpMma = 8;
+constexpr int kWarpTma = 9;
+constexpr int kSegDepth = 4;
+constexpr int kMaxCtas = 160;
+constexpr int kMaxSmem = 232448;
+constexpr uint32_t kHalf = kBN * 128;  // bytes of 128 rows of 128 bytes
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 8.0f;          // log2 growth of a maximum that moves the reference
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint32_t kCounterOffset = 256;  // workspace: status word, counters, partials
+constexpr uint32_t kPartOffset = 4096;
+constexpr int kMinTiles = 2;
+
+// n / d for 0 <= n < 2^31 by a multiplication (d fixed for the launch): with
+// 2^(s-1) < d <= 2^s and mul = floor(2^32 (2^s - d) / d) + 1, n / d is
+// (mulhi(n, mul) + n) >> s (Granlund and Montgomery 1994).
+struct Divider {
+  uint32_t mul, shift;
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+  }
+};
+inline Divider divider(int d) {
+  Divider v;
+  v.shift = 0;
+  while ((1ll << v.shift) < d) ++v.shift;
+  v.mul = (uint32_t)(((1ull << 32) * ((1ull << v.shift) - d)) / d + 1);
+  return v;
+}
+
+struct Params {
+  CacheView c;
+  int Hq, G, max_rows, causal, window;
+  Divider by_G;
+  float scale;
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  __nv_bfloat16* out;
+  float* lse;
+  unsigned* counters;  // [kMaxCtas], zero between calls
+  float* part;         // [kMaxCtas][2] records: O, then (m, l) [rows]
+};
+
+__host__ __device__ constexpr size_t record_floats(int rows, int DP) {
+  return (size_t)rows * DP + (size_t)rows * 2;
+}
+
+struct Req {
+  int row0, m, ctx;
+  int tiles, rows;  // row tiles, and the packed rows of each (the last may have fewer)
+};
+
+// Request n's rows and context, clamped so that whatever the tables hold no
+// address is out of range and no loop is long.
+template <int ROWS>
+__device__ __forceinline__ Req load_req(const Params& p, int n) {
+  int a = __ldg(p.c.row_off + n), b = __ldg(p.c.row_off + n + 1), ctx = __ldg(p.c.ctx + n);
+  a = min(max(a, 0), p.c.T);
+  b = min(max(b, a), p.c.T);
+  const int cap = p.c.max_pages << p.c.log_page;
+  Req r;
+  r.row0 = a;
+  r.m = min(b - a, p.max_rows);
+  r.ctx = min(max(ctx, -(1 << 29)), cap);
+  // as few tiles as hold the rows, all of one size: the tile count measures the work
+  const int M = r.m * p.G;
+  r.tiles = (M + ROWS - 1) / ROWS;
+  r.rows = r.tiles > 1 ? (M + r.tiles - 1) / r.tiles : M;
+  return r;
+}
+
+// The rows and positions of one item.
+struct Item {
+  int r0, nrows, lo, hi, tile0, ntiles;
+};
+__device__ __forceinline__ Item item_of(const Params& p, const Req& q, int qt) {
+  Item it;
+  it.r0 = qt * q.rows;
+  it.nrows = min(q.rows, q.m * p.G - it.r0);
+  const int j0 = p.by_G(it.r0), j1 = p.by_G(it.r0 + it.nrows - 1);
+  it.hi = max(p.causal ? q.ctx + j1 + 1 : q.ctx + q.m, 0);
+  it.lo = p.window > 0 ? min(max(q.ctx + j0 - p.window + 1, 0), it.hi) : 0;
+  it.tile0 = it.lo / kBN;
+  it.ntiles = max(1, (it.hi + kBN - 1) / kBN - it.tile0);
+  return it;
+}
+
+// Where packed row r of head h goes: its index in [T][Hq].
+__device__ __forceinline__ int64_t out_row(const Params& p, int row0, int h, int r) {
+  const int j = p.by_G(r);
+  return (int64_t)(row0 + j) * p.Hq + (int64_t)h * p.G + (r - j * p.G);
+}
+// Its query: 8 values from d on (zeros past D).
+__device__ __forceinline__ uint4 load_q(const Params& p, int row0, int h, int r, int d) {
+  if (d >= p.c.D) return make_uint4(0, 0, 0, 0);
+  const int j = p.by_G(r);
+  return __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)(row0 + j) * p.q_stride +
+                                              ((int64_t)h * p.G + (r - j * p.G)) * p.c.D + d));
+}
+
+struct Segment {  // part of an item that this block computes
+  int row0, m, ctx, h, r0, nrows, lo, hi, tile0, ntiles;
+  int split;        // 0: the whole item, 1 / 2: its partial result goes to record 0 / 1
+  int first, last;  // the item's blocks
+  int pad[3];
+};
+static_assert(sizeof(Segment) == 64, "a segment's words");
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                         uint32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait_sleep(bar, parity, 1000)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kWaitNs) {
+      *abort_flag = 1;
+      set_flag(status, kFlagWaitTimeout);
+      return false;
+    }
+  }
+}
+
+// Registers a thread after the roles part.
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Barrier `id` of n threads; the second form tells each whether any brought `v`.
+__device__ __forceinline__ void group_sync(int id, int n) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ bool group_any(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void soft_sync() { group_sync(1, kSoftThreads); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Blocks 0 .. ctas-1 take `each` tiles, the first `extra` of them one more.
+struct Range {
+  int64_t each, u0, u1;  // u0 .. u1 - 1: this block's tiles
+  int ctas, extra;
+  int n;                 // the request of tile u0
+  int64_t before;        // tiles of the requests before n
+  Req q;                 // request n
+
+  __device__ __forceinline__ int block_of(int64_t u) const {
+    const int64_t wide = extra * (each + 1);
+    return u < wide ? (int)(u / (each + 1)) : extra + (int)((u - wide) / each);
+  }
+};
+struct Found {  // the request of a block's first tile, from the thread that finds it
+  int64_t before;
+  int n;
+  Req q;
+};
+
+// Tiles of a request over all heads and every step-th row tile from `first` on.
+__device__ __forceinline__ int64_t req_tiles(const Params& p, const Req& q, int first, int step) {
+  int64_t u = 0;
+#pragma unroll 1
+  for (int qt = first; qt < q.tiles; qt += step) u += item_of(p, q, qt).ntiles;
+  return u * p.c.Hkv;
+}
+
+// Every block's range of tiles, from a scan over the requests (all threads).
+template <int ROWS, int THREADS>
+__device__ __forceinline__ Range plan(const Params& p, int64_t* s_sum, Found* s_found) {
+  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const int per = (p.c.R + THREADS - 1) / THREADS;
+  int64_t local = 0;
+  Req q = {};
+#pragma unroll 1
+  for (int i = 0; i < per; ++i) {
+    const int n = tid * per + i;
+    q = Req{};
+    if (n < p.c.R) q = load_req<ROWS>(p, n);
+    const bool many = q.tiles > 4;
+    if (!many) local += req_tiles(p, q, 0, 1);
+    // requests of many row tiles: the warp together
+    for (uint32_t left = __ballot_sync(0xffffffffu, many); left != 0; left &= left - 1) {
+      const int src = __ffs(left) - 1;
+      Req o;
+      o.row0 = 0;
+      o.m = __shfl_sync(0xffffffffu, q.m, src);
+      o.ctx = __shfl_sync(0xffffffffu, q.ctx, src);
+      o.tiles = __shfl_sync(0xffffffffu, q.tiles, src);
+      o.rows = __shfl_sync(0xffffffffu, q.rows, src);
+      int64_t u = req_tiles(p, o, lane, 32);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
+      if (lane == src) local += u;
+    }
+  }
+  int64_t incl = local;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) s_sum[wid] = incl;
+  __syncthreads();
+  int64_t base = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < wid) base += s_sum[w];
+    total += s_sum[w];
+  }
+  Range r;
+  // few tiles: fewer blocks, kMinTiles each, rather than more partial results
+  r.ctas = (int)min((int64_t)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
+  r.u0 = r.u1 = 0;
+  if ((int)blockIdx.x >= r.ctas) return r;
+  r.each = total < (1ll << 31) ? (int64_t)((uint32_t)total / (uint32_t)r.ctas) : total / r.ctas;
+  r.extra = (int)(total - r.each * r.ctas);
+  r.u0 = r.each * blockIdx.x + min((int)blockIdx.x, r.extra);
+  r.u1 = r.u0 + r.each + ((int)blockIdx.x < r.extra);
+  int64_t at = base + incl - local;
+  if (at <= r.u0 && r.u0 < at + local) {
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+      const int n = tid * per + i;
+      if (n >= p.c.R) break;
+      if (per > 1) q = load_req<ROWS>(p, n);
+      const int64_t u = per == 1 ? local : req_tiles(p, q, 0, 1);
+      if (r.u0 < at + u) {
+        s_found->n = n;
+        s_found->before = at;
+        s_found->q = q;
+        break;
+      }
+      at += u;
+    }
+  }
+  __syncthreads();
+  r.n = s_found->n;
+  r.before = s_found->before;
+  r.q = s_found->q;
+  return r;
+}
+
+// The TMA warp: walks the block's range, queues its segments (an empty one at the
+// end) and has `load(rows, none)` load each tile: rows[b] is the pool's row of box
+// b's first position, or `none` (past the pool, so that the box reads as zeros)
+// where no row of the item sees the box.  Stops when a wait of load's failed.
+template <int ROWS, class Load>
+__device__ __forceinline__ void produce(const Params& p, const Range& rg, Segment* s_seg,
+                                        uint32_t b_segFull, uint32_t b_segEmpty,
+                                        volatile int* s_abort, Load&& load) {
+  const int lane = threadIdx.x & 31;
+  const int log_page = p.c.log_page, page = 1 << log_page;
+  const int box_rows = min(page, kBN), n_boxes = kBN / box_rows;
+  const int none = (int)(p.c.n_pages * p.c.Hkv) << log_page;
+  int n = rg.n;
+  Req q = rg.q;
+  int64_t u = rg.u0;
+  int qt = 0, h, off;
+  {
+    // the row tile, head and position tile of u0 within its request
+    int64_t v = u - rg.before;
+    while (q.tiles > 1) {
+      const int64_t mine = qt + lane < q.tiles ? (int64_t)item_of(p, q, qt + lane).ntiles * p.c.Hkv
+                                               : 0;
+      int64_t incl = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, v < incl);
+      if (past != 0 || qt + 32 >= q.tiles) {
+        const int src = past != 0 ? __ffs(past) - 1 : 0;
+        v -= __shfl_sync(0xffffffffu, incl - mine, src);
+        qt += src;
+        break;
+      }
+      v -= __shfl_sync(0xffffffffu, incl, 31);
+      qt += 32;
+    }
+    const int nt = item_of(p, q, qt).ntiles;
+    h = v < (1ll << 31) ? (int)((uint32_t)v / (uint32_t)nt) : (int)(v / nt);
+    off = (int)(v - (int64_t)h * nt);
+  }
+#pragma unroll 1
+  for (int sn = 0;; ++sn) {
+    const int ss = sn % kSegDepth;
+    const bool ok =
+        wait_bar(b_segEmpty + 8 * ss, ((sn / kSegDepth) & 1) ^ 1, s_abort, p.c.status);
+    if (!__all_sync(0xffffffffu, ok)) return;
+    Segment sg;
+    const Item it = item_of(p, q, qt);
+    const bool end = u >= rg.u1;
+    sg.row0 = q.row0;
+    sg.m = q.m;
+    sg.ctx = q.ctx;
+    sg.h = h;
+    sg.r0 = it.r0;
+    sg.nrows = it.nrows;
+    sg.lo = it.lo;
+    sg.hi = it.hi;
+    sg.tile0 = it.tile0 + off;
+    sg.ntiles = end ? 0 : (int)min((int64_t)(it.ntiles - off), rg.u1 - u);
+    sg.split = sg.first = sg.last = 0;
+    if (off != 0 || sg.ntiles != it.ntiles) {
+      sg.first = rg.block_of(u - off);
+      sg.last = rg.block_of(u - off + it.ntiles - 1);
+      sg.split = (int)blockIdx.x == sg.first ? 2 : 1;
+    }
+    if (lane == 0) {
+      s_seg[ss] = sg;
+      mbar_arrive(b_segFull + 8 * ss);
+    }
+    if (end) return;
+    if (lane == 0 && __ldg(p.c.row_off + n + 1) - __ldg(p.c.row_off + n) > p.max_rows)
+      set_flag(p.c.status, kFlagRowRange);
+    auto lookup = [&](int tile) {  // lane b: box b
+      if (lane >= n_boxes) return none;
+      const int pos = tile * kBN + lane * box_rows;
+      if (pos >= sg.hi || pos + box_rows <= sg.lo) return none;
+      const int64_t id = page_of(p.c, n, pos);
+      if (id < 0) return none;
+      return (int)((id * p.c.Hkv + h) << log_page) + (pos & (page - 1));
+    };
+    int next = lookup(sg.tile0);
+#pragma unroll 1
+    for (int i = 0; i < sg.ntiles; ++i) {
+      int y[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) y[b] = __shfl_sync(0xffffffffu, next, b);
+      if (i + 1 < sg.ntiles) next = lookup(sg.tile0 + i + 1);  // in flight under the waits
+      if (!load(y, none)) return;
+    }
+    u += sg.ntiles;
+    off = 0;
+    if (sg.tile0 + sg.ntiles == it.tile0 + it.ntiles && ++h == p.c.Hkv) {
+      h = 0;
+      if (++qt == q.tiles) {
+        qt = 0;
+        while (u < rg.u1 && ++n < p.c.R) {
+          q = load_req<ROWS>(p, n);
+          if (q.tiles > 0) break;
+        }
+      }
+    }
+  }
+}
+
+// Joins the partial results of an item's blocks (all softmax threads of the last
+// one to finish).  `buf`, 32 KB of shared memory: the blocks' (m, l) of a
+// group of rows, then their weights 2^(m - M) / L; the sums run over the blocks in
+// order, eight values a thread.  kLanesOnRows: records hold O as [DP / 4][ROWS][4],
+// else [ROWS][DP]; a warp's loads are contiguous either way.
+template <int DP, int ROWS, bool kLanesOnRows>
+__device__ __forceinline__ void join(const Params& p, const Segment& sg, float2* buf) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int np = sg.last - sg.first + 1;
+  constexpr size_t rec = record_floats(ROWS, DP);
+  const float* rec0 = p.part + ((size_t)sg.first * 2 + 1) * rec;  // the first block's, then
+  const float* recs = p.part + ((size_t)sg.first * 2 + 2) * rec;  // two records a block on
+  auto part = [&](int i) { return i == 0 ? rec0 : recs + (size_t)(i - 1) * 2 * rec; };
+  const int group = min(sg.nrows, 4096 / np);
+#pragma unroll 1
+  for (int r0 = 0; r0 < sg.nrows; r0 += group) {
+    const int g = min(group, sg.nrows - r0);
+#pragma unroll 1
+    for (int i = tid; i < np * g; i += kSoftThreads) {
+      const int b = i / g, row = i - b * g;
+      buf[i] = __ldcg(reinterpret_cast<const float2*>(part(b) + (size_t)ROWS * DP) + r0 + row);
+    }
+    soft_sync();
+#pragma unroll 1
+    for (int row = warp; row < g; row += kSoftThreads / 32) {
+      float M = -INFINITY, L = 0.f;
+      for (int b = lane; b < np; b += 32) M = fmaxf(M, buf[b * g + row].x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      for (int b = lane; b < np; b += 32) {
+        const float2 ml = buf[b * g + row];
+        L = fmaf(ml.y, ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M), L);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      for (int b = lane; b < np; b += 32) {
+        const float m = buf[b * g + row].x;
+        buf[b * g + row].x = m == -INFINITY ? 0.f : ex2_approx(m - M) * inv;
+      }
+      if (lane == 0 && p.lse != nullptr)
+        p.lse[out_row(p, sg.row0, sg.h, sg.r0 + r0 + row)] =
+            L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    }
+    soft_sync();
+#pragma unroll 1
+    for (int task = tid; task < g * (DP / 8); task += kSoftThreads) {
+      const int d8 = kLanesOnRows ? task / g : task % (DP / 8);
+      const int row = kLanesOnRows ? task - d8 * g : task / (DP / 8);
+      if (d8 * 8 >= p.c.D) continue;
+      const size_t at = kLanesOnRows ? (size_t)d8 * 2 * ROWS + r0 + row
+                                     : (size_t)(r0 + row) * (DP / 4) + d8 * 2;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 1
+      for (int b0 = 0; b0 < np; b0 += 4) {
+        float4 u[4], v[4];  // four blocks' loads in flight
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (b0 + i < np) {
+            const float4* r = reinterpret_cast<const float4*>(part(b0 + i)) + at;
+            u[i] = __ldcg(r);
+            v[i] = __ldcg(r + (kLanesOnRows ? ROWS : 1));
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (b0 + i < np) {
+            const float f = buf[(b0 + i) * g + row].x;
+            x.x = fmaf(u[i].x, f, x.x);
+            x.y = fmaf(u[i].y, f, x.y);
+            x.z = fmaf(u[i].z, f, x.z);
+            x.w = fmaf(u[i].w, f, x.w);
+            y.x = fmaf(v[i].x, f, y.x);
+            y.y = fmaf(v[i].y, f, y.y);
+            y.z = fmaf(v[i].z, f, y.z);
+            y.w = fmaf(v[i].w, f, y.w);
+          }
+      }
+      *reinterpret_cast<uint4*>(p.out + out_row(p, sg.row0, sg.h, sg.r0 + r0 + row) * p.c.D +
+                                d8 * 8) =
+          make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y),
+                     pack_bf16(y.z, y.w));
+    }
+    soft_sync();
+  }
+}
+
+// After a block wrote its part of a split item (all softmax threads): the last of
+// the item's blocks joins.  s_last is a word of shared memory, buf 32 KB.
+template <int DP, int ROWS, bool kLanesOnRows>
+__device__ __forceinline__ void finish_split(const Params& p, const Segment& sg,
+                                             volatile int* s_last, float2* buf) {
+  __threadfence();
+  soft_sync();
+  if (threadIdx.x == 0) {
+    const unsigned want = (unsigned)(sg.last - sg.first);
+    const unsigned old = atomicAdd(p.counters + sg.first, 1u);
+    *s_last = old == want;
+    if (old == want) p.counters[sg.first] = 0;
+  }
+  soft_sync();
+  if (*s_last) {
+    __threadfence();
+    join<DP, ROWS, kLanesOnRows>(p, sg, buf);
+  }
+}
+
+}  // namespace attend
+
+// The kernels' launchers (attend_few.cu, attend_many.cu).
+cudaError_t launch_attend_few(const AttendArgs& a, const attend::Params& p, cudaStream_t st);
+cudaError_t launch_attend_many(const AttendArgs& a, const attend::Params& p, cudaStream_t st);
+
+}  // namespace dspark

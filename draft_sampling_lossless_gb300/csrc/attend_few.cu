@@ -1,0 +1,751 @@
+// Attention of up to 32 packed rows a head (single tokens, verified blocks) over
+// the paged cache.
+//
+// HBM bounds it: a position's key and value (512 bytes of bf16 at D = 128) meet
+// 32 rows at most, far below the tensor cores' 284 operations a byte.  What is left
+// is to keep up with the loads, so both products are turned over, with the
+// positions or D as the 128 MMA rows and the few packed rows as N:
+//
+//   S^T = K Q^T    (128 positions x rows),   O^T = V^T P^T   (D x rows)
+//
+// A softmax thread is a position: it has that position's scores of all rows,
+// sums its own exponentials (joined over the positions once, at the end), and no
+// maximum is taken per tile.  P = 2^(s - m) against a reference m of each row that
+// only moves, for all rows at once, when some score passes it by 8 powers of
+// two: any reference gives the same quotient and fp32 has the range.
+//
+// P enters its product as two 16-bit terms, its rounding and the rounding of the
+// rest (columns of N side by side; a row that one position dominates would
+// otherwise carry that rounding straight into the result).
+//
+// bf16: K tiles (as A, K-major) and V tiles (as A, transposed) are multiplied where
+// the TMA put them.  e4m3: K's codes are A of an e4m3 product, with Q as two e4m3
+// terms, q 2^-a = q1 + q2 / 16, which hold a bf16's eight bits exactly (down to
+// 2^-13 of the row's largest; below, to 2^-21 of it); its scale is the
+// thread's own position's, a factor of the scores.  V's codes become halves,
+// exactly, on the way to shared memory (four more warps), and its scale goes into
+// P: P = 2^(s + e - m) with e its exponent, and l sums 2^-e P.
+//
+// Two streams, a warpgroup each with its own S, P, O and m, take alternate tiles.
+// See attend.cuh for the split of the work.
+#include "attend.cuh"
+
+namespace dspark {
+
+namespace {
+
+using namespace attend;
+
+constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kColO = 128;       // S at 0 and 64, O at 128 and 192
+constexpr float kUnset = 3.0e38f;     // -m of a row that has seen nothing
+constexpr int kExpDepth = 8;          // tiles of exponent bytes held
+
+template <int DP, int NR, bool E4M3>
+struct Few {
+  static constexpr int kThreads = E4M3 ? 512 : 320;
+  static constexpr int kNH = DP / 64;
+  static constexpr int kQRows = E4M3 ? 2 * NR : (NR < 16 ? 16 : NR);  // N of the scores
+  static constexpr uint32_t kSlot = E4M3 ? kHalf : kHalf * kNH;       // a tile as loaded
+  static constexpr uint32_t kQHalf = kQRows * 128;
+  static constexpr uint32_t kQBytes = kQHalf * (E4M3 ? 1 : kNH);
+  static constexpr uint32_t kVf = E4M3 ? kHalf * kNH : 0;             // V as halves
+  static constexpr uint32_t kExp = E4M3 ? kExpDepth * 256 : 0;
+  static constexpr uint32_t kMisc = 4096;
+  static constexpr int kFit =
+      (int)((kMaxSmem - 2 * kHalf - kQBytes - 2 * kVf - kExp - kMisc) / kSlot);
+  static constexpr int kSlots = kFit > 12 ? 12 : kFit;
+  static constexpr uint32_t kPOff = kSlots * kSlot;  // P of each stream; the join's buffer
+  static constexpr uint32_t kVfOff = kPOff + 2 * kHalf;
+  static constexpr uint32_t kQOff = kVfOff + 2 * kVf;
+  static constexpr uint32_t kExpOff = kQOff + kQBytes;
+  static constexpr uint32_t kMiscOff = kExpOff + kExp;
+  static constexpr uint32_t kTotal = kMiscOff + kMisc;
+  static_assert(kTotal <= kMaxSmem && kSlots >= 4, "shared memory");
+};
+
+struct Misc {  // shared words
+  float nm[2][32];      // -m of each stream's rows
+  float f[2][32];       // what a move of the references multiplies by
+  float wm[2][4][32];   // the warps' maxima, then sums
+  float w[2][32];       // weights of the streams
+  float inv[32];
+  float a[32];          // scale of the scores of a row (e4m3: with that of q)
+  int64_t at[32];       // output rows
+  int64_t sum[16];
+  Found found;
+  Segment seg[kSegDepth];
+  uint64_t bars[2 * 12 + 2 * kSegDepth + 7 + 4 + kExpDepth + 1];
+  int abort_flag, last;
+  uint32_t tmem;
+};
+static_assert(sizeof(Misc) <= 4096, "shared words");
+
+// Reduces v[r] over a warp's lanes; row r's result lands in lanes r * 32 / NR on.
+template <int NR, class Op>
+__device__ __forceinline__ float reduce_rows(float (&v)[NR], Op op) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int half = NR / 2; half >= 1; half >>= 1, o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const bool up = lane & o;
+      const float keep = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+#pragma unroll
+  for (; o >= 1; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// The scores of a thread's position: x[r] = log2 of row r's exponential, up to the
+// reference (e4m3: times 2^e of the value's exponent e).
+template <int NR, bool E4M3>
+__device__ __forceinline__ void load_scores(uint32_t t_s, const Misc* ms, float c2, float ck,
+                                            float ev, float (&x)[NR]) {
+  if constexpr (!E4M3) {
+    uint32_t v[NR];
+    if constexpr (NR == 8)
+      tmem_ld_32x32b_x8(t_s, v);
+    else if constexpr (NR == 16)
+      tmem_ld_32x32b_x16(t_s, v);
+    else
+      tmem_ld_32x32b_x32(t_s, v);
+    tmem_wait_ld_regs(v);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) x[r] = __uint_as_float(v[r]) * c2;
+  } else {
+    constexpr int kB = NR < 16 ? NR : 16;
+#pragma unroll
+    for (int r0 = 0; r0 < NR; r0 += kB) {
+      uint32_t u[kB], v[kB];
+      if constexpr (kB == 8) {
+        tmem_ld_32x32b_x8(t_s + r0, u);
+        tmem_ld_32x32b_x8(t_s + NR + r0, v);
+      } else {
+        tmem_ld_32x32b_x16(t_s + r0, u);
+        tmem_ld_32x32b_x16(t_s + NR + r0, v);
+      }
+      tmem_wait_ld_regs(u, v);
+#pragma unroll
+      for (int r = 0; r < kB; r += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(ms->a + r0 + r);
+        const float af[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float y = fmaf(__uint_as_float(v[r + k]), 0.0625f, __uint_as_float(u[r + k]));
+          x[r0 + r + k] = fmaf(y * af[k], ck, ev);
+        }
+      }
+    }
+  }
+}
+
+template <int DP, int NR, bool E4M3>
+__global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
+    attend_few_kernel(const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
+  using F = Few<DP, NR, E4M3>;
+  constexpr int NS = F::kSlots, NH = F::kNH;
+  constexpr int kConvWarps = E4M3 ? 4 : 0;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Misc* ms = reinterpret_cast<Misc*>(smem + F::kMiscOff);
+  const uint32_t b_full = smem_u32(ms->bars), b_empty = b_full + 8 * NS;
+  const uint32_t b_segFull = b_empty + 8 * NS, b_segEmpty = b_segFull + 8 * kSegDepth;
+  const uint32_t b_q = b_segEmpty + 8 * kSegDepth;
+  const uint32_t b_s = b_q + 8, b_p = b_s + 16, b_o = b_p + 16;
+  const uint32_t b_vfFull = b_o + 16, b_vfEmpty = b_vfFull + 16, b_exp = b_vfEmpty + 16;
+  const uint32_t b_drain = b_exp + 8 * kExpDepth;
+  volatile int* s_abort = &ms->abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t* status = p.c.status;
+  if (smem_u32(smem) & 1023) return;  // never: the declared alignment, which the swizzle needs
+
+  if (tid == 0) {
+    *s_abort = 0;
+    for (int i = 0; i < 2 * NS; ++i) mbar_init(b_full + 8 * i, 1);
+    for (int i = 0; i < kSegDepth; ++i) {
+      mbar_init(b_segFull + 8 * i, 1);
+      mbar_init(b_segEmpty + 8 * i, 9 + kConvWarps);  // the MMA thread and the other warps
+    }
+    mbar_init(b_q, kSoftThreads);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_s + 8 * i, 1);
+      mbar_init(b_p + 8 * i, 128);
+      mbar_init(b_o + 8 * i, 1);
+      mbar_init(b_vfFull + 8 * i, 128);
+      mbar_init(b_vfEmpty + 8 * i, 1);
+    }
+    for (int i = 0; i < kExpDepth; ++i) mbar_init(b_exp + 8 * i, 1);
+    mbar_init(b_drain, 1);
+    fence_mbar_init();
+  }
+  const Range rg = plan<32, F::kThreads>(p, ms->sum, &ms->found);
+  if (rg.u0 >= rg.u1) return;  // no tiles for this block
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(&ms->tmem), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem;
+
+  // e4m3: 512 threads of 128 registers become 256 x 168, 128 x 80 and 128 x 88
+  if (warp == kWarpTma) {
+    if (E4M3) reg_dec<80>();
+    // ------------------------------------------------------------ loads
+    const int box_rows = min(1 << p.c.log_page, kBN), n_boxes = kBN / box_rows;
+    if (lane == 0) {
+      tma_prefetch(&tm_k);
+      tma_prefetch(&tm_v);
+    }
+    uint32_t seq = 0;  // tiles loaded; K is ring entry 2 seq, V 2 seq + 1
+    produce<32>(p, rg, ms->seg, b_segFull, b_segEmpty, s_abort, [&](const int (&y)[8], int none) {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t e = 2 * seq + kv, slot = e % NS;
+        const bool ok = wait_bar(b_empty + 8 * slot, ((e / NS) & 1) ^ 1, s_abort, status);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        if (elect_one()) {
+          const uint32_t full = b_full + 8 * slot;
+          const uint32_t dst = smem_u32(smem) + slot * F::kSlot;
+          mbar_arrive_expect_tx(full, F::kSlot);
+#pragma unroll
+          for (int b = 0; b < 8; ++b)
+            if (b < n_boxes) {
+              if constexpr (E4M3) {
+                tma_load_2d(dst + b * box_rows * 128, kv ? &tm_v : &tm_k, full, 0, y[b]);
+              } else {
+#pragma unroll
+                for (int half = 0; half < NH; ++half)
+                  tma_load_2d(dst + half * kHalf + b * box_rows * 128, kv ? &tm_v : &tm_k, full,
+                              half * 64, y[b]);
+              }
+            }
+          if constexpr (E4M3) {
+            // both exponent rows of the tile, with its K (a buffer of tile i is read
+            // before P of tile i, and tile i + 8 is not loaded before that)
+            if (kv == 0) {
+              const uint32_t be = b_exp + 8 * (seq % kExpDepth);
+              const uint32_t de = smem_u32(smem + F::kExpOff) + (seq % kExpDepth) * 256;
+              int n = 0;
+#pragma unroll
+              for (int b = 0; b < 8; ++b) {
+                if (b >= n_boxes) break;
+                if (y[b] != none) {
+                  ++n;
+                  continue;
+                }
+                // a box of zeros: any scale does, but not one that moves the reference
+                uint32_t* ex = reinterpret_cast<uint32_t*>(smem + F::kExpOff +
+                                                           (seq % kExpDepth) * 256 + b * box_rows);
+                for (int i = 0; i < box_rows / 4; ++i) ex[i] = ex[i + 32] = 0x7f7f7f7fu;
+              }
+              mbar_arrive_expect_tx(be, 2 * n * box_rows);
+              const uint64_t pol = policy_evict_first();
+#pragma unroll
+              for (int b = 0; b < 8; ++b)
+                if (b < n_boxes && y[b] != none) {
+                  bulk_load_hint(de + b * box_rows, p.c.k_exp + y[b], box_rows, be, pol);
+                  bulk_load_hint(de + 128 + b * box_rows, p.c.v_exp + y[b], box_rows, be, pol);
+                }
+            }
+          }
+        }
+        __syncwarp();
+      }
+      ++seq;
+      return true;
+    });
+    if (*s_abort) {
+      // the copies in flight land before the block's shared memory goes
+      const uint32_t done = 2 * seq;
+      for (uint32_t e = done > NS ? done - NS : 0; e < done; ++e)
+        mbar_wait(b_full + 8 * (e % NS), (e / NS) & 1);
+      if constexpr (E4M3)
+        for (uint32_t e = seq > kExpDepth ? seq - kExpDepth : 0; e < seq; ++e)
+          mbar_wait(b_exp + 8 * (e % kExpDepth), (e / kExpDepth) & 1);
+    }
+  } else if (warp == kWarpMma) {
+    if (E4M3) reg_dec<80>();
+    // ------------------------------------------------------------ products
+    if (elect_one()) {
+      constexpr uint32_t kIdS = E4M3 ? idesc_0_f32(128, F::kQRows) : idesc_bf16_f32(128, F::kQRows);
+      constexpr uint32_t kIdO = (E4M3 ? idesc_0_f32(128, 2 * NR) : idesc_bf16_f32(128, 2 * NR)) |
+                                kIdescTransposeA | kIdescTransposeB;
+      const int ksteps = E4M3 ? (p.c.D + 31) / 32 : p.c.D / 16;
+      const uint32_t at0 = smem_u32(smem);
+      uint32_t base = 0, ph_q = 0, ph_p = 0;  // base: tiles of the segments before
+      bool ok = true;
+      auto need = [&](uint32_t e) {
+        ok = ok && wait_bar(b_full + 8 * (e % NS), (e / NS) & 1, s_abort, status);
+        tc_fence_after();
+      };
+      auto scores = [&](int s, uint32_t e) {
+        const uint64_t a = desc_kmajor_sw128(at0 + (e % NS) * F::kSlot);
+        const uint64_t b = desc_kmajor_sw128(at0 + F::kQOff);
+        for (int k = 0; k < ksteps; ++k) {
+          if constexpr (E4M3)
+            mma_e4m3(tmem + s * 64, a + k * 2, b + k * 2, kIdS, k > 0);
+          else
+            mma_bf16(tmem + s * 64, a + (k >> 2) * (kHalf >> 4) + (k & 3) * 2,
+                     b + (k >> 2) * (F::kQHalf >> 4) + (k & 3) * 2, kIdS, k > 0);
+        }
+        mma_commit(b_s + 8 * s);
+        mma_commit(b_empty + 8 * (e % NS));
+      };
+      for (int sn = 0; ok; ++sn) {
+        const int ss = sn % kSegDepth;
+        ok = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status);
+        if (!ok) break;
+        const int nt = ms->seg[ss].ntiles;
+        mbar_arrive(b_segEmpty + 8 * ss);
+        if (nt == 0) break;
+        ok = wait_bar(b_q, ph_q, s_abort, status);
+        if (!ok) break;
+        ph_q ^= 1;
+        tc_fence_after();
+        const uint32_t e0 = 2 * base;  // K of tile i: e0 + 2 i, V: one more
+        for (int i = 0; i < 2 && i < nt && ok; ++i) {
+          need(e0 + 2 * i);
+          if (ok) scores(i, e0 + 2 * i);
+        }
+        for (int i = 0; i < nt && ok; ++i) {
+          const int s = i & 1;
+          const uint32_t ev = e0 + 2 * i + 1, vf = (base + i) & 1;
+          if constexpr (E4M3) {
+            ok = wait_bar(b_vfFull + 8 * vf, ((base + i) >> 1) & 1, s_abort, status);
+          } else {
+            need(ev);
+          }
+          ok = ok && wait_bar(b_p + 8 * s, (ph_p >> s) & 1, s_abort, status);
+          ph_p ^= 1u << s;
+          if (!ok) break;
+          tc_fence_after();
+          // D = 64: both groups of 64 MMA rows read the same values
+          const uint64_t a = desc_mnmajor_sw128(
+              E4M3 ? at0 + F::kVfOff + vf * F::kVf : at0 + (ev % NS) * F::kSlot,
+              NH > 1 ? kHalf : 0);
+          const uint64_t b = desc_mnmajor_sw128(at0 + F::kPOff + s * kHalf, 0);
+          for (int k = 0; k < kBN / 16; ++k)
+            mma_bf16(tmem + kColO + s * 64, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdO,
+                     i >= 2 || k > 0);
+          mma_commit(E4M3 ? b_vfEmpty + 8 * vf : b_empty + 8 * (ev % NS));
+          if (i + 2 < nt) {
+            need(ev + 3);
+            if (ok) scores(s, ev + 3);
+          } else {
+            mma_commit(b_o + 8 * s);
+          }
+        }
+        base += nt;
+      }
+      if (!ok) {
+        mma_commit(b_drain);
+        mbar_wait(b_drain, 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    if (E4M3) reg_inc<168>();
+    // ------------------------------------------------------------ softmax
+    const int s = warp >> 2;    // the stream
+    const int pt = tid & 127;   // position of the tile, value of D at the end
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + s * 64, t_o = tmem + lanes + kColO + s * 64;
+    const float c2 = p.scale * kLog2e;
+    uint8_t* my_p = smem + F::kPOff + s * kHalf + pt * 128;
+    uint32_t ph_s = 0, ph_o = 0, base = 0;
+    for (int sn = 0;; ++sn) {
+      const int ss = sn % kSegDepth;
+      const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status);
+      // all leave together; the barrier also ends the previous segment's use of Q
+      if (group_any(1, kSoftThreads, !got)) break;
+      const Segment sg = ms->seg[ss];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
+      if (sg.ntiles == 0) break;
+
+      // Q: 16 lanes a row, 8 values a lane; rows past the item's are zero
+#pragma unroll
+      for (int i = tid; i < (E4M3 ? NR : F::kQRows) * 16; i += kSoftThreads) {
+        const int row = i >> 4, ch = i & 15;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row < sg.nrows) x = load_q(p, sg.row0, sg.h, sg.r0 + row, ch * 8);
+        uint8_t* dst = smem + F::kQOff + row * 128;
+        if constexpr (!E4M3) {
+          if (ch < DP / 8)
+            *reinterpret_cast<uint4*>(dst + (ch >> 3) * F::kQHalf +
+                                      (((ch & 7) ^ (row & 7)) << 4)) = x;
+        } else {
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          float f[8], amax = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[2 * k] = __uint_as_float(w[k] << 16);
+            f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            amax = max3(amax, fabsf(f[2 * k]), fabsf(f[2 * k + 1]));
+          }
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o, 16));
+          // q 2^-a within the codes' range; a non-finite q stays one
+          const int a = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -100), 120);
+          const float inv = __uint_as_float((uint32_t)(127 - a) << 23);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float u = f[2 * k] * inv, v = f[2 * k + 1] * inv;
+            hi[k] = e4m3x2(u, v);
+            uint32_t h;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi[k]));
+            const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
+            lo[k] = e4m3x2((u - g.x) * 16.f, (v - g.y) * 16.f);
+          }
+          // 8 codes a lane: half a 16-byte chunk
+          const uint32_t at = ((((uint32_t)ch >> 1) ^ (row & 7)) << 4) + (ch & 1) * 8;
+          *reinterpret_cast<uint2*>(dst + at) =
+              make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(dst + NR * 128 + at) =
+              make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          const float scale = __uint_as_float((uint32_t)(127 + a) << 23) * c2;
+          if (ch == 0) ms->a[row] = amax < INFINITY ? scale : NAN;
+        }
+      }
+      if (tid < 2 * 32) ms->nm[tid >> 5][tid & 31] = (tid & 31) < sg.nrows ? kUnset : 0.f;
+      fence_proxy_async_smem();
+      mbar_arrive(b_q);
+      soft_sync();  // nm (and a) before the first tile
+
+      float l[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) l[r] = 0.f;
+      // positions that every row sees
+      const int all_hi = p.causal ? sg.ctx + p.by_G(sg.r0) + 1 : sg.ctx + sg.m;
+      const int all_lo =
+          p.window == 0 ? 0 : sg.ctx + p.by_G(sg.r0 + sg.nrows - 1) - p.window + 1;
+#pragma unroll 1
+      for (int i = s; i < sg.ntiles; i += 2) {
+        const int t0 = (sg.tile0 + i) * kBN;
+        float ck = 0.f, ev = 0.f, un = 1.f;
+        if constexpr (E4M3) {
+          // scales of this thread's position (any byte gives finite factors)
+          const uint32_t q = base + i;
+          wait_bar(b_exp + 8 * (q % kExpDepth), (q / kExpDepth) & 1, s_abort, status);
+          const uint8_t* ex = smem + F::kExpOff + (q % kExpDepth) * 256 + pt;
+          const int ek = min(max((int)ex[0], 1), 254), ee = min(max((int)ex[128], 1), 253);
+          ck = __uint_as_float((uint32_t)ek << 23);
+          ev = (float)(ee - 127);
+          un = __uint_as_float((uint32_t)(254 - ee) << 23);
+        }
+        wait_bar(b_s + 8 * s, ph_s, s_abort, status);
+        __syncwarp();
+        ph_s ^= 1;
+        tc_fence_after();
+        // rows r_lo .. r_hi - 1 see this thread's position
+        int r_lo = 0, r_hi = NR;
+        const bool mask = t0 < all_lo || t0 + kBN > all_hi;
+        if (mask) {
+          const int c = t0 + pt;
+          if (!p.causal) {
+            if (c >= sg.ctx + sg.m) r_lo = NR;
+          } else {
+            // row r is at position ctx + r / G: it sees c from r = (c - ctx) G on
+            r_lo = min(max(min(max(c - sg.ctx, 0), 1 << 20) * p.G - sg.r0, 0), NR);
+            if (p.window > 0) {
+              const int j = min((int64_t)c + p.window - sg.ctx, (int64_t)1 << 20);
+              r_hi = min(max(max(j, 0) * p.G - sg.r0, 0), NR);
+            }
+          }
+        }
+        float x[NR];
+        load_scores<NR, E4M3>(t_s, ms, c2, ck, ev, x);
+        float top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < NR; r += 4) {
+          const float4 nm = *reinterpret_cast<const float4*>(&ms->nm[s][r]);
+          x[r] += nm.x;
+          x[r + 1] += nm.y;
+          x[r + 2] += nm.z;
+          x[r + 3] += nm.w;
+          if (mask)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (r + k < r_lo || r + k >= r_hi) x[r + k] = -INFINITY;
+          top = max3(top, x[r], x[r + 1]);
+          top = max3(top, x[r + 2], x[r + 3]);
+        }
+        if (group_any(2 + s, 128, top > kGrow)) {
+          // the references move to the tile's maxima (rarely after the first tile)
+          load_scores<NR, E4M3>(t_s, ms, c2, ck, ev, x);
+          {
+            float y[NR];
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+              y[r] = mask && (r < r_lo || r >= r_hi) ? -INFINITY : x[r];
+            const float m = reduce_rows<NR>(y, [](float a, float b) { return fmaxf(a, b); });
+            if (lane % (32 / NR) == 0) ms->wm[s][warp & 3][lane / (32 / NR)] = m;
+          }
+          group_sync(2 + s, 128);
+          if (pt < NR) {
+            const float old = -ms->nm[s][pt];
+            const float m = max3(fmaxf(old, ms->wm[s][0][pt]),
+                                 fmaxf(ms->wm[s][1][pt], ms->wm[s][2][pt]), ms->wm[s][3][pt]);
+            ms->nm[s][pt] = -m;
+            ms->f[s][pt] = ex2_approx(old - m);
+          }
+          group_sync(2 + s, 128);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            l[r] *= ms->f[s][r];
+            x[r] = mask && (r < r_lo || r >= r_hi) ? -INFINITY : x[r] + ms->nm[s][r];
+          }
+          if (i >= 2) {
+#pragma unroll 1
+            for (int c = 0; c < 2 * NR; c += 8) {
+              uint32_t o[8];
+              tmem_ld_32x32b_x8(t_o + c, o);
+              tmem_wait_ld_regs(o);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * ms->f[s][c % NR + k]);
+              tmem_st_32x32b_x8(t_o + c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // P: the position's row of [rounded | rest], 8 packed rows a chunk
+#pragma unroll
+        for (int r0 = 0; r0 < NR; r0 += 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = ex2_approx(x[r0 + 2 * k]), b = ex2_approx(x[r0 + 2 * k + 1]);
+            float ra, rb;
+            if constexpr (E4M3) {
+              l[r0 + 2 * k] = fmaf(a, un, l[r0 + 2 * k]);
+              l[r0 + 2 * k + 1] = fmaf(b, un, l[r0 + 2 * k + 1]);
+              hi[k] = pack_half(a, b);
+              const float2 h = __half22float2(*reinterpret_cast<__half2*>(&hi[k]));
+              ra = a - h.x;
+              rb = b - h.y;
+              lo[k] = pack_half(ra, rb);
+            } else {
+              l[r0 + 2 * k] += a;
+              l[r0 + 2 * k + 1] += b;
+              hi[k] = pack_bf16(a, b);
+              ra = a - __uint_as_float(hi[k] << 16);
+              rb = b - __uint_as_float(hi[k] & 0xffff0000u);
+              lo[k] = pack_bf16(ra, rb);
+            }
+          }
+          *reinterpret_cast<uint4*>(my_p + (((r0 >> 3) ^ (pt & 7)) << 4)) =
+              make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(my_p + ((((NR + r0) >> 3) ^ (pt & 7)) << 4)) =
+              make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        if constexpr (!E4M3) {
+          // values that no row sees: 0 * NaN must not reach a sum
+          const int c = t0 + pt;
+          if (t0 < sg.lo || t0 + kBN > sg.hi) {
+            const uint32_t e = 2 * (base + i) + 1, slot = e % NS;
+            wait_bar(b_full + 8 * slot, (e / NS) & 1, s_abort, status);
+            if (c < sg.lo || c >= sg.hi) {
+              uint8_t* v = smem + slot * F::kSlot + pt * 128;
+#pragma unroll
+              for (int k = 0; k < DP / 8; ++k)
+                *reinterpret_cast<uint4*>(v + (k >> 3) * kHalf + (k & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(b_p + 8 * s);
+      }
+      const bool has = s < sg.ntiles;
+      if (has) {
+        wait_bar(b_o + 8 * s, ph_o, s_abort, status);
+        ph_o ^= 1;
+      }
+      __syncwarp();
+      tc_fence_after();
+      base += sg.ntiles;
+
+      // the streams' sums and a common reference
+      {
+        const float v = reduce_rows<NR>(l, [](float a, float b) { return a + b; });
+        if (lane % (32 / NR) == 0) ms->wm[s][warp & 3][lane / (32 / NR)] = v;
+      }
+      soft_sync();
+      float* rec = p.part + ((size_t)blockIdx.x * 2 + (sg.split == 2 ? 1 : 0)) *
+                                record_floats(32, DP);
+      if (tid < NR && tid < sg.nrows) {
+        float m[2], t[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          t[k] = (ms->wm[k][0][tid] + ms->wm[k][1][tid]) + (ms->wm[k][2][tid] + ms->wm[k][3][tid]);
+          m[k] = -ms->nm[k][tid];
+        }
+        const float M = fmaxf(m[0], m[1]);
+        const float w0 = ex2_approx(m[0] - M), w1 = ex2_approx(m[1] - M);
+        const float L = fmaf(t[0], w0, t[1] * w1);
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int64_t at = out_row(p, sg.row0, sg.h, sg.r0 + tid);
+        ms->w[0][tid] = sg.split ? w0 : w0 * inv;
+        ms->w[1][tid] = sg.split ? w1 : w1 * inv;
+        ms->at[tid] = at * p.c.D;
+        if (sg.split)
+          __stcg(reinterpret_cast<float2*>(rec + 32 * DP) + tid,
+                 make_float2(M == -kUnset ? -INFINITY : M, L));
+        else if (p.lse != nullptr)
+          p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+      }
+      soft_sync();
+      // O: each warpgroup hands the other its share of half the rows
+      float* buf = reinterpret_cast<float*>(smem + F::kPOff);  // P is no longer read
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        const bool mine = pass == 1;
+        const int first = ((s == 0) == mine ? 0 : NR / 2);
+#pragma unroll 1
+        for (int r0 = first; r0 < first + NR / 2 && r0 < sg.nrows; r0 += 4) {
+          uint32_t u[8], v[8];  // four rows; x8 loads reach past them within S and O
+          if (has) {
+            tmem_ld_32x32b_x8(t_o + (r0 & ~7), u);
+            tmem_ld_32x32b_x8(t_o + NR + (r0 & ~7), v);
+            tmem_wait_ld_regs(u, v);
+          }
+          if (pt < DP) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = r0 + k;
+              if (r < sg.nrows) {
+                const float a = __uint_as_float(r0 & 4 ? u[4 + k] : u[k]);
+                const float b = __uint_as_float(r0 & 4 ? v[4 + k] : v[k]);
+                float o = has ? (a + b) * ms->w[s][r] : 0.f;
+                if (!mine) {
+                  buf[r * DP + pt] = o;
+                } else {
+                  o += buf[r * DP + pt];
+                  if (sg.split)
+                    __stcg(rec + r * DP + pt, o);
+                  else if (pt < p.c.D)
+                    p.out[ms->at[r] + pt] = __float2bfloat16(o);
+                }
+              }
+            }
+          }
+          __syncwarp();
+        }
+        if (pass == 0) soft_sync();
+      }
+      if (sg.split)
+        finish_split<DP, 32, false>(p, sg, &ms->last, reinterpret_cast<float2*>(buf));
+      tc_fence_before();
+    }
+  } else if (E4M3 && warp < 12) {
+    reg_dec<80>();  // completes the warpgroup
+  } else if (E4M3) {
+    reg_dec<88>();
+    // ------------------------------------------------------------ V's codes to halves
+    const int ct = tid - 384;  // 8 lanes a row of 128 codes, 16 codes a lane
+    uint32_t base = 0;
+    for (int sn = 0;; ++sn) {
+      const int ss = sn % kSegDepth;
+      const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status);
+      if (group_any(4, 128, !got)) break;
+      const int nt = ms->seg[ss].ntiles, tile0 = ms->seg[ss].tile0;
+      const int lo = ms->seg[ss].lo, hi = ms->seg[ss].hi;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
+      if (nt == 0) break;
+#pragma unroll 1
+      for (int i = 0; i < nt; ++i) {
+        const uint32_t q = base + i, e = 2 * q + 1, slot = e % NS, vf = q & 1;
+        const int t0 = (tile0 + i) * kBN;
+        const bool edge = t0 < lo || t0 + kBN > hi;
+        wait_bar(b_full + 8 * slot, (e / NS) & 1, s_abort, status);
+        wait_bar(b_vfEmpty + 8 * vf, ((q >> 1) & 1) ^ 1, s_abort, status);
+        const uint8_t* src = smem + slot * F::kSlot;
+        uint8_t* dst = smem + F::kVfOff + vf * F::kVf;
+        const int c = ct & 7;
+#pragma unroll 4
+        for (int k = 0; k < 8; ++k) {
+          const int row = k * 16 + (ct >> 3);
+          uint4 w = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
+          if (edge && (t0 + row < lo || t0 + row >= hi)) w = make_uint4(0, 0, 0, 0);
+          uint32_t h[8];
+          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * j]) : "h"((uint16_t)in[j]));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * j + 1]) : "h"((uint16_t)(in[j] >> 16)));
+          }
+          if (c < DP / 16) {
+            // lanes 0-3 and 4-7 of a row write chunks of the two halves of D: even ones
+            // and odd ones first, so that the eight fall in different banks
+            uint8_t* to = dst + (c >> 2) * kHalf + row * 128;
+            const int first = 2 * (c & 3) + (c >> 2), second = first ^ 1;
+            const bool odd = c >> 2;
+            *reinterpret_cast<uint4*>(to + ((first ^ (row & 7)) << 4)) =
+                odd ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(to + ((second ^ (row & 7)) << 4)) =
+                odd ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(b_vfFull + 8 * vf);
+        group_sync(4, 128);
+        if (ct == 0) mbar_arrive(b_empty + 8 * slot);
+      }
+      base += nt;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int DP, int NR, bool E4M3>
+cudaError_t launch_one(const AttendArgs& a, const Params& p, cudaStream_t st) {
+  using F = Few<DP, NR, E4M3>;
+  auto kernel = attend_few_kernel<DP, NR, E4M3>;
+  cudaError_t e = ensure_smem_attr((const void*)kernel, F::kTotal);
+  if (e != cudaSuccess) return e;
+  const int grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+  DSPARK_LAUNCH(kKindAttend, st,
+                kernel<<<grid, F::kThreads, F::kTotal, st>>>(a.desc->tm_k, a.desc->tm_v, p));
+  return cudaGetLastError();
+}
+
+template <int DP, bool E4M3>
+cudaError_t launch_rows(const AttendArgs& a, const Params& p, cudaStream_t st) {
+  const int rows = p.max_rows * p.G;
+  if (rows <= 8) return launch_one<DP, 8, E4M3>(a, p, st);
+  if (rows <= 16) return launch_one<DP, 16, E4M3>(a, p, st);
+  return launch_one<DP, 32, E4M3>(a, p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_few(const AttendArgs& a, const attend::Params& p, cudaStream_t st) {
+  const bool e4m3 = p.c.k_exp != nullptr;
+  if (p.c.D > 64)
+    return e4m3 ? launch_rows<128, true>(a, p, st) : launch_rows<128, false>(a, p, st);
+  return e4m3 ? launch_rows<64, true>(a, p, st) : launch_rows<64, false>(a, p, st);
+}
+
+}  // namespace dspark

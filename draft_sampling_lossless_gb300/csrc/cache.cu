@@ -24,12 +24,6 @@ __device__ __forceinline__ int row_exponent(float amax) {
   return e < kMinExp ? kMinExp : e;
 }
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-
 // Two e4m3 codes (low and high byte of `w`) times f, as packed bf16.  Every
 // code is a half, and its product with a power of two exact in bf16 as long as
 // it is a normal number there.

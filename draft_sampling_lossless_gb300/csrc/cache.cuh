@@ -63,6 +63,13 @@ __device__ __forceinline__ int64_t page_of(const CacheView& c, int n, int64_t p)
   return -1;
 }
 
+// Two values rounded to e4m3 (to nearest even, to the largest past it; NaN stays).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
 // The launchers: enqueue on `st`.
 cudaError_t launch_cache_append(const CacheView& c, bool e4m3, const void* k, int64_t k_stride,
                                 const void* v, int64_t v_stride, cudaStream_t st);
@@ -82,6 +89,5 @@ struct AttendArgs {
 };
 size_t attend_workspace_bytes(int T, int group, int D);
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st);
-cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t st);
 
 }  // namespace dspark

@@ -41,9 +41,8 @@ int cuda_fail(cudaError_t e, const char* where) {
   } while (0)
 
 // The pools' rows of D values as a 2-D tensor; boxes of one page, or 128 of its
-// rows.  bf16: 64 values (128 bytes) wide, 128-byte swizzled as the MMA
-// operands they land in; e4m3: the whole row, plain.  Values past D read as
-// zeros, rows past the last page too.
+// rows, 128 bytes wide (64 values, or 128 codes) and swizzled as the MMA operands
+// they land in.  Values past D read as zeros, rows past the last page too.
 cudaError_t encode_pool(CUtensorMap* m, const CacheDesc& d, void* pool) {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() {
     void* f = nullptr;
@@ -59,12 +58,10 @@ cudaError_t encode_pool(CUtensorMap* m, const CacheDesc& d, void* pool) {
   const cuuint64_t size = e4m3 ? 1 : 2;
   cuuint64_t dims[2] = {(cuuint64_t)d.D, (cuuint64_t)d.n_pages * d.Hkv * d.page};
   cuuint64_t strides[1] = {(cuuint64_t)d.D * size};
-  cuuint32_t box[2] = {e4m3 ? (d.D > 64 ? 128u : 64u) : 64u,
-                       (cuuint32_t)(d.page < 128 ? d.page : 128)};
+  cuuint32_t box[2] = {e4m3 ? 128u : 64u, (cuuint32_t)(d.page < 128 ? d.page : 128)};
   cuuint32_t es[2] = {1, 1};
   return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool,
-            dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
