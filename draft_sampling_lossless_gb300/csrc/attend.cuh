@@ -32,7 +32,6 @@ constexpr int kMaxSmem = 232448;
 constexpr uint32_t kHalf = kBN * 128;  // bytes of 128 rows of 128 bytes
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kGrow = 8.0f;          // log2 growth of a maximum that moves the reference
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint32_t kCounterOffset = 256;  // workspace: status word, counters, partials
 constexpr uint32_t kPartOffset = 4096;
@@ -129,7 +128,8 @@ struct Segment {  // part of an item that this block computes
   int row0, m, ctx, h, r0, nrows, lo, hi, tile0, ntiles;
   int split;        // 0: the whole item, 1 / 2: its partial result goes to record 0 / 1
   int first, last;  // the item's blocks
-  int pad[3];
+  int n;            // its request
+  int pad[2];
 };
 static_assert(sizeof(Segment) == 64, "a segment's words");
 
@@ -343,6 +343,7 @@ __device__ __forceinline__ void produce(const Params& p, const Range& rg, Segmen
     Segment sg;
     const Item it = item_of(p, q, qt);
     const bool end = u >= rg.u1;
+    sg.n = n;
     sg.row0 = q.row0;
     sg.m = q.m;
     sg.ctx = q.ctx;

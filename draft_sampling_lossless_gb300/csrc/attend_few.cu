@@ -10,9 +10,11 @@
 //
 // A softmax thread is a position: it has that position's scores of all rows,
 // sums its own exponentials (joined over the positions once, at the end), and no
-// maximum is taken per tile.  P = 2^(s - m) against a reference m of each row that
-// only moves, for all rows at once, when some score passes it by 8 powers of
-// two: any reference gives the same quotient and fp32 has the range.
+// maximum is taken per tile.  P = 2^(s - m) against a reference m of each row: the
+// score of the item's first position that all rows see.  Any reference gives the
+// same quotient as long as P stays in range; where a score passes it by too much
+// (64 powers of two in bf16, 15 in halves), or no position serves all rows, the
+// references move to the tile's maxima, O and the sums with them.
 //
 // P enters its product as two 16-bit terms, its rounding and the rounding of the
 // rest (columns of N side by side; a row that one position dominates would
@@ -27,6 +29,8 @@
 // P: P = 2^(s + e - m) with e its exponent, and l sums 2^-e P.
 //
 // Two streams, a warpgroup each with its own S, P, O and m, take alternate tiles.
+// Roles: warps 0-7 softmax, 8 the MMAs, 9 the TMA loads, 10 and 11 fetch the next
+// item's Q (and the scales of e4m3 tiles), 12-15 convert V.  Every wait is bounded.
 // See attend.cuh for the split of the work.
 #include "attend.cuh"
 
@@ -40,10 +44,11 @@ constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kColO = 128;       // S at 0 and 64, O at 128 and 192
 constexpr float kUnset = 3.0e38f;     // -m of a row that has seen nothing
 constexpr int kExpDepth = 8;          // tiles of exponent bytes held
+constexpr int kHelpers = 64;          // threads of warps 10 and 11
 
 template <int DP, int NR, bool E4M3>
 struct Few {
-  static constexpr int kThreads = E4M3 ? 512 : 320;
+  static constexpr int kThreads = E4M3 ? 512 : 384;
   static constexpr int kNH = DP / 64;
   static constexpr int kQRows = E4M3 ? 2 * NR : (NR < 16 ? 16 : NR);  // N of the scores
   static constexpr uint32_t kSlot = E4M3 ? kHalf : kHalf * kNH;       // a tile as loaded
@@ -53,12 +58,12 @@ struct Few {
   static constexpr uint32_t kExp = E4M3 ? kExpDepth * 256 : 0;
   static constexpr uint32_t kMisc = 4096;
   static constexpr int kFit =
-      (int)((kMaxSmem - 2 * kHalf - kQBytes - 2 * kVf - kExp - kMisc) / kSlot);
+      (int)((kMaxSmem - 2 * kHalf - 2 * kQBytes - 2 * kVf - kExp - kMisc) / kSlot);
   static constexpr int kSlots = kFit > 12 ? 12 : kFit;
   static constexpr uint32_t kPOff = kSlots * kSlot;  // P of each stream; the join's buffer
   static constexpr uint32_t kVfOff = kPOff + 2 * kHalf;
   static constexpr uint32_t kQOff = kVfOff + 2 * kVf;
-  static constexpr uint32_t kExpOff = kQOff + kQBytes;
+  static constexpr uint32_t kExpOff = kQOff + 2 * kQBytes;
   static constexpr uint32_t kMiscOff = kExpOff + kExp;
   static constexpr uint32_t kTotal = kMiscOff + kMisc;
   static_assert(kTotal <= kMaxSmem && kSlots >= 4, "shared memory");
@@ -68,14 +73,11 @@ struct Misc {  // shared words
   float nm[2][32];      // -m of each stream's rows
   float f[2][32];       // what a move of the references multiplies by
   float wm[2][4][32];   // the warps' maxima, then sums
-  float w[2][32];       // weights of the streams
-  float inv[32];
-  float a[32];          // scale of the scores of a row (e4m3: with that of q)
-  int64_t at[32];       // output rows
+  float a[2][32];       // e4m3: scale of the scores of a row, of each Q buffer
   int64_t sum[16];
   Found found;
   Segment seg[kSegDepth];
-  uint64_t bars[2 * 12 + 2 * kSegDepth + 7 + 4 + kExpDepth + 1];
+  uint64_t bars[2 * 12 + 2 * kSegDepth + 4 + 6 + 4 + 2 * kExpDepth + 1];
   int abort_flag, last;
   uint32_t tmem;
 };
@@ -109,8 +111,8 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
 // The scores of a thread's position: x[r] = log2 of row r's exponential, up to the
 // reference (e4m3: times 2^e of the value's exponent e).
 template <int NR, bool E4M3>
-__device__ __forceinline__ void load_scores(uint32_t t_s, const Misc* ms, float c2, float ck,
-                                            float ev, float (&x)[NR]) {
+__device__ __forceinline__ void load_scores(uint32_t t_s, const float* row_scale, float c2,
+                                            float ck, float ev, float (&x)[NR]) {
   if constexpr (!E4M3) {
     uint32_t v[NR];
     if constexpr (NR == 8)
@@ -137,7 +139,7 @@ __device__ __forceinline__ void load_scores(uint32_t t_s, const Misc* ms, float 
       tmem_wait_ld_regs(u, v);
 #pragma unroll
       for (int r = 0; r < kB; r += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(ms->a + r0 + r);
+        const float4 a = *reinterpret_cast<const float4*>(row_scale + r0 + r);
         const float af[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -156,14 +158,17 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   using F = Few<DP, NR, E4M3>;
   constexpr int NS = F::kSlots, NH = F::kNH;
   constexpr int kConvWarps = E4M3 ? 4 : 0;
+  // P's largest exponent, and how far above the first score its reference starts
+  constexpr float kLimit = E4M3 ? 15.f : 64.f, kAbove = E4M3 ? 8.f : 0.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc* ms = reinterpret_cast<Misc*>(smem + F::kMiscOff);
   const uint32_t b_full = smem_u32(ms->bars), b_empty = b_full + 8 * NS;
   const uint32_t b_segFull = b_empty + 8 * NS, b_segEmpty = b_segFull + 8 * kSegDepth;
-  const uint32_t b_q = b_segEmpty + 8 * kSegDepth;
-  const uint32_t b_s = b_q + 8, b_p = b_s + 16, b_o = b_p + 16;
-  const uint32_t b_vfFull = b_o + 16, b_vfEmpty = b_vfFull + 16, b_exp = b_vfEmpty + 16;
-  const uint32_t b_drain = b_exp + 8 * kExpDepth;
+  const uint32_t b_qFull = b_segEmpty + 8 * kSegDepth, b_qEmpty = b_qFull + 16;
+  const uint32_t b_s = b_qEmpty + 16, b_p = b_s + 16, b_o = b_p + 16;
+  const uint32_t b_vfFull = b_o + 16, b_vfEmpty = b_vfFull + 16;
+  const uint32_t b_expFull = b_vfEmpty + 16, b_expEmpty = b_expFull + 8 * kExpDepth;
+  const uint32_t b_drain = b_expEmpty + 8 * kExpDepth;
   volatile int* s_abort = &ms->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t* status = p.c.status;
@@ -174,17 +179,21 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     for (int i = 0; i < 2 * NS; ++i) mbar_init(b_full + 8 * i, 1);
     for (int i = 0; i < kSegDepth; ++i) {
       mbar_init(b_segFull + 8 * i, 1);
-      mbar_init(b_segEmpty + 8 * i, 9 + kConvWarps);  // the MMA thread and the other warps
+      mbar_init(b_segEmpty + 8 * i, 11 + kConvWarps);  // the MMA thread and the other warps
     }
-    mbar_init(b_q, kSoftThreads);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(b_qFull + 8 * i, kHelpers);
+      mbar_init(b_qEmpty + 8 * i, 1);
       mbar_init(b_s + 8 * i, 1);
       mbar_init(b_p + 8 * i, 128);
       mbar_init(b_o + 8 * i, 1);
       mbar_init(b_vfFull + 8 * i, 128);
       mbar_init(b_vfEmpty + 8 * i, 1);
     }
-    for (int i = 0; i < kExpDepth; ++i) mbar_init(b_exp + 8 * i, 1);
+    for (int i = 0; i < kExpDepth; ++i) {
+      mbar_init(b_expFull + 8 * i, kHelpers);
+      mbar_init(b_expEmpty + 8 * i, 4);  // the warps of the tile's stream
+    }
     mbar_init(b_drain, 1);
     fence_mbar_init();
   }
@@ -231,35 +240,6 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
                               half * 64, y[b]);
               }
             }
-          if constexpr (E4M3) {
-            // both exponent rows of the tile, with its K (a buffer of tile i is read
-            // before P of tile i, and tile i + 8 is not loaded before that)
-            if (kv == 0) {
-              const uint32_t be = b_exp + 8 * (seq % kExpDepth);
-              const uint32_t de = smem_u32(smem + F::kExpOff) + (seq % kExpDepth) * 256;
-              int n = 0;
-#pragma unroll
-              for (int b = 0; b < 8; ++b) {
-                if (b >= n_boxes) break;
-                if (y[b] != none) {
-                  ++n;
-                  continue;
-                }
-                // a box of zeros: any scale does, but not one that moves the reference
-                uint32_t* ex = reinterpret_cast<uint32_t*>(smem + F::kExpOff +
-                                                           (seq % kExpDepth) * 256 + b * box_rows);
-                for (int i = 0; i < box_rows / 4; ++i) ex[i] = ex[i + 32] = 0x7f7f7f7fu;
-              }
-              mbar_arrive_expect_tx(be, 2 * n * box_rows);
-              const uint64_t pol = policy_evict_first();
-#pragma unroll
-              for (int b = 0; b < 8; ++b)
-                if (b < n_boxes && y[b] != none) {
-                  bulk_load_hint(de + b * box_rows, p.c.k_exp + y[b], box_rows, be, pol);
-                  bulk_load_hint(de + 128 + b * box_rows, p.c.v_exp + y[b], box_rows, be, pol);
-                }
-            }
-          }
         }
         __syncwarp();
       }
@@ -271,9 +251,6 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       const uint32_t done = 2 * seq;
       for (uint32_t e = done > NS ? done - NS : 0; e < done; ++e)
         mbar_wait(b_full + 8 * (e % NS), (e / NS) & 1);
-      if constexpr (E4M3)
-        for (uint32_t e = seq > kExpDepth ? seq - kExpDepth : 0; e < seq; ++e)
-          mbar_wait(b_exp + 8 * (e % kExpDepth), (e / kExpDepth) & 1);
     }
   } else if (warp == kWarpMma) {
     if (E4M3) reg_dec<80>();
@@ -284,15 +261,15 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
                                 kIdescTransposeA | kIdescTransposeB;
       const int ksteps = E4M3 ? (p.c.D + 31) / 32 : p.c.D / 16;
       const uint32_t at0 = smem_u32(smem);
-      uint32_t base = 0, ph_q = 0, ph_p = 0;  // base: tiles of the segments before
+      uint32_t base = 0, ph_p = 0;  // base: tiles of the segments before
       bool ok = true;
       auto need = [&](uint32_t e) {
         ok = ok && wait_bar(b_full + 8 * (e % NS), (e / NS) & 1, s_abort, status);
         tc_fence_after();
       };
-      auto scores = [&](int s, uint32_t e) {
+      auto scores = [&](int s, uint32_t e, int qb) {
         const uint64_t a = desc_kmajor_sw128(at0 + (e % NS) * F::kSlot);
-        const uint64_t b = desc_kmajor_sw128(at0 + F::kQOff);
+        const uint64_t b = desc_kmajor_sw128(at0 + F::kQOff + qb * F::kQBytes);
         for (int k = 0; k < ksteps; ++k) {
           if constexpr (E4M3)
             mma_e4m3(tmem + s * 64, a + k * 2, b + k * 2, kIdS, k > 0);
@@ -310,14 +287,14 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         const int nt = ms->seg[ss].ntiles;
         mbar_arrive(b_segEmpty + 8 * ss);
         if (nt == 0) break;
-        ok = wait_bar(b_q, ph_q, s_abort, status);
+        const int qb = sn & 1;
+        ok = wait_bar(b_qFull + 8 * qb, (sn >> 1) & 1, s_abort, status);
         if (!ok) break;
-        ph_q ^= 1;
         tc_fence_after();
         const uint32_t e0 = 2 * base;  // K of tile i: e0 + 2 i, V: one more
         for (int i = 0; i < 2 && i < nt && ok; ++i) {
           need(e0 + 2 * i);
-          if (ok) scores(i, e0 + 2 * i);
+          if (ok) scores(i, e0 + 2 * i, qb);
         }
         for (int i = 0; i < nt && ok; ++i) {
           const int s = i & 1;
@@ -342,11 +319,12 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           mma_commit(E4M3 ? b_vfEmpty + 8 * vf : b_empty + 8 * (ev % NS));
           if (i + 2 < nt) {
             need(ev + 3);
-            if (ok) scores(s, ev + 3);
+            if (ok) scores(s, ev + 3, qb);
           } else {
             mma_commit(b_o + 8 * s);
           }
         }
+        mma_commit(b_qEmpty + 8 * qb);
         base += nt;
       }
       if (!ok) {
@@ -368,63 +346,12 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth;
       const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status);
-      // all leave together; the barrier also ends the previous segment's use of Q
+      // all leave together
       if (group_any(1, kSoftThreads, !got)) break;
       const Segment sg = ms->seg[ss];
       __syncwarp();
       if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
       if (sg.ntiles == 0) break;
-
-      // Q: 16 lanes a row, 8 values a lane; rows past the item's are zero
-#pragma unroll
-      for (int i = tid; i < (E4M3 ? NR : F::kQRows) * 16; i += kSoftThreads) {
-        const int row = i >> 4, ch = i & 15;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (row < sg.nrows) x = load_q(p, sg.row0, sg.h, sg.r0 + row, ch * 8);
-        uint8_t* dst = smem + F::kQOff + row * 128;
-        if constexpr (!E4M3) {
-          if (ch < DP / 8)
-            *reinterpret_cast<uint4*>(dst + (ch >> 3) * F::kQHalf +
-                                      (((ch & 7) ^ (row & 7)) << 4)) = x;
-        } else {
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          float f[8], amax = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            f[2 * k] = __uint_as_float(w[k] << 16);
-            f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-            amax = max3(amax, fabsf(f[2 * k]), fabsf(f[2 * k + 1]));
-          }
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o, 16));
-          // q 2^-a within the codes' range; a non-finite q stays one
-          const int a = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -100), 120);
-          const float inv = __uint_as_float((uint32_t)(127 - a) << 23);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float u = f[2 * k] * inv, v = f[2 * k + 1] * inv;
-            hi[k] = e4m3x2(u, v);
-            uint32_t h;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi[k]));
-            const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
-            lo[k] = e4m3x2((u - g.x) * 16.f, (v - g.y) * 16.f);
-          }
-          // 8 codes a lane: half a 16-byte chunk
-          const uint32_t at = ((((uint32_t)ch >> 1) ^ (row & 7)) << 4) + (ch & 1) * 8;
-          *reinterpret_cast<uint2*>(dst + at) =
-              make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          *reinterpret_cast<uint2*>(dst + NR * 128 + at) =
-              make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-          const float scale = __uint_as_float((uint32_t)(127 + a) << 23) * c2;
-          if (ch == 0) ms->a[row] = amax < INFINITY ? scale : NAN;
-        }
-      }
-      if (tid < 2 * 32) ms->nm[tid >> 5][tid & 31] = (tid & 31) < sg.nrows ? kUnset : 0.f;
-      fence_proxy_async_smem();
-      mbar_arrive(b_q);
-      soft_sync();  // nm (and a) before the first tile
 
       float l[NR];
 #pragma unroll
@@ -433,16 +360,19 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       const int all_hi = p.causal ? sg.ctx + p.by_G(sg.r0) + 1 : sg.ctx + sg.m;
       const int all_lo =
           p.window == 0 ? 0 : sg.ctx + p.by_G(sg.r0 + sg.nrows - 1) - p.window + 1;
+      if (E4M3) wait_bar(b_qFull + 8 * (sn & 1), (sn >> 1) & 1, s_abort, status);
 #pragma unroll 1
       for (int i = s; i < sg.ntiles; i += 2) {
         const int t0 = (sg.tile0 + i) * kBN;
         float ck = 0.f, ev = 0.f, un = 1.f;
         if constexpr (E4M3) {
           // scales of this thread's position (any byte gives finite factors)
-          const uint32_t q = base + i;
-          wait_bar(b_exp + 8 * (q % kExpDepth), (q / kExpDepth) & 1, s_abort, status);
-          const uint8_t* ex = smem + F::kExpOff + (q % kExpDepth) * 256 + pt;
+          const uint32_t q = (base + i) % kExpDepth;
+          wait_bar(b_expFull + 8 * q, ((base + i) / kExpDepth) & 1, s_abort, status);
+          const uint8_t* ex = smem + F::kExpOff + q * 256 + pt;
           const int ek = min(max((int)ex[0], 1), 254), ee = min(max((int)ex[128], 1), 253);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_expEmpty + 8 * q);
           ck = __uint_as_float((uint32_t)ek << 23);
           ev = (float)(ee - 127);
           un = __uint_as_float((uint32_t)(254 - ee) << 23);
@@ -468,7 +398,20 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           }
         }
         float x[NR];
-        load_scores<NR, E4M3>(t_s, ms, c2, ck, ev, x);
+        load_scores<NR, E4M3>(t_s, ms->a[sn & 1], c2, ck, ev, x);
+        if (i == s) {
+          // the references: the scores of a position that every row sees
+          const int c0 = max(all_lo - t0, 0);
+          if (c0 < min(all_hi - t0, kBN)) {
+            if (pt == c0)
+#pragma unroll
+              for (int r = 0; r < NR; ++r)
+                ms->nm[s][r] = fabsf(x[r]) < 1.0e30f ? -(x[r] + kAbove) : kUnset;
+          } else if (pt < NR) {
+            ms->nm[s][pt] = kUnset;
+          }
+          group_sync(2 + s, 128);
+        }
         float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < NR; r += 4) {
@@ -484,9 +427,9 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           top = max3(top, x[r], x[r + 1]);
           top = max3(top, x[r + 2], x[r + 3]);
         }
-        if (group_any(2 + s, 128, top > kGrow)) {
-          // the references move to the tile's maxima (rarely after the first tile)
-          load_scores<NR, E4M3>(t_s, ms, c2, ck, ev, x);
+        if (group_any(2 + s, 128, top > kLimit)) {
+          // the references move to the tile's maxima (rarely)
+          load_scores<NR, E4M3>(t_s, ms->a[sn & 1], c2, ck, ev, x);
           {
             float y[NR];
 #pragma unroll
@@ -573,6 +516,10 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         mbar_arrive(b_p + 8 * s);
       }
       const bool has = s < sg.ntiles;
+      {
+        const float v = reduce_rows<NR>(l, [](float a, float b) { return a + b; });
+        if (lane % (32 / NR) == 0) ms->wm[s][warp & 3][lane / (32 / NR)] = v;
+      }
       if (has) {
         wait_bar(b_o + 8 * s, ph_o, s_abort, status);
         ph_o ^= 1;
@@ -580,81 +527,189 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       __syncwarp();
       tc_fence_after();
       base += sg.ntiles;
-
-      // the streams' sums and a common reference
-      {
-        const float v = reduce_rows<NR>(l, [](float a, float b) { return a + b; });
-        if (lane % (32 / NR) == 0) ms->wm[s][warp & 3][lane / (32 / NR)] = v;
-      }
       soft_sync();
+
+      // lane r: the weights of row r in the two streams, and where the row goes
+      const bool both = sg.ntiles > 1;
       float* rec = p.part + ((size_t)blockIdx.x * 2 + (sg.split == 2 ? 1 : 0)) *
                                 record_floats(32, DP);
-      if (tid < NR && tid < sg.nrows) {
+      float w_mine = 0.f;
+      int64_t at = 0;
+      if (lane < sg.nrows) {
         float m[2], t[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          t[k] = (ms->wm[k][0][tid] + ms->wm[k][1][tid]) + (ms->wm[k][2][tid] + ms->wm[k][3][tid]);
-          m[k] = -ms->nm[k][tid];
+          t[k] = (ms->wm[k][0][lane] + ms->wm[k][1][lane]) +
+                 (ms->wm[k][2][lane] + ms->wm[k][3][lane]);
+          m[k] = k == 0 || both ? -ms->nm[k][lane] : -kUnset;
         }
         const float M = fmaxf(m[0], m[1]);
-        const float w0 = ex2_approx(m[0] - M), w1 = ex2_approx(m[1] - M);
-        const float L = fmaf(t[0], w0, t[1] * w1);
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int64_t at = out_row(p, sg.row0, sg.h, sg.r0 + tid);
-        ms->w[0][tid] = sg.split ? w0 : w0 * inv;
-        ms->w[1][tid] = sg.split ? w1 : w1 * inv;
-        ms->at[tid] = at * p.c.D;
-        if (sg.split)
-          __stcg(reinterpret_cast<float2*>(rec + 32 * DP) + tid,
-                 make_float2(M == -kUnset ? -INFINITY : M, L));
-        else if (p.lse != nullptr)
-          p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+        const float w0 = ex2_approx(m[0] - M), w1 = both ? ex2_approx(m[1] - M) : 0.f;
+        const float L = both ? fmaf(t[0], w0, t[1] * w1) : t[0] * w0;
+        w_mine = s == 0 ? w0 : w1;
+        at = out_row(p, sg.row0, sg.h, sg.r0 + lane);
+        if (!sg.split) w_mine *= L == 0.f ? 0.f : 1.f / L;
+        if (warp == 0) {
+          if (sg.split)
+            __stcg(reinterpret_cast<float2*>(rec + 32 * DP) + lane,
+                   make_float2(M == -kUnset ? -INFINITY : M, L));
+          else if (p.lse != nullptr)
+            p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+        }
+        at *= p.c.D;
+      }
+      __syncwarp();
+      // O of this thread's value of D; each warpgroup hands the other its share of
+      // half the rows, through the other's P (no longer read)
+      float o[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) o[r] = 0.f;
+      if (has) {
+#pragma unroll
+        for (int r0 = 0; r0 < NR; r0 += 8) {
+          uint32_t u[8], v[8];
+          tmem_ld_32x32b_x8(t_o + r0, u);
+          tmem_ld_32x32b_x8(t_o + NR + r0, v);
+          tmem_wait_ld_regs(u, v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            o[r0 + k] = (__uint_as_float(u[k]) + __uint_as_float(v[k])) *
+                        __shfl_sync(0xffffffffu, w_mine, r0 + k);
+        }
+      }
+      float* give = reinterpret_cast<float*>(smem + F::kPOff + (s ^ 1) * kHalf) + pt;
+      const float* take = reinterpret_cast<const float*>(smem + F::kPOff + s * kHalf) + pt;
+      if (pt < DP) {
+#pragma unroll
+        for (int r = 0; r < NR / 2; ++r) give[r * DP] = s == 0 ? o[NR / 2 + r] : o[r];
       }
       soft_sync();
-      // O: each warpgroup hands the other its share of half the rows
-      float* buf = reinterpret_cast<float*>(smem + F::kPOff);  // P is no longer read
-#pragma unroll 1
-      for (int pass = 0; pass < 2; ++pass) {
-        const bool mine = pass == 1;
-        const int first = ((s == 0) == mine ? 0 : NR / 2);
-#pragma unroll 1
-        for (int r0 = first; r0 < first + NR / 2 && r0 < sg.nrows; r0 += 4) {
-          uint32_t u[8], v[8];  // four rows; x8 loads reach past them within S and O
-          if (has) {
-            tmem_ld_32x32b_x8(t_o + (r0 & ~7), u);
-            tmem_ld_32x32b_x8(t_o + NR + (r0 & ~7), v);
-            tmem_wait_ld_regs(u, v);
-          }
-          if (pt < DP) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = r0 + k;
-              if (r < sg.nrows) {
-                const float a = __uint_as_float(r0 & 4 ? u[4 + k] : u[k]);
-                const float b = __uint_as_float(r0 & 4 ? v[4 + k] : v[k]);
-                float o = has ? (a + b) * ms->w[s][r] : 0.f;
-                if (!mine) {
-                  buf[r * DP + pt] = o;
-                } else {
-                  o += buf[r * DP + pt];
-                  if (sg.split)
-                    __stcg(rec + r * DP + pt, o);
-                  else if (pt < p.c.D)
-                    p.out[ms->at[r] + pt] = __float2bfloat16(o);
-                }
-              }
-            }
-          }
-          __syncwarp();
+      for (int k = 0; k < NR / 2; ++k) {
+        const int r = s * (NR / 2) + k;
+        const int64_t to = __shfl_sync(0xffffffffu, at, r);
+        if (r < sg.nrows && pt < DP) {
+          const float v = (s == 0 ? o[k] : o[NR / 2 + k]) + take[k * DP];
+          if (sg.split)
+            __stcg(rec + r * DP + pt, v);
+          else if (pt < p.c.D)
+            p.out[to + pt] = __float2bfloat16(v);
         }
-        if (pass == 0) soft_sync();
       }
       if (sg.split)
-        finish_split<DP, 32, false>(p, sg, &ms->last, reinterpret_cast<float2*>(buf));
+        finish_split<DP, 32, false>(p, sg, &ms->last,
+                                    reinterpret_cast<float2*>(smem + F::kPOff));
       tc_fence_before();
     }
-  } else if (E4M3 && warp < 12) {
-    reg_dec<80>();  // completes the warpgroup
+  } else if (warp < 12) {
+    if (E4M3) reg_dec<80>();
+    // ------------------------------------------------------------ Q, scales
+    const int ht = tid - 320;
+    uint32_t base = 0;
+    for (int sn = 0;; ++sn) {
+      const int ss = sn % kSegDepth, qb = sn & 1;
+      const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status) &&
+                       wait_bar(b_qEmpty + 8 * qb, ((sn >> 1) & 1) ^ 1, s_abort, status);
+      if (group_any(5, kHelpers, !got)) break;
+      const Segment sg = ms->seg[ss];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
+      if (sg.ntiles == 0) break;
+      // Q: 16 lanes a row, 8 values a lane; rows past the item's are zero
+      constexpr int kRowsIn = E4M3 ? NR : F::kQRows, kIters = kRowsIn * 16 / kHelpers;
+      uint4 x[kIters];
+#pragma unroll
+      for (int k = 0; k < kIters; ++k) {
+        const int row = (ht >> 4) + 4 * k, ch = ht & 15;
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (row < sg.nrows) x[k] = load_q(p, sg.row0, sg.h, sg.r0 + row, ch * 8);
+      }
+#pragma unroll
+      for (int k = 0; k < kIters; ++k) {
+        const int row = (ht >> 4) + 4 * k, ch = ht & 15;
+        uint8_t* dst = smem + F::kQOff + qb * F::kQBytes + row * 128;
+        if constexpr (!E4M3) {
+          if (ch < DP / 8)
+            *reinterpret_cast<uint4*>(dst + (ch >> 3) * F::kQHalf +
+                                      (((ch & 7) ^ (row & 7)) << 4)) = x[k];
+        } else {
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          float f[8], amax = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[2 * j] = __uint_as_float(w[j] << 16);
+            f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            amax = max3(amax, fabsf(f[2 * j]), fabsf(f[2 * j + 1]));
+          }
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o, 16));
+          // q 2^-a within the codes' range
+          const int a = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -100), 120);
+          const float inv = __uint_as_float((uint32_t)(127 - a) << 23);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float u = f[2 * j] * inv, v = f[2 * j + 1] * inv;
+            hi[j] = e4m3x2(u, v);
+            uint32_t h;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi[j]));
+            const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
+            lo[j] = e4m3x2((u - g.x) * 16.f, (v - g.y) * 16.f);
+          }
+          // 8 codes a lane: half a 16-byte chunk
+          const uint32_t to = ((((uint32_t)ch >> 1) ^ (row & 7)) << 4) + (ch & 1) * 8;
+          *reinterpret_cast<uint2*>(dst + to) =
+              make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(dst + NR * 128 + to) =
+              make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          // an infinite q has no product with a value
+          if (ch == 0)
+            ms->a[qb][row] = amax < INFINITY ? __uint_as_float((uint32_t)(127 + a) << 23) *
+                                                   (p.scale * kLog2e)
+                                             : NAN;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(b_qFull + 8 * qb);
+      if constexpr (E4M3) {
+        // the tiles' exponent bytes, four positions a lane: warp 10 K's, warp 11 V's; four
+        // tiles' loads in flight
+        const uint8_t* exps = warp == 10 ? p.c.k_exp : p.c.v_exp;
+        const int log_page = p.c.log_page, n = sg.n;
+#pragma unroll 1
+        for (int i0 = 0; i0 < sg.ntiles; i0 += 4) {
+          int64_t id[4];
+          uint32_t b[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int pos = (sg.tile0 + i0 + k) * kBN + lane * 4;
+            const bool in = i0 + k < sg.ntiles && pos < sg.hi && pos + 4 > sg.lo;
+            id[k] = in ? page_of(p.c, n, pos) : -1;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int pos = (sg.tile0 + i0 + k) * kBN + lane * 4;
+            // a page that reads as zeros: any scale does, but not one that moves the
+            // references
+            b[k] = id[k] < 0 ? 0x7f7f7f7fu
+                             : __ldg(reinterpret_cast<const uint32_t*>(
+                                   exps + (((id[k] * p.c.Hkv + sg.h) << log_page) +
+                                           (pos & ((1 << log_page) - 1)))));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (i0 + k >= sg.ntiles) break;
+            const uint32_t t = base + i0 + k, q = t % kExpDepth;
+            wait_bar(b_expEmpty + 8 * q, ((t / kExpDepth) & 1) ^ 1, s_abort, status);
+            *reinterpret_cast<uint32_t*>(smem + F::kExpOff + q * 256 + (warp - 10) * 128 +
+                                         lane * 4) = b[k];
+            mbar_arrive(b_expFull + 8 * q);
+          }
+        }
+      }
+      base += sg.ntiles;
+    }
   } else if (E4M3) {
     reg_dec<88>();
     // ------------------------------------------------------------ V's codes to halves

@@ -43,6 +43,7 @@ using namespace attend;
 constexpr int kRows = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;  // S at 0 and 128, O at 256 and 256 + DP
+constexpr float kGrow = 8.0f;    // log2 growth of a maximum that moves the reference
 
 template <int DP, bool E4M3>
 struct Many {
