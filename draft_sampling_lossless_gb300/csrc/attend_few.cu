@@ -40,8 +40,6 @@ namespace {
 
 using namespace attend;
 
-constexpr uint32_t kTmemCols = 256;
-constexpr uint32_t kColO = 128;       // S at 0 and 64, O at 128 and 192
 constexpr float kUnset = 3.0e38f;     // -m of a row that has seen nothing
 constexpr int kExpDepth = 8;          // tiles of exponent bytes held
 constexpr int kHelpers = 64;          // threads of warps 10 and 11
@@ -49,6 +47,10 @@ constexpr int kHelpers = 64;          // threads of warps 10 and 11
 template <int DP, int NR, bool E4M3>
 struct Few {
   static constexpr int kThreads = E4M3 ? 512 : 384;
+  // tiles of scores ahead: e4m3 tiles come twice as fast, and one's softmax is longer
+  static constexpr int kSBufs = E4M3 ? 4 : 2;
+  static constexpr uint32_t kColO = 64 * kSBufs;  // tensor memory: S, 64 columns each, then O
+  static constexpr uint32_t kTmemCols = E4M3 ? 512 : 256;
   static constexpr int kNH = DP / 64;
   static constexpr int kQRows = E4M3 ? 2 * NR : (NR < 16 ? 16 : NR);  // N of the scores
   static constexpr uint32_t kSlot = E4M3 ? kHalf : kHalf * kNH;       // a tile as loaded
@@ -77,7 +79,7 @@ struct Misc {  // shared words
   int64_t sum[16];
   Found found;
   Segment seg[kSegDepth];
-  uint64_t bars[2 * 12 + 2 * kSegDepth + 4 + 6 + 4 + 2 * kExpDepth + 1];
+  uint64_t bars[2 * 12 + 2 * kSegDepth + 4 + 8 + 4 + 2 * kExpDepth + 1];
   int abort_flag, last;
   uint32_t tmem;
 };
@@ -108,46 +110,40 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return d;
 }
 
-// The scores of a thread's position: x[r] = log2 of row r's exponential, up to the
-// reference (e4m3: times 2^e of the value's exponent e).
-template <int NR, bool E4M3>
-__device__ __forceinline__ void load_scores(uint32_t t_s, const float* row_scale, float c2,
-                                            float ck, float ev, float (&x)[NR]) {
-  if constexpr (!E4M3) {
-    uint32_t v[NR];
-    if constexpr (NR == 8)
-      tmem_ld_32x32b_x8(t_s, v);
-    else if constexpr (NR == 16)
-      tmem_ld_32x32b_x16(t_s, v);
+// The scores of a thread's position, N rows from r0 on: x[k] = log2 of row r0 + k's
+// exponential (e4m3: times 2^e of the value's exponent e), plus nm[r0 + k].
+template <int N, int NR, bool E4M3>
+__device__ __forceinline__ void load_scores(uint32_t t_s, int r0, const float* nm,
+                                            const float* row_scale, float c2, float ck, float ev,
+                                            float* x) {
+  uint32_t u[N], v[E4M3 ? N : 1];
+  if constexpr (N == 8)
+    tmem_ld_32x32b_x8(t_s + r0, u);
+  else if constexpr (N == 16)
+    tmem_ld_32x32b_x16(t_s + r0, u);
+  else
+    tmem_ld_32x32b_x32(t_s + r0, u);
+  if constexpr (E4M3) {
+    if constexpr (N == 8)
+      tmem_ld_32x32b_x8(t_s + NR + r0, v);
     else
-      tmem_ld_32x32b_x32(t_s, v);
-    tmem_wait_ld_regs(v);
-#pragma unroll
-    for (int r = 0; r < NR; ++r) x[r] = __uint_as_float(v[r]) * c2;
+      tmem_ld_32x32b_x16(t_s + NR + r0, v);
+    tmem_wait_ld_regs(u, v);
   } else {
-    constexpr int kB = NR < 16 ? NR : 16;
+    tmem_wait_ld_regs(u);
+  }
 #pragma unroll
-    for (int r0 = 0; r0 < NR; r0 += kB) {
-      uint32_t u[kB], v[kB];
-      if constexpr (kB == 8) {
-        tmem_ld_32x32b_x8(t_s + r0, u);
-        tmem_ld_32x32b_x8(t_s + NR + r0, v);
-      } else {
-        tmem_ld_32x32b_x16(t_s + r0, u);
-        tmem_ld_32x32b_x16(t_s + NR + r0, v);
-      }
-      tmem_wait_ld_regs(u, v);
-#pragma unroll
-      for (int r = 0; r < kB; r += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(row_scale + r0 + r);
-        const float af[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float y = fmaf(__uint_as_float(v[r + k]), 0.0625f, __uint_as_float(u[r + k]));
-          x[r0 + r + k] = fmaf(y * af[k], ck, ev);
-        }
-      }
+  for (int k = 0; k < N; k += 2) {
+    unsigned long long y = pack2(__uint_as_float(u[k]), __uint_as_float(u[k + 1]));
+    const float2 n2 = *reinterpret_cast<const float2*>(nm + r0 + k);
+    if constexpr (E4M3) {
+      y = fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), pack2(0.0625f, 0.0625f), y);
+      const float2 a = *reinterpret_cast<const float2*>(row_scale + r0 + k);
+      y = fma2(mul2(y, pack2(a.x, a.y)), pack2(ck, ck), add2(pack2(n2.x, n2.y), pack2(ev, ev)));
+    } else {
+      y = fma2(y, pack2(c2, c2), pack2(n2.x, n2.y));
     }
+    unpack2(y, x[k], x[k + 1]);
   }
 }
 
@@ -156,16 +152,18 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     attend_few_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
   using F = Few<DP, NR, E4M3>;
-  constexpr int NS = F::kSlots, NH = F::kNH;
+  constexpr int NS = F::kSlots, NH = F::kNH, SB = F::kSBufs;
   constexpr int kConvWarps = E4M3 ? 4 : 0;
   // P's largest exponent, and how far above the first score its reference starts
   constexpr float kLimit = E4M3 ? 15.f : 64.f, kAbove = E4M3 ? 8.f : 0.f;
+  // what the rest of P is multiplied by: halves end at 2^-24, this keeps 2^-35
+  constexpr float kRest = E4M3 ? 2048.f : 1.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc* ms = reinterpret_cast<Misc*>(smem + F::kMiscOff);
   const uint32_t b_full = smem_u32(ms->bars), b_empty = b_full + 8 * NS;
   const uint32_t b_segFull = b_empty + 8 * NS, b_segEmpty = b_segFull + 8 * kSegDepth;
   const uint32_t b_qFull = b_segEmpty + 8 * kSegDepth, b_qEmpty = b_qFull + 16;
-  const uint32_t b_s = b_qEmpty + 16, b_p = b_s + 16, b_o = b_p + 16;
+  const uint32_t b_s = b_qEmpty + 16, b_p = b_s + 32, b_o = b_p + 16;
   const uint32_t b_vfFull = b_o + 16, b_vfEmpty = b_vfFull + 16;
   const uint32_t b_expFull = b_vfEmpty + 16, b_expEmpty = b_expFull + 8 * kExpDepth;
   const uint32_t b_drain = b_expEmpty + 8 * kExpDepth;
@@ -185,6 +183,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       mbar_init(b_qFull + 8 * i, kHelpers);
       mbar_init(b_qEmpty + 8 * i, 1);
       mbar_init(b_s + 8 * i, 1);
+      mbar_init(b_s + 16 + 8 * i, 1);
       mbar_init(b_p + 8 * i, 128);
       mbar_init(b_o + 8 * i, 1);
       mbar_init(b_vfFull + 8 * i, 128);
@@ -200,7 +199,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   const Range rg = plan<32, F::kThreads>(p, ms->sum, &ms->found);
   if (rg.u0 >= rg.u1) return;  // no tiles for this block
   if (warp == kWarpMma) {
-    tmem_alloc(smem_u32(&ms->tmem), kTmemCols);
+    tmem_alloc(smem_u32(&ms->tmem), F::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -267,17 +266,17 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         ok = ok && wait_bar(b_full + 8 * (e % NS), (e / NS) & 1, s_abort, status);
         tc_fence_after();
       };
-      auto scores = [&](int s, uint32_t e, int qb) {
+      auto scores = [&](int sb, uint32_t e, int qb) {
         const uint64_t a = desc_kmajor_sw128(at0 + (e % NS) * F::kSlot);
         const uint64_t b = desc_kmajor_sw128(at0 + F::kQOff + qb * F::kQBytes);
         for (int k = 0; k < ksteps; ++k) {
           if constexpr (E4M3)
-            mma_e4m3(tmem + s * 64, a + k * 2, b + k * 2, kIdS, k > 0);
+            mma_e4m3(tmem + sb * 64, a + k * 2, b + k * 2, kIdS, k > 0);
           else
-            mma_bf16(tmem + s * 64, a + (k >> 2) * (kHalf >> 4) + (k & 3) * 2,
+            mma_bf16(tmem + sb * 64, a + (k >> 2) * (kHalf >> 4) + (k & 3) * 2,
                      b + (k >> 2) * (F::kQHalf >> 4) + (k & 3) * 2, kIdS, k > 0);
         }
-        mma_commit(b_s + 8 * s);
+        mma_commit(b_s + 8 * sb);
         mma_commit(b_empty + 8 * (e % NS));
       };
       for (int sn = 0; ok; ++sn) {
@@ -292,7 +291,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t e0 = 2 * base;  // K of tile i: e0 + 2 i, V: one more
-        for (int i = 0; i < 2 && i < nt && ok; ++i) {
+        for (int i = 0; i < SB && i < nt && ok; ++i) {
           need(e0 + 2 * i);
           if (ok) scores(i, e0 + 2 * i, qb);
         }
@@ -314,14 +313,13 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
               NH > 1 ? kHalf : 0);
           const uint64_t b = desc_mnmajor_sw128(at0 + F::kPOff + s * kHalf, 0);
           for (int k = 0; k < kBN / 16; ++k)
-            mma_bf16(tmem + kColO + s * 64, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdO,
+            mma_bf16(tmem + F::kColO + s * 64, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdO,
                      i >= 2 || k > 0);
           mma_commit(E4M3 ? b_vfEmpty + 8 * vf : b_empty + 8 * (ev % NS));
-          if (i + 2 < nt) {
-            need(ev + 3);
-            if (ok) scores(s, ev + 3, qb);
-          } else {
-            mma_commit(b_o + 8 * s);
+          mma_commit(b_o + 8 * s);
+          if (i + SB < nt) {
+            need(ev + 2 * SB - 1);
+            if (ok) scores(i % SB, ev + 2 * SB - 1, qb);
           }
         }
         mma_commit(b_qEmpty + 8 * qb);
@@ -339,7 +337,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     const int s = warp >> 2;    // the stream
     const int pt = tid & 127;   // position of the tile, value of D at the end
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + s * 64, t_o = tmem + lanes + kColO + s * 64;
+    const uint32_t t_o = tmem + lanes + F::kColO + s * 64;
     const float c2 = p.scale * kLog2e;
     uint8_t* my_p = smem + F::kPOff + s * kHalf + pt * 128;
     uint32_t ph_s = 0, ph_o = 0, base = 0;
@@ -377,9 +375,11 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           ev = (float)(ee - 127);
           un = __uint_as_float((uint32_t)(254 - ee) << 23);
         }
-        wait_bar(b_s + 8 * s, ph_s, s_abort, status);
+        const int sb = i % SB;
+        const uint32_t t_s = tmem + lanes + sb * 64;
+        wait_bar(b_s + 8 * sb, (ph_s >> sb) & 1, s_abort, status);
         __syncwarp();
-        ph_s ^= 1;
+        ph_s ^= 1u << sb;
         tc_fence_after();
         // rows r_lo .. r_hi - 1 see this thread's position
         int r_lo = 0, r_hi = NR;
@@ -398,60 +398,71 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           }
         }
         float x[NR];
-        load_scores<NR, E4M3>(t_s, ms->a[sn & 1], c2, ck, ev, x);
-        if (i == s) {
-          // the references: the scores of a position that every row sees
-          const int c0 = max(all_lo - t0, 0);
-          if (c0 < min(all_hi - t0, kBN)) {
-            if (pt == c0)
+        bool prior = i < 2;  // the products before this tile's are done
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          if (pass == 0 && i == s) {
+            // the references: the scores of a position that every row sees
+            const int c0 = max(all_lo - t0, 0);
+            const bool any = c0 < min(all_hi - t0, kBN);
+            if (pt < 32) ms->nm[s][pt] = any ? 0.f : kUnset;
+            group_sync(2 + s, 128);
+            if (any && (pt >> 5) == (c0 >> 5)) {
+#pragma unroll 1
+              for (int r0 = 0; r0 < NR; r0 += 8) {
+                load_scores<8, NR, E4M3>(t_s, r0, ms->nm[s], ms->a[sn & 1], c2, ck, ev, x);
+                if (pt == c0)
 #pragma unroll
-              for (int r = 0; r < NR; ++r)
-                ms->nm[s][r] = fabsf(x[r]) < 1.0e30f ? -(x[r] + kAbove) : kUnset;
-          } else if (pt < NR) {
-            ms->nm[s][pt] = kUnset;
+                  for (int k = 0; k < 8; ++k)
+                    ms->nm[s][r0 + k] = fabsf(x[k]) < 1.0e30f ? -(x[k] + kAbove) : kUnset;
+                __syncwarp();
+              }
+            }
+            group_sync(2 + s, 128);
           }
-          group_sync(2 + s, 128);
-        }
-        float top = -INFINITY;
+          constexpr int kN = E4M3 && NR > 16 ? 16 : NR;
+          float top = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < NR; r += 4) {
-          const float4 nm = *reinterpret_cast<const float4*>(&ms->nm[s][r]);
-          x[r] += nm.x;
-          x[r + 1] += nm.y;
-          x[r + 2] += nm.z;
-          x[r + 3] += nm.w;
+          for (int r0 = 0; r0 < NR; r0 += kN)
+            load_scores<kN, NR, E4M3>(t_s, r0, ms->nm[s], ms->a[sn & 1], c2, ck, ev, x + r0);
           if (mask)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (r + k < r_lo || r + k >= r_hi) x[r + k] = -INFINITY;
-          top = max3(top, x[r], x[r + 1]);
-          top = max3(top, x[r + 2], x[r + 3]);
-        }
-        if (group_any(2 + s, 128, top > kLimit)) {
-          // the references move to the tile's maxima (rarely)
-          load_scores<NR, E4M3>(t_s, ms->a[sn & 1], c2, ck, ev, x);
-          {
-            float y[NR];
-#pragma unroll
             for (int r = 0; r < NR; ++r)
-              y[r] = mask && (r < r_lo || r >= r_hi) ? -INFINITY : x[r];
-            const float m = reduce_rows<NR>(y, [](float a, float b) { return fmaxf(a, b); });
-            if (lane % (32 / NR) == 0) ms->wm[s][warp & 3][lane / (32 / NR)] = m;
+              if (r < r_lo || r >= r_hi) x[r] = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < NR; r += 2) top = max3(top, x[r], x[r + 1]);
+          if (!group_any(2 + s, 128, pass == 0 && top > kLimit)) break;
+
+          // the references move past the tile's maxima (rarely)
+          if (!prior) {
+            wait_bar(b_o + 8 * s, ph_o, s_abort, status);
+            __syncwarp();
+            ph_o ^= 1;
+            tc_fence_after();
+          }
+          if (pt < 32) ms->f[s][pt] = 0.f;
+          group_sync(2 + s, 128);
+#pragma unroll 1
+          for (int r0 = 0; r0 < NR; r0 += 8) {
+            float y[8];
+            load_scores<8, NR, E4M3>(t_s, r0, ms->f[s], ms->a[sn & 1], c2, ck, ev, y);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (mask && (r0 + k < r_lo || r0 + k >= r_hi)) y[k] = -INFINITY;
+            const float m = reduce_rows<8>(y, [](float a, float b) { return fmaxf(a, b); });
+            if ((lane & 3) == 0) ms->wm[s][warp & 3][r0 + (lane >> 2)] = m;
           }
           group_sync(2 + s, 128);
           if (pt < NR) {
             const float old = -ms->nm[s][pt];
-            const float m = max3(fmaxf(old, ms->wm[s][0][pt]),
-                                 fmaxf(ms->wm[s][1][pt], ms->wm[s][2][pt]), ms->wm[s][3][pt]);
+            const float m = fmaxf(old, kAbove + max3(fmaxf(ms->wm[s][0][pt], ms->wm[s][1][pt]),
+                                                     ms->wm[s][2][pt], ms->wm[s][3][pt]));
             ms->nm[s][pt] = -m;
             ms->f[s][pt] = ex2_approx(old - m);
           }
           group_sync(2 + s, 128);
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            l[r] *= ms->f[s][r];
-            x[r] = mask && (r < r_lo || r >= r_hi) ? -INFINITY : x[r] + ms->nm[s][r];
-          }
+          for (int r = 0; r < NR; ++r) l[r] *= ms->f[s][r];
           if (i >= 2) {
 #pragma unroll 1
             for (int c = 0; c < 2 * NR; c += 8) {
@@ -465,6 +476,12 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
             }
             tmem_wait_st();
           }
+          prior = true;
+        }
+        if (!prior) {
+          wait_bar(b_o + 8 * s, ph_o, s_abort, status);
+          __syncwarp();
+          ph_o ^= 1;
         }
         // P: the position's row of [rounded | rest], 8 packed rows a chunk
 #pragma unroll
@@ -479,8 +496,9 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
               l[r0 + 2 * k + 1] = fmaf(b, un, l[r0 + 2 * k + 1]);
               hi[k] = pack_half(a, b);
               const float2 h = __half22float2(*reinterpret_cast<__half2*>(&hi[k]));
-              ra = a - h.x;
-              rb = b - h.y;
+              unpack2(fma2(pack2(h.x, h.y), pack2(-kRest, -kRest),
+                           mul2(pack2(a, b), pack2(kRest, kRest))),
+                      ra, rb);
               lo[k] = pack_half(ra, rb);
             } else {
               l[r0 + 2 * k] += a;
@@ -573,7 +591,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           tmem_wait_ld_regs(u, v);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            o[r0 + k] = (__uint_as_float(u[k]) + __uint_as_float(v[k])) *
+            o[r0 + k] = fmaf(__uint_as_float(v[k]), 1.f / kRest, __uint_as_float(u[k])) *
                         __shfl_sync(0xffffffffu, w_mine, r0 + k);
         }
       }
@@ -713,7 +731,11 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   } else if (E4M3) {
     reg_dec<88>();
     // ------------------------------------------------------------ V's codes to halves
-    const int ct = tid - 384;  // 8 lanes a row of 128 codes, 16 codes a lane
+    // a warp takes eight rows of 64 codes at a time, 16 codes a lane; each eight lanes
+    // have rows that differ in their lowest and highest bit, so that neither the
+    // (swizzled) loads nor the stores share a bank
+    const int ct = tid - 384, c = lane & 3;
+    const int row8 = (lane >> 3) ^ (lane & 4 ? 5 : 0);
     uint32_t base = 0;
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth;
@@ -733,31 +755,38 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         wait_bar(b_vfEmpty + 8 * vf, ((q >> 1) & 1) ^ 1, s_abort, status);
         const uint8_t* src = smem + slot * F::kSlot;
         uint8_t* dst = smem + F::kVfOff + vf * F::kVf;
-        const int c = ct & 7;
-#pragma unroll 4
-        for (int k = 0; k < 8; ++k) {
-          const int row = k * 16 + (ct >> 3);
-          uint4 w = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
-          if (edge && (t0 + row < lo || t0 + row >= hi)) w = make_uint4(0, 0, 0, 0);
-          uint32_t h[8];
-          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+        if (edge) {
+          // values that no row sees: 0 * NaN must not reach a sum
+          const int row = ct;
+          if (t0 + row < lo || t0 + row >= hi)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * j]) : "h"((uint16_t)in[j]));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * j + 1]) : "h"((uint16_t)(in[j] >> 16)));
-          }
-          if (c < DP / 16) {
-            // lanes 0-3 and 4-7 of a row write chunks of the two halves of D: even ones
-            // and odd ones first, so that the eight fall in different banks
-            uint8_t* to = dst + (c >> 2) * kHalf + row * 128;
-            const int first = 2 * (c & 3) + (c >> 2), second = first ^ 1;
-            const bool odd = c >> 2;
-            *reinterpret_cast<uint4*>(to + ((first ^ (row & 7)) << 4)) =
-                odd ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(to + ((second ^ (row & 7)) << 4)) =
-                odd ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
-          }
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(smem + slot * F::kSlot + row * 128 + k * 16) =
+                  make_uint4(0, 0, 0, 0);
+          group_sync(4, 128);
         }
+#pragma unroll
+        for (int half = 0; half < NH; ++half)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = (k * 4 + (warp & 3)) * 8 + row8;
+            const uint4 w = *reinterpret_cast<const uint4*>(
+                src + row * 128 + (((half * 4 + c) ^ row8) << 4));
+            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            uint32_t h[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * j]) : "h"((uint16_t)in[j]));
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+                  : "=r"(h[2 * j + 1])
+                  : "h"((uint16_t)(in[j] >> 16)));
+            }
+            uint8_t* to = dst + half * kHalf + row * 128;
+            *reinterpret_cast<uint4*>(to + (((2 * c) ^ row8) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ row8) << 4)) =
+                make_uint4(h[4], h[5], h[6], h[7]);
+          }
         fence_proxy_async_smem();
         mbar_arrive(b_vfFull + 8 * vf);
         group_sync(4, 128);
@@ -770,7 +799,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   __syncthreads();
   if (warp == kWarpMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, F::kTmemCols);
   }
 }
 
