@@ -4,13 +4,15 @@
 // For each request and key/value head h, the rows of all G = Hq / Hkv query heads
 // that share h are packed, r = j * G + g, and cut into row tiles; an item is one row
 // tile of one head of one request, its work the tiles of 128 positions that its
-// rows see.  All items' tiles, in the order (request, row tile, head, position),
-// are split evenly over the blocks: a block that gets part of an item leaves
-// its O, m, l in the workspace, and the last of the item's blocks to finish joins
-// them in block order (results do not depend on which one that is).  The lengths are
-// read on the device: every block finds its own range with a scan over the
-// requests.  The TMA warp walks the range and hands the others their parts of items
-// through a short queue of segments.
+// rows see.  The items, in the order (request, row tile, head), are split evenly over
+// the blocks, an item counting its tiles and kItemCost more for what it costs besides.
+// A block that gets part of an item leaves its O, m, l in the workspace, and the last
+// of the item's blocks to finish joins them in block order (results do not depend on
+// which one that is).  A join takes as long as a few tiles, so a cut that falls
+// within kSnap tiles of an item's end moves there.  The lengths are read on the
+// device: every block finds its own range with a scan over the requests.  One warp
+// walks the range, loads K, and hands the others their parts of items through a
+// short queue of segments.
 #pragma once
 
 #include "cache.cuh"
@@ -32,10 +34,12 @@ constexpr int kMaxSmem = 232448;
 constexpr uint32_t kHalf = kBN * 128;  // bytes of 128 rows of 128 bytes
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int kWaitTries = 1 << 22;
 constexpr uint32_t kCounterOffset = 256;  // workspace: status word, counters, partials
 constexpr uint32_t kPartOffset = 4096;
-constexpr int kMinTiles = 2;
+constexpr int kItemCost = 2;  // in tiles: Q, the final sums and the store of an item
+constexpr int kSnap = 3;
+constexpr int kMinUnits = 6;  // fewer blocks rather than less work for each
 
 // n / d for 0 <= n < 2^31 by a multiplication (d fixed for the launch): with
 // 2^(s-1) < d <= 2^s and mul = floor(2^32 (2^s - d) / d) + 1, n / d is
@@ -133,21 +137,22 @@ struct Segment {  // part of an item that this block computes
 };
 static_assert(sizeof(Segment) == 64, "a segment's words");
 
+// Waits for a phase; gives up when another role has, or after kWaitTries tries (each
+// suspended for a while by the hardware).  Short: it is inlined in every role's loop,
+// and the loops of a block's roles share the instruction caches.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          uint32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (;;) {
+  int tries = kWaitTries;
 #pragma unroll 1
-    for (int i = 0; i < 16; ++i)
-      if (mbar_try_wait_sleep(bar, parity, 1000)) return true;
+  while (!mbar_try_wait(bar, parity)) {
     if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > kWaitNs) {
+    if (--tries == 0) {
       *abort_flag = 1;
       set_flag(status, kFlagWaitTimeout);
       return false;
     }
   }
+  return true;
 }
 
 // Registers a thread after the roles part.
@@ -189,34 +194,34 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Blocks 0 .. ctas-1 take `each` tiles, the first `extra` of them one more.
+// Blocks 0 .. ctas-1 take `each` units (tiles and items' costs), the first `extra` of
+// them one more.
+struct Found {  // the request that holds a unit, from the thread that finds it
+  int64_t before;  // units of the requests before it
+  int n;
+  Req q;
+};
 struct Range {
-  int64_t each, u0, u1;  // u0 .. u1 - 1: this block's tiles
+  int64_t each, u0, u1;  // u0 .. u1 - 1: this block's units
   int ctas, extra;
-  int n;                 // the request of tile u0
-  int64_t before;        // tiles of the requests before n
-  Req q;                 // request n
+  bool last;             // u1 is the end of all work
 
   __device__ __forceinline__ int block_of(int64_t u) const {
     const int64_t wide = extra * (each + 1);
     return u < wide ? (int)(u / (each + 1)) : extra + (int)((u - wide) / each);
   }
 };
-struct Found {  // the request of a block's first tile, from the thread that finds it
-  int64_t before;
-  int n;
-  Req q;
-};
 
-// Tiles of a request over all heads and every step-th row tile from `first` on.
-__device__ __forceinline__ int64_t req_tiles(const Params& p, const Req& q, int first, int step) {
+// Units of a request over all heads and every step-th row tile from `first` on.
+__device__ __forceinline__ int64_t req_units(const Params& p, const Req& q, int first, int step) {
   int64_t u = 0;
 #pragma unroll 1
-  for (int qt = first; qt < q.tiles; qt += step) u += item_of(p, q, qt).ntiles;
+  for (int qt = first; qt < q.tiles; qt += step) u += item_of(p, q, qt).ntiles + kItemCost;
   return u * p.c.Hkv;
 }
 
-// Every block's range of tiles, from a scan over the requests (all threads).
+// Every block's range of units, from a scan over the requests (all threads);
+// s_found[0] and [1] get the requests of u0 and u1.
 template <int ROWS, int THREADS>
 __device__ __forceinline__ Range plan(const Params& p, int64_t* s_sum, Found* s_found) {
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
@@ -229,7 +234,7 @@ __device__ __forceinline__ Range plan(const Params& p, int64_t* s_sum, Found* s_
     q = Req{};
     if (n < p.c.R) q = load_req<ROWS>(p, n);
     const bool many = q.tiles > 4;
-    if (!many) local += req_tiles(p, q, 0, 1);
+    if (!many) local += req_units(p, q, 0, 1);
     // requests of many row tiles: the warp together
     for (uint32_t left = __ballot_sync(0xffffffffu, many); left != 0; left &= left - 1) {
       const int src = __ffs(left) - 1;
@@ -239,7 +244,7 @@ __device__ __forceinline__ Range plan(const Params& p, int64_t* s_sum, Found* s_
       o.ctx = __shfl_sync(0xffffffffu, q.ctx, src);
       o.tiles = __shfl_sync(0xffffffffu, q.tiles, src);
       o.rows = __shfl_sync(0xffffffffu, q.rows, src);
-      int64_t u = req_tiles(p, o, lane, 32);
+      int64_t u = req_units(p, o, lane, 32);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
       if (lane == src) local += u;
@@ -260,142 +265,214 @@ __device__ __forceinline__ Range plan(const Params& p, int64_t* s_sum, Found* s_
     total += s_sum[w];
   }
   Range r;
-  // few tiles: fewer blocks, kMinTiles each, rather than more partial results
-  r.ctas = (int)min((int64_t)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
+  r.ctas = (int)min((int64_t)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
   r.u0 = r.u1 = 0;
   if ((int)blockIdx.x >= r.ctas) return r;
   r.each = total < (1ll << 31) ? (int64_t)((uint32_t)total / (uint32_t)r.ctas) : total / r.ctas;
   r.extra = (int)(total - r.each * r.ctas);
   r.u0 = r.each * blockIdx.x + min((int)blockIdx.x, r.extra);
   r.u1 = r.u0 + r.each + ((int)blockIdx.x < r.extra);
+  r.last = r.u1 == total;
   int64_t at = base + incl - local;
-  if (at <= r.u0 && r.u0 < at + local) {
+  if (at < r.u1 + 1 && r.u0 < at + local) {
 #pragma unroll 1
     for (int i = 0; i < per; ++i) {
       const int n = tid * per + i;
       if (n >= p.c.R) break;
       if (per > 1) q = load_req<ROWS>(p, n);
-      const int64_t u = per == 1 ? local : req_tiles(p, q, 0, 1);
-      if (r.u0 < at + u) {
-        s_found->n = n;
-        s_found->before = at;
-        s_found->q = q;
-        break;
+      const int64_t u = per == 1 ? local : req_units(p, q, 0, 1);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t x = k ? r.u1 : r.u0;
+        if (at <= x && x < at + u) {
+          s_found[k].n = n;
+          s_found[k].before = at;
+          s_found[k].q = q;
+        }
       }
       at += u;
     }
   }
   __syncthreads();
-  r.n = s_found->n;
-  r.before = s_found->before;
-  r.q = s_found->q;
   return r;
 }
 
-// The TMA warp: walks the block's range, queues its segments (an empty one at the
-// end) and has `load(rows, none)` load each tile: rows[b] is the pool's row of box
-// b's first position, or `none` (past the pool, so that the box reads as zeros)
-// where no row of the item sees the box.  Stops when a wait of load's failed.
-template <int ROWS, class Load>
-__device__ __forceinline__ void produce(const Params& p, const Range& rg, Segment* s_seg,
-                                        uint32_t b_segFull, uint32_t b_segEmpty,
-                                        volatile int* s_abort, Load&& load) {
+// A place in the order of items: `tile` of head h of row tile qt of request n;
+// n = R is the end.
+struct Place {
+  Req q;
+  int64_t a;  // units before the item
+  int n, qt, h, tile;
+};
+
+// What a cut does to an item of nt tiles: up to `low` tiles in, it moves to the
+// item's start, from nt - high on to its end.
+__device__ __forceinline__ int snap_low(int nt) { return min(kSnap, nt >> 1); }
+__device__ __forceinline__ int snap_high(int nt) { return min(kSnap, nt - snap_low(nt) - 1); }
+
+template <int ROWS>
+__device__ __forceinline__ void next_item(const Params& p, Place& w, int nt) {
+  w.a += nt + kItemCost;
+  w.tile = 0;
+  if (++w.h < p.c.Hkv) return;
+  w.h = 0;
+  if (++w.qt < w.q.tiles) return;
+  w.qt = 0;
+#pragma unroll 1
+  while (++w.n < p.c.R) {
+    w.q = load_req<ROWS>(p, w.n);
+    if (w.q.tiles > 0) break;
+  }
+}
+
+// The place of unit u, a cut between two blocks (warp-collective).
+template <int ROWS>
+__device__ __forceinline__ Place locate(const Params& p, const Found& f, int64_t u) {
+  const int lane = threadIdx.x & 31;
+  Place w;
+  w.q = f.q;
+  w.n = f.n;
+  w.qt = 0;
+  int64_t v = u - f.before;
+#pragma unroll 1
+  while (w.q.tiles > 1) {
+    const int64_t mine =
+        w.qt + lane < w.q.tiles
+            ? (int64_t)(item_of(p, w.q, w.qt + lane).ntiles + kItemCost) * p.c.Hkv
+            : 0;
+    int64_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, v < incl);
+    if (past != 0 || w.qt + 32 >= w.q.tiles) {
+      const int src = past != 0 ? __ffs(past) - 1 : 0;
+      v -= __shfl_sync(0xffffffffu, incl - mine, src);
+      w.qt += src;
+      break;
+    }
+    v -= __shfl_sync(0xffffffffu, incl, 31);
+    w.qt += 32;
+  }
+  const int nt = item_of(p, w.q, w.qt).ntiles, units = nt + kItemCost;
+  w.h = v < (1ll << 31) ? (int)((uint32_t)v / (uint32_t)units) : (int)(v / units);
+  const int off = (int)(v - (int64_t)w.h * units);
+  w.a = u - off;
+  const int t = off - kItemCost;
+  w.tile = t <= snap_low(nt) ? 0 : t;
+  if (t >= nt - snap_high(nt)) next_item<ROWS>(p, w, nt);
+  return w;
+}
+
+// Loads a segment's tiles: `issue(rows, mine, none)` for each, where rows[b] is the pool's row
+// of box b's first position, or `none` (past the pool, so that the box reads as
+// zeros) where no row of the item sees the box; `mine`, lane b's own of them.  False
+// when issue failed.
+template <class Issue>
+__device__ __forceinline__ bool load_segment(const Params& p, const Segment& sg, Issue& issue) {
   const int lane = threadIdx.x & 31;
   const int log_page = p.c.log_page, page = 1 << log_page;
   const int box_rows = min(page, kBN), n_boxes = kBN / box_rows;
   const int none = (int)(p.c.n_pages * p.c.Hkv) << log_page;
-  int n = rg.n;
-  Req q = rg.q;
-  int64_t u = rg.u0;
-  int qt = 0, h, off;
-  {
-    // the row tile, head and position tile of u0 within its request
-    int64_t v = u - rg.before;
-    while (q.tiles > 1) {
-      const int64_t mine = qt + lane < q.tiles ? (int64_t)item_of(p, q, qt + lane).ntiles * p.c.Hkv
-                                               : 0;
-      int64_t incl = mine;
+  auto lookup = [&](int tile) {  // lane b: box b
+    if (lane >= n_boxes) return none;
+    const int pos = tile * kBN + lane * box_rows;
+    if (pos >= sg.hi || pos + box_rows <= sg.lo) return none;
+    const int64_t id = page_of(p.c, sg.n, pos);
+    if (id < 0) return none;
+    return (int)((id * p.c.Hkv + sg.h) << log_page) + (pos & (page - 1));
+  };
+  int next = lookup(sg.tile0);
+#pragma unroll 1
+  for (int i = 0; i < sg.ntiles; ++i) {
+    const int mine = next;
+    int y[8];
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, v < incl);
-      if (past != 0 || qt + 32 >= q.tiles) {
-        const int src = past != 0 ? __ffs(past) - 1 : 0;
-        v -= __shfl_sync(0xffffffffu, incl - mine, src);
-        qt += src;
-        break;
-      }
-      v -= __shfl_sync(0xffffffffu, incl, 31);
-      qt += 32;
-    }
-    const int nt = item_of(p, q, qt).ntiles;
-    h = v < (1ll << 31) ? (int)((uint32_t)v / (uint32_t)nt) : (int)(v / nt);
-    off = (int)(v - (int64_t)h * nt);
+    for (int b = 0; b < 8; ++b) y[b] = __shfl_sync(0xffffffffu, mine, b);
+    if (i + 1 < sg.ntiles) next = lookup(sg.tile0 + i + 1);  // in flight under the waits
+    if (!issue(y, mine, none)) return false;
   }
+  return true;
+}
+
+// Walks the block's range: queues its segments (an empty one at the end) and loads
+// the tiles of each; flush() after each.
+template <int ROWS, class Issue, class Flush>
+__device__ __forceinline__ void produce(const Params& p, const Range& rg, const Found* s_found,
+                                        Segment* s_seg, uint32_t b_segFull, uint32_t b_segEmpty,
+                                        volatile int* s_abort, Issue& issue, Flush& flush) {
+  const int lane = threadIdx.x & 31;
+  Place w = locate<ROWS>(p, s_found[0], rg.u0), e;
+  e.n = p.c.R;
+  e.qt = e.h = e.tile = 0;
+  if (!rg.last) e = locate<ROWS>(p, s_found[1], rg.u1);
 #pragma unroll 1
   for (int sn = 0;; ++sn) {
     const int ss = sn % kSegDepth;
     const bool ok =
         wait_bar(b_segEmpty + 8 * ss, ((sn / kSegDepth) & 1) ^ 1, s_abort, p.c.status);
     if (!__all_sync(0xffffffffu, ok)) return;
+    const bool at_end = w.n == e.n && w.qt == e.qt && w.h == e.h;
+    const bool end = w.n >= p.c.R || (at_end && w.tile >= e.tile);
     Segment sg;
-    const Item it = item_of(p, q, qt);
-    const bool end = u >= rg.u1;
-    sg.n = n;
-    sg.row0 = q.row0;
-    sg.m = q.m;
-    sg.ctx = q.ctx;
-    sg.h = h;
-    sg.r0 = it.r0;
-    sg.nrows = it.nrows;
-    sg.lo = it.lo;
-    sg.hi = it.hi;
-    sg.tile0 = it.tile0 + off;
-    sg.ntiles = end ? 0 : (int)min((int64_t)(it.ntiles - off), rg.u1 - u);
-    sg.split = sg.first = sg.last = 0;
-    if (off != 0 || sg.ntiles != it.ntiles) {
-      sg.first = rg.block_of(u - off);
-      sg.last = rg.block_of(u - off + it.ntiles - 1);
-      sg.split = (int)blockIdx.x == sg.first ? 2 : 1;
+    int nt = 0, stop = 0;
+    if (end) {
+      sg.ntiles = 0;
+    } else {
+      const Item it = item_of(p, w.q, w.qt);
+      nt = it.ntiles;
+      stop = at_end ? e.tile : nt;
+      sg.n = w.n;
+      sg.row0 = w.q.row0;
+      sg.m = w.q.m;
+      sg.ctx = w.q.ctx;
+      sg.h = w.h;
+      sg.r0 = it.r0;
+      sg.nrows = it.nrows;
+      sg.lo = it.lo;
+      sg.hi = it.hi;
+      sg.tile0 = it.tile0 + w.tile;
+      sg.ntiles = stop - w.tile;
+      sg.split = sg.first = sg.last = 0;
+      if (sg.ntiles != nt) {
+        sg.first = rg.block_of(w.a + kItemCost + snap_low(nt));
+        sg.last = rg.block_of(w.a + kItemCost + nt - snap_high(nt) - 1);
+        sg.split = (int)blockIdx.x == sg.first ? 2 : 1;
+      }
     }
     if (lane == 0) {
       s_seg[ss] = sg;
       mbar_arrive(b_segFull + 8 * ss);
     }
     if (end) return;
-    if (lane == 0 && __ldg(p.c.row_off + n + 1) - __ldg(p.c.row_off + n) > p.max_rows)
+    if (lane == 0 && __ldg(p.c.row_off + sg.n + 1) - __ldg(p.c.row_off + sg.n) > p.max_rows)
       set_flag(p.c.status, kFlagRowRange);
-    auto lookup = [&](int tile) {  // lane b: box b
-      if (lane >= n_boxes) return none;
-      const int pos = tile * kBN + lane * box_rows;
-      if (pos >= sg.hi || pos + box_rows <= sg.lo) return none;
-      const int64_t id = page_of(p.c, n, pos);
-      if (id < 0) return none;
-      return (int)((id * p.c.Hkv + h) << log_page) + (pos & (page - 1));
-    };
-    int next = lookup(sg.tile0);
+    if (!load_segment(p, sg, issue)) return;
+    flush();
+    if (stop == nt)
+      next_item<ROWS>(p, w, nt);
+    else
+      w.tile = stop;
+  }
+}
+
+// Another warp's loads of the same segments.
+template <class Issue, class Flush>
+__device__ __forceinline__ void follow(const Params& p, Segment* s_seg, uint32_t b_segFull,
+                                       uint32_t b_segEmpty, volatile int* s_abort, Issue& issue,
+                                       Flush& flush) {
 #pragma unroll 1
-    for (int i = 0; i < sg.ntiles; ++i) {
-      int y[8];
-#pragma unroll
-      for (int b = 0; b < 8; ++b) y[b] = __shfl_sync(0xffffffffu, next, b);
-      if (i + 1 < sg.ntiles) next = lookup(sg.tile0 + i + 1);  // in flight under the waits
-      if (!load(y, none)) return;
-    }
-    u += sg.ntiles;
-    off = 0;
-    if (sg.tile0 + sg.ntiles == it.tile0 + it.ntiles && ++h == p.c.Hkv) {
-      h = 0;
-      if (++qt == q.tiles) {
-        qt = 0;
-        while (u < rg.u1 && ++n < p.c.R) {
-          q = load_req<ROWS>(p, n);
-          if (q.tiles > 0) break;
-        }
-      }
-    }
+  for (int sn = 0;; ++sn) {
+    const int ss = sn % kSegDepth;
+    const bool ok = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, p.c.status);
+    if (!__all_sync(0xffffffffu, ok)) return;
+    const Segment sg = s_seg[ss];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(b_segEmpty + 8 * ss);
+    if (sg.ntiles == 0 || !load_segment(p, sg, issue)) return;
+    flush();
   }
 }
 

@@ -12,26 +12,26 @@
 // sums its own exponentials (joined over the positions once, at the end), and no
 // maximum is taken per tile.  P = 2^(s - m) against a reference m of each row: the
 // score of the item's first position that all rows see.  Any reference gives the
-// same quotient as long as P stays in range; where a score passes it by too much
-// (64 powers of two in bf16, 15 in halves), or no position serves all rows, the
-// references move to the tile's maxima, O and the sums with them.
+// same quotient as long as P stays in range; where a score passes it by 64 powers of
+// two, or no position serves all rows, the references move to the tile's maxima,
+// O and the sums with them.  e4m3 terms have less range: there the references
+// are the first tile's maxima, and move when a score passes them by five powers.
 //
-// P enters its product as two 16-bit terms, its rounding and the rounding of the
+// bf16: P enters its product as two bf16 terms, its rounding and the rounding of the
 // rest (columns of N side by side; a row that one position dominates would
 // otherwise carry that rounding straight into the result).
 //
-// bf16: K tiles (as A, K-major) and V tiles (as A, transposed) are multiplied where
-// the TMA put them.  e4m3: K's codes are A of an e4m3 product, with Q as two e4m3
-// terms, q 2^-a = q1 + q2 / 16, which hold a bf16's eight bits exactly (down to
-// 2^-13 of the row's largest; below, to 2^-21 of it); its scale is the
-// thread's own position's, a factor of the scores.  V's codes become halves,
-// exactly, on the way to shared memory (four more warps), and its scale goes into
-// P: P = 2^(s + e - m) with e its exponent, and l sums 2^-e P.
+// e4m3: the codes are multiplied as they are stored.  Q comes as two e4m3 terms,
+// q 2^-a = q1 + q2 / 16, which hold a bf16's eight bits exactly (down to
+// 2^-13 of the row's largest; below, to 2^-21 of it), P as four, each the
+// rounding of what the ones before left, times 16 (16 bits; all of it down to 2^-21).
+// A position's scales are its thread's own: K's a factor of the scores; V's, with
+// exponent e, goes into P = 2^(s + e - m), and l sums 2^-e P.
 //
 // Two streams, a warpgroup each with its own S, P, O and m, take alternate tiles.
-// Roles: warps 0-7 softmax, 8 the MMAs, 9 the TMA loads, 10 and 11 fetch the next
-// item's Q (and the scales of e4m3 tiles), 12-15 convert V.  Every wait is bounded.
-// See attend.cuh for the split of the work.
+// Roles: warps 0-7 softmax, 8 the MMAs, 9 and 10 the loads of K and V (and their
+// scales), 11 fetches the next item's Q.  Every wait is bounded.  See attend.cuh for
+// the split of the work.
 #include "attend.cuh"
 
 namespace dspark {
@@ -42,29 +42,31 @@ using namespace attend;
 
 constexpr float kUnset = 3.0e38f;     // -m of a row that has seen nothing
 constexpr int kExpDepth = 8;          // tiles of exponent bytes held
-constexpr int kHelpers = 64;          // threads of warps 10 and 11
 
 template <int DP, int NR, bool E4M3>
 struct Few {
-  static constexpr int kThreads = E4M3 ? 512 : 384;
+  static constexpr int kThreads = 384;
+  static constexpr int kNH = DP / 64;
+  static constexpr int kParts = E4M3 ? 4 : 2;                         // terms of P
+  static constexpr int kQRows = E4M3 ? 2 * NR : (NR < 16 ? 16 : NR);  // N of the scores
   // tiles of scores ahead: e4m3 tiles come twice as fast, and one's softmax is longer
   static constexpr int kSBufs = E4M3 ? 4 : 2;
-  static constexpr uint32_t kColO = 64 * kSBufs;  // tensor memory: S, 64 columns each, then O
+  // tensor memory: S, 64 columns each, then O of the streams
+  static constexpr uint32_t kColO = 64 * kSBufs, kOCols = E4M3 ? 128 : 64;
   static constexpr uint32_t kTmemCols = E4M3 ? 512 : 256;
-  static constexpr int kNH = DP / 64;
-  static constexpr int kQRows = E4M3 ? 2 * NR : (NR < 16 ? 16 : NR);  // N of the scores
-  static constexpr uint32_t kSlot = E4M3 ? kHalf : kHalf * kNH;       // a tile as loaded
+  static constexpr uint32_t kSlot = E4M3 ? kHalf : kHalf * kNH;       // a tile
   static constexpr uint32_t kQHalf = kQRows * 128;
   static constexpr uint32_t kQBytes = kQHalf * (E4M3 ? 1 : kNH);
-  static constexpr uint32_t kVf = E4M3 ? kHalf * kNH : 0;             // V as halves
   static constexpr uint32_t kExp = E4M3 ? kExpDepth * 256 : 0;
   static constexpr uint32_t kMisc = 4096;
-  static constexpr int kFit =
-      (int)((kMaxSmem - 2 * kHalf - 2 * kQBytes - 2 * kVf - kExp - kMisc) / kSlot);
+  static constexpr int kFit = (int)((kMaxSmem - 2 * kHalf - 2 * kQBytes - kExp - kMisc) / kSlot);
   static constexpr int kSlots = kFit > 12 ? 12 : kFit;
+  // K and V go through one ring by two warps.  A slot that they use in turn (an odd
+  // ring) is safe while a tile's scores are at most (slots - 1) / 2 tiles ahead of its
+  // products: no warp then waits for a phase two ahead of the slot's.
+  static_assert(kSlots % 2 == 0 || kSlots >= 2 * kSBufs + 1, "ring");
   static constexpr uint32_t kPOff = kSlots * kSlot;  // P of each stream; the join's buffer
-  static constexpr uint32_t kVfOff = kPOff + 2 * kHalf;
-  static constexpr uint32_t kQOff = kVfOff + 2 * kVf;
+  static constexpr uint32_t kQOff = kPOff + 2 * kHalf;
   static constexpr uint32_t kExpOff = kQOff + 2 * kQBytes;
   static constexpr uint32_t kMiscOff = kExpOff + kExp;
   static constexpr uint32_t kTotal = kMiscOff + kMisc;
@@ -77,9 +79,9 @@ struct Misc {  // shared words
   float wm[2][4][32];   // the warps' maxima, then sums
   float a[2][32];       // e4m3: scale of the scores of a row, of each Q buffer
   int64_t sum[16];
-  Found found;
+  Found found[2];
   Segment seg[kSegDepth];
-  uint64_t bars[2 * 12 + 2 * kSegDepth + 4 + 8 + 4 + 2 * kExpDepth + 1];
+  uint64_t bars[2 * 12 + 2 * kSegDepth + 4 + 8 + 2 * kExpDepth + 1];
   int abort_flag, last;
   uint32_t tmem;
 };
@@ -104,10 +106,18 @@ __device__ __forceinline__ float reduce_rows(float (&v)[NR], Op op) {
   return v[0];
 }
 
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
+// Two values as four e4m3 terms each: v = t0 + t1 / 16 + t2 / 256 + t3 / 4096.
+__device__ __forceinline__ void e4m3_terms(float a, float b, uint32_t (&t)[4]) {
+  const unsigned long long up = pack2(16.f, 16.f), down = pack2(-16.f, -16.f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    t[k] = e4m3x2(a, b);
+    if (k == 3) break;
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)t[k]));
+    const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
+    unpack2(fma2(pack2(g.x, g.y), down, mul2(pack2(a, b), up)), a, b);
+  }
 }
 
 // The scores of a thread's position, N rows from r0 on: x[k] = log2 of row r0 + k's
@@ -153,19 +163,15 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
   using F = Few<DP, NR, E4M3>;
   constexpr int NS = F::kSlots, NH = F::kNH, SB = F::kSBufs;
-  constexpr int kConvWarps = E4M3 ? 4 : 0;
-  // P's largest exponent, and how far above the first score its reference starts
-  constexpr float kLimit = E4M3 ? 15.f : 64.f, kAbove = E4M3 ? 8.f : 0.f;
-  // what the rest of P is multiplied by: halves end at 2^-24, this keeps 2^-35
-  constexpr float kRest = E4M3 ? 2048.f : 1.f;
+  // P's largest exponent, and where a maximum puts the reference: e4m3 ends at 448
+  constexpr float kLimit = E4M3 ? 8.f : 64.f, kAbove = E4M3 ? -3.f : 0.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc* ms = reinterpret_cast<Misc*>(smem + F::kMiscOff);
   const uint32_t b_full = smem_u32(ms->bars), b_empty = b_full + 8 * NS;
   const uint32_t b_segFull = b_empty + 8 * NS, b_segEmpty = b_segFull + 8 * kSegDepth;
   const uint32_t b_qFull = b_segEmpty + 8 * kSegDepth, b_qEmpty = b_qFull + 16;
   const uint32_t b_s = b_qEmpty + 16, b_p = b_s + 32, b_o = b_p + 16;
-  const uint32_t b_vfFull = b_o + 16, b_vfEmpty = b_vfFull + 16;
-  const uint32_t b_expFull = b_vfEmpty + 16, b_expEmpty = b_expFull + 8 * kExpDepth;
+  const uint32_t b_expFull = b_o + 16, b_expEmpty = b_expFull + 8 * kExpDepth;
   const uint32_t b_drain = b_expEmpty + 8 * kExpDepth;
   volatile int* s_abort = &ms->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -177,26 +183,24 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     for (int i = 0; i < 2 * NS; ++i) mbar_init(b_full + 8 * i, 1);
     for (int i = 0; i < kSegDepth; ++i) {
       mbar_init(b_segFull + 8 * i, 1);
-      mbar_init(b_segEmpty + 8 * i, 11 + kConvWarps);  // the MMA thread and the other warps
+      mbar_init(b_segEmpty + 8 * i, 11);  // the MMA thread and the other warps
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(b_qFull + 8 * i, kHelpers);
+      mbar_init(b_qFull + 8 * i, 32);
       mbar_init(b_qEmpty + 8 * i, 1);
       mbar_init(b_s + 8 * i, 1);
       mbar_init(b_s + 16 + 8 * i, 1);
       mbar_init(b_p + 8 * i, 128);
       mbar_init(b_o + 8 * i, 1);
-      mbar_init(b_vfFull + 8 * i, 128);
-      mbar_init(b_vfEmpty + 8 * i, 1);
     }
     for (int i = 0; i < kExpDepth; ++i) {
-      mbar_init(b_expFull + 8 * i, kHelpers);
+      mbar_init(b_expFull + 8 * i, 64);
       mbar_init(b_expEmpty + 8 * i, 4);  // the warps of the tile's stream
     }
     mbar_init(b_drain, 1);
     fence_mbar_init();
   }
-  const Range rg = plan<32, F::kThreads>(p, ms->sum, &ms->found);
+  const Range rg = plan<32, F::kThreads>(p, ms->sum, ms->found);
   if (rg.u0 >= rg.u1) return;  // no tiles for this block
   if (warp == kWarpMma) {
     tmem_alloc(smem_u32(&ms->tmem), F::kTmemCols);
@@ -207,56 +211,75 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
 
-  // e4m3: 512 threads of 128 registers become 256 x 168, 128 x 80 and 128 x 88
-  if (warp == kWarpTma) {
-    if (E4M3) reg_dec<80>();
+  if (warp == kWarpTma || warp == kWarpTma + 1) {
     // ------------------------------------------------------------ loads
+    const int kv = warp - kWarpTma;  // warp 9 K, warp 10 V
+    const CUtensorMap* map = kv ? &tm_v : &tm_k;
     const int box_rows = min(1 << p.c.log_page, kBN), n_boxes = kBN / box_rows;
-    if (lane == 0) {
-      tma_prefetch(&tm_k);
-      tma_prefetch(&tm_v);
-    }
-    uint32_t seq = 0;  // tiles loaded; K is ring entry 2 seq, V 2 seq + 1
-    produce<32>(p, rg, ms->seg, b_segFull, b_segEmpty, s_abort, [&](const int (&y)[8], int none) {
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t e = 2 * seq + kv, slot = e % NS;
-        const bool ok = wait_bar(b_empty + 8 * slot, ((e / NS) & 1) ^ 1, s_abort, status);
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        if (elect_one()) {
-          const uint32_t full = b_full + 8 * slot;
-          const uint32_t dst = smem_u32(smem) + slot * F::kSlot;
-          mbar_arrive_expect_tx(full, F::kSlot);
-#pragma unroll
-          for (int b = 0; b < 8; ++b)
-            if (b < n_boxes) {
-              if constexpr (E4M3) {
-                tma_load_2d(dst + b * box_rows * 128, kv ? &tm_v : &tm_k, full, 0, y[b]);
-              } else {
-#pragma unroll
-                for (int half = 0; half < NH; ++half)
-                  tma_load_2d(dst + half * kHalf + b * box_rows * 128, kv ? &tm_v : &tm_k, full,
-                              half * 64, y[b]);
-              }
-            }
-        }
-        __syncwarp();
+    if (lane == 0) tma_prefetch(map);
+    uint32_t e = kv;  // ring entries: K and V of each tile in turn
+    // e4m3: four positions' exponent bytes a lane, stored one tile after their load
+    const uint8_t* exps = kv ? p.c.v_exp : p.c.k_exp;
+    const int my_box = lane * 4 / box_rows, my_at = lane * 4 % box_rows;
+    uint32_t held = 0;
+    auto store_exps = [&](uint32_t tile) {
+      const uint32_t q = tile % kExpDepth;
+      wait_bar(b_expEmpty + 8 * q, ((tile / kExpDepth) & 1) ^ 1, s_abort, status);
+      reinterpret_cast<uint32_t*>(smem + F::kExpOff + q * 256 + kv * 128)[lane] = held;
+      mbar_arrive(b_expFull + 8 * q);
+    };
+    uint32_t stored = 0;  // tiles whose bytes are stored
+    auto issue = [&](const int (&y)[8], int mine, int none) {
+      if constexpr (E4M3) {
+        // a box that reads as zeros: any scale does, but not one that moves the references
+        const int row = __shfl_sync(0xffffffffu, mine, my_box);
+        uint32_t now = 0x7f7f7f7fu;
+        if (row != none)
+          now = __ldg(reinterpret_cast<const uint32_t*>(exps + row + my_at));
+        if (stored < e / 2) store_exps(stored++);
+        held = now;
       }
-      ++seq;
+      const uint32_t slot = e % NS;
+      const bool ok = wait_bar(b_empty + 8 * slot, ((e / NS) & 1) ^ 1, s_abort, status);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      if (elect_one()) {
+        const uint32_t full = b_full + 8 * slot;
+        const uint32_t dst = smem_u32(smem) + slot * F::kSlot;
+        mbar_arrive_expect_tx(full, F::kSlot);
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+          if (b < n_boxes) {
+            if constexpr (E4M3) {
+              tma_load_2d(dst + b * box_rows * 128, map, full, 0, y[b]);
+            } else {
+#pragma unroll
+              for (int half = 0; half < NH; ++half)
+                tma_load_2d(dst + half * kHalf + b * box_rows * 128, map, full, half * 64, y[b]);
+            }
+          }
+      }
+      __syncwarp();
+      e += 2;
       return true;
-    });
+    };
+    auto flush = [&]() {
+      if (E4M3 && stored < e / 2) store_exps(stored++);
+    };
+    if (kv == 0)
+      produce<32>(p, rg, ms->found, ms->seg, b_segFull, b_segEmpty, s_abort, issue, flush);
+    else
+      follow(p, ms->seg, b_segFull, b_segEmpty, s_abort, issue, flush);
     if (*s_abort) {
       // the copies in flight land before the block's shared memory goes
-      const uint32_t done = 2 * seq;
-      for (uint32_t e = done > NS ? done - NS : 0; e < done; ++e)
-        mbar_wait(b_full + 8 * (e % NS), (e / NS) & 1);
+      for (uint32_t i = e > NS ? e - NS : kv; i < e; ++i)
+        if ((i & 1) == kv) mbar_wait(b_full + 8 * (i % NS), (i / NS) & 1);
     }
   } else if (warp == kWarpMma) {
-    if (E4M3) reg_dec<80>();
     // ------------------------------------------------------------ products
     if (elect_one()) {
       constexpr uint32_t kIdS = E4M3 ? idesc_0_f32(128, F::kQRows) : idesc_bf16_f32(128, F::kQRows);
-      constexpr uint32_t kIdO = (E4M3 ? idesc_0_f32(128, 2 * NR) : idesc_bf16_f32(128, 2 * NR)) |
+      constexpr uint32_t kIdO = (E4M3 ? idesc_0_f32(128, F::kParts * NR)
+                                      : idesc_bf16_f32(128, F::kParts * NR)) |
                                 kIdescTransposeA | kIdescTransposeB;
       const int ksteps = E4M3 ? (p.c.D + 31) / 32 : p.c.D / 16;
       const uint32_t at0 = smem_u32(smem);
@@ -297,25 +320,24 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         }
         for (int i = 0; i < nt && ok; ++i) {
           const int s = i & 1;
-          const uint32_t ev = e0 + 2 * i + 1, vf = (base + i) & 1;
-          if constexpr (E4M3) {
-            ok = wait_bar(b_vfFull + 8 * vf, ((base + i) >> 1) & 1, s_abort, status);
-          } else {
-            need(ev);
-          }
+          const uint32_t ev = e0 + 2 * i + 1;
+          need(ev);
           ok = ok && wait_bar(b_p + 8 * s, (ph_p >> s) & 1, s_abort, status);
           ph_p ^= 1u << s;
           if (!ok) break;
           tc_fence_after();
           // D = 64: both groups of 64 MMA rows read the same values
-          const uint64_t a = desc_mnmajor_sw128(
-              E4M3 ? at0 + F::kVfOff + vf * F::kVf : at0 + (ev % NS) * F::kSlot,
-              NH > 1 ? kHalf : 0);
+          const uint64_t a = desc_mnmajor_sw128(at0 + (ev % NS) * F::kSlot, NH > 1 ? kHalf : 0);
           const uint64_t b = desc_mnmajor_sw128(at0 + F::kPOff + s * kHalf, 0);
-          for (int k = 0; k < kBN / 16; ++k)
-            mma_bf16(tmem + F::kColO + s * 64, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdO,
-                     i >= 2 || k > 0);
-          mma_commit(E4M3 ? b_vfEmpty + 8 * vf : b_empty + 8 * (ev % NS));
+          const uint32_t o = tmem + F::kColO + s * F::kOCols;
+          if constexpr (E4M3) {
+            for (int k = 0; k < kBN / 32; ++k)
+              mma_e4m3(o, a + k * (4096 >> 4), b + k * (4096 >> 4), kIdO, i >= 2 || k > 0);
+          } else {
+            for (int k = 0; k < kBN / 16; ++k)
+              mma_bf16(o, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdO, i >= 2 || k > 0);
+          }
+          mma_commit(b_empty + 8 * (ev % NS));
           mma_commit(b_o + 8 * s);
           if (i + SB < nt) {
             need(ev + 2 * SB - 1);
@@ -332,12 +354,11 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp < 8) {
-    if (E4M3) reg_inc<168>();
     // ------------------------------------------------------------ softmax
     const int s = warp >> 2;    // the stream
     const int pt = tid & 127;   // position of the tile, value of D at the end
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_o = tmem + lanes + F::kColO + s * 64;
+    const uint32_t t_o = tmem + lanes + F::kColO + s * F::kOCols;
     const float c2 = p.scale * kLog2e;
     uint8_t* my_p = smem + F::kPOff + s * kHalf + pt * 128;
     uint32_t ph_s = 0, ph_o = 0, base = 0;
@@ -404,21 +425,23 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           if (pass == 0 && i == s) {
             // the references: the scores of a position that every row sees
             const int c0 = max(all_lo - t0, 0);
-            const bool any = c0 < min(all_hi - t0, kBN);
-            if (pt < 32) ms->nm[s][pt] = any ? 0.f : kUnset;
+            const bool any = !E4M3 && c0 < min(all_hi - t0, kBN);
+            if (pt < 32) ms->nm[s][pt] = any || pt >= sg.nrows ? 0.f : kUnset;
             group_sync(2 + s, 128);
-            if (any && (pt >> 5) == (c0 >> 5)) {
+            if (any) {
+              if ((pt >> 5) == (c0 >> 5)) {
 #pragma unroll 1
-              for (int r0 = 0; r0 < NR; r0 += 8) {
-                load_scores<8, NR, E4M3>(t_s, r0, ms->nm[s], ms->a[sn & 1], c2, ck, ev, x);
-                if (pt == c0)
+                for (int r0 = 0; r0 < NR; r0 += 8) {
+                  load_scores<8, NR, E4M3>(t_s, r0, ms->nm[s], ms->a[sn & 1], c2, ck, ev, x);
+                  if (pt == c0)
 #pragma unroll
-                  for (int k = 0; k < 8; ++k)
-                    ms->nm[s][r0 + k] = fabsf(x[k]) < 1.0e30f ? -(x[k] + kAbove) : kUnset;
-                __syncwarp();
+                    for (int k = 0; k < 8; ++k)
+                      ms->nm[s][r0 + k] = fabsf(x[k]) < 1.0e30f ? -x[k] : kUnset;
+                  __syncwarp();
+                }
               }
+              group_sync(2 + s, 128);
             }
-            group_sync(2 + s, 128);
           }
           constexpr int kN = E4M3 && NR > 16 ? 16 : NR;
           float top = -INFINITY;
@@ -465,7 +488,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           for (int r = 0; r < NR; ++r) l[r] *= ms->f[s][r];
           if (i >= 2) {
 #pragma unroll 1
-            for (int c = 0; c < 2 * NR; c += 8) {
+            for (int c = 0; c < F::kParts * NR; c += 8) {
               uint32_t o[8];
               tmem_ld_32x32b_x8(t_o + c, o);
               tmem_wait_ld_regs(o);
@@ -483,50 +506,54 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           __syncwarp();
           ph_o ^= 1;
         }
-        // P: the position's row of [rounded | rest], 8 packed rows a chunk
+        // P: the position's row of its terms, 8 packed rows at a time
 #pragma unroll
         for (int r0 = 0; r0 < NR; r0 += 8) {
-          uint32_t hi[4], lo[4];
+          if constexpr (E4M3) {
+            uint32_t t[4][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float a = ex2_approx(x[r0 + 2 * k]), b = ex2_approx(x[r0 + 2 * k + 1]);
-            float ra, rb;
-            if constexpr (E4M3) {
+            for (int k = 0; k < 4; ++k) {
+              const float a = ex2_approx(x[r0 + 2 * k]), b = ex2_approx(x[r0 + 2 * k + 1]);
               l[r0 + 2 * k] = fmaf(a, un, l[r0 + 2 * k]);
               l[r0 + 2 * k + 1] = fmaf(b, un, l[r0 + 2 * k + 1]);
-              hi[k] = pack_half(a, b);
-              const float2 h = __half22float2(*reinterpret_cast<__half2*>(&hi[k]));
-              unpack2(fma2(pack2(h.x, h.y), pack2(-kRest, -kRest),
-                           mul2(pack2(a, b), pack2(kRest, kRest))),
-                      ra, rb);
-              lo[k] = pack_half(ra, rb);
-            } else {
+              uint32_t c[4];
+              e4m3_terms(a, b, c);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) t[q][k] = c[q];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int at = q * NR + r0;
+              *reinterpret_cast<uint2*>(my_p + (((at >> 4) ^ (pt & 7)) << 4) + (at & 8)) =
+                  make_uint2(t[q][0] | (t[q][1] << 16), t[q][2] | (t[q][3] << 16));
+            }
+          } else {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float a = ex2_approx(x[r0 + 2 * k]), b = ex2_approx(x[r0 + 2 * k + 1]);
               l[r0 + 2 * k] += a;
               l[r0 + 2 * k + 1] += b;
               hi[k] = pack_bf16(a, b);
-              ra = a - __uint_as_float(hi[k] << 16);
-              rb = b - __uint_as_float(hi[k] & 0xffff0000u);
-              lo[k] = pack_bf16(ra, rb);
+              lo[k] = pack_bf16(a - __uint_as_float(hi[k] << 16),
+                                b - __uint_as_float(hi[k] & 0xffff0000u));
             }
+            *reinterpret_cast<uint4*>(my_p + (((r0 >> 3) ^ (pt & 7)) << 4)) =
+                make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(my_p + ((((NR + r0) >> 3) ^ (pt & 7)) << 4)) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
-          *reinterpret_cast<uint4*>(my_p + (((r0 >> 3) ^ (pt & 7)) << 4)) =
-              make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(my_p + ((((NR + r0) >> 3) ^ (pt & 7)) << 4)) =
-              make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-        if constexpr (!E4M3) {
-          // values that no row sees: 0 * NaN must not reach a sum
-          const int c = t0 + pt;
-          if (t0 < sg.lo || t0 + kBN > sg.hi) {
-            const uint32_t e = 2 * (base + i) + 1, slot = e % NS;
-            wait_bar(b_full + 8 * slot, (e / NS) & 1, s_abort, status);
-            if (c < sg.lo || c >= sg.hi) {
-              uint8_t* v = smem + slot * F::kSlot + pt * 128;
+        // values that no row sees: 0 * NaN must not reach a sum
+        if (t0 < sg.lo || t0 + kBN > sg.hi) {
+          const uint32_t e = 2 * (base + i) + 1, slot = e % NS;
+          wait_bar(b_full + 8 * slot, (e / NS) & 1, s_abort, status);
+          if (t0 + pt < sg.lo || t0 + pt >= sg.hi) {
+            uint8_t* v = smem + slot * F::kSlot + pt * 128;
 #pragma unroll
-              for (int k = 0; k < DP / 8; ++k)
-                *reinterpret_cast<uint4*>(v + (k >> 3) * kHalf + (k & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
+            for (int k = 0; k < (int)(F::kSlot / 2048); ++k)
+              *reinterpret_cast<uint4*>(v + (k >> 3) * kHalf + (k & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
           }
         }
         fence_proxy_async_smem();
@@ -585,14 +612,20 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       if (has) {
 #pragma unroll
         for (int r0 = 0; r0 < NR; r0 += 8) {
-          uint32_t u[8], v[8];
-          tmem_ld_32x32b_x8(t_o + r0, u);
-          tmem_ld_32x32b_x8(t_o + NR + r0, v);
-          tmem_wait_ld_regs(u, v);
+          uint32_t u[F::kParts][8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            o[r0 + k] = fmaf(__uint_as_float(v[k]), 1.f / kRest, __uint_as_float(u[k])) *
-                        __shfl_sync(0xffffffffu, w_mine, r0 + k);
+          for (int q = 0; q < F::kParts; ++q) tmem_ld_32x32b_x8(t_o + q * NR + r0, u[q]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float v = 0.f;
+#pragma unroll
+            for (int q = F::kParts - 1; q >= 0; --q) {
+              asm volatile("" : "+r"(u[q][k]));
+              v = fmaf(v, E4M3 ? 0.0625f : 1.f, __uint_as_float(u[q][k]));
+            }
+            o[r0 + k] = v * __shfl_sync(0xffffffffu, w_mine, r0 + k);
+          }
         }
       }
       float* give = reinterpret_cast<float*>(smem + F::kPOff + (s ^ 1) * kHalf) + pt;
@@ -619,180 +652,77 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
                                     reinterpret_cast<float2*>(smem + F::kPOff));
       tc_fence_before();
     }
-  } else if (warp < 12) {
-    if (E4M3) reg_dec<80>();
-    // ------------------------------------------------------------ Q, scales
-    const int ht = tid - 320;
-    uint32_t base = 0;
+  } else {
+    // ------------------------------------------------------------ Q
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth, qb = sn & 1;
       const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status) &&
                        wait_bar(b_qEmpty + 8 * qb, ((sn >> 1) & 1) ^ 1, s_abort, status);
-      if (group_any(5, kHelpers, !got)) break;
+      if (__any_sync(0xffffffffu, !got)) break;
       const Segment sg = ms->seg[ss];
       __syncwarp();
       if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
       if (sg.ntiles == 0) break;
       // Q: 16 lanes a row, 8 values a lane; rows past the item's are zero
-      constexpr int kRowsIn = E4M3 ? NR : F::kQRows, kIters = kRowsIn * 16 / kHelpers;
-      uint4 x[kIters];
+      constexpr int kRowsIn = E4M3 ? NR : F::kQRows, kIters = kRowsIn < 16 ? kRowsIn / 2 : 8;
+#pragma unroll 1
+      for (int row0 = 0; row0 < kRowsIn; row0 += 2 * kIters) {
+        uint4 x[kIters];
 #pragma unroll
-      for (int k = 0; k < kIters; ++k) {
-        const int row = (ht >> 4) + 4 * k, ch = ht & 15;
-        x[k] = make_uint4(0, 0, 0, 0);
-        if (row < sg.nrows) x[k] = load_q(p, sg.row0, sg.h, sg.r0 + row, ch * 8);
-      }
+        for (int k = 0; k < kIters; ++k) {
+          const int row = row0 + (lane >> 4) + 2 * k, ch = lane & 15;
+          x[k] = make_uint4(0, 0, 0, 0);
+          if (row < sg.nrows) x[k] = load_q(p, sg.row0, sg.h, sg.r0 + row, ch * 8);
+        }
 #pragma unroll
-      for (int k = 0; k < kIters; ++k) {
-        const int row = (ht >> 4) + 4 * k, ch = ht & 15;
-        uint8_t* dst = smem + F::kQOff + qb * F::kQBytes + row * 128;
-        if constexpr (!E4M3) {
-          if (ch < DP / 8)
-            *reinterpret_cast<uint4*>(dst + (ch >> 3) * F::kQHalf +
-                                      (((ch & 7) ^ (row & 7)) << 4)) = x[k];
-        } else {
-          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-          float f[8], amax = 0.f;
+        for (int k = 0; k < kIters; ++k) {
+          const int row = row0 + (lane >> 4) + 2 * k, ch = lane & 15;
+          uint8_t* dst = smem + F::kQOff + qb * F::kQBytes + row * 128;
+          if constexpr (!E4M3) {
+            if (ch < DP / 8)
+              *reinterpret_cast<uint4*>(dst + (ch >> 3) * F::kQHalf +
+                                        (((ch & 7) ^ (row & 7)) << 4)) = x[k];
+          } else {
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            float f[8], amax = 0.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f[2 * j] = __uint_as_float(w[j] << 16);
-            f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-            amax = max3(amax, fabsf(f[2 * j]), fabsf(f[2 * j + 1]));
+            for (int j = 0; j < 4; ++j) {
+              f[2 * j] = __uint_as_float(w[j] << 16);
+              f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+              amax = max3(amax, fabsf(f[2 * j]), fabsf(f[2 * j + 1]));
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+              amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o, 16));
+            // q 2^-a within the codes' range
+            const int a = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -100), 120);
+            const float inv = __uint_as_float((uint32_t)(127 - a) << 23);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float u = f[2 * j] * inv, v = f[2 * j + 1] * inv;
+              hi[j] = e4m3x2(u, v);
+              uint32_t h;
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi[j]));
+              const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
+              lo[j] = e4m3x2((u - g.x) * 16.f, (v - g.y) * 16.f);
+            }
+            // 8 codes a lane: half a 16-byte chunk
+            const uint32_t to = ((((uint32_t)ch >> 1) ^ (row & 7)) << 4) + (ch & 1) * 8;
+            *reinterpret_cast<uint2*>(dst + to) =
+                make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            *reinterpret_cast<uint2*>(dst + NR * 128 + to) =
+                make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+            // an infinite q has no product with a value
+            if (ch == 0)
+              ms->a[qb][row] = amax < INFINITY ? __uint_as_float((uint32_t)(127 + a) << 23) *
+                                                     (p.scale * kLog2e)
+                                               : NAN;
           }
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o, 16));
-          // q 2^-a within the codes' range
-          const int a = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -100), 120);
-          const float inv = __uint_as_float((uint32_t)(127 - a) << 23);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float u = f[2 * j] * inv, v = f[2 * j + 1] * inv;
-            hi[j] = e4m3x2(u, v);
-            uint32_t h;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)hi[j]));
-            const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
-            lo[j] = e4m3x2((u - g.x) * 16.f, (v - g.y) * 16.f);
-          }
-          // 8 codes a lane: half a 16-byte chunk
-          const uint32_t to = ((((uint32_t)ch >> 1) ^ (row & 7)) << 4) + (ch & 1) * 8;
-          *reinterpret_cast<uint2*>(dst + to) =
-              make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          *reinterpret_cast<uint2*>(dst + NR * 128 + to) =
-              make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-          // an infinite q has no product with a value
-          if (ch == 0)
-            ms->a[qb][row] = amax < INFINITY ? __uint_as_float((uint32_t)(127 + a) << 23) *
-                                                   (p.scale * kLog2e)
-                                             : NAN;
         }
       }
       fence_proxy_async_smem();
       mbar_arrive(b_qFull + 8 * qb);
-      if constexpr (E4M3) {
-        // the tiles' exponent bytes, four positions a lane: warp 10 K's, warp 11 V's; four
-        // tiles' loads in flight
-        const uint8_t* exps = warp == 10 ? p.c.k_exp : p.c.v_exp;
-        const int log_page = p.c.log_page, n = sg.n;
-#pragma unroll 1
-        for (int i0 = 0; i0 < sg.ntiles; i0 += 4) {
-          int64_t id[4];
-          uint32_t b[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int pos = (sg.tile0 + i0 + k) * kBN + lane * 4;
-            const bool in = i0 + k < sg.ntiles && pos < sg.hi && pos + 4 > sg.lo;
-            id[k] = in ? page_of(p.c, n, pos) : -1;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int pos = (sg.tile0 + i0 + k) * kBN + lane * 4;
-            // a page that reads as zeros: any scale does, but not one that moves the
-            // references
-            b[k] = id[k] < 0 ? 0x7f7f7f7fu
-                             : __ldg(reinterpret_cast<const uint32_t*>(
-                                   exps + (((id[k] * p.c.Hkv + sg.h) << log_page) +
-                                           (pos & ((1 << log_page) - 1)))));
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (i0 + k >= sg.ntiles) break;
-            const uint32_t t = base + i0 + k, q = t % kExpDepth;
-            wait_bar(b_expEmpty + 8 * q, ((t / kExpDepth) & 1) ^ 1, s_abort, status);
-            *reinterpret_cast<uint32_t*>(smem + F::kExpOff + q * 256 + (warp - 10) * 128 +
-                                         lane * 4) = b[k];
-            mbar_arrive(b_expFull + 8 * q);
-          }
-        }
-      }
-      base += sg.ntiles;
-    }
-  } else if (E4M3) {
-    reg_dec<88>();
-    // ------------------------------------------------------------ V's codes to halves
-    // a warp takes eight rows of 64 codes at a time, 16 codes a lane; each eight lanes
-    // have rows that differ in their lowest and highest bit, so that neither the
-    // (swizzled) loads nor the stores share a bank
-    const int ct = tid - 384, c = lane & 3;
-    const int row8 = (lane >> 3) ^ (lane & 4 ? 5 : 0);
-    uint32_t base = 0;
-    for (int sn = 0;; ++sn) {
-      const int ss = sn % kSegDepth;
-      const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status);
-      if (group_any(4, 128, !got)) break;
-      const int nt = ms->seg[ss].ntiles, tile0 = ms->seg[ss].tile0;
-      const int lo = ms->seg[ss].lo, hi = ms->seg[ss].hi;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
-      if (nt == 0) break;
-#pragma unroll 1
-      for (int i = 0; i < nt; ++i) {
-        const uint32_t q = base + i, e = 2 * q + 1, slot = e % NS, vf = q & 1;
-        const int t0 = (tile0 + i) * kBN;
-        const bool edge = t0 < lo || t0 + kBN > hi;
-        wait_bar(b_full + 8 * slot, (e / NS) & 1, s_abort, status);
-        wait_bar(b_vfEmpty + 8 * vf, ((q >> 1) & 1) ^ 1, s_abort, status);
-        const uint8_t* src = smem + slot * F::kSlot;
-        uint8_t* dst = smem + F::kVfOff + vf * F::kVf;
-        if (edge) {
-          // values that no row sees: 0 * NaN must not reach a sum
-          const int row = ct;
-          if (t0 + row < lo || t0 + row >= hi)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(smem + slot * F::kSlot + row * 128 + k * 16) =
-                  make_uint4(0, 0, 0, 0);
-          group_sync(4, 128);
-        }
-#pragma unroll
-        for (int half = 0; half < NH; ++half)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int row = (k * 4 + (warp & 3)) * 8 + row8;
-            const uint4 w = *reinterpret_cast<const uint4*>(
-                src + row * 128 + (((half * 4 + c) ^ row8) << 4));
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-            uint32_t h[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * j]) : "h"((uint16_t)in[j]));
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
-                  : "=r"(h[2 * j + 1])
-                  : "h"((uint16_t)(in[j] >> 16)));
-            }
-            uint8_t* to = dst + half * kHalf + row * 128;
-            *reinterpret_cast<uint4*>(to + (((2 * c) ^ row8) << 4)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ row8) << 4)) =
-                make_uint4(h[4], h[5], h[6], h[7]);
-          }
-        fence_proxy_async_smem();
-        mbar_arrive(b_vfFull + 8 * vf);
-        group_sync(4, 128);
-        if (ct == 0) mbar_arrive(b_empty + 8 * slot);
-      }
-      base += nt;
     }
   }
   tc_fence_before();

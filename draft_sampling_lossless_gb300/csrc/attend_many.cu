@@ -29,8 +29,8 @@
 // scales are powers of two), between the loads and the products.
 //
 // Roles: warps 0-7 the two softmax warpgroups (they also load Q and store), warp 8
-// issues the MMAs, warp 9 the TMA loads (10 and 11 complete its warpgroup), warps
-// 12-15 convert.  Every wait is bounded; a timeout sets DSPARK_DEVFLAG_TIMEOUT and
+// issues the MMAs, warps 9 and 10 the TMA loads of K and V (11 completes the
+// warpgroup), warps 12-15 convert.  Every wait is bounded; a timeout sets DSPARK_DEVFLAG_TIMEOUT and
 // ends the kernel.  See attend.cuh for the split of the work.
 #include "attend.cuh"
 
@@ -69,7 +69,7 @@ struct Many {
 
 struct Misc {  // shared words
   int64_t sum[16];
-  Found found;
+  Found found[2];
   Segment seg[kSegDepth];
   uint64_t bars[2 * 12 + 2 * 4 + 2 * kSegDepth + 8];
   int abort_flag, last;
@@ -251,12 +251,12 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
       mbar_init(b_empty + 8 * i, 1);
     }
     for (int i = 0; i < F::kRawSlots; ++i) {
-      mbar_init(b_rawFull + 8 * i, 1);
+      mbar_init(b_rawFull + 8 * i, 33);  // the load, and 32 lanes' exponent bytes
       mbar_init(b_rawEmpty + 8 * i, 1);
     }
     for (int i = 0; i < kSegDepth; ++i) {
       mbar_init(b_segFull + 8 * i, 1);
-      mbar_init(b_segEmpty + 8 * i, E4M3 ? 13 : 9);  // the MMA thread and the other warps
+      mbar_init(b_segEmpty + 8 * i, E4M3 ? 14 : 10);  // the MMA thread and the other warps
     }
     mbar_init(b_q, kSoftThreads);
     for (int i = 0; i < 2; ++i) {
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
     mbar_init(b_drain, 1);
     fence_mbar_init();
   }
-  const Range rg = plan<kRows, F::kThreads>(p, ms->sum, &ms->found);
+  const Range rg = plan<kRows, F::kThreads>(p, ms->sum, ms->found);
   if (rg.u0 >= rg.u1) return;  // no tiles for this block
   if (warp == kWarpMma) {
     tmem_alloc(smem_u32(&ms->tmem), kTmemCols);
@@ -280,61 +280,68 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
 
   // bf16: 384 threads of 168 registers become 256 x 216 and 128 x 72;
   // e4m3: 512 of 128 become 256 x 176, 128 x 72 and 128 x 88
-  if (warp == kWarpTma) {
+  if (warp == kWarpTma || warp == kWarpTma + 1) {
     reg_dec<72>();
     // ------------------------------------------------------------ loads
+    const int kv = warp - kWarpTma;  // warp 9 K, warp 10 V
+    const CUtensorMap* map = kv ? &tm_v : &tm_k;
+    const uint8_t* exps = kv ? p.c.v_exp : p.c.k_exp;
     const int box_rows = min(1 << p.c.log_page, kBN), n_boxes = kBN / box_rows;
-    if (lane == 0) {
-      tma_prefetch(&tm_k);
-      tma_prefetch(&tm_v);
-    }
+    if (lane == 0) tma_prefetch(map);
     constexpr uint32_t kRing = E4M3 ? NRAW : NS;
     const uint32_t full0 = E4M3 ? b_rawFull : b_full, empty0 = E4M3 ? b_rawEmpty : b_empty;
-    uint32_t e = 0;  // ring entries: K and V of each tile in turn
-    auto load = [&](const int (&y)[8], int none) {
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv, ++e) {
-        const uint32_t slot = e % kRing, full = full0 + 8 * slot;
-        const bool ok = wait_bar(empty0 + 8 * slot, ((e / kRing) & 1) ^ 1, s_abort, status);
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        if (elect_one()) {
-          const CUtensorMap* map = kv ? &tm_v : &tm_k;
-          if constexpr (E4M3) {
-            const uint32_t dst = smem_u32(smem + F::kRawOff) + slot * kHalf;
-            const uint32_t dexp = smem_u32(smem + F::kExpOff) + slot * 128;
-            const uint8_t* exps = kv ? p.c.v_exp : p.c.k_exp;
-            const uint64_t pol = policy_evict_first();
-            int n = 0;
-#pragma unroll
-            for (int b = 0; b < 8; ++b) n += b < n_boxes && y[b] != none;
-            mbar_arrive_expect_tx(full, kHalf + n * box_rows);
-#pragma unroll
-            for (int b = 0; b < 8; ++b)
-              if (b < n_boxes) {
-                tma_load_2d(dst + b * box_rows * 128, map, full, 0, y[b]);
-                if (y[b] != none)
-                  bulk_load_hint(dexp + b * box_rows, exps + y[b], box_rows, full, pol);
-              }
-          } else {
-            const uint32_t dst = smem_u32(s_kv) + slot * F::kTile;
-            mbar_arrive_expect_tx(full, F::kTile);
-#pragma unroll
-            for (int b = 0; b < 8; ++b)
-              if (b < n_boxes)
-#pragma unroll
-                for (int half = 0; half < NH; ++half)
-                  tma_load_2d(dst + half * kHalf + b * box_rows * 128, map, full, half * 64, y[b]);
-          }
-        }
-        __syncwarp();
+    uint32_t e = kv;  // ring entries: K and V of each tile in turn
+    // e4m3: four positions' exponent bytes a lane, stored with the next tile's load
+    const int my_box = lane * 4 / box_rows, my_at = lane * 4 % box_rows;
+    uint32_t held = 0, stored = kv;  // entries whose bytes are stored
+    auto flush = [&]() {
+      if (!E4M3 || stored >= e) return;
+      const uint32_t slot = stored % kRing;
+      reinterpret_cast<uint32_t*>(smem + F::kExpOff + slot * 128)[lane] = held;
+      mbar_arrive(full0 + 8 * slot);
+      stored += 2;
+    };
+    auto issue = [&](const int (&y)[8], int mine, int none) {
+      if constexpr (E4M3) {
+        const int row = __shfl_sync(0xffffffffu, mine, my_box);
+        uint32_t now = 0x7f7f7f7fu;
+        if (row != none) now = __ldg(reinterpret_cast<const uint32_t*>(exps + row + my_at));
+        flush();
+        held = now;
       }
+      const uint32_t slot = e % kRing, full = full0 + 8 * slot;
+      const bool ok = wait_bar(empty0 + 8 * slot, ((e / kRing) & 1) ^ 1, s_abort, status);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      if (elect_one()) {
+        if constexpr (E4M3) {
+          const uint32_t dst = smem_u32(smem + F::kRawOff) + slot * kHalf;
+          mbar_arrive_expect_tx(full, kHalf);
+#pragma unroll
+          for (int b = 0; b < 8; ++b)
+            if (b < n_boxes) tma_load_2d(dst + b * box_rows * 128, map, full, 0, y[b]);
+        } else {
+          const uint32_t dst = smem_u32(s_kv) + slot * F::kTile;
+          mbar_arrive_expect_tx(full, F::kTile);
+#pragma unroll
+          for (int b = 0; b < 8; ++b)
+            if (b < n_boxes)
+#pragma unroll
+              for (int half = 0; half < NH; ++half)
+                tma_load_2d(dst + half * kHalf + b * box_rows * 128, map, full, half * 64, y[b]);
+        }
+      }
+      __syncwarp();
+      e += 2;
       return true;
     };
-    produce<kRows>(p, rg, ms->seg, b_segFull, b_segEmpty, s_abort, load);
+    if (kv == 0)
+      produce<kRows>(p, rg, ms->found, ms->seg, b_segFull, b_segEmpty, s_abort, issue, flush);
+    else
+      follow(p, ms->seg, b_segFull, b_segEmpty, s_abort, issue, flush);
     if (*s_abort) {
       // the copies in flight land before the block's shared memory goes
-      for (uint32_t i = e > kRing ? e - kRing : 0; i < e; ++i)
-        mbar_wait(full0 + 8 * (i % kRing), (i / kRing) & 1);
+      for (uint32_t i = e > kRing ? e - kRing : kv; i < e; ++i)
+        if ((i & 1) == kv) mbar_wait(full0 + 8 * (i % kRing), (i / kRing) & 1);
     }
   } else if (warp == kWarpMma) {
     reg_dec<72>();
