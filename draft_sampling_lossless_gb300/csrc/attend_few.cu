@@ -13,9 +13,8 @@
 // maximum is taken per tile.  P = 2^(s - m) against a reference m of each row: the
 // score of the item's first position that all rows see.  Any reference gives the
 // same quotient as long as P stays in range; where a score passes it by 64 powers of
-// two, or no position serves all rows, the references move to the tile's maxima,
-// O and the sums with them.  e4m3 terms have less range: there the references
-// are the first tile's maxima, and move when a score passes them by five powers.
+// two (8 in e4m3, which has less range and starts at the first tile's maxima), the
+// row's reference moves to the tile's maximum, O and the sum with it.
 //
 // bf16: P enters its product as two bf16 terms, its rounding and the rounding of the
 // rest (columns of N side by side; a row that one position dominates would
@@ -75,7 +74,9 @@ struct Few {
 
 struct Misc {  // shared words
   float nm[2][32];      // -m of each stream's rows
-  float f[2][32];       // what a move of the references multiplies by
+  float f[2][32];       // what a move of the references multiplies by,
+  float d[2][32];       // and its logarithm, negated
+  float zero[32];
   float wm[2][4][32];   // the warps' maxima, then sums
   float a[2][32];       // e4m3: scale of the scores of a row, of each Q buffer
   int64_t sum[16];
@@ -120,24 +121,35 @@ __device__ __forceinline__ void e4m3_terms(float a, float b, uint32_t (&t)[4]) {
   }
 }
 
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N]) {
+  if constexpr (N == 8)
+    tmem_ld_32x32b_x8(taddr, v);
+  else if constexpr (N == 16)
+    tmem_ld_32x32b_x16(taddr, v);
+  else
+    tmem_ld_32x32b_x32(taddr, v);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[N]) {
+  if constexpr (N == 8)
+    tmem_st_32x32b_x8(taddr, v);
+  else if constexpr (N == 16)
+    tmem_st_32x32b_x16(taddr, v);
+  else
+    tmem_st_32x32b_x32(taddr, v);
+}
+
 // The scores of a thread's position, N rows from r0 on: x[k] = log2 of row r0 + k's
 // exponential (e4m3: times 2^e of the value's exponent e), plus nm[r0 + k].
 template <int N, int NR, bool E4M3>
 __device__ __forceinline__ void load_scores(uint32_t t_s, int r0, const float* nm,
                                             const float* row_scale, float c2, float ck, float ev,
                                             float* x) {
-  uint32_t u[N], v[E4M3 ? N : 1];
-  if constexpr (N == 8)
-    tmem_ld_32x32b_x8(t_s + r0, u);
-  else if constexpr (N == 16)
-    tmem_ld_32x32b_x16(t_s + r0, u);
-  else
-    tmem_ld_32x32b_x32(t_s + r0, u);
+  uint32_t u[N], v[N];
+  tmem_ld<N>(t_s + r0, u);
   if constexpr (E4M3) {
-    if constexpr (N == 8)
-      tmem_ld_32x32b_x8(t_s + NR + r0, v);
-    else
-      tmem_ld_32x32b_x16(t_s + NR + r0, v);
+    tmem_ld<N>(t_s + NR + r0, v);
     tmem_wait_ld_regs(u, v);
   } else {
     tmem_wait_ld_regs(u);
@@ -163,8 +175,9 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
   using F = Few<DP, NR, E4M3>;
   constexpr int NS = F::kSlots, NH = F::kNH, SB = F::kSBufs;
-  // P's largest exponent, and where a maximum puts the reference: e4m3 ends at 448
-  constexpr float kLimit = E4M3 ? 8.f : 64.f, kAbove = E4M3 ? -3.f : 0.f;
+  // P's largest exponent (e4m3 ends at 448); rows above half of it move along with one
+  // that passed it
+  constexpr float kLimit = E4M3 ? 8.f : 64.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc* ms = reinterpret_cast<Misc*>(smem + F::kMiscOff);
   const uint32_t b_full = smem_u32(ms->bars), b_empty = b_full + 8 * NS;
@@ -178,6 +191,9 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   uint32_t* status = p.c.status;
   if (smem_u32(smem) & 1023) return;  // never: the declared alignment, which the swizzle needs
 
+  if (tid < 32) {
+    ms->zero[tid] = 0.f;
+  }
   if (tid == 0) {
     *s_abort = 0;
     for (int i = 0; i < 2 * NS; ++i) mbar_init(b_full + 8 * i, 1);
@@ -211,7 +227,9 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
 
+  // 384 threads of 168 registers become 256 x 192 and 128 x 120
   if (warp == kWarpTma || warp == kWarpTma + 1) {
+    reg_dec<120>();
     // ------------------------------------------------------------ loads
     const int kv = warp - kWarpTma;  // warp 9 K, warp 10 V
     const CUtensorMap* map = kv ? &tm_v : &tm_k;
@@ -275,6 +293,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         if ((i & 1) == kv) mbar_wait(b_full + 8 * (i % NS), (i / NS) & 1);
     }
   } else if (warp == kWarpMma) {
+    reg_dec<120>();
     // ------------------------------------------------------------ products
     if (elect_one()) {
       constexpr uint32_t kIdS = E4M3 ? idesc_0_f32(128, F::kQRows) : idesc_bf16_f32(128, F::kQRows);
@@ -354,6 +373,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp < 8) {
+    reg_inc<192>();
     // ------------------------------------------------------------ softmax
     const int s = warp >> 2;    // the stream
     const int pt = tid & 127;   // position of the tile, value of D at the end
@@ -419,87 +439,128 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           }
         }
         float x[NR];
-        bool prior = i < 2;  // the products before this tile's are done
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-          if (pass == 0 && i == s) {
-            // the references: the scores of a position that every row sees
-            const int c0 = max(all_lo - t0, 0);
-            const bool any = !E4M3 && c0 < min(all_hi - t0, kBN);
-            if (pt < 32) ms->nm[s][pt] = any || pt >= sg.nrows ? 0.f : kUnset;
-            group_sync(2 + s, 128);
-            if (any) {
-              if ((pt >> 5) == (c0 >> 5)) {
-#pragma unroll 1
-                for (int r0 = 0; r0 < NR; r0 += 8) {
-                  load_scores<8, NR, E4M3>(t_s, r0, ms->nm[s], ms->a[sn & 1], c2, ck, ev, x);
-                  if (pt == c0)
+        constexpr int kN = NR < 16 ? NR : 16, kB = kN;
+        const float* nm = i == s ? ms->zero : ms->nm[s];
+        // blocks of rows that the item does not have are left out throughout
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                      ms->nm[s][r0 + k] = fabsf(x[k]) < 1.0e30f ? -x[k] : kUnset;
-                  __syncwarp();
-                }
-              }
-              group_sync(2 + s, 128);
-            }
+        for (int r0 = 0; r0 < NR; r0 += kN)
+          if (r0 < sg.nrows) {
+            load_scores<kN, NR, E4M3>(t_s, r0, nm, ms->a[sn & 1], c2, ck, ev, x + r0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < kN; ++k) x[r0 + k] = -INFINITY;
           }
-          constexpr int kN = E4M3 && NR > 16 ? 16 : NR;
-          float top = -INFINITY;
+        if (i == s) {
+          // the references: the scores of a position that every row sees
+          const int c0 = max(all_lo - t0, 0);
+          if (c0 < min(all_hi - t0, kBN)) {
+            if (pt == c0)
 #pragma unroll
-          for (int r0 = 0; r0 < NR; r0 += kN)
-            load_scores<kN, NR, E4M3>(t_s, r0, ms->nm[s], ms->a[sn & 1], c2, ck, ev, x + r0);
-          if (mask)
+              for (int r = 0; r < NR; ++r)
+                ms->nm[s][r] = fabsf(x[r]) < 1.0e30f ? -x[r] : kUnset;
+          } else if (pt < NR) {
+            ms->nm[s][pt] = pt < sg.nrows ? kUnset : 0.f;
+          }
+          group_sync(2 + s, 128);
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
-              if (r < r_lo || r >= r_hi) x[r] = -INFINITY;
+          for (int r0 = 0; r0 < NR; r0 += 8)
+            if (r0 < sg.nrows)
 #pragma unroll
-          for (int r = 0; r < NR; r += 2) top = max3(top, x[r], x[r + 1]);
-          if (!group_any(2 + s, 128, pass == 0 && top > kLimit)) break;
-
-          // the references move past the tile's maxima (rarely)
+              for (int k = 0; k < 8; ++k) x[r0 + k] += ms->nm[s][r0 + k];
+        }
+        if (mask)
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            if (r < r_lo || r >= r_hi) x[r] = -INFINITY;
+        float top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < NR; r += 2) top = max3(top, x[r], x[r + 1]);
+        bool prior = i < 2;  // the products before this tile's are done
+        if (group_any(2 + s, 128, top > kLimit || (E4M3 && i == s))) {
+          // references move to the tile's maxima
           if (!prior) {
             wait_bar(b_o + 8 * s, ph_o, s_abort, status);
             __syncwarp();
             ph_o ^= 1;
             tc_fence_after();
+            prior = true;
           }
-          if (pt < 32) ms->f[s][pt] = 0.f;
-          group_sync(2 + s, 128);
+          if (i > s || !group_any(2 + s, 128, top > 1.0e30f)) {
+            // from the scores against the present ones
+            int best = 0;
+#pragma unroll
+            for (int r0 = 0; r0 < NR; r0 += 8)
+              if (r0 < sg.nrows)
+#pragma unroll
+                for (int r = r0; r < r0 + 8; ++r) {
+                  // integers in the order of the floats
+                  const int b = __float_as_int(x[r]);
+                  const int m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+                  if (lane == r) best = m;
+                }
+            if (lane < NR)
+              ms->wm[s][warp & 3][lane] = __int_as_float(best ^ ((best >> 31) & 0x7fffffff));
+            group_sync(2 + s, 128);
+            if (pt < NR) {
+              const float m = max3(fmaxf(ms->wm[s][0][pt], ms->wm[s][1][pt]), ms->wm[s][2][pt],
+                                   ms->wm[s][3][pt]);
+              const float d = m > (i == s ? 0.f : kLimit / 2) ? m : 0.f;
+              ms->nm[s][pt] -= d;
+              ms->d[s][pt] = d;
+              ms->f[s][pt] = ex2_approx(-d);
+            }
+            group_sync(2 + s, 128);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) x[r] -= ms->d[s][r];
+          } else {
+            // rows without a reference yet: the maxima of the scores themselves
 #pragma unroll 1
-          for (int r0 = 0; r0 < NR; r0 += 8) {
-            float y[8];
-            load_scores<8, NR, E4M3>(t_s, r0, ms->f[s], ms->a[sn & 1], c2, ck, ev, y);
+            for (int r0 = 0; r0 < NR; r0 += kB) {
+              float y[kB];
+              load_scores<kB, NR, E4M3>(t_s, r0, ms->zero, ms->a[sn & 1], c2, ck, ev, y);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (mask && (r0 + k < r_lo || r0 + k >= r_hi)) y[k] = -INFINITY;
-            const float m = reduce_rows<8>(y, [](float a, float b) { return fmaxf(a, b); });
-            if ((lane & 3) == 0) ms->wm[s][warp & 3][r0 + (lane >> 2)] = m;
-          }
-          group_sync(2 + s, 128);
-          if (pt < NR) {
-            const float old = -ms->nm[s][pt];
-            const float m = fmaxf(old, kAbove + max3(fmaxf(ms->wm[s][0][pt], ms->wm[s][1][pt]),
-                                                     ms->wm[s][2][pt], ms->wm[s][3][pt]));
-            ms->nm[s][pt] = -m;
-            ms->f[s][pt] = ex2_approx(old - m);
-          }
-          group_sync(2 + s, 128);
+              for (int k = 0; k < kB; ++k)
+                if (mask && (r0 + k < r_lo || r0 + k >= r_hi)) y[k] = -INFINITY;
+              const float m = reduce_rows<kB>(y, [](float a, float b) { return fmaxf(a, b); });
+              if (lane % (32 / kB) == 0) ms->wm[s][warp & 3][r0 + lane / (32 / kB)] = m;
+            }
+            group_sync(2 + s, 128);
+            if (pt < NR) {
+              const float old = -ms->nm[s][pt];
+              const float m = max3(fmaxf(ms->wm[s][0][pt], ms->wm[s][1][pt]), ms->wm[s][2][pt],
+                                   ms->wm[s][3][pt]);
+              const bool moves = m - old > kLimit;
+              if (moves) ms->nm[s][pt] = -m;
+              ms->f[s][pt] = moves ? ex2_approx(old - m) : 1.f;
+            }
+            group_sync(2 + s, 128);
 #pragma unroll
-          for (int r = 0; r < NR; ++r) l[r] *= ms->f[s][r];
+            for (int r0 = 0; r0 < NR; r0 += kN)
+              load_scores<kN, NR, E4M3>(t_s, r0, ms->nm[s], ms->a[sn & 1], c2, ck, ev, x + r0);
+            if (mask)
+#pragma unroll
+              for (int r = 0; r < NR; ++r)
+                if (r < r_lo || r >= r_hi) x[r] = -INFINITY;
+          }
           if (i >= 2) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r) l[r] *= ms->f[s][r];
 #pragma unroll 1
-            for (int c = 0; c < F::kParts * NR; c += 8) {
-              uint32_t o[8];
-              tmem_ld_32x32b_x8(t_o + c, o);
+            for (int c = 0; c < F::kParts * NR; c += kB) {
+              uint32_t o[kB];
+              bool moved = false;  // alike in every thread
+#pragma unroll
+              for (int k = 0; k < kB; ++k) moved |= ms->f[s][c % NR + k] != 1.f;
+              if (!moved) continue;
+              tmem_ld<kB>(t_o + c, o);
               tmem_wait_ld_regs(o);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
+              for (int k = 0; k < kB; ++k)
                 o[k] = __float_as_uint(__uint_as_float(o[k]) * ms->f[s][c % NR + k]);
-              tmem_st_32x32b_x8(t_o + c, o);
+              tmem_st<kB>(t_o + c, o);
             }
             tmem_wait_st();
           }
-          prior = true;
         }
         if (!prior) {
           wait_bar(b_o + 8 * s, ph_o, s_abort, status);
@@ -509,6 +570,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         // P: the position's row of its terms, 8 packed rows at a time
 #pragma unroll
         for (int r0 = 0; r0 < NR; r0 += 8) {
+          if (r0 >= sg.nrows) break;  // their columns of O are not read
           if constexpr (E4M3) {
             uint32_t t[4][4];
 #pragma unroll
@@ -612,6 +674,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       if (has) {
 #pragma unroll
         for (int r0 = 0; r0 < NR; r0 += 8) {
+          if (r0 >= sg.nrows) break;
           uint32_t u[F::kParts][8];
 #pragma unroll
           for (int q = 0; q < F::kParts; ++q) tmem_ld_32x32b_x8(t_o + q * NR + r0, u[q]);
@@ -653,6 +716,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       tc_fence_before();
     }
   } else {
+    reg_dec<120>();
     // ------------------------------------------------------------ Q
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth, qb = sn & 1;
