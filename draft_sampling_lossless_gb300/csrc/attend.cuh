@@ -25,9 +25,6 @@ namespace attend {
 using namespace sm100;
 
 constexpr int kBN = 128;               // positions a tile
-constexpr int kSoftThreads = 256;      // the two softmax warpgroups, warps 0-7
-constexpr int kWarpMma = 8;
-constexpr int kWarpTma = 9;
 constexpr int kSegDepth = 4;
 constexpr int kMaxCtas = 160;
 constexpr int kMaxSmem = 232448;
@@ -181,7 +178,6 @@ __device__ __forceinline__ bool group_any(int id, int n, bool v) {
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void soft_sync() { group_sync(1, kSoftThreads); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t d;
@@ -251,19 +247,21 @@ __device__ __forceinline__ Range plan(const Params& p, int64_t* s_sum, Found* s_
     }
   }
   int64_t incl = local;
-#pragma unroll
+#pragma unroll 1
   for (int d = 1; d < 32; d <<= 1) {
     const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += o;
   }
   if (lane == 31) s_sum[wid] = incl;
   __syncthreads();
-  int64_t base = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < wid) base += s_sum[w];
-    total += s_sum[w];
+  int64_t sums = lane < THREADS / 32 ? s_sum[lane] : 0;
+#pragma unroll 1
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, sums, d);
+    if (lane >= d) sums += o;
   }
+  const int64_t total = __shfl_sync(0xffffffffu, sums, 31);
+  const int64_t base = __shfl_sync(0xffffffffu, sums, wid) - __shfl_sync(0xffffffffu, incl, 31);
   Range r;
   r.ctas = (int)min((int64_t)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
   r.u0 = r.u1 = 0;
@@ -297,12 +295,12 @@ __device__ __forceinline__ Range plan(const Params& p, int64_t* s_sum, Found* s_
   return r;
 }
 
-// A place in the order of items: `tile` of head h of row tile qt of request n;
-// n = R is the end.
+// A place in the order of items: `tile` of the nt of head h of row tile qt of request
+// n; n = R is the end.
 struct Place {
   Req q;
   int64_t a;  // units before the item
-  int n, qt, h, tile;
+  int n, qt, h, tile, nt;
 };
 
 // What a cut does to an item of nt tiles: up to `low` tiles in, it moves to the
@@ -310,10 +308,12 @@ struct Place {
 __device__ __forceinline__ int snap_low(int nt) { return min(kSnap, nt >> 1); }
 __device__ __forceinline__ int snap_high(int nt) { return min(kSnap, nt - snap_low(nt) - 1); }
 
+// The first tile of the next item (whose nt is not known yet).
 template <int ROWS>
-__device__ __forceinline__ void next_item(const Params& p, Place& w, int nt) {
-  w.a += nt + kItemCost;
+__device__ __forceinline__ void next_item(const Params& p, Place& w) {
+  w.a += w.nt + kItemCost;
   w.tile = 0;
+  w.nt = 1;
   if (++w.h < p.c.Hkv) return;
   w.h = 0;
   if (++w.qt < w.q.tiles) return;
@@ -341,7 +341,7 @@ __device__ __forceinline__ Place locate(const Params& p, const Found& f, int64_t
             ? (int64_t)(item_of(p, w.q, w.qt + lane).ntiles + kItemCost) * p.c.Hkv
             : 0;
     int64_t incl = mine;
-#pragma unroll
+#pragma unroll 1
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += o;
@@ -356,132 +356,117 @@ __device__ __forceinline__ Place locate(const Params& p, const Found& f, int64_t
     v -= __shfl_sync(0xffffffffu, incl, 31);
     w.qt += 32;
   }
-  const int nt = item_of(p, w.q, w.qt).ntiles, units = nt + kItemCost;
+  w.nt = item_of(p, w.q, w.qt).ntiles;
+  const int units = w.nt + kItemCost;
   w.h = v < (1ll << 31) ? (int)((uint32_t)v / (uint32_t)units) : (int)(v / units);
   const int off = (int)(v - (int64_t)w.h * units);
   w.a = u - off;
   const int t = off - kItemCost;
-  w.tile = t <= snap_low(nt) ? 0 : t;
-  if (t >= nt - snap_high(nt)) next_item<ROWS>(p, w, nt);
+  w.tile = t <= snap_low(w.nt) ? 0 : t >= w.nt - snap_high(w.nt) ? w.nt : t;
   return w;
 }
 
-// Loads a segment's tiles: `issue(rows, mine, none)` for each, where rows[b] is the pool's row
-// of box b's first position, or `none` (past the pool, so that the box reads as
-// zeros) where no row of the item sees the box; `mine`, lane b's own of them.  False
-// when issue failed.
-template <class Issue>
-__device__ __forceinline__ bool load_segment(const Params& p, const Segment& sg, Issue& issue) {
+// A loading warp: the one that leads walks the block's range and queues its segments (an
+// empty one at the end); each loads the tiles of every segment.  `issue(mine, none)`
+// loads a tile: lane b's `mine` is the pool's row of box b's first position, or `none` (past the
+// pool, so that the box reads as zeros) where no row of the item sees the box; false when it
+// failed.  flush() after each segment.
+template <int ROWS, class Issue, class Flush>
+__device__ __forceinline__ void load_all(const Params& p, const Range& rg, bool lead,
+                                         const Found* s_found, Segment* s_seg,
+                                         uint32_t b_segFull, uint32_t b_segEmpty,
+                                         volatile int* s_abort, Issue& issue, Flush& flush) {
   const int lane = threadIdx.x & 31;
   const int log_page = p.c.log_page, page = 1 << log_page;
   const int box_rows = min(page, kBN), n_boxes = kBN / box_rows;
   const int none = (int)(p.c.n_pages * p.c.Hkv) << log_page;
-  auto lookup = [&](int tile) {  // lane b: box b
-    if (lane >= n_boxes) return none;
-    const int pos = tile * kBN + lane * box_rows;
-    if (pos >= sg.hi || pos + box_rows <= sg.lo) return none;
-    const int64_t id = page_of(p.c, sg.n, pos);
-    if (id < 0) return none;
-    return (int)((id * p.c.Hkv + sg.h) << log_page) + (pos & (page - 1));
-  };
-  int next = lookup(sg.tile0);
+  Place w = {}, e = {};
+  if (lead) {
 #pragma unroll 1
-  for (int i = 0; i < sg.ntiles; ++i) {
-    const int mine = next;
-    int y[8];
-#pragma unroll
-    for (int b = 0; b < 8; ++b) y[b] = __shfl_sync(0xffffffffu, mine, b);
-    if (i + 1 < sg.ntiles) next = lookup(sg.tile0 + i + 1);  // in flight under the waits
-    if (!issue(y, mine, none)) return false;
-  }
-  return true;
-}
-
-// Walks the block's range: queues its segments (an empty one at the end) and loads
-// the tiles of each; flush() after each.
-template <int ROWS, class Issue, class Flush>
-__device__ __forceinline__ void produce(const Params& p, const Range& rg, const Found* s_found,
-                                        Segment* s_seg, uint32_t b_segFull, uint32_t b_segEmpty,
-                                        volatile int* s_abort, Issue& issue, Flush& flush) {
-  const int lane = threadIdx.x & 31;
-  Place w = locate<ROWS>(p, s_found[0], rg.u0), e;
-  e.n = p.c.R;
-  e.qt = e.h = e.tile = 0;
-  if (!rg.last) e = locate<ROWS>(p, s_found[1], rg.u1);
-#pragma unroll 1
-  for (int sn = 0;; ++sn) {
-    const int ss = sn % kSegDepth;
-    const bool ok =
-        wait_bar(b_segEmpty + 8 * ss, ((sn / kSegDepth) & 1) ^ 1, s_abort, p.c.status);
-    if (!__all_sync(0xffffffffu, ok)) return;
-    const bool at_end = w.n == e.n && w.qt == e.qt && w.h == e.h;
-    const bool end = w.n >= p.c.R || (at_end && w.tile >= e.tile);
-    Segment sg;
-    int nt = 0, stop = 0;
-    if (end) {
-      sg.ntiles = 0;
-    } else {
-      const Item it = item_of(p, w.q, w.qt);
-      nt = it.ntiles;
-      stop = at_end ? e.tile : nt;
-      sg.n = w.n;
-      sg.row0 = w.q.row0;
-      sg.m = w.q.m;
-      sg.ctx = w.q.ctx;
-      sg.h = w.h;
-      sg.r0 = it.r0;
-      sg.nrows = it.nrows;
-      sg.lo = it.lo;
-      sg.hi = it.hi;
-      sg.tile0 = it.tile0 + w.tile;
-      sg.ntiles = stop - w.tile;
-      sg.split = sg.first = sg.last = 0;
-      if (sg.ntiles != nt) {
-        sg.first = rg.block_of(w.a + kItemCost + snap_low(nt));
-        sg.last = rg.block_of(w.a + kItemCost + nt - snap_high(nt) - 1);
-        sg.split = (int)blockIdx.x == sg.first ? 2 : 1;
+    for (int k = 1; k >= 0; --k) {
+      if (k == 1) {
+        e.n = p.c.R;
+        if (rg.last) continue;
       }
+      w = locate<ROWS>(p, s_found[k], k ? rg.u1 : rg.u0);
+      if (k == 1) e = w;
     }
-    if (lane == 0) {
-      s_seg[ss] = sg;
-      mbar_arrive(b_segFull + 8 * ss);
-    }
-    if (end) return;
-    if (lane == 0 && __ldg(p.c.row_off + sg.n + 1) - __ldg(p.c.row_off + sg.n) > p.max_rows)
-      set_flag(p.c.status, kFlagRowRange);
-    if (!load_segment(p, sg, issue)) return;
-    flush();
-    if (stop == nt)
-      next_item<ROWS>(p, w, nt);
-    else
-      w.tile = stop;
   }
-}
-
-// Another warp's loads of the same segments.
-template <class Issue, class Flush>
-__device__ __forceinline__ void follow(const Params& p, Segment* s_seg, uint32_t b_segFull,
-                                       uint32_t b_segEmpty, volatile int* s_abort, Issue& issue,
-                                       Flush& flush) {
 #pragma unroll 1
   for (int sn = 0;; ++sn) {
     const int ss = sn % kSegDepth;
-    const bool ok = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, p.c.status);
+    const uint32_t parity = (sn / kSegDepth) & 1;
+    const bool ok = wait_bar((lead ? b_segEmpty : b_segFull) + 8 * ss, lead ? parity ^ 1 : parity,
+                             s_abort, p.c.status);
     if (!__all_sync(0xffffffffu, ok)) return;
-    const Segment sg = s_seg[ss];
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(b_segEmpty + 8 * ss);
-    if (sg.ntiles == 0 || !load_segment(p, sg, issue)) return;
+    Segment sg;
+    if (lead) {
+      auto at_e = [&]() { return w.n == e.n && w.qt == e.qt && w.h == e.h; };
+      bool end = w.n >= p.c.R || (at_e() && w.tile >= e.tile);
+      if (!end && w.tile >= w.nt) {
+        next_item<ROWS>(p, w);
+        end = w.n >= p.c.R || (at_e() && w.tile >= e.tile);
+      }
+      if (end) {
+        sg.ntiles = 0;
+      } else {
+        const Item it = item_of(p, w.q, w.qt);
+        const int nt = it.ntiles, stop = at_e() ? e.tile : nt;
+        sg.n = w.n;
+        sg.row0 = w.q.row0;
+        sg.m = w.q.m;
+        sg.ctx = w.q.ctx;
+        sg.h = w.h;
+        sg.r0 = it.r0;
+        sg.nrows = it.nrows;
+        sg.lo = it.lo;
+        sg.hi = it.hi;
+        sg.tile0 = it.tile0 + w.tile;
+        sg.ntiles = stop - w.tile;
+        sg.split = sg.first = sg.last = 0;
+        if (sg.ntiles != nt) {
+          sg.first = rg.block_of(w.a + kItemCost + snap_low(nt));
+          sg.last = rg.block_of(w.a + kItemCost + nt - snap_high(nt) - 1);
+          sg.split = (int)blockIdx.x == sg.first ? 2 : 1;
+        }
+        w.tile = stop;
+        w.nt = nt;
+      }
+      if (lane == 0) {
+        s_seg[ss] = sg;
+        mbar_arrive(b_segFull + 8 * ss);
+        if (sg.ntiles != 0 &&
+            __ldg(p.c.row_off + sg.n + 1) - __ldg(p.c.row_off + sg.n) > p.max_rows)
+          set_flag(p.c.status, kFlagRowRange);
+      }
+    } else {
+      sg = s_seg[ss];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
+    }
+    if (sg.ntiles == 0) return;
+    int next = none;
+#pragma unroll 1
+    for (int i = -1; i < sg.ntiles; ++i) {
+      const int mine = next;
+      next = none;  // lane b: box b of the next tile, in flight under the waits
+      const int pos = (sg.tile0 + i + 1) * kBN + lane * box_rows;
+      if (i + 1 < sg.ntiles && lane < n_boxes && pos < sg.hi && pos + box_rows > sg.lo) {
+        const int64_t id = page_of(p.c, sg.n, pos);
+        if (id >= 0) next = (int)((id * p.c.Hkv + sg.h) << log_page) + (pos & (page - 1));
+      }
+      if (i >= 0 && !issue(mine, none)) return;
+    }
     flush();
   }
 }
 
-// Joins the partial results of an item's blocks (all softmax threads of the last
-// one to finish).  `buf`, 32 KB of shared memory: the blocks' (m, l) of a
+// Joins the partial results of an item's blocks (the THREADS softmax threads, warps 0
+// on, of the last one to finish).  `buf`, 32 KB of shared memory: the blocks' (m, l) of a
 // group of rows, then their weights 2^(m - M) / L; the sums run over the blocks in
 // order, eight values a thread.  kLanesOnRows: records hold O as [DP / 4][ROWS][4],
 // else [ROWS][DP]; a warp's loads are contiguous either way.
-template <int DP, int ROWS, bool kLanesOnRows>
+template <int DP, int ROWS, int THREADS, bool kLanesOnRows>
 __device__ __forceinline__ void join(const Params& p, const Segment& sg, float2* buf) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int np = sg.last - sg.first + 1;
@@ -494,13 +479,13 @@ __device__ __forceinline__ void join(const Params& p, const Segment& sg, float2*
   for (int r0 = 0; r0 < sg.nrows; r0 += group) {
     const int g = min(group, sg.nrows - r0);
 #pragma unroll 1
-    for (int i = tid; i < np * g; i += kSoftThreads) {
+    for (int i = tid; i < np * g; i += THREADS) {
       const int b = i / g, row = i - b * g;
       buf[i] = __ldcg(reinterpret_cast<const float2*>(part(b) + (size_t)ROWS * DP) + r0 + row);
     }
-    soft_sync();
+    group_sync(1, THREADS);
 #pragma unroll 1
-    for (int row = warp; row < g; row += kSoftThreads / 32) {
+    for (int row = warp; row < g; row += THREADS / 32) {
       float M = -INFINITY, L = 0.f;
       for (int b = lane; b < np; b += 32) M = fmaxf(M, buf[b * g + row].x);
 #pragma unroll
@@ -520,9 +505,9 @@ __device__ __forceinline__ void join(const Params& p, const Segment& sg, float2*
         p.lse[out_row(p, sg.row0, sg.h, sg.r0 + r0 + row)] =
             L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
     }
-    soft_sync();
+    group_sync(1, THREADS);
 #pragma unroll 1
-    for (int task = tid; task < g * (DP / 8); task += kSoftThreads) {
+    for (int task = tid; task < g * (DP / 8); task += THREADS) {
       const int d8 = kLanesOnRows ? task / g : task % (DP / 8);
       const int row = kLanesOnRows ? task - d8 * g : task / (DP / 8);
       if (d8 * 8 >= p.c.D) continue;
@@ -558,27 +543,27 @@ __device__ __forceinline__ void join(const Params& p, const Segment& sg, float2*
           make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y),
                      pack_bf16(y.z, y.w));
     }
-    soft_sync();
+    group_sync(1, THREADS);
   }
 }
 
 // After a block wrote its part of a split item (all softmax threads): the last of
 // the item's blocks joins.  s_last is a word of shared memory, buf 32 KB.
-template <int DP, int ROWS, bool kLanesOnRows>
+template <int DP, int ROWS, int THREADS, bool kLanesOnRows>
 __device__ __forceinline__ void finish_split(const Params& p, const Segment& sg,
                                              volatile int* s_last, float2* buf) {
   __threadfence();
-  soft_sync();
+  group_sync(1, THREADS);
   if (threadIdx.x == 0) {
     const unsigned want = (unsigned)(sg.last - sg.first);
     const unsigned old = atomicAdd(p.counters + sg.first, 1u);
     *s_last = old == want;
     if (old == want) p.counters[sg.first] = 0;
   }
-  soft_sync();
+  group_sync(1, THREADS);
   if (*s_last) {
     __threadfence();
-    join<DP, ROWS, kLanesOnRows>(p, sg, buf);
+    join<DP, ROWS, THREADS, kLanesOnRows>(p, sg, buf);
   }
 }
 

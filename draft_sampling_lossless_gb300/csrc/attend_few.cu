@@ -27,10 +27,11 @@
 // A position's scales are its thread's own: K's a factor of the scores; V's, with
 // exponent e, goes into P = 2^(s + e - m), and l sums 2^-e P.
 //
-// Two streams, a warpgroup each with its own S, P, O and m, take alternate tiles.
-// Roles: warps 0-7 softmax, 8 the MMAs, 9 and 10 the loads of K and V (and their
-// scales), 11 fetches the next item's Q.  Every wait is bounded.  See attend.cuh for
-// the split of the work.
+// Two streams, each a warpgroup (or two, for half of the rows each) with its own S, P,
+// O and m, take alternate tiles.
+// Roles: the first 8 (or 16) warps softmax, then one the MMAs, two the loads of K
+// and V (and their scales), one fetches the next item's Q.  Every wait is
+// bounded.  See attend.cuh for the split of the work.
 #include "attend.cuh"
 
 namespace dspark {
@@ -44,42 +45,51 @@ constexpr int kExpDepth = 8;          // tiles of exponent bytes held
 
 template <int DP, int NR, bool E4M3>
 struct Few {
-  static constexpr int kThreads = 384;
+  // Softmax threads a position: rows of e4m3 terms want more warps for their longer
+  // chains of conversions
+  static constexpr int kSplit = E4M3 && NR > 16 ? 2 : 1;
+  static constexpr int kSoft = 256 * kSplit;   // softmax threads; then four warps
+  static constexpr int kWarpMma = kSoft / 32, kWarpTma = kWarpMma + 1;
+  static constexpr int kThreads = kSoft + 128;
   static constexpr int kNH = DP / 64;
   static constexpr int kParts = E4M3 ? 4 : 2;                         // terms of P
   static constexpr int kQRows = E4M3 ? 2 * NR : (NR < 16 ? 16 : NR);  // N of the scores
   // tiles of scores ahead: e4m3 tiles come twice as fast, and one's softmax is longer
   static constexpr int kSBufs = E4M3 ? 4 : 2;
-  // tensor memory: S, 64 columns each, then O of the streams
+  // tensor memory: S, 64 columns each, then O of the streams, then (bf16) the
+  // positions' own sums, l; e4m3's are in shared memory
   static constexpr uint32_t kColO = 64 * kSBufs, kOCols = E4M3 ? 128 : 64;
-  static constexpr uint32_t kTmemCols = E4M3 ? 512 : 256;
+  static constexpr uint32_t kColL = kColO + 2 * kOCols;
+  static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kSlot = E4M3 ? kHalf : kHalf * kNH;       // a tile
   static constexpr uint32_t kQHalf = kQRows * 128;
   static constexpr uint32_t kQBytes = kQHalf * (E4M3 ? 1 : kNH);
   static constexpr uint32_t kExp = E4M3 ? kExpDepth * 256 : 0;
+  static constexpr uint32_t kL = E4M3 ? NR * 1024 : 0;
   static constexpr uint32_t kMisc = 4096;
-  static constexpr int kFit = (int)((kMaxSmem - 2 * kHalf - 2 * kQBytes - kExp - kMisc) / kSlot);
+  static constexpr int kFit =
+      (int)((kMaxSmem - 2 * kHalf - 2 * kQBytes - kExp - kL - kMisc) / kSlot);
   static constexpr int kSlots = kFit > 12 ? 12 : kFit;
   // K and V go through one ring by two warps.  A slot that they use in turn (an odd
   // ring) is safe while a tile's scores are at most (slots - 1) / 2 tiles ahead of its
   // products: no warp then waits for a phase two ahead of the slot's.
   static_assert(kSlots % 2 == 0 || kSlots >= 2 * kSBufs + 1, "ring");
-  static constexpr uint32_t kPOff = kSlots * kSlot;  // P of each stream; the join's buffer
+  // P of each stream (at an item's end its O, then the join's buffer)
+  static constexpr uint32_t kPOff = kSlots * kSlot;
   static constexpr uint32_t kQOff = kPOff + 2 * kHalf;
   static constexpr uint32_t kExpOff = kQOff + 2 * kQBytes;
-  static constexpr uint32_t kMiscOff = kExpOff + kExp;
+  static constexpr uint32_t kLOff = kExpOff + kExp;
+  static constexpr uint32_t kMiscOff = kLOff + kL;
   static constexpr uint32_t kTotal = kMiscOff + kMisc;
   static_assert(kTotal <= kMaxSmem && kSlots >= 4, "shared memory");
 };
 
 struct Misc {  // shared words
   float nm[2][32];      // -m of each stream's rows
-  float f[2][32];       // what a move of the references multiplies by,
-  float d[2][32];       // and its logarithm, negated
-  float zero[32];
+  float f[2][32];       // what a move of the references multiplies by
   float wm[2][4][32];   // the warps' maxima, then sums
   float a[2][32];       // e4m3: scale of the scores of a row, of each Q buffer
-  int64_t sum[16];
+  int64_t sum[32];
   Found found[2];
   Segment seg[kSegDepth];
   uint64_t bars[2 * 12 + 2 * kSegDepth + 4 + 8 + 2 * kExpDepth + 1];
@@ -121,54 +131,6 @@ __device__ __forceinline__ void e4m3_terms(float a, float b, uint32_t (&t)[4]) {
   }
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N]) {
-  if constexpr (N == 8)
-    tmem_ld_32x32b_x8(taddr, v);
-  else if constexpr (N == 16)
-    tmem_ld_32x32b_x16(taddr, v);
-  else
-    tmem_ld_32x32b_x32(taddr, v);
-}
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[N]) {
-  if constexpr (N == 8)
-    tmem_st_32x32b_x8(taddr, v);
-  else if constexpr (N == 16)
-    tmem_st_32x32b_x16(taddr, v);
-  else
-    tmem_st_32x32b_x32(taddr, v);
-}
-
-// The scores of a thread's position, N rows from r0 on: x[k] = log2 of row r0 + k's
-// exponential (e4m3: times 2^e of the value's exponent e), plus nm[r0 + k].
-template <int N, int NR, bool E4M3>
-__device__ __forceinline__ void load_scores(uint32_t t_s, int r0, const float* nm,
-                                            const float* row_scale, float c2, float ck, float ev,
-                                            float* x) {
-  uint32_t u[N], v[N];
-  tmem_ld<N>(t_s + r0, u);
-  if constexpr (E4M3) {
-    tmem_ld<N>(t_s + NR + r0, v);
-    tmem_wait_ld_regs(u, v);
-  } else {
-    tmem_wait_ld_regs(u);
-  }
-#pragma unroll
-  for (int k = 0; k < N; k += 2) {
-    unsigned long long y = pack2(__uint_as_float(u[k]), __uint_as_float(u[k + 1]));
-    const float2 n2 = *reinterpret_cast<const float2*>(nm + r0 + k);
-    if constexpr (E4M3) {
-      y = fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), pack2(0.0625f, 0.0625f), y);
-      const float2 a = *reinterpret_cast<const float2*>(row_scale + r0 + k);
-      y = fma2(mul2(y, pack2(a.x, a.y)), pack2(ck, ck), add2(pack2(n2.x, n2.y), pack2(ev, ev)));
-    } else {
-      y = fma2(y, pack2(c2, c2), pack2(n2.x, n2.y));
-    }
-    unpack2(y, x[k], x[k + 1]);
-  }
-}
-
 template <int DP, int NR, bool E4M3>
 __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     attend_few_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -191,34 +153,34 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   uint32_t* status = p.c.status;
   if (smem_u32(smem) & 1023) return;  // never: the declared alignment, which the swizzle needs
 
-  if (tid < 32) {
-    ms->zero[tid] = 0.f;
-  }
   if (tid == 0) {
     *s_abort = 0;
+#pragma unroll 1
     for (int i = 0; i < 2 * NS; ++i) mbar_init(b_full + 8 * i, 1);
+#pragma unroll 1
     for (int i = 0; i < kSegDepth; ++i) {
       mbar_init(b_segFull + 8 * i, 1);
-      mbar_init(b_segEmpty + 8 * i, 11);  // the MMA thread and the other warps
+      mbar_init(b_segEmpty + 8 * i, 3 + F::kSoft / 32);  // the MMA thread and the other warps
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_qFull + 8 * i, 32);
       mbar_init(b_qEmpty + 8 * i, 1);
       mbar_init(b_s + 8 * i, 1);
       mbar_init(b_s + 16 + 8 * i, 1);
-      mbar_init(b_p + 8 * i, 128);
+      mbar_init(b_p + 8 * i, F::kSoft / 2);
       mbar_init(b_o + 8 * i, 1);
     }
+#pragma unroll 1
     for (int i = 0; i < kExpDepth; ++i) {
       mbar_init(b_expFull + 8 * i, 64);
-      mbar_init(b_expEmpty + 8 * i, 4);  // the warps of the tile's stream
+      mbar_init(b_expEmpty + 8 * i, F::kSoft / 64);  // the warps of the tile's stream
     }
     mbar_init(b_drain, 1);
     fence_mbar_init();
   }
   const Range rg = plan<32, F::kThreads>(p, ms->sum, ms->found);
   if (rg.u0 >= rg.u1) return;  // no tiles for this block
-  if (warp == kWarpMma) {
+  if (warp == F::kWarpMma) {
     tmem_alloc(smem_u32(&ms->tmem), F::kTmemCols);
     tmem_relinquish();
   }
@@ -227,11 +189,9 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
 
-  // 384 threads of 168 registers become 256 x 192 and 128 x 120
-  if (warp == kWarpTma || warp == kWarpTma + 1) {
-    reg_dec<120>();
+  if (warp == F::kWarpTma || warp == F::kWarpTma + 1) {
     // ------------------------------------------------------------ loads
-    const int kv = warp - kWarpTma;  // warp 9 K, warp 10 V
+    const int kv = warp - F::kWarpTma;  // the first K, the second V
     const CUtensorMap* map = kv ? &tm_v : &tm_k;
     const int box_rows = min(1 << p.c.log_page, kBN), n_boxes = kBN / box_rows;
     if (lane == 0) tma_prefetch(map);
@@ -240,60 +200,49 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     const uint8_t* exps = kv ? p.c.v_exp : p.c.k_exp;
     const int my_box = lane * 4 / box_rows, my_at = lane * 4 % box_rows;
     uint32_t held = 0;
-    auto store_exps = [&](uint32_t tile) {
-      const uint32_t q = tile % kExpDepth;
-      wait_bar(b_expEmpty + 8 * q, ((tile / kExpDepth) & 1) ^ 1, s_abort, status);
+    uint32_t stored = 0;  // tiles whose bytes are stored
+    auto flush = [&]() {
+      if (!E4M3 || stored >= e / 2) return;
+      const uint32_t q = stored % kExpDepth;
+      wait_bar(b_expEmpty + 8 * q, ((stored / kExpDepth) & 1) ^ 1, s_abort, status);
       reinterpret_cast<uint32_t*>(smem + F::kExpOff + q * 256 + kv * 128)[lane] = held;
       mbar_arrive(b_expFull + 8 * q);
+      ++stored;
     };
-    uint32_t stored = 0;  // tiles whose bytes are stored
-    auto issue = [&](const int (&y)[8], int mine, int none) {
+    auto issue = [&](int mine, int none) {
       if constexpr (E4M3) {
         // a box that reads as zeros: any scale does, but not one that moves the references
         const int row = __shfl_sync(0xffffffffu, mine, my_box);
         uint32_t now = 0x7f7f7f7fu;
         if (row != none)
           now = __ldg(reinterpret_cast<const uint32_t*>(exps + row + my_at));
-        if (stored < e / 2) store_exps(stored++);
+        flush();
         held = now;
       }
-      const uint32_t slot = e % NS;
+      const uint32_t slot = e % NS, full = b_full + 8 * slot;
       const bool ok = wait_bar(b_empty + 8 * slot, ((e / NS) & 1) ^ 1, s_abort, status);
       if (!__all_sync(0xffffffffu, ok)) return false;
-      if (elect_one()) {
-        const uint32_t full = b_full + 8 * slot;
-        const uint32_t dst = smem_u32(smem) + slot * F::kSlot;
-        mbar_arrive_expect_tx(full, F::kSlot);
-#pragma unroll
-        for (int b = 0; b < 8; ++b)
-          if (b < n_boxes) {
-            if constexpr (E4M3) {
-              tma_load_2d(dst + b * box_rows * 128, map, full, 0, y[b]);
-            } else {
-#pragma unroll
-              for (int half = 0; half < NH; ++half)
-                tma_load_2d(dst + half * kHalf + b * box_rows * 128, map, full, half * 64, y[b]);
-            }
-          }
+      if (elect_one()) mbar_arrive_expect_tx(full, F::kSlot);
+      uint32_t dst = smem_u32(smem) + slot * F::kSlot;
+#pragma unroll 1
+      for (int b = 0; b < n_boxes; ++b, dst += box_rows * 128) {
+        const int y = __shfl_sync(0xffffffffu, mine, b);
+        if (elect_one()) {
+          tma_load_2d(dst, map, full, 0, y);
+          if (!E4M3 && NH > 1) tma_load_2d(dst + kHalf, map, full, 64, y);
+        }
       }
       __syncwarp();
       e += 2;
       return true;
     };
-    auto flush = [&]() {
-      if (E4M3 && stored < e / 2) store_exps(stored++);
-    };
-    if (kv == 0)
-      produce<32>(p, rg, ms->found, ms->seg, b_segFull, b_segEmpty, s_abort, issue, flush);
-    else
-      follow(p, ms->seg, b_segFull, b_segEmpty, s_abort, issue, flush);
+    load_all<32>(p, rg, kv == 0, ms->found, ms->seg, b_segFull, b_segEmpty, s_abort, issue, flush);
     if (*s_abort) {
       // the copies in flight land before the block's shared memory goes
       for (uint32_t i = e > NS ? e - NS : kv; i < e; ++i)
         if ((i & 1) == kv) mbar_wait(b_full + 8 * (i % NS), (i / NS) & 1);
     }
-  } else if (warp == kWarpMma) {
-    reg_dec<120>();
+  } else if (warp == F::kWarpMma) {
     // ------------------------------------------------------------ products
     if (elect_one()) {
       constexpr uint32_t kIdS = E4M3 ? idesc_0_f32(128, F::kQRows) : idesc_bf16_f32(128, F::kQRows);
@@ -311,6 +260,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       auto scores = [&](int sb, uint32_t e, int qb) {
         const uint64_t a = desc_kmajor_sw128(at0 + (e % NS) * F::kSlot);
         const uint64_t b = desc_kmajor_sw128(at0 + F::kQOff + qb * F::kQBytes);
+#pragma unroll 1
         for (int k = 0; k < ksteps; ++k) {
           if constexpr (E4M3)
             mma_e4m3(tmem + sb * 64, a + k * 2, b + k * 2, kIdS, k > 0);
@@ -333,6 +283,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t e0 = 2 * base;  // K of tile i: e0 + 2 i, V: one more
+#pragma unroll 1
         for (int i = 0; i < SB && i < nt && ok; ++i) {
           need(e0 + 2 * i);
           if (ok) scores(i, e0 + 2 * i, qb);
@@ -350,9 +301,11 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           const uint64_t b = desc_mnmajor_sw128(at0 + F::kPOff + s * kHalf, 0);
           const uint32_t o = tmem + F::kColO + s * F::kOCols;
           if constexpr (E4M3) {
+#pragma unroll 1
             for (int k = 0; k < kBN / 32; ++k)
               mma_e4m3(o, a + k * (4096 >> 4), b + k * (4096 >> 4), kIdO, i >= 2 || k > 0);
           } else {
+#pragma unroll 1
             for (int k = 0; k < kBN / 16; ++k)
               mma_bf16(o, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdO, i >= 2 || k > 0);
           }
@@ -372,34 +325,74 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < 8) {
-    reg_inc<192>();
+  } else if (warp < F::kSoft / 32) {
     // ------------------------------------------------------------ softmax
-    const int s = warp >> 2;    // the stream
-    const int pt = tid & 127;   // position of the tile, value of D at the end
+    // Every step goes over the rows in a loop of eight at a time: the code of a tile
+    // has to stay in the instruction caches, which all roles share.
+    const int s = (warp >> 2) & 1;               // the stream
+    const int r_first = (warp >> 3) * 8;         // this thread's rows: eight from here,
+    constexpr int kStep = 8 * F::kSplit;         // every kStep rows
+    const int wg = 2 + (warp >> 2);              // its warpgroup's barrier
+    const int pt = tid & 127;                    // position of the tile, value of D at the end
+    const bool owner = pt < NR && ((pt >> 3) & (F::kSplit - 1)) == warp >> 3;  // of row pt
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_o = tmem + lanes + F::kColO + s * F::kOCols;
+    const uint32_t t_l = tmem + lanes + F::kColL + s * 32;
     const float c2 = p.scale * kLog2e;
+    float* nm = ms->nm[s];
+    float* f = ms->f[s];
     uint8_t* my_p = smem + F::kPOff + s * kHalf + pt * 128;
+    float4* my_l = reinterpret_cast<float4*>(smem + F::kLOff) + s * 128 + pt;
     uint32_t ph_s = 0, ph_o = 0, base = 0;
+    // this position's sums of 8 rows
+    auto load_l = [&](int r0, float (&v)[8]) {
+      if constexpr (E4M3) {
+        const float4 a = my_l[r0 * 64], b = my_l[r0 * 64 + 256];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      } else {
+        uint32_t u[8];
+        tmem_ld_32x32b_x8(t_l + r0, u);
+        tmem_wait_ld_regs(u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(u[k]);
+      }
+    };
+    auto store_l = [&](int r0, const float (&v)[8]) {
+      if constexpr (E4M3) {
+        my_l[r0 * 64] = make_float4(v[0], v[1], v[2], v[3]);
+        my_l[r0 * 64 + 256] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        uint32_t u[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(v[k]);
+        tmem_st_32x32b_x8(t_l + r0, u);
+      }
+    };
+#pragma unroll 1
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth;
       const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status);
       // all leave together
-      if (group_any(1, kSoftThreads, !got)) break;
+      if (group_any(1, F::kSoft, !got)) break;
       const Segment sg = ms->seg[ss];
       __syncwarp();
       if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
       if (sg.ntiles == 0) break;
 
-      float l[NR];
-#pragma unroll
-      for (int r = 0; r < NR; ++r) l[r] = 0.f;
+      if (owner) nm[pt] = pt < sg.nrows ? kUnset : 0.f;
+      {
+        const float zero[8] = {};
+#pragma unroll 1
+        for (int r0 = r_first; r0 < sg.nrows; r0 += kStep) store_l(r0, zero);
+      }
+      group_sync(wg, 128);
       // positions that every row sees
       const int all_hi = p.causal ? sg.ctx + p.by_G(sg.r0) + 1 : sg.ctx + sg.m;
       const int all_lo =
           p.window == 0 ? 0 : sg.ctx + p.by_G(sg.r0 + sg.nrows - 1) - p.window + 1;
       if (E4M3) wait_bar(b_qFull + 8 * (sn & 1), (sn >> 1) & 1, s_abort, status);
+      const float* row_scale = ms->a[sn & 1];
 #pragma unroll 1
       for (int i = s; i < sg.ntiles; i += 2) {
         const int t0 = (sg.tile0 + i) * kBN;
@@ -438,146 +431,129 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
             }
           }
         }
-        float x[NR];
-        constexpr int kN = NR < 16 ? NR : 16, kB = kN;
-        const float* nm = i == s ? ms->zero : ms->nm[s];
-        // blocks of rows that the item does not have are left out throughout
-#pragma unroll
-        for (int r0 = 0; r0 < NR; r0 += kN)
-          if (r0 < sg.nrows) {
-            load_scores<kN, NR, E4M3>(t_s, r0, nm, ms->a[sn & 1], c2, ck, ev, x + r0);
-          } else {
-#pragma unroll
-            for (int k = 0; k < kN; ++k) x[r0 + k] = -INFINITY;
-          }
-        if (i == s) {
-          // the references: the scores of a position that every row sees
-          const int c0 = max(all_lo - t0, 0);
-          if (c0 < min(all_hi - t0, kBN)) {
-            if (pt == c0)
-#pragma unroll
-              for (int r = 0; r < NR; ++r)
-                ms->nm[s][r] = fabsf(x[r]) < 1.0e30f ? -x[r] : kUnset;
-          } else if (pt < NR) {
-            ms->nm[s][pt] = pt < sg.nrows ? kUnset : 0.f;
-          }
-          group_sync(2 + s, 128);
-#pragma unroll
-          for (int r0 = 0; r0 < NR; r0 += 8)
-            if (r0 < sg.nrows)
-#pragma unroll
-              for (int k = 0; k < 8; ++k) x[r0 + k] += ms->nm[s][r0 + k];
-        }
-        if (mask)
-#pragma unroll
-          for (int r = 0; r < NR; ++r)
-            if (r < r_lo || r >= r_hi) x[r] = -INFINITY;
+        // The logarithms to base 2 of the rows' exponentials (e4m3: times 2^e of the
+        // value's exponent e), back to S, and whether one passes its reference by too
+        // much.  Eights of rows that the item does not have are left out throughout.
         float top = -INFINITY;
+#pragma unroll 1
+        for (int r0 = r_first; r0 < sg.nrows; r0 += kStep) {
+          uint32_t u[8];
+          float y[8];
+          tmem_ld_32x32b_x8(t_s + r0, u);
+          if constexpr (E4M3) {
+            uint32_t v[8];
+            tmem_ld_32x32b_x8(t_s + NR + r0, v);
+            tmem_wait_ld_regs(u, v);
 #pragma unroll
-        for (int r = 0; r < NR; r += 2) top = max3(top, x[r], x[r + 1]);
-        bool prior = i < 2;  // the products before this tile's are done
-        if (group_any(2 + s, 128, top > kLimit || (E4M3 && i == s))) {
-          // references move to the tile's maxima
-          if (!prior) {
-            wait_bar(b_o + 8 * s, ph_o, s_abort, status);
-            __syncwarp();
-            ph_o ^= 1;
-            tc_fence_after();
-            prior = true;
+            for (int k = 0; k < 8; k += 2) {
+              const float2 a = *reinterpret_cast<const float2*>(row_scale + r0 + k);
+              const unsigned long long x =
+                  fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
+                       pack2(0.0625f, 0.0625f),
+                       pack2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])));
+              unpack2(fma2(mul2(x, pack2(a.x, a.y)), pack2(ck, ck), pack2(ev, ev)), y[k], y[k + 1]);
+            }
+          } else {
+            tmem_wait_ld_regs(u);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(u[k]) * c2;
           }
-          if (i > s || !group_any(2 + s, 128, top > 1.0e30f)) {
-            // from the scores against the present ones
+          if (mask)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (r0 + k < r_lo || r0 + k >= r_hi) y[k] = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            top = max3(top, y[k] + nm[r0 + k], y[k + 1] + nm[r0 + k + 1]);
+            u[k] = __float_as_uint(y[k]);
+            u[k + 1] = __float_as_uint(y[k + 1]);
+          }
+          tmem_st_32x32b_x8(t_s + r0, u);
+        }
+        tmem_wait_st();
+        const bool moves = group_any(wg, 128, top > kLimit);
+        if (i >= 2) {  // the products before this tile's are done
+          wait_bar(b_o + 8 * s, ph_o, s_abort, status);
+          __syncwarp();
+          ph_o ^= 1;
+          tc_fence_after();
+        }
+        if (moves) {
+          // references move to the tile's maxima
+#pragma unroll 1
+          for (int r0 = r_first; r0 < sg.nrows; r0 += kStep) {
+            uint32_t u[8];
+            tmem_ld_32x32b_x8(t_s + r0, u);
+            tmem_wait_ld_regs(u);
             int best = 0;
 #pragma unroll
-            for (int r0 = 0; r0 < NR; r0 += 8)
-              if (r0 < sg.nrows)
-#pragma unroll
-                for (int r = r0; r < r0 + 8; ++r) {
-                  // integers in the order of the floats
-                  const int b = __float_as_int(x[r]);
-                  const int m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
-                  if (lane == r) best = m;
-                }
-            if (lane < NR)
-              ms->wm[s][warp & 3][lane] = __int_as_float(best ^ ((best >> 31) & 0x7fffffff));
-            group_sync(2 + s, 128);
-            if (pt < NR) {
-              const float m = max3(fmaxf(ms->wm[s][0][pt], ms->wm[s][1][pt]), ms->wm[s][2][pt],
-                                   ms->wm[s][3][pt]);
-              const float d = m > (i == s ? 0.f : kLimit / 2) ? m : 0.f;
-              ms->nm[s][pt] -= d;
-              ms->d[s][pt] = d;
-              ms->f[s][pt] = ex2_approx(-d);
+            for (int k = 0; k < 8; ++k) {
+              // integers in the order of the floats
+              const int b = (int)u[k];
+              const int m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+              if (lane == k) best = m;
             }
-            group_sync(2 + s, 128);
-#pragma unroll
-            for (int r = 0; r < NR; ++r) x[r] -= ms->d[s][r];
-          } else {
-            // rows without a reference yet: the maxima of the scores themselves
-#pragma unroll 1
-            for (int r0 = 0; r0 < NR; r0 += kB) {
-              float y[kB];
-              load_scores<kB, NR, E4M3>(t_s, r0, ms->zero, ms->a[sn & 1], c2, ck, ev, y);
-#pragma unroll
-              for (int k = 0; k < kB; ++k)
-                if (mask && (r0 + k < r_lo || r0 + k >= r_hi)) y[k] = -INFINITY;
-              const float m = reduce_rows<kB>(y, [](float a, float b) { return fmaxf(a, b); });
-              if (lane % (32 / kB) == 0) ms->wm[s][warp & 3][r0 + lane / (32 / kB)] = m;
-            }
-            group_sync(2 + s, 128);
-            if (pt < NR) {
-              const float old = -ms->nm[s][pt];
-              const float m = max3(fmaxf(ms->wm[s][0][pt], ms->wm[s][1][pt]), ms->wm[s][2][pt],
-                                   ms->wm[s][3][pt]);
-              const bool moves = m - old > kLimit;
-              if (moves) ms->nm[s][pt] = -m;
-              ms->f[s][pt] = moves ? ex2_approx(old - m) : 1.f;
-            }
-            group_sync(2 + s, 128);
-#pragma unroll
-            for (int r0 = 0; r0 < NR; r0 += kN)
-              load_scores<kN, NR, E4M3>(t_s, r0, ms->nm[s], ms->a[sn & 1], c2, ck, ev, x + r0);
-            if (mask)
-#pragma unroll
-              for (int r = 0; r < NR; ++r)
-                if (r < r_lo || r >= r_hi) x[r] = -INFINITY;
+            if (lane < 8)
+              ms->wm[s][warp & 3][r0 + lane] = __int_as_float(best ^ ((best >> 31) & 0x7fffffff));
           }
+          group_sync(wg, 128);
+          if (owner && pt < sg.nrows) {
+            const float old = -nm[pt];
+            const float m = max3(fmaxf(ms->wm[s][0][pt], ms->wm[s][1][pt]), ms->wm[s][2][pt],
+                                 ms->wm[s][3][pt]);
+            const bool moved = m - old > kLimit / 2;
+            if (moved) nm[pt] = -m;
+            f[pt] = moved ? ex2_approx(old - m) : 1.f;
+          } else if (owner) {
+            f[pt] = 1.f;
+          }
+          group_sync(wg, 128);
           if (i >= 2) {
-#pragma unroll
-            for (int r = 0; r < NR; ++r) l[r] *= ms->f[s][r];
 #pragma unroll 1
-            for (int c = 0; c < F::kParts * NR; c += kB) {
-              uint32_t o[kB];
+            for (int r0 = r_first; r0 < sg.nrows; r0 += kStep) {
+              float w[8], v[8];
               bool moved = false;  // alike in every thread
 #pragma unroll
-              for (int k = 0; k < kB; ++k) moved |= ms->f[s][c % NR + k] != 1.f;
+              for (int k = 0; k < 8; ++k) {
+                w[k] = f[r0 + k];
+                moved |= w[k] != 1.f;
+              }
               if (!moved) continue;
-              tmem_ld<kB>(t_o + c, o);
-              tmem_wait_ld_regs(o);
+              load_l(r0, v);
 #pragma unroll
-              for (int k = 0; k < kB; ++k)
-                o[k] = __float_as_uint(__uint_as_float(o[k]) * ms->f[s][c % NR + k]);
-              tmem_st<kB>(t_o + c, o);
+              for (int k = 0; k < 8; ++k) v[k] *= w[k];
+              store_l(r0, v);
+#pragma unroll 1
+              for (int q = 0; q < F::kParts; ++q) {
+                uint32_t o[8];
+                tmem_ld_32x32b_x8(t_o + q * NR + r0, o);
+                tmem_wait_ld_regs(o);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * w[k]);
+                tmem_st_32x32b_x8(t_o + q * NR + r0, o);
+              }
             }
             tmem_wait_st();
           }
         }
-        if (!prior) {
-          wait_bar(b_o + 8 * s, ph_o, s_abort, status);
-          __syncwarp();
-          ph_o ^= 1;
-        }
-        // P: the position's row of its terms, 8 packed rows at a time
+        // P: the position's row of its terms
+#pragma unroll 1
+        for (int r0 = r_first; r0 < sg.nrows; r0 += kStep) {
+          uint32_t u[8];
+          float l[8];
+          tmem_ld_32x32b_x8(t_s + r0, u);
+          load_l(r0, l);
+          tmem_wait_ld_regs(u);
 #pragma unroll
-        for (int r0 = 0; r0 < NR; r0 += 8) {
-          if (r0 >= sg.nrows) break;  // their columns of O are not read
+          for (int k = 0; k < 8; ++k)
+            u[k] = __float_as_uint(ex2_approx(__uint_as_float(u[k]) + nm[r0 + k]));
           if constexpr (E4M3) {
             uint32_t t[4][4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float a = ex2_approx(x[r0 + 2 * k]), b = ex2_approx(x[r0 + 2 * k + 1]);
-              l[r0 + 2 * k] = fmaf(a, un, l[r0 + 2 * k]);
-              l[r0 + 2 * k + 1] = fmaf(b, un, l[r0 + 2 * k + 1]);
+              const float a = __uint_as_float(u[2 * k]), b = __uint_as_float(u[2 * k + 1]);
+              l[2 * k] = fmaf(a, un, l[2 * k]);
+              l[2 * k + 1] = fmaf(b, un, l[2 * k + 1]);
               uint32_t c[4];
               e4m3_terms(a, b, c);
 #pragma unroll
@@ -593,9 +569,9 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float a = ex2_approx(x[r0 + 2 * k]), b = ex2_approx(x[r0 + 2 * k + 1]);
-              l[r0 + 2 * k] += a;
-              l[r0 + 2 * k + 1] += b;
+              const float a = __uint_as_float(u[2 * k]), b = __uint_as_float(u[2 * k + 1]);
+              l[2 * k] += a;
+              l[2 * k + 1] += b;
               hi[k] = pack_bf16(a, b);
               lo[k] = pack_bf16(a - __uint_as_float(hi[k] << 16),
                                 b - __uint_as_float(hi[k] & 0xffff0000u));
@@ -605,9 +581,10 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
             *reinterpret_cast<uint4*>(my_p + ((((NR + r0) >> 3) ^ (pt & 7)) << 4)) =
                 make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
+          store_l(r0, l);
         }
         // values that no row sees: 0 * NaN must not reach a sum
-        if (t0 < sg.lo || t0 + kBN > sg.hi) {
+        if (r_first == 0 && (t0 < sg.lo || t0 + kBN > sg.hi)) {
           const uint32_t e = 2 * (base + i) + 1, slot = e % NS;
           wait_bar(b_full + 8 * slot, (e / NS) & 1, s_abort, status);
           if (t0 + pt < sg.lo || t0 + pt >= sg.hi) {
@@ -623,100 +600,99 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         mbar_arrive(b_p + 8 * s);
       }
       const bool has = s < sg.ntiles;
-      {
-        const float v = reduce_rows<NR>(l, [](float a, float b) { return a + b; });
-        if (lane % (32 / NR) == 0) ms->wm[s][warp & 3][lane / (32 / NR)] = v;
-      }
       if (has) {
         wait_bar(b_o + 8 * s, ph_o, s_abort, status);
         ph_o ^= 1;
       }
       __syncwarp();
       tc_fence_after();
+      tmem_wait_st();
       base += sg.ntiles;
-      soft_sync();
 
-      // lane r: the weights of row r in the two streams, and where the row goes
-      const bool both = sg.ntiles > 1;
-      float* rec = p.part + ((size_t)blockIdx.x * 2 + (sg.split == 2 ? 1 : 0)) *
-                                record_floats(32, DP);
-      float w_mine = 0.f;
-      int64_t at = 0;
-      if (lane < sg.nrows) {
-        float m[2], t[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          t[k] = (ms->wm[k][0][lane] + ms->wm[k][1][lane]) +
-                 (ms->wm[k][2][lane] + ms->wm[k][3][lane]);
-          m[k] = k == 0 || both ? -ms->nm[k][lane] : -kUnset;
-        }
-        const float M = fmaxf(m[0], m[1]);
-        const float w0 = ex2_approx(m[0] - M), w1 = both ? ex2_approx(m[1] - M) : 0.f;
-        const float L = both ? fmaf(t[0], w0, t[1] * w1) : t[0] * w0;
-        w_mine = s == 0 ? w0 : w1;
-        at = out_row(p, sg.row0, sg.h, sg.r0 + lane);
-        if (!sg.split) w_mine *= L == 0.f ? 0.f : 1.f / L;
-        if (warp == 0) {
-          if (sg.split)
-            __stcg(reinterpret_cast<float2*>(rec + 32 * DP) + lane,
-                   make_float2(M == -kUnset ? -INFINITY : M, L));
-          else if (p.lse != nullptr)
-            p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-        }
-        at *= p.c.D;
-      }
-      __syncwarp();
-      // O of this thread's value of D; each warpgroup hands the other its share of
-      // half the rows, through the other's P (no longer read)
-      float o[NR];
-#pragma unroll
-      for (int r = 0; r < NR; ++r) o[r] = 0.f;
-      if (has) {
-#pragma unroll
-        for (int r0 = 0; r0 < NR; r0 += 8) {
-          if (r0 >= sg.nrows) break;
+      // The streams' sums, then their O, a thread's value of D, through shared memory
+      // (P is no longer read)
+      float* o_s = reinterpret_cast<float*>(smem + F::kPOff + s * kHalf);
+#pragma unroll 1
+      for (int r0 = r_first; r0 < sg.nrows; r0 += kStep) {
+        float v[8];
+        load_l(r0, v);
+        const float sum = reduce_rows<8>(v, [](float a, float b) { return a + b; });
+        if (lane % 4 == 0) ms->wm[s][warp & 3][r0 + lane / 4] = sum;
+        if (has) {
           uint32_t u[F::kParts][8];
 #pragma unroll
           for (int q = 0; q < F::kParts; ++q) tmem_ld_32x32b_x8(t_o + q * NR + r0, u[q]);
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            float v = 0.f;
+            float x = 0.f;
 #pragma unroll
             for (int q = F::kParts - 1; q >= 0; --q) {
               asm volatile("" : "+r"(u[q][k]));
-              v = fmaf(v, E4M3 ? 0.0625f : 1.f, __uint_as_float(u[q][k]));
+              x = fmaf(x, E4M3 ? 0.0625f : 1.f, __uint_as_float(u[q][k]));
             }
-            o[r0 + k] = v * __shfl_sync(0xffffffffu, w_mine, r0 + k);
+            if (pt < DP) o_s[(r0 + k) * DP + pt] = x;
           }
         }
       }
-      float* give = reinterpret_cast<float*>(smem + F::kPOff + (s ^ 1) * kHalf) + pt;
-      const float* take = reinterpret_cast<const float*>(smem + F::kPOff + s * kHalf) + pt;
-      if (pt < DP) {
+      group_sync(1, F::kSoft);
+      const bool both = sg.ntiles > 1;
+      const float* o0 = reinterpret_cast<const float*>(smem + F::kPOff);
+      float* rec = p.part + ((size_t)blockIdx.x * 2 + (sg.split == 2 ? 1 : 0)) *
+                                record_floats(32, DP);
+#pragma unroll 1
+      for (int task = tid; task < sg.nrows * (DP / 8); task += F::kSoft) {
+        const int r = task / (DP / 8), d = task % (DP / 8) * 8;
+        float m[2], t[2];
 #pragma unroll
-        for (int r = 0; r < NR / 2; ++r) give[r * DP] = s == 0 ? o[NR / 2 + r] : o[r];
-      }
-      soft_sync();
+        for (int k = 0; k < 2; ++k) {
+          t[k] = (ms->wm[k][0][r] + ms->wm[k][1][r]) + (ms->wm[k][2][r] + ms->wm[k][3][r]);
+          m[k] = k == 0 || both ? -ms->nm[k][r] : -kUnset;
+        }
+        const float M = fmaxf(m[0], m[1]);
+        float w0 = ex2_approx(m[0] - M), w1 = both ? ex2_approx(m[1] - M) : 0.f;
+        const float L = both ? fmaf(t[0], w0, t[1] * w1) : t[0] * w0;
+        if (!sg.split) {
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          w0 *= inv;
+          w1 *= inv;
+        }
+        float v[8];
 #pragma unroll
-      for (int k = 0; k < NR / 2; ++k) {
-        const int r = s * (NR / 2) + k;
-        const int64_t to = __shfl_sync(0xffffffffu, at, r);
-        if (r < sg.nrows && pt < DP) {
-          const float v = (s == 0 ? o[k] : o[NR / 2 + k]) + take[k * DP];
-          if (sg.split)
-            __stcg(rec + r * DP + pt, v);
-          else if (pt < p.c.D)
-            p.out[to + pt] = __float2bfloat16(v);
+        for (int k = 0; k < 8; k += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(o0 + r * DP + d + k);
+          v[k] = a.x * w0, v[k + 1] = a.y * w0, v[k + 2] = a.z * w0, v[k + 3] = a.w * w0;
+          if (both) {
+            const float4 b = *reinterpret_cast<const float4*>(o0 + kHalf / 4 + r * DP + d + k);
+            v[k] = fmaf(b.x, w1, v[k]);
+            v[k + 1] = fmaf(b.y, w1, v[k + 1]);
+            v[k + 2] = fmaf(b.z, w1, v[k + 2]);
+            v[k + 3] = fmaf(b.w, w1, v[k + 3]);
+          }
+        }
+        if (sg.split) {
+          float4* to = reinterpret_cast<float4*>(rec + r * DP + d);
+          __stcg(to, make_float4(v[0], v[1], v[2], v[3]));
+          __stcg(to + 1, make_float4(v[4], v[5], v[6], v[7]));
+          if (d == 0)
+            __stcg(reinterpret_cast<float2*>(rec + 32 * DP) + r,
+                   make_float2(M == -kUnset ? -INFINITY : M, L));
+        } else {
+          const int64_t at = out_row(p, sg.row0, sg.h, sg.r0 + r);
+          if (d < p.c.D)
+            *reinterpret_cast<uint4*>(p.out + at * p.c.D + d) =
+                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                           pack_bf16(v[6], v[7]));
+          if (d == 0 && p.lse != nullptr)
+            p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
         }
       }
       if (sg.split)
-        finish_split<DP, 32, false>(p, sg, &ms->last,
-                                    reinterpret_cast<float2*>(smem + F::kPOff));
+        finish_split<DP, 32, F::kSoft, false>(p, sg, &ms->last,
+                                              reinterpret_cast<float2*>(smem + F::kPOff));
       tc_fence_before();
     }
   } else {
-    reg_dec<120>();
     // ------------------------------------------------------------ Q
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth, qb = sn & 1;
@@ -727,10 +703,11 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
       if (sg.ntiles == 0) break;
-      // Q: 16 lanes a row, 8 values a lane; rows past the item's are zero
-      constexpr int kRowsIn = E4M3 ? NR : F::kQRows, kIters = kRowsIn < 16 ? kRowsIn / 2 : 8;
+      // Q: 16 lanes a row, 8 values a lane; what its last 8 rows hold past the item's
+      // are zeros (the columns of S beyond are not read)
+      constexpr int kIters = 4;
 #pragma unroll 1
-      for (int row0 = 0; row0 < kRowsIn; row0 += 2 * kIters) {
+      for (int row0 = 0; row0 < sg.nrows; row0 += 2 * kIters) {
         uint4 x[kIters];
 #pragma unroll
         for (int k = 0; k < kIters; ++k) {
@@ -791,7 +768,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) {
+  if (warp == F::kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, F::kTmemCols);
   }

@@ -41,6 +41,9 @@ namespace {
 using namespace attend;
 
 constexpr int kRows = 256;
+constexpr int kSoftThreads = 256;  // the two softmax warpgroups, warps 0-7
+constexpr int kWarpMma = 8;
+constexpr int kWarpTma = 9;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;  // S at 0 and 128, O at 256 and 256 + DP
 constexpr float kGrow = 8.0f;    // log2 growth of a maximum that moves the reference
@@ -246,6 +249,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
 
   if (tid == 0) {
     *s_abort = 0;
+#pragma unroll 1
     for (int i = 0; i < NS; ++i) {
       mbar_init(b_full + 8 * i, E4M3 ? 128 : 1);
       mbar_init(b_empty + 8 * i, 1);
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
       mbar_arrive(full0 + 8 * slot);
       stored += 2;
     };
-    auto issue = [&](const int (&y)[8], int mine, int none) {
+    auto issue = [&](int mine, int none) {
       if constexpr (E4M3) {
         const int row = __shfl_sync(0xffffffffu, mine, my_box);
         uint32_t now = 0x7f7f7f7fu;
@@ -312,32 +316,23 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
       const uint32_t slot = e % kRing, full = full0 + 8 * slot;
       const bool ok = wait_bar(empty0 + 8 * slot, ((e / kRing) & 1) ^ 1, s_abort, status);
       if (!__all_sync(0xffffffffu, ok)) return false;
-      if (elect_one()) {
-        if constexpr (E4M3) {
-          const uint32_t dst = smem_u32(smem + F::kRawOff) + slot * kHalf;
-          mbar_arrive_expect_tx(full, kHalf);
-#pragma unroll
-          for (int b = 0; b < 8; ++b)
-            if (b < n_boxes) tma_load_2d(dst + b * box_rows * 128, map, full, 0, y[b]);
-        } else {
-          const uint32_t dst = smem_u32(s_kv) + slot * F::kTile;
-          mbar_arrive_expect_tx(full, F::kTile);
-#pragma unroll
-          for (int b = 0; b < 8; ++b)
-            if (b < n_boxes)
-#pragma unroll
-              for (int half = 0; half < NH; ++half)
-                tma_load_2d(dst + half * kHalf + b * box_rows * 128, map, full, half * 64, y[b]);
+      uint32_t dst = E4M3 ? smem_u32(smem + F::kRawOff) + slot * kHalf
+                          : smem_u32(s_kv) + slot * F::kTile;
+      if (elect_one()) mbar_arrive_expect_tx(full, E4M3 ? kHalf : F::kTile);
+#pragma unroll 1
+      for (int b = 0; b < n_boxes; ++b, dst += box_rows * 128) {
+        const int y = __shfl_sync(0xffffffffu, mine, b);
+        if (elect_one()) {
+          tma_load_2d(dst, map, full, 0, y);
+          if (!E4M3 && NH > 1) tma_load_2d(dst + kHalf, map, full, 64, y);
         }
       }
       __syncwarp();
       e += 2;
       return true;
     };
-    if (kv == 0)
-      produce<kRows>(p, rg, ms->found, ms->seg, b_segFull, b_segEmpty, s_abort, issue, flush);
-    else
-      follow(p, ms->seg, b_segFull, b_segEmpty, s_abort, issue, flush);
+    load_all<kRows>(p, rg, kv == 0, ms->found, ms->seg, b_segFull, b_segEmpty, s_abort, issue,
+                    flush);
     if (*s_abort) {
       // the copies in flight land before the block's shared memory goes
       for (uint32_t i = e > kRing ? e - kRing : kv; i < e; ++i)
@@ -600,7 +595,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
         // the copies of a row in the streams: a common reference first
         const int parts = sg.ntiles > 1 ? 2 * rep : rep;
         s_xch[tid] = make_float2(mine, l);
-        soft_sync();
+        group_sync(1, kSoftThreads);
         const int rr = lrow % rp;
         float M = -INFINITY, L = 0.f;
 #pragma unroll
@@ -613,7 +608,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
             L = fmaf(ml.y, ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M), L);
           }
         const float w = mine == -INFINITY ? 0.f : ex2_approx(mine - M);
-        soft_sync();
+        group_sync(1, kSoftThreads);
         if (tid < rp) s_xch[tid] = make_float2(M, L);
         // then their sums through shared memory (Q is no longer read): as many
         // columns a round as 32 KB hold for the rows there are
@@ -641,7 +636,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
               __syncwarp();
             }
           }
-          soft_sync();
+          group_sync(1, kSoftThreads);
           for (int task = tid; task < brows << log_c4; task += kSoftThreads) {
             const int row = task >> log_c4, d4 = task & ((1 << log_c4) - 1);
             if (row >= sg.nrows) break;
@@ -667,7 +662,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
                   make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
             }
           }
-          soft_sync();
+          group_sync(1, kSoftThreads);
         }
         if (tid < sg.nrows) {
           if (sg.split) {
@@ -679,7 +674,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
         }
       }
       if (sg.split)
-        finish_split<DP, kRows, true>(p, sg, &ms->last, reinterpret_cast<float2*>(s_q));
+        finish_split<DP, kRows, kSoftThreads, true>(p, sg, &ms->last, reinterpret_cast<float2*>(s_q));
       tc_fence_before();
     }
   } else if (warp < 12) {
