@@ -203,8 +203,11 @@ struct Range {
   bool last;             // u1 is the end of all work
 
   __device__ __forceinline__ int block_of(int64_t u) const {
-    const int64_t wide = extra * (each + 1);
-    return u < wide ? (int)(u / (each + 1)) : extra + (int)((u - wide) / each);
+    const int64_t wide = extra * (each + 1), d = u < wide ? each + 1 : each;
+    const int64_t n = u < wide ? u : u - wide;
+    const int q = n < (1ll << 31) && d < (1ll << 31) ? (int)((uint32_t)n / (uint32_t)d)
+                                                     : (int)(n / d);
+    return u < wide ? q : extra + q;
   }
 };
 
@@ -367,15 +370,15 @@ __device__ __forceinline__ Place locate(const Params& p, const Found& f, int64_t
 }
 
 // A loading warp: the one that leads walks the block's range and queues its segments (an
-// empty one at the end); each loads the tiles of every segment.  `issue(mine, none)`
-// loads a tile: lane b's `mine` is the pool's row of box b's first position, or `none` (past the
-// pool, so that the box reads as zeros) where no row of the item sees the box; false when it
-// failed.  flush() after each segment.
+// empty one at the end); each loads the tiles of every segment.  `issue(rows, box, none)`
+// loads a tile: lane box + b's `rows` is the pool's row of the first position of its box b, or
+// `none` (past the pool, so that the box reads as zeros) where no row of the item sees
+// the box; false when it failed.  flush() after each segment.
 template <int ROWS, class Issue, class Flush>
 __device__ __forceinline__ void load_all(const Params& p, const Range& rg, bool lead,
                                          const Found* s_found, Segment* s_seg,
                                          uint32_t b_segFull, uint32_t b_segEmpty,
-                                         volatile int* s_abort, Issue& issue, Flush& flush) {
+                                         volatile int* s_abort, Issue&& issue, Flush&& flush) {
   const int lane = threadIdx.x & 31;
   const int log_page = p.c.log_page, page = 1 << log_page;
   const int box_rows = min(page, kBN), n_boxes = kBN / box_rows;
@@ -445,17 +448,22 @@ __device__ __forceinline__ void load_all(const Params& p, const Range& rg, bool 
       if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
     }
     if (sg.ntiles == 0) return;
-    int next = none;
+    // 32 boxes' rows a time, a box a lane; the next 32 in flight under the loads of these
+    auto lookup = [&](int i) {
+      const int pos = (sg.tile0 + i) * kBN + lane * box_rows;
+      if (i + lane / n_boxes >= sg.ntiles || pos >= sg.hi || pos + box_rows <= sg.lo) return none;
+      const int64_t id = page_of(p.c, sg.n, pos);
+      return id < 0 ? none : (int)((id * p.c.Hkv + sg.h) << log_page) + (pos & (page - 1));
+    };
+    int rows = lookup(0), next = none;
 #pragma unroll 1
-    for (int i = -1; i < sg.ntiles; ++i) {
-      const int mine = next;
-      next = none;  // lane b: box b of the next tile, in flight under the waits
-      const int pos = (sg.tile0 + i + 1) * kBN + lane * box_rows;
-      if (i + 1 < sg.ntiles && lane < n_boxes && pos < sg.hi && pos + box_rows > sg.lo) {
-        const int64_t id = page_of(p.c, sg.n, pos);
-        if (id >= 0) next = (int)((id * p.c.Hkv + sg.h) << log_page) + (pos & (page - 1));
+    for (int i = 0, box = 0; i < sg.ntiles; ++i, box += n_boxes) {
+      if (box == 32) {
+        rows = next;
+        box = 0;
       }
-      if (i >= 0 && !issue(mine, none)) return;
+      if (box == 0 && i + 32 / n_boxes < sg.ntiles) next = lookup(i + 32 / n_boxes);
+      if (!issue(rows, box, none)) return;
     }
     flush();
   }

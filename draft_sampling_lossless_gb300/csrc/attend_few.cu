@@ -153,41 +153,30 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   uint32_t* status = p.c.status;
   if (smem_u32(smem) & 1023) return;  // never: the declared alignment, which the swizzle needs
 
-  if (tid == 0) {
-    *s_abort = 0;
-#pragma unroll 1
-    for (int i = 0; i < 2 * NS; ++i) mbar_init(b_full + 8 * i, 1);
-#pragma unroll 1
-    for (int i = 0; i < kSegDepth; ++i) {
-      mbar_init(b_segFull + 8 * i, 1);
-      mbar_init(b_segEmpty + 8 * i, 3 + F::kSoft / 32);  // the MMA thread and the other warps
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(b_qFull + 8 * i, 32);
-      mbar_init(b_qEmpty + 8 * i, 1);
-      mbar_init(b_s + 8 * i, 1);
-      mbar_init(b_s + 16 + 8 * i, 1);
-      mbar_init(b_p + 8 * i, F::kSoft / 2);
-      mbar_init(b_o + 8 * i, 1);
-    }
-#pragma unroll 1
-    for (int i = 0; i < kExpDepth; ++i) {
-      mbar_init(b_expFull + 8 * i, 64);
-      mbar_init(b_expEmpty + 8 * i, F::kSoft / 64);  // the warps of the tile's stream
-    }
-    mbar_init(b_drain, 1);
-    fence_mbar_init();
-  }
-  const Range rg = plan<32, F::kThreads>(p, ms->sum, ms->found);
-  if (rg.u0 >= rg.u1) return;  // no tiles for this block
+  // a barrier a thread: its address is that of its place, its count its role's
   if (warp == F::kWarpMma) {
+    for (uint32_t bar = b_full + 8 * lane; bar <= b_drain; bar += 8 * 32) {
+      uint32_t n = 1;
+      if (bar >= b_segEmpty && bar < b_qFull) n = 3 + F::kSoft / 32;  // the MMA thread, other warps
+      else if (bar >= b_qFull && bar < b_qEmpty) n = 32;
+      else if (bar >= b_p && bar < b_o) n = F::kSoft / 2;
+      else if (bar >= b_expFull && bar < b_expEmpty) n = 32;
+      else if (bar >= b_expEmpty && bar < b_drain) n = F::kSoft / 64;  // its stream's warps
+      mbar_init(bar, n);
+    }
+    if (lane == 0) *s_abort = 0;
+    fence_mbar_init();
     tmem_alloc(smem_u32(&ms->tmem), F::kTmemCols);
     tmem_relinquish();
+    tc_fence_before();
   }
-  tc_fence_before();
-  __syncthreads();
+  const Range rg = plan<32, F::kThreads>(p, ms->sum, ms->found);
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
+  if (rg.u0 >= rg.u1) {  // no tiles for this block
+    if (warp == F::kWarpMma) tmem_dealloc(tmem, F::kTmemCols);
+    return;
+  }
 
   if (warp == F::kWarpTma || warp == F::kWarpTma + 1) {
     // ------------------------------------------------------------ loads
@@ -196,47 +185,30 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     const int box_rows = min(1 << p.c.log_page, kBN), n_boxes = kBN / box_rows;
     if (lane == 0) tma_prefetch(map);
     uint32_t e = kv;  // ring entries: K and V of each tile in turn
-    // e4m3: four positions' exponent bytes a lane, stored one tile after their load
-    const uint8_t* exps = kv ? p.c.v_exp : p.c.k_exp;
-    const int my_box = lane * 4 / box_rows, my_at = lane * 4 % box_rows;
-    uint32_t held = 0;
-    uint32_t stored = 0;  // tiles whose bytes are stored
-    auto flush = [&]() {
-      if (!E4M3 || stored >= e / 2) return;
-      const uint32_t q = stored % kExpDepth;
-      wait_bar(b_expEmpty + 8 * q, ((stored / kExpDepth) & 1) ^ 1, s_abort, status);
-      reinterpret_cast<uint32_t*>(smem + F::kExpOff + q * 256 + kv * 128)[lane] = held;
-      mbar_arrive(b_expFull + 8 * q);
-      ++stored;
-    };
-    auto issue = [&](int mine, int none) {
-      if constexpr (E4M3) {
-        // a box that reads as zeros: any scale does, but not one that moves the references
-        const int row = __shfl_sync(0xffffffffu, mine, my_box);
-        uint32_t now = 0x7f7f7f7fu;
-        if (row != none)
-          now = __ldg(reinterpret_cast<const uint32_t*>(exps + row + my_at));
-        flush();
-        held = now;
-      }
+    auto issue = [&](int rows, int box, int) {
       const uint32_t slot = e % NS, full = b_full + 8 * slot;
       const bool ok = wait_bar(b_empty + 8 * slot, ((e / NS) & 1) ^ 1, s_abort, status);
       if (!__all_sync(0xffffffffu, ok)) return false;
-      if (elect_one()) mbar_arrive_expect_tx(full, F::kSlot);
       uint32_t dst = smem_u32(smem) + slot * F::kSlot;
-#pragma unroll 1
-      for (int b = 0; b < n_boxes; ++b, dst += box_rows * 128) {
-        const int y = __shfl_sync(0xffffffffu, mine, b);
-        if (elect_one()) {
-          tma_load_2d(dst, map, full, 0, y);
-          if (!E4M3 && NH > 1) tma_load_2d(dst + kHalf, map, full, 64, y);
+      int y[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) y[b] = __shfl_sync(0xffffffffu, rows, box + b);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(full, F::kSlot);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          if (b >= n_boxes) break;
+          tma_load_2d(dst, map, full, 0, y[b]);
+          if (!E4M3 && NH > 1) tma_load_2d(dst + kHalf, map, full, 64, y[b]);
+          dst += box_rows * 128;
         }
       }
       __syncwarp();
       e += 2;
       return true;
     };
-    load_all<32>(p, rg, kv == 0, ms->found, ms->seg, b_segFull, b_segEmpty, s_abort, issue, flush);
+    load_all<32>(p, rg, kv == 0, ms->found, ms->seg, b_segFull, b_segEmpty, s_abort, issue,
+                 [] {});
     if (*s_abort) {
       // the copies in flight land before the block's shared memory goes
       for (uint32_t i = e > NS ? e - NS : kv; i < e; ++i)
@@ -693,7 +665,9 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       tc_fence_before();
     }
   } else {
-    // ------------------------------------------------------------ Q
+    // ------------------------------------------------------------ Q, e4m3's scales
+    uint32_t base = 0;  // tiles of the segments before
+#pragma unroll 1
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth, qb = sn & 1;
       const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status) &&
@@ -764,6 +738,36 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       }
       fence_proxy_async_smem();
       mbar_arrive(b_qFull + 8 * qb);
+      if constexpr (!E4M3) continue;
+      // the exponent bytes of K and V, four positions a lane, four tiles a time
+      const int page_mask = (1 << p.c.log_page) - 1;
+#pragma unroll 1
+      for (int i0 = 0; i0 < sg.ntiles; i0 += 4) {
+        uint32_t x[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int pos = (sg.tile0 + i0 + k) * kBN + lane * 4;
+          // where no row looks, any scale does, but not one that moves the references
+          x[k][0] = x[k][1] = 0x7f7f7f7fu;
+          if (pos >= sg.hi || pos + 4 <= sg.lo || i0 + k >= sg.ntiles) continue;
+          const int64_t id = page_of(p.c, sg.n, pos);
+          if (id < 0) continue;
+          const int64_t at = ((id * p.c.Hkv + sg.h) << p.c.log_page) + (pos & page_mask);
+          x[k][0] = __ldg(reinterpret_cast<const uint32_t*>(p.c.k_exp + at));
+          x[k][1] = __ldg(reinterpret_cast<const uint32_t*>(p.c.v_exp + at));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (i0 + k >= sg.ntiles) break;
+          const uint32_t tile = base + i0 + k, q = tile % kExpDepth;
+          wait_bar(b_expEmpty + 8 * q, ((tile / kExpDepth) & 1) ^ 1, s_abort, status);
+          uint32_t* to = reinterpret_cast<uint32_t*>(smem + F::kExpOff + q * 256) + lane;
+          to[0] = x[k][0];
+          to[32] = x[k][1];
+          mbar_arrive(b_expFull + 8 * q);
+        }
+      }
+      base += sg.ntiles;
     }
   }
   tc_fence_before();

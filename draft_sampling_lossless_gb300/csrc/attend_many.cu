@@ -282,10 +282,10 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
 
-  // bf16: 384 threads of 168 registers become 256 x 216 and 128 x 72;
-  // e4m3: 512 of 128 become 256 x 176, 128 x 72 and 128 x 88
+  // bf16: 384 threads of 168 registers become 256 x 208 and 128 x 88;
+  // e4m3: 512 of 128 become 256 x 168 and 256 x 88
   if (warp == kWarpTma || warp == kWarpTma + 1) {
-    reg_dec<72>();
+    reg_dec<88>();
     // ------------------------------------------------------------ loads
     const int kv = warp - kWarpTma;  // warp 9 K, warp 10 V
     const CUtensorMap* map = kv ? &tm_v : &tm_k;
@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
       mbar_arrive(full0 + 8 * slot);
       stored += 2;
     };
-    auto issue = [&](int mine, int none) {
+    auto issue = [&](int rows, int box, int none) {
       if constexpr (E4M3) {
-        const int row = __shfl_sync(0xffffffffu, mine, my_box);
+        const int row = __shfl_sync(0xffffffffu, rows, box + my_box);
         uint32_t now = 0x7f7f7f7fu;
         if (row != none) now = __ldg(reinterpret_cast<const uint32_t*>(exps + row + my_at));
         flush();
@@ -318,13 +318,17 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) return false;
       uint32_t dst = E4M3 ? smem_u32(smem + F::kRawOff) + slot * kHalf
                           : smem_u32(s_kv) + slot * F::kTile;
-      if (elect_one()) mbar_arrive_expect_tx(full, E4M3 ? kHalf : F::kTile);
-#pragma unroll 1
-      for (int b = 0; b < n_boxes; ++b, dst += box_rows * 128) {
-        const int y = __shfl_sync(0xffffffffu, mine, b);
-        if (elect_one()) {
-          tma_load_2d(dst, map, full, 0, y);
-          if (!E4M3 && NH > 1) tma_load_2d(dst + kHalf, map, full, 64, y);
+      int y[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) y[b] = __shfl_sync(0xffffffffu, rows, box + b);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(full, E4M3 ? kHalf : F::kTile);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          if (b >= n_boxes) break;
+          tma_load_2d(dst, map, full, 0, y[b]);
+          if (!E4M3 && NH > 1) tma_load_2d(dst + kHalf, map, full, 64, y[b]);
+          dst += box_rows * 128;
         }
       }
       __syncwarp();
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
         if ((i & 1) == kv) mbar_wait(full0 + 8 * (i % kRing), (i / kRing) & 1);
     }
   } else if (warp == kWarpMma) {
-    reg_dec<72>();
+    reg_dec<88>();
     // ------------------------------------------------------------ products
     if (elect_one()) {
       constexpr uint32_t kIdS = idesc_bf16_f32(128, kBN);
@@ -452,8 +456,8 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp < 8) {
-    if (E4M3) reg_inc<176>();
-    else reg_inc<216>();
+    if (E4M3) reg_inc<168>();
+    else reg_inc<208>();
     // ------------------------------------------------------------ softmax
     const int s = warp >> 2;  // the stream
     const int lrow = tid & 127;
@@ -678,7 +682,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
       tc_fence_before();
     }
   } else if (warp < 12) {
-    reg_dec<72>();  // completes the warpgroup
+    reg_dec<88>();  // completes the warpgroup
   } else if (E4M3) {
     reg_dec<88>();
     // ------------------------------------------------------------ codes to bf16
