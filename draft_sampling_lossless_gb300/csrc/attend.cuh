@@ -135,17 +135,15 @@ struct Segment {  // part of an item that this block computes
 static_assert(sizeof(Segment) == 64, "a segment's words");
 
 // Waits for a phase; gives up when another role has, or after kWaitTries tries (each
-// suspended for a while by the hardware).  Short: it is inlined in every role's loop,
-// and the loops of a block's roles share the instruction caches.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                         uint32_t* status) {
+// suspended for a while by the hardware), and tells the others; the block reports
+// that at its end.  Short: it is inlined in every role's loop, and the loops of a
+// block's roles share the instruction caches.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   int tries = kWaitTries;
 #pragma unroll 1
   while (!mbar_try_wait(bar, parity)) {
-    if (*abort_flag) return false;
-    if (--tries == 0) {
+    if (--tries == 0 || *abort_flag) {
       *abort_flag = 1;
-      set_flag(status, kFlagWaitTimeout);
       return false;
     }
   }
@@ -400,7 +398,7 @@ __device__ __forceinline__ void load_all(const Params& p, const Range& rg, bool 
     const int ss = sn % kSegDepth;
     const uint32_t parity = (sn / kSegDepth) & 1;
     const bool ok = wait_bar((lead ? b_segEmpty : b_segFull) + 8 * ss, lead ? parity ^ 1 : parity,
-                             s_abort, p.c.status);
+                             s_abort);
     if (!__all_sync(0xffffffffu, ok)) return;
     Segment sg;
     if (lead) {

@@ -48,11 +48,12 @@ struct Few {
   // Softmax threads a position: rows of e4m3 terms want more warps for their longer
   // chains of conversions
   static constexpr int kSplit = E4M3 && NR > 16 ? 2 : 1;
-  static constexpr int kSoft = 256 * kSplit;   // softmax threads; then four warps
-  static constexpr int kWarpMma = kSoft / 32, kWarpTma = kWarpMma + 1;
-  static constexpr int kThreads = kSoft + 128;
+  static constexpr int kSoft = 256 * kSplit;   // softmax threads; then five warps
+  static constexpr int kWarpS = kSoft / 32, kWarpTma = kWarpS + 1, kWarpO = kWarpS + 4;
+  static constexpr int kThreads = kSoft + 160;
   static constexpr int kNH = DP / 64;
   static constexpr int kParts = E4M3 ? 4 : 2;                         // terms of P
+  static constexpr int kPN = (kParts * NR + 15) / 16 * 16;            // N of the products
   static constexpr int kQRows = E4M3 ? 2 * NR : (NR < 16 ? 16 : NR);  // N of the scores
   // tiles of scores ahead: e4m3 tiles come twice as fast, and one's softmax is longer
   static constexpr int kSBufs = E4M3 ? 4 : 2;
@@ -70,10 +71,7 @@ struct Few {
   static constexpr int kFit =
       (int)((kMaxSmem - 2 * kHalf - 2 * kQBytes - kExp - kL - kMisc) / kSlot);
   static constexpr int kSlots = kFit > 12 ? 12 : kFit;
-  // K and V go through one ring by two warps.  A slot that they use in turn (an odd
-  // ring) is safe while a tile's scores are at most (slots - 1) / 2 tiles ahead of its
-  // products: no warp then waits for a phase two ahead of the slot's.
-  static_assert(kSlots % 2 == 0 || kSlots >= 2 * kSBufs + 1, "ring");
+  static constexpr int kSlotsK = kSlots / 2, kSlotsV = kSlots - kSlotsK;
   // P of each stream (at an item's end its O, then the join's buffer)
   static constexpr uint32_t kPOff = kSlots * kSlot;
   static constexpr uint32_t kQOff = kPOff + 2 * kHalf;
@@ -92,7 +90,7 @@ struct Misc {  // shared words
   int64_t sum[32];
   Found found[2];
   Segment seg[kSegDepth];
-  uint64_t bars[2 * 12 + 2 * kSegDepth + 4 + 8 + 2 * kExpDepth + 1];
+  uint64_t bars[2 * 12 + 2 * kSegDepth + 4 + 4 + 8 + 2 * kExpDepth + 2];
   int abort_flag, last;
   uint32_t tmem;
 };
@@ -136,7 +134,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     attend_few_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
   using F = Few<DP, NR, E4M3>;
-  constexpr int NS = F::kSlots, NH = F::kNH, SB = F::kSBufs;
+  constexpr int NS = F::kSlots, NK = F::kSlotsK, NV = F::kSlotsV, NH = F::kNH, SB = F::kSBufs;
   // P's largest exponent (e4m3 ends at 448); rows above half of it move along with one
   // that passed it
   constexpr float kLimit = E4M3 ? 8.f : 64.f;
@@ -145,23 +143,23 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   const uint32_t b_full = smem_u32(ms->bars), b_empty = b_full + 8 * NS;
   const uint32_t b_segFull = b_empty + 8 * NS, b_segEmpty = b_segFull + 8 * kSegDepth;
   const uint32_t b_qFull = b_segEmpty + 8 * kSegDepth, b_qEmpty = b_qFull + 16;
-  const uint32_t b_s = b_qEmpty + 16, b_p = b_s + 32, b_o = b_p + 16;
+  const uint32_t b_s = b_qEmpty + 16, b_sFree = b_s + 32, b_p = b_sFree + 32, b_o = b_p + 16;
   const uint32_t b_expFull = b_o + 16, b_expEmpty = b_expFull + 8 * kExpDepth;
   const uint32_t b_drain = b_expEmpty + 8 * kExpDepth;
   volatile int* s_abort = &ms->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t* status = p.c.status;
   if (smem_u32(smem) & 1023) return;  // never: the declared alignment, which the swizzle needs
 
   // a barrier a thread: its address is that of its place, its count its role's
-  if (warp == F::kWarpMma) {
-    for (uint32_t bar = b_full + 8 * lane; bar <= b_drain; bar += 8 * 32) {
+  if (warp == F::kWarpS) {
+    for (uint32_t bar = b_full + 8 * lane; bar <= b_drain + 8; bar += 8 * 32) {
       uint32_t n = 1;
-      if (bar >= b_segEmpty && bar < b_qFull) n = 3 + F::kSoft / 32;  // the MMA thread, other warps
+      if (bar >= b_segEmpty && bar < b_qFull) n = 4 + F::kSoft / 32;  // all but the warp that fills
       else if (bar >= b_qFull && bar < b_qEmpty) n = 32;
-      else if (bar >= b_p && bar < b_o) n = F::kSoft / 2;
+      else if (E4M3 && bar >= b_qEmpty && bar < b_s) n = 1 + F::kSoft / 32;  // a's readers
+      else if (bar >= b_sFree && bar < b_o) n = F::kSoft / 64;  // a stream's warps
       else if (bar >= b_expFull && bar < b_expEmpty) n = 32;
-      else if (bar >= b_expEmpty && bar < b_drain) n = F::kSoft / 64;  // its stream's warps
+      else if (bar >= b_expEmpty && bar < b_drain) n = F::kSoft / 64;
       mbar_init(bar, n);
     }
     if (lane == 0) *s_abort = 0;
@@ -174,7 +172,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
   if (rg.u0 >= rg.u1) {  // no tiles for this block
-    if (warp == F::kWarpMma) tmem_dealloc(tmem, F::kTmemCols);
+    if (warp == F::kWarpS) tmem_dealloc(tmem, F::kTmemCols);
     return;
   }
 
@@ -184,10 +182,11 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     const CUtensorMap* map = kv ? &tm_v : &tm_k;
     const int box_rows = min(1 << p.c.log_page, kBN), n_boxes = kBN / box_rows;
     if (lane == 0) tma_prefetch(map);
-    uint32_t e = kv;  // ring entries: K and V of each tile in turn
+    const int slots = kv ? NV : NK, slot0 = kv ? NK : 0;  // its ring
+    uint32_t at = 0, tiles = 0, parity = 1;
     auto issue = [&](int rows, int box, int) {
-      const uint32_t slot = e % NS, full = b_full + 8 * slot;
-      const bool ok = wait_bar(b_empty + 8 * slot, ((e / NS) & 1) ^ 1, s_abort, status);
+      const uint32_t slot = slot0 + at, full = b_full + 8 * slot;
+      const bool ok = wait_bar(b_empty + 8 * slot, parity, s_abort);
       if (!__all_sync(0xffffffffu, ok)) return false;
       uint32_t dst = smem_u32(smem) + slot * F::kSlot;
       int y[8];
@@ -204,96 +203,125 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         }
       }
       __syncwarp();
-      e += 2;
+      ++tiles;
+      if (++at == slots) {
+        at = 0;
+        parity ^= 1;
+      }
       return true;
     };
     load_all<32>(p, rg, kv == 0, ms->found, ms->seg, b_segFull, b_segEmpty, s_abort, issue,
                  [] {});
     if (*s_abort) {
       // the copies in flight land before the block's shared memory goes
-      for (uint32_t i = e > NS ? e - NS : kv; i < e; ++i)
-        if ((i & 1) == kv) mbar_wait(b_full + 8 * (i % NS), (i / NS) & 1);
+      for (uint32_t i = tiles > slots ? tiles - slots : 0; i < tiles; ++i)
+        mbar_wait(b_full + 8 * (slot0 + i % slots), (i / slots) & 1);
     }
-  } else if (warp == F::kWarpMma) {
-    // ------------------------------------------------------------ products
+  } else if (warp == F::kWarpS) {
+    // ------------------------------------------------------------ scores
     if (elect_one()) {
       constexpr uint32_t kIdS = E4M3 ? idesc_0_f32(128, F::kQRows) : idesc_bf16_f32(128, F::kQRows);
-      constexpr uint32_t kIdO = (E4M3 ? idesc_0_f32(128, F::kParts * NR)
-                                      : idesc_bf16_f32(128, F::kParts * NR)) |
-                                kIdescTransposeA | kIdescTransposeB;
       const int ksteps = E4M3 ? (p.c.D + 31) / 32 : p.c.D / 16;
-      const uint32_t at0 = smem_u32(smem);
-      uint32_t base = 0, ph_p = 0;  // base: tiles of the segments before
+      const uint64_t k0 = desc_kmajor_sw128(smem_u32(smem));
+      const uint64_t q0 = desc_kmajor_sw128(smem_u32(smem) + F::kQOff);
+      uint32_t t = 0, at = 0, parity = 0;  // tiles so far, the ring's slot
       bool ok = true;
-      auto need = [&](uint32_t e) {
-        ok = ok && wait_bar(b_full + 8 * (e % NS), (e / NS) & 1, s_abort, status);
-        tc_fence_after();
-      };
-      auto scores = [&](int sb, uint32_t e, int qb) {
-        const uint64_t a = desc_kmajor_sw128(at0 + (e % NS) * F::kSlot);
-        const uint64_t b = desc_kmajor_sw128(at0 + F::kQOff + qb * F::kQBytes);
 #pragma unroll 1
-        for (int k = 0; k < ksteps; ++k) {
-          if constexpr (E4M3)
-            mma_e4m3(tmem + sb * 64, a + k * 2, b + k * 2, kIdS, k > 0);
-          else
-            mma_bf16(tmem + sb * 64, a + (k >> 2) * (kHalf >> 4) + (k & 3) * 2,
-                     b + (k >> 2) * (F::kQHalf >> 4) + (k & 3) * 2, kIdS, k > 0);
-        }
-        mma_commit(b_s + 8 * sb);
-        mma_commit(b_empty + 8 * (e % NS));
-      };
       for (int sn = 0; ok; ++sn) {
-        const int ss = sn % kSegDepth;
-        ok = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status);
+        const int ss = sn % kSegDepth, qb = sn & 1;
+        ok = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort);
         if (!ok) break;
         const int nt = ms->seg[ss].ntiles;
         mbar_arrive(b_segEmpty + 8 * ss);
         if (nt == 0) break;
-        const int qb = sn & 1;
-        ok = wait_bar(b_qFull + 8 * qb, (sn >> 1) & 1, s_abort, status);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t e0 = 2 * base;  // K of tile i: e0 + 2 i, V: one more
+        ok = wait_bar(b_qFull + 8 * qb, (sn >> 1) & 1, s_abort);
 #pragma unroll 1
-        for (int i = 0; i < SB && i < nt && ok; ++i) {
-          need(e0 + 2 * i);
-          if (ok) scores(i, e0 + 2 * i, qb);
-        }
-        for (int i = 0; i < nt && ok; ++i) {
-          const int s = i & 1;
-          const uint32_t ev = e0 + 2 * i + 1;
-          need(ev);
-          ok = ok && wait_bar(b_p + 8 * s, (ph_p >> s) & 1, s_abort, status);
-          ph_p ^= 1u << s;
+        for (int i = 0; i < nt && ok; ++i, ++t) {
+          const uint32_t sb = t % SB;
+          ok = wait_bar(b_sFree + 8 * sb, ((t / SB) & 1) ^ 1, s_abort) &&
+               wait_bar(b_full + 8 * at, parity, s_abort);
           if (!ok) break;
           tc_fence_after();
-          // D = 64: both groups of 64 MMA rows read the same values
-          const uint64_t a = desc_mnmajor_sw128(at0 + (ev % NS) * F::kSlot, NH > 1 ? kHalf : 0);
-          const uint64_t b = desc_mnmajor_sw128(at0 + F::kPOff + s * kHalf, 0);
-          const uint32_t o = tmem + F::kColO + s * F::kOCols;
-          if constexpr (E4M3) {
-#pragma unroll 1
-            for (int k = 0; k < kBN / 32; ++k)
-              mma_e4m3(o, a + k * (4096 >> 4), b + k * (4096 >> 4), kIdO, i >= 2 || k > 0);
-          } else {
-#pragma unroll 1
-            for (int k = 0; k < kBN / 16; ++k)
-              mma_bf16(o, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdO, i >= 2 || k > 0);
+          uint64_t a = k0 + at * (F::kSlot >> 4), b = q0 + qb * (F::kQBytes >> 4);
+#pragma unroll 2
+          for (int k = 0; k < ksteps; ++k) {
+            if constexpr (E4M3) {
+              mma_e4m3(tmem + sb * 64, a, b, kIdS, k > 0);
+            } else {
+              mma_bf16(tmem + sb * 64, a, b, kIdS, k > 0);
+            }
+            a += 2;
+            b += 2;
+            if (!E4M3 && k == 3) {
+              a += (kHalf >> 4) - 8;
+              b += (F::kQHalf >> 4) - 8;
+            }
           }
-          mma_commit(b_empty + 8 * (ev % NS));
-          mma_commit(b_o + 8 * s);
-          if (i + SB < nt) {
-            need(ev + 2 * SB - 1);
-            if (ok) scores(i % SB, ev + 2 * SB - 1, qb);
+          mma_commit(b_s + 8 * sb);
+          mma_commit(b_empty + 8 * at);
+          if (++at == NK) {
+            at = 0;
+            parity ^= 1;
           }
         }
-        mma_commit(b_qEmpty + 8 * qb);
-        base += nt;
+        if (ok) mma_commit(b_qEmpty + 8 * qb);
       }
       if (!ok) {
         mma_commit(b_drain);
         mbar_wait(b_drain, 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp == F::kWarpO) {
+    // ------------------------------------------------------------ outputs
+    if (elect_one()) {
+      constexpr uint32_t kIdO =
+          (E4M3 ? idesc_0_f32(128, F::kPN) : idesc_bf16_f32(128, F::kPN)) | kIdescTransposeA |
+          kIdescTransposeB;
+      // D = 64: both groups of 64 MMA rows read the same values
+      const uint64_t v0 = desc_mnmajor_sw128(smem_u32(smem) + NK * F::kSlot, NH > 1 ? kHalf : 0);
+      const uint64_t p0 = desc_mnmajor_sw128(smem_u32(smem) + F::kPOff, 0);
+      uint32_t at = 0, parity = 0, ph_p = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int sn = 0; ok; ++sn) {
+        const int ss = sn % kSegDepth;
+        ok = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort);
+        if (!ok) break;
+        const int nt = ms->seg[ss].ntiles;
+        mbar_arrive(b_segEmpty + 8 * ss);
+        if (nt == 0) break;
+#pragma unroll 1
+        for (int i = 0; i < nt; ++i) {
+          const int s = i & 1;
+          ok = wait_bar(b_full + 8 * (NK + at), parity, s_abort) &&
+               wait_bar(b_p + 8 * s, (ph_p >> s) & 1, s_abort);
+          if (!ok) break;
+          ph_p ^= 1u << s;
+          tc_fence_after();
+          uint64_t a = v0 + at * (F::kSlot >> 4), b = p0 + s * (kHalf >> 4);
+          const uint32_t o = tmem + F::kColO + s * F::kOCols;
+          constexpr int kSteps = kBN / (E4M3 ? 32 : 16);  // of 4096 or 2048 bytes
+#pragma unroll 2
+          for (int k = 0; k < kSteps; ++k) {
+            if constexpr (E4M3)
+              mma_e4m3(o, a, b, kIdO, i >= 2 || k > 0);
+            else
+              mma_bf16(o, a, b, kIdO, i >= 2 || k > 0);
+            a += kHalf / kSteps >> 4;
+            b += kHalf / kSteps >> 4;
+          }
+          mma_commit(b_empty + 8 * (NK + at));
+          mma_commit(b_o + 8 * s);
+          if (++at == NV) {
+            at = 0;
+            parity ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        mma_commit(b_drain + 8);
+        mbar_wait(b_drain + 8, 0);
       }
     }
     __syncwarp();
@@ -315,7 +343,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     float* f = ms->f[s];
     uint8_t* my_p = smem + F::kPOff + s * kHalf + pt * 128;
     float4* my_l = reinterpret_cast<float4*>(smem + F::kLOff) + s * 128 + pt;
-    uint32_t ph_s = 0, ph_o = 0, base = 0;
+    uint32_t ph_o = 0, base = 0;  // base: tiles of the segments before
     // this position's sums of 8 rows
     auto load_l = [&](int r0, float (&v)[8]) {
       if constexpr (E4M3) {
@@ -344,7 +372,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
 #pragma unroll 1
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth;
-      const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status);
+      const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort);
       // all leave together
       if (group_any(1, F::kSoft, !got)) break;
       const Segment sg = ms->seg[ss];
@@ -363,7 +391,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       const int all_hi = p.causal ? sg.ctx + p.by_G(sg.r0) + 1 : sg.ctx + sg.m;
       const int all_lo =
           p.window == 0 ? 0 : sg.ctx + p.by_G(sg.r0 + sg.nrows - 1) - p.window + 1;
-      if (E4M3) wait_bar(b_qFull + 8 * (sn & 1), (sn >> 1) & 1, s_abort, status);
+      if (E4M3) wait_bar(b_qFull + 8 * (sn & 1), (sn >> 1) & 1, s_abort);
       const float* row_scale = ms->a[sn & 1];
 #pragma unroll 1
       for (int i = s; i < sg.ntiles; i += 2) {
@@ -372,7 +400,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         if constexpr (E4M3) {
           // scales of this thread's position (any byte gives finite factors)
           const uint32_t q = (base + i) % kExpDepth;
-          wait_bar(b_expFull + 8 * q, ((base + i) / kExpDepth) & 1, s_abort, status);
+          wait_bar(b_expFull + 8 * q, ((base + i) / kExpDepth) & 1, s_abort);
           const uint8_t* ex = smem + F::kExpOff + q * 256 + pt;
           const int ek = min(max((int)ex[0], 1), 254), ee = min(max((int)ex[128], 1), 253);
           __syncwarp();
@@ -381,11 +409,9 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           ev = (float)(ee - 127);
           un = __uint_as_float((uint32_t)(254 - ee) << 23);
         }
-        const int sb = i % SB;
-        const uint32_t t_s = tmem + lanes + sb * 64;
-        wait_bar(b_s + 8 * sb, (ph_s >> sb) & 1, s_abort, status);
+        const uint32_t sb = (base + i) % SB, t_s = tmem + lanes + sb * 64;
+        wait_bar(b_s + 8 * sb, ((base + i) / SB) & 1, s_abort);
         __syncwarp();
-        ph_s ^= 1u << sb;
         tc_fence_after();
         // rows r_lo .. r_hi - 1 see this thread's position
         int r_lo = 0, r_hi = NR;
@@ -445,7 +471,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         tmem_wait_st();
         const bool moves = group_any(wg, 128, top > kLimit);
         if (i >= 2) {  // the products before this tile's are done
-          wait_bar(b_o + 8 * s, ph_o, s_abort, status);
+          wait_bar(b_o + 8 * s, ph_o, s_abort);
           __syncwarp();
           ph_o ^= 1;
           tc_fence_after();
@@ -557,8 +583,8 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         }
         // values that no row sees: 0 * NaN must not reach a sum
         if (r_first == 0 && (t0 < sg.lo || t0 + kBN > sg.hi)) {
-          const uint32_t e = 2 * (base + i) + 1, slot = e % NS;
-          wait_bar(b_full + 8 * slot, (e / NS) & 1, s_abort, status);
+          const uint32_t slot = NK + (base + i) % NV;
+          wait_bar(b_full + 8 * slot, ((base + i) / NV) & 1, s_abort);
           if (t0 + pt < sg.lo || t0 + pt >= sg.hi) {
             uint8_t* v = smem + slot * F::kSlot + pt * 128;
 #pragma unroll
@@ -569,11 +595,17 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(b_p + 8 * s);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(b_p + 8 * s);
+          mbar_arrive(b_sFree + 8 * sb);
+        }
       }
+      __syncwarp();
+      if (E4M3 && lane == 0) mbar_arrive(b_qEmpty + 8 * (sn & 1));
       const bool has = s < sg.ntiles;
       if (has) {
-        wait_bar(b_o + 8 * s, ph_o, s_abort, status);
+        wait_bar(b_o + 8 * s, ph_o, s_abort);
         ph_o ^= 1;
       }
       __syncwarp();
@@ -670,35 +702,40 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
 #pragma unroll 1
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth, qb = sn & 1;
-      const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status) &&
-                       wait_bar(b_qEmpty + 8 * qb, ((sn >> 1) & 1) ^ 1, s_abort, status);
+      const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort) &&
+                       wait_bar(b_qEmpty + 8 * qb, ((sn >> 1) & 1) ^ 1, s_abort);
       if (__any_sync(0xffffffffu, !got)) break;
       const Segment sg = ms->seg[ss];
       __syncwarp();
       if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
       if (sg.ntiles == 0) break;
-      // Q: 16 lanes a row, 8 values a lane; what its last 8 rows hold past the item's
-      // are zeros (the columns of S beyond are not read)
-      constexpr int kIters = 4;
+      // Q: 16 lanes a row, 8 values a lane, four rows in flight; what its last 8 rows hold
+      // past the item's are zeros (the columns of S beyond are not read)
+      const int ch = lane & 15;
 #pragma unroll 1
-      for (int row0 = 0; row0 < sg.nrows; row0 += 2 * kIters) {
-        uint4 x[kIters];
+      for (int r8 = 0; r8 < sg.nrows; r8 += 8) {
+        const int row0 = r8 + (lane >> 4);
+        uint4 x[4];
 #pragma unroll
-        for (int k = 0; k < kIters; ++k) {
-          const int row = row0 + (lane >> 4) + 2 * k, ch = lane & 15;
+        for (int k = 0; k < 4; ++k) {
           x[k] = make_uint4(0, 0, 0, 0);
-          if (row < sg.nrows) x[k] = load_q(p, sg.row0, sg.h, sg.r0 + row, ch * 8);
+          if (row0 + 2 * k < sg.nrows)
+            x[k] = load_q(p, sg.row0, sg.h, sg.r0 + row0 + 2 * k, ch * 8);
         }
-#pragma unroll
-        for (int k = 0; k < kIters; ++k) {
-          const int row = row0 + (lane >> 4) + 2 * k, ch = lane & 15;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const int row = row0 + 2 * k;
+          const uint4 now = x[0];
+          x[0] = x[1];
+          x[1] = x[2];
+          x[2] = x[3];
           uint8_t* dst = smem + F::kQOff + qb * F::kQBytes + row * 128;
           if constexpr (!E4M3) {
             if (ch < DP / 8)
               *reinterpret_cast<uint4*>(dst + (ch >> 3) * F::kQHalf +
-                                        (((ch & 7) ^ (row & 7)) << 4)) = x[k];
+                                        (((ch & 7) ^ (row & 7)) << 4)) = now;
           } else {
-            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            const uint32_t w[4] = {now.x, now.y, now.z, now.w};
             float f[8], amax = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -739,40 +776,39 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(b_qFull + 8 * qb);
       if constexpr (!E4M3) continue;
-      // the exponent bytes of K and V, four positions a lane, four tiles a time
-      const int page_mask = (1 << p.c.log_page) - 1;
+      // the exponent bytes of K and V, four positions a lane; a tile's are loaded while
+      // those of the one before wait for room.  Where no row looks, any scale does, but
+      // not one that moves the references.
+      const int log_page = p.c.log_page, end_pos = min(sg.hi, p.c.max_pages << log_page);
+      const int32_t* table = p.c.pages + (int64_t)sg.n * p.c.max_pages;
+      auto page = [&](int pos) {
+        return pos < end_pos && pos + 4 > sg.lo ? __ldg(table + (pos >> log_page)) : -1;
+      };
+      int pos = sg.tile0 * kBN + lane * 4, id = page(pos);
 #pragma unroll 1
-      for (int i0 = 0; i0 < sg.ntiles; i0 += 4) {
-        uint32_t x[4][2];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int pos = (sg.tile0 + i0 + k) * kBN + lane * 4;
-          // where no row looks, any scale does, but not one that moves the references
-          x[k][0] = x[k][1] = 0x7f7f7f7fu;
-          if (pos >= sg.hi || pos + 4 <= sg.lo || i0 + k >= sg.ntiles) continue;
-          const int64_t id = page_of(p.c, sg.n, pos);
-          if (id < 0) continue;
-          const int64_t at = ((id * p.c.Hkv + sg.h) << p.c.log_page) + (pos & page_mask);
-          x[k][0] = __ldg(reinterpret_cast<const uint32_t*>(p.c.k_exp + at));
-          x[k][1] = __ldg(reinterpret_cast<const uint32_t*>(p.c.v_exp + at));
+      for (uint32_t tile = base, end = base + sg.ntiles; tile < end; ++tile, pos += kBN) {
+        uint32_t x = 0x7f7f7f7fu, y = x;
+        if (id >= 0 && id < p.c.n_pages) {
+          const int64_t at = (((int64_t)id * p.c.Hkv + sg.h) << log_page) +
+                             (pos & ((1 << log_page) - 1));
+          x = __ldg(reinterpret_cast<const uint32_t*>(p.c.k_exp + at));
+          y = __ldg(reinterpret_cast<const uint32_t*>(p.c.v_exp + at));
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (i0 + k >= sg.ntiles) break;
-          const uint32_t tile = base + i0 + k, q = tile % kExpDepth;
-          wait_bar(b_expEmpty + 8 * q, ((tile / kExpDepth) & 1) ^ 1, s_abort, status);
-          uint32_t* to = reinterpret_cast<uint32_t*>(smem + F::kExpOff + q * 256) + lane;
-          to[0] = x[k][0];
-          to[32] = x[k][1];
-          mbar_arrive(b_expFull + 8 * q);
-        }
+        id = page(pos + kBN);
+        const uint32_t q = tile % kExpDepth;
+        wait_bar(b_expEmpty + 8 * q, ((tile / kExpDepth) & 1) ^ 1, s_abort);
+        uint32_t* to = reinterpret_cast<uint32_t*>(smem + F::kExpOff + q * 256) + lane;
+        to[0] = x;
+        to[32] = y;
+        mbar_arrive(b_expFull + 8 * q);
       }
       base += sg.ntiles;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == F::kWarpMma) {
+  if (tid == 0 && *s_abort) set_flag(p.c.status, kFlagWaitTimeout);
+  if (warp == F::kWarpS) {
     tc_fence_after();
     tmem_dealloc(tmem, F::kTmemCols);
   }

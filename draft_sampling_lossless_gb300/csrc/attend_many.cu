@@ -244,7 +244,6 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
   const uint32_t b_rawFull = b_drain + 8, b_rawEmpty = b_rawFull + 8 * F::kRawSlots;
   volatile int* s_abort = &ms->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t* status = p.c.status;
   if (smem_u32(smem) & 1023) return;  // never: the declared alignment, which the swizzle needs
 
   if (tid == 0) {
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
         held = now;
       }
       const uint32_t slot = e % kRing, full = full0 + 8 * slot;
-      const bool ok = wait_bar(empty0 + 8 * slot, ((e / kRing) & 1) ^ 1, s_abort, status);
+      const bool ok = wait_bar(empty0 + 8 * slot, ((e / kRing) & 1) ^ 1, s_abort);
       if (!__all_sync(0xffffffffu, ok)) return false;
       uint32_t dst = E4M3 ? smem_u32(smem + F::kRawOff) + slot * kHalf
                           : smem_u32(s_kv) + slot * F::kTile;
@@ -354,11 +353,11 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
       uint32_t ph_q = 0, ph_p = 0;
       bool ok = true;
       auto need = [&](uint32_t e) {
-        ok = ok && wait_bar(b_full + 8 * (e % NS), (e / NS) & 1, s_abort, status);
+        ok = ok && wait_bar(b_full + 8 * (e % NS), (e / NS) & 1, s_abort);
         tc_fence_after();
       };
       auto need_p = [&](int s) {
-        ok = ok && wait_bar(b_p + 8 * s, (ph_p >> s) & 1, s_abort, status);
+        ok = ok && wait_bar(b_p + 8 * s, (ph_p >> s) & 1, s_abort);
         ph_p ^= 1u << s;
         tc_fence_after();
       };
@@ -384,13 +383,13 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
       auto release = [&](uint32_t e) { mma_commit(b_empty + 8 * (e % NS)); };
       for (int sn = 0; ok; ++sn) {
         const int ss = sn % kSegDepth;
-        ok = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status);
+        ok = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort);
         if (!ok) break;
         const int nt = ms->seg[ss].ntiles;
         const bool two = ms->seg[ss].nrows > 128;
         mbar_arrive(b_segEmpty + 8 * ss);
         if (nt == 0) break;
-        ok = wait_bar(b_q, ph_q, s_abort, status);
+        ok = wait_bar(b_q, ph_q, s_abort);
         if (!ok) break;
         ph_q ^= 1;
         tc_fence_after();
@@ -468,7 +467,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
     uint32_t base = 0;
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth;
-      const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status);
+      const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort);
       // all leave together; the barrier also ends the previous segment's use of s_q
       if (group_any(1, kSoftThreads, !got)) break;
       const Segment sg = ms->seg[ss];
@@ -522,7 +521,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
       const int step = two ? 1 : 2, i0 = two ? 0 : s;
       for (int i = i0; i < sg.ntiles; i += step) {
         const int t0 = (sg.tile0 + i) * kBN;
-        wait_bar(b_s + 8 * s, ph_s, s_abort, status);
+        wait_bar(b_s + 8 * s, ph_s, s_abort);
         __syncwarp();
         ph_s ^= 1;
         tc_fence_after();
@@ -538,7 +537,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
         // (e4m3: the conversion has zeroed them)
         if (!E4M3 && (!two || s == 0) && (t0 < sg.lo || t0 + kBN > sg.hi)) {
           const uint32_t e = 2 * (base + i) + 1, slot = e % NS;
-          wait_bar(b_full + 8 * slot, (e / NS) & 1, s_abort, status);
+          wait_bar(b_full + 8 * slot, (e / NS) & 1, s_abort);
           uint8_t* tile = s_kv + slot * F::kTile;
           zero_rows<DP>(tile, 0, sg.lo - t0, lrow);
           zero_rows<DP>(tile, max(sg.hi - t0, 0), kBN, lrow);
@@ -551,7 +550,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
       }
       const bool has = i0 < sg.ntiles;
       if (has) {
-        wait_bar(b_o + 8 * s, ph_o, s_abort, status);
+        wait_bar(b_o + 8 * s, ph_o, s_abort);
         __syncwarp();
         ph_o ^= 1;
         tc_fence_after();
@@ -690,7 +689,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
     uint32_t e = 0;
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth;
-      const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort, status);
+      const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort);
       if (group_any(4, 128, !got)) break;
       const int nt = ms->seg[ss].ntiles, tile0 = ms->seg[ss].tile0;
       const int lo = ms->seg[ss].lo, hi = ms->seg[ss].hi;
@@ -702,8 +701,8 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
         const uint32_t raw = e % NRAW, slot = e % NS;
         const int t0 = (tile0 + (i >> 1)) * kBN;
         const bool edge = t0 < lo || t0 + kBN > hi;
-        wait_bar(b_rawFull + 8 * raw, (e / NRAW) & 1, s_abort, status);
-        wait_bar(b_empty + 8 * slot, ((e / NS) & 1) ^ 1, s_abort, status);
+        wait_bar(b_rawFull + 8 * raw, (e / NRAW) & 1, s_abort);
+        wait_bar(b_empty + 8 * slot, ((e / NS) & 1) ^ 1, s_abort);
         const uint8_t* src = smem + F::kRawOff + raw * kHalf;
         const uint8_t* exps = smem + F::kExpOff + raw * 128;
         uint8_t* dst = s_kv + slot * F::kTile;
@@ -739,6 +738,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *s_abort) set_flag(p.c.status, kFlagWaitTimeout);
   if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
