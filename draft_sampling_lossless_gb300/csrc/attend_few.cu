@@ -45,20 +45,16 @@ constexpr int kExpDepth = 8;          // tiles of exponent bytes held
 
 template <int DP, int NR, bool E4M3>
 struct Few {
-  // Softmax threads a position: rows of e4m3 terms want more warps for their longer
-  // chains of conversions
-  static constexpr int kSplit = E4M3 && NR > 16 ? 2 : 1;
-  static constexpr int kSoft = 256 * kSplit;   // softmax threads; then five warps
+  static constexpr int kSoft = 256;  // softmax threads, two warpgroups; then five warps
   static constexpr int kWarpS = kSoft / 32, kWarpTma = kWarpS + 1, kWarpO = kWarpS + 4;
   static constexpr int kThreads = kSoft + 160;
   static constexpr int kNH = DP / 64;
   static constexpr int kParts = E4M3 ? 4 : 2;                         // terms of P
   static constexpr int kPN = (kParts * NR + 15) / 16 * 16;            // N of the products
   static constexpr int kQRows = E4M3 ? 2 * NR : (NR < 16 ? 16 : NR);  // N of the scores
-  // tiles of scores ahead: e4m3 tiles come twice as fast, and one's softmax is longer
-  static constexpr int kSBufs = E4M3 ? 4 : 2;
-  // tensor memory: S, 64 columns each, then O of the streams, then (bf16) the
-  // positions' own sums, l; e4m3's are in shared memory
+  static constexpr int kSBufs = E4M3 ? 3 : 4;  // tiles of scores ahead
+  // tensor memory: S, 64 columns each, then O of the streams, then the positions' own
+  // sums, l
   static constexpr uint32_t kColO = 64 * kSBufs, kOCols = E4M3 ? 128 : 64;
   static constexpr uint32_t kColL = kColO + 2 * kOCols;
   static constexpr uint32_t kTmemCols = 512;
@@ -66,18 +62,16 @@ struct Few {
   static constexpr uint32_t kQHalf = kQRows * 128;
   static constexpr uint32_t kQBytes = kQHalf * (E4M3 ? 1 : kNH);
   static constexpr uint32_t kExp = E4M3 ? kExpDepth * 256 : 0;
-  static constexpr uint32_t kL = E4M3 ? NR * 1024 : 0;
   static constexpr uint32_t kMisc = 4096;
   static constexpr int kFit =
-      (int)((kMaxSmem - 2 * kHalf - 2 * kQBytes - kExp - kL - kMisc) / kSlot);
+      (int)((kMaxSmem - 2 * kHalf - 2 * kQBytes - kExp - kMisc) / kSlot);
   static constexpr int kSlots = kFit > 12 ? 12 : kFit;
   static constexpr int kSlotsK = kSlots / 2, kSlotsV = kSlots - kSlotsK;
   // P of each stream (at an item's end its O, then the join's buffer)
   static constexpr uint32_t kPOff = kSlots * kSlot;
   static constexpr uint32_t kQOff = kPOff + 2 * kHalf;
   static constexpr uint32_t kExpOff = kQOff + 2 * kQBytes;
-  static constexpr uint32_t kLOff = kExpOff + kExp;
-  static constexpr uint32_t kMiscOff = kLOff + kL;
+  static constexpr uint32_t kMiscOff = kExpOff + kExp;
   static constexpr uint32_t kTotal = kMiscOff + kMisc;
   static_assert(kTotal <= kMaxSmem && kSlots >= 4, "shared memory");
 };
@@ -329,12 +323,9 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     // ------------------------------------------------------------ softmax
     // Every step goes over the rows in a loop of eight at a time: the code of a tile
     // has to stay in the instruction caches, which all roles share.
-    const int s = (warp >> 2) & 1;               // the stream
-    const int r_first = (warp >> 3) * 8;         // this thread's rows: eight from here,
-    constexpr int kStep = 8 * F::kSplit;         // every kStep rows
-    const int wg = 2 + (warp >> 2);              // its warpgroup's barrier
-    const int pt = tid & 127;                    // position of the tile, value of D at the end
-    const bool owner = pt < NR && ((pt >> 3) & (F::kSplit - 1)) == warp >> 3;  // of row pt
+    const int s = warp >> 2;   // the stream
+    const int wg = 2 + s;      // its barrier
+    const int pt = tid & 127;  // position of the tile, value of D at the end
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_o = tmem + lanes + F::kColO + s * F::kOCols;
     const uint32_t t_l = tmem + lanes + F::kColL + s * 32;
@@ -342,32 +333,20 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     float* nm = ms->nm[s];
     float* f = ms->f[s];
     uint8_t* my_p = smem + F::kPOff + s * kHalf + pt * 128;
-    float4* my_l = reinterpret_cast<float4*>(smem + F::kLOff) + s * 128 + pt;
     uint32_t ph_o = 0, base = 0;  // base: tiles of the segments before
     // this position's sums of 8 rows
     auto load_l = [&](int r0, float (&v)[8]) {
-      if constexpr (E4M3) {
-        const float4 a = my_l[r0 * 64], b = my_l[r0 * 64 + 256];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-      } else {
-        uint32_t u[8];
-        tmem_ld_32x32b_x8(t_l + r0, u);
-        tmem_wait_ld_regs(u);
+      uint32_t u[8];
+      tmem_ld_32x32b_x8(t_l + r0, u);
+      tmem_wait_ld_regs(u);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(u[k]);
-      }
+      for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(u[k]);
     };
     auto store_l = [&](int r0, const float (&v)[8]) {
-      if constexpr (E4M3) {
-        my_l[r0 * 64] = make_float4(v[0], v[1], v[2], v[3]);
-        my_l[r0 * 64 + 256] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        uint32_t u[8];
+      uint32_t u[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(v[k]);
-        tmem_st_32x32b_x8(t_l + r0, u);
-      }
+      for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(v[k]);
+      tmem_st_32x32b_x8(t_l + r0, u);
     };
 #pragma unroll 1
     for (int sn = 0;; ++sn) {
@@ -380,11 +359,11 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
       if (sg.ntiles == 0) break;
 
-      if (owner) nm[pt] = pt < sg.nrows ? kUnset : 0.f;
+      if (pt < NR) nm[pt] = pt < sg.nrows ? kUnset : 0.f;
       {
         const float zero[8] = {};
 #pragma unroll 1
-        for (int r0 = r_first; r0 < sg.nrows; r0 += kStep) store_l(r0, zero);
+        for (int r0 = 0; r0 < sg.nrows; r0 += 8) store_l(r0, zero);
       }
       group_sync(wg, 128);
       // positions that every row sees
@@ -434,7 +413,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         // much.  Eights of rows that the item does not have are left out throughout.
         float top = -INFINITY;
 #pragma unroll 1
-        for (int r0 = r_first; r0 < sg.nrows; r0 += kStep) {
+        for (int r0 = 0; r0 < sg.nrows; r0 += 8) {
           uint32_t u[8];
           float y[8];
           tmem_ld_32x32b_x8(t_s + r0, u);
@@ -479,7 +458,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         if (moves) {
           // references move to the tile's maxima
 #pragma unroll 1
-          for (int r0 = r_first; r0 < sg.nrows; r0 += kStep) {
+          for (int r0 = 0; r0 < sg.nrows; r0 += 8) {
             uint32_t u[8];
             tmem_ld_32x32b_x8(t_s + r0, u);
             tmem_wait_ld_regs(u);
@@ -495,20 +474,20 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
               ms->wm[s][warp & 3][r0 + lane] = __int_as_float(best ^ ((best >> 31) & 0x7fffffff));
           }
           group_sync(wg, 128);
-          if (owner && pt < sg.nrows) {
+          if (pt < sg.nrows) {
             const float old = -nm[pt];
             const float m = max3(fmaxf(ms->wm[s][0][pt], ms->wm[s][1][pt]), ms->wm[s][2][pt],
                                  ms->wm[s][3][pt]);
             const bool moved = m - old > kLimit / 2;
             if (moved) nm[pt] = -m;
             f[pt] = moved ? ex2_approx(old - m) : 1.f;
-          } else if (owner) {
+          } else if (pt < NR) {
             f[pt] = 1.f;
           }
           group_sync(wg, 128);
           if (i >= 2) {
 #pragma unroll 1
-            for (int r0 = r_first; r0 < sg.nrows; r0 += kStep) {
+            for (int r0 = 0; r0 < sg.nrows; r0 += 8) {
               float w[8], v[8];
               bool moved = false;  // alike in every thread
 #pragma unroll
@@ -536,7 +515,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         }
         // P: the position's row of its terms
 #pragma unroll 1
-        for (int r0 = r_first; r0 < sg.nrows; r0 += kStep) {
+        for (int r0 = 0; r0 < sg.nrows; r0 += 8) {
           uint32_t u[8];
           float l[8];
           tmem_ld_32x32b_x8(t_s + r0, u);
@@ -582,7 +561,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
           store_l(r0, l);
         }
         // values that no row sees: 0 * NaN must not reach a sum
-        if (r_first == 0 && (t0 < sg.lo || t0 + kBN > sg.hi)) {
+        if (t0 < sg.lo || t0 + kBN > sg.hi) {
           const uint32_t slot = NK + (base + i) % NV;
           wait_bar(b_full + 8 * slot, ((base + i) / NV) & 1, s_abort);
           if (t0 + pt < sg.lo || t0 + pt >= sg.hi) {
@@ -617,7 +596,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       // (P is no longer read)
       float* o_s = reinterpret_cast<float*>(smem + F::kPOff + s * kHalf);
 #pragma unroll 1
-      for (int r0 = r_first; r0 < sg.nrows; r0 += kStep) {
+      for (int r0 = 0; r0 < sg.nrows; r0 += 8) {
         float v[8];
         load_l(r0, v);
         const float sum = reduce_rows<8>(v, [](float a, float b) { return a + b; });
