@@ -51,8 +51,6 @@ constexpr float kGrow = 8.0f;    // log2 growth of a maximum that moves the refe
 template <int DP, bool E4M3>
 struct Many {
   static constexpr int kThreads = E4M3 ? 512 : 384;
-  // scores that a softmax thread holds: of 32 positions each
-  static constexpr int kHeld = E4M3 ? 2 : 4;
   static constexpr uint32_t kTile = kHalf * (DP / 64);  // a K, V or Q tile of bf16
   // Q of both streams; at an item's end 32 KB to join through and the streams' (m, l)
   static constexpr uint32_t kXch = 32768;
@@ -118,31 +116,28 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&v)[32], uint32_t t_at
   tmem_st_32x32b_x32(t_at, out);
 }
 
-// One tile's P for a warp: its rows' scores of NC * 32 positions from column col0
+// One tile's P for a warp: its rows' scores of nc * 32 positions from column col0
 // of S on, the running reference and sum, and P over S's columns (zero outside
-// the warp's own positions).  HELD chunks of 32 scores stay in registers; where
-// that is not all of them, they are read again for the exponentials.
-template <int NC, int HELD, int DP>
-__device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, int col0, bool mask,
+// the warp's own positions).  Loops of 32 positions at a time, read twice: the code
+// of all roles' loops has to stay in the instruction caches.
+template <int DP>
+__device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, int col0, int nc, bool mask,
                                              int rel_lo, int rel_hi, float c2, bool first,
                                              float& m_ref, float& l) {
-  constexpr int kHeld = NC < HELD ? NC : HELD;
-  uint32_t v[kHeld][32];
+  const int end = col0 + 32 * nc;
   float top = -INFINITY;
-#pragma unroll
-  for (int k0 = 0; k0 < NC; k0 += kHeld) {
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) tmem_ld_32x32b_x32(t_s + col0 + 32 * (k0 + k), v[k]);
-    tmem_wait_ld();
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[k][i]));
-      if (mask) mask_chunk(v[k], col0 + 32 * (k0 + k), rel_lo, rel_hi);
-      top = max_chunk(v[k], top);
+#pragma unroll 1
+  for (int c = col0; c < end; c += 32) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(t_s + c, v);
+    tmem_wait_ld_regs(v);
+    if (mask) {
+      mask_chunk(v, c, rel_lo, rel_hi);
+      tmem_st_32x32b_x32(t_s + c, v);
     }
+    top = max_chunk(v, top);
   }
-  if (NC > kHeld) tmem_ld_32x32b_x32(t_s + col0, v[0]);
+  if (mask) tmem_wait_st();
   if (first) {
     m_ref = top;
   } else if (__any_sync(0xffffffffu, (top - m_ref) * c2 > kGrow)) {
@@ -152,7 +147,6 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, int col
       m_ref = top;
     }
     l *= f;
-    if (NC > kHeld) tmem_wait_ld_regs(v[0]);
 #pragma unroll 1
     for (int ch = 0; ch < DP; ch += 32) {
       uint32_t o[32];
@@ -165,23 +159,20 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, int col
   }
   const float mc = m_ref == -INFINITY ? 0.f : m_ref * c2;
   unsigned long long sum[2] = {0, 0};  // two packed zeros each
-#pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    if (NC > kHeld) {
-      // the next chunk's load is in flight under this one's exponentials
-      tmem_wait_ld_regs(v[k & 1]);
-      if (k + 1 < NC) tmem_ld_32x32b_x32(t_s + col0 + 32 * (k + 1), v[(k + 1) & 1]);
-      if (mask) mask_chunk(v[k & 1], col0 + 32 * k, rel_lo, rel_hi);
-    }
-    exp_chunk(v[k & (kHeld - 1)], t_s + col0 + 32 * k, c2, mc, sum);
+#pragma unroll 1
+  for (int c = col0; c < end; c += 32) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(t_s + c, v);
+    tmem_wait_ld_regs(v);
+    exp_chunk(v, t_s + c, c2, mc, sum);
   }
-  if (NC < 4) {
+  if (nc < 4) {
     uint32_t z[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) z[i] = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k < col0 / 32 || k >= col0 / 32 + NC) tmem_st_32x32b_x32(t_s + 32 * k, z);
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32)
+      if (c < col0 || c >= end) tmem_st_32x32b_x32(t_s + c, z);
   }
   float a, b;
   unpack2(add2(sum[0], sum[1]), a, b);
@@ -528,12 +519,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
         const bool mask = t0 < max_lo || t0 + kBN > min_hi;
         const bool first = i == i0;
         const int rel_lo = row_lo - t0, rel_hi = row_hi - t0;
-        if (rep == 1)
-          softmax_tile<4, F::kHeld, DP>(t_s, t_o, col0, mask, rel_lo, rel_hi, c2, first, m_ref, l);
-        else if (rep == 2)
-          softmax_tile<2, F::kHeld, DP>(t_s, t_o, col0, mask, rel_lo, rel_hi, c2, first, m_ref, l);
-        else
-          softmax_tile<1, F::kHeld, DP>(t_s, t_o, col0, mask, rel_lo, rel_hi, c2, first, m_ref, l);
+        softmax_tile<DP>(t_s, t_o, col0, 4 / rep, mask, rel_lo, rel_hi, c2, first, m_ref, l);
         // (e4m3: the conversion has zeroed them)
         if (!E4M3 && (!two || s == 0) && (t0 < sg.lo || t0 + kBN > sg.hi)) {
           const uint32_t e = 2 * (base + i) + 1, slot = e % NS;
