@@ -94,23 +94,34 @@ __global__ void __launch_bounds__(kThreads)
                                     p.c * 8) = x[i];
       } else {
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        float f[8], amax = 0.f;
-        bool finite = true;
+        float f[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           f[2 * j] = __uint_as_float(w[j] << 16);
           f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float a = fabsf(f[j]);
-          const bool fin = a < INFINITY;
-          finite &= fin;
-          amax = fmaxf(amax, fin ? a : 0.f);
-        }
+        // the largest magnitude: bf16 without the sign are ordered as 16-bit integers
+        constexpr uint32_t kMag = 0x7fff7fffu;
+        uint32_t top = __vmaxu2(__vmaxu2(w[0] & kMag, w[1] & kMag),
+                                __vmaxu2(w[2] & kMag, w[3] & kMag));
 #pragma unroll
         for (int o = LP / 2; o > 0; o >>= 1)
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float amax = __uint_as_float(max(top >> 16, top & 0xffffu) << 16);
+        bool finite = true;
+        if (__any_sync(0xffffffffu, !(amax < INFINITY))) {  // of the finite values, then
+          amax = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float a = fabsf(f[j]);
+            const bool fin = a < INFINITY;
+            finite &= fin;
+            amax = fmaxf(amax, fin ? a : 0.f);
+          }
+#pragma unroll
+          for (int o = LP / 2; o > 0; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        }
         const int e = row_exponent(amax);
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
         uint32_t code[4];
