@@ -3,7 +3,7 @@
 //
 // Both move each byte once and compute next to nothing, so HBM bounds them:
 // 2 * Hkv * (2 D read + 2 D or D + 1 written) bytes a row for the append, the
-// reverse for the read.  One warp takes one row: it has up to eight 16-byte
+// reverse for the read.  One warp takes one row: it has four 16-byte
 // loads a lane in flight, the append's issued before the request lookup that
 // says where they go, so the lookup's round trips hide behind them.
 #include "cache.cuh"
@@ -12,7 +12,7 @@ namespace dspark {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMinExp = -100;  // smallest exponent kept for a row
 
@@ -54,7 +54,7 @@ template <bool E4M3, int LP>
 __global__ void __launch_bounds__(kThreads)
     cache_append_kernel(const CacheView c, const __nv_bfloat16* __restrict__ k, int64_t k_stride,
                         const __nv_bfloat16* __restrict__ v, int64_t v_stride) {
-  constexpr int kBatch = 8;
+  constexpr int kBatch = 4;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= c.T) return;
   const int steps = (2 * c.Hkv * LP + 31) / 32;
@@ -143,7 +143,7 @@ template <bool E4M3, int LP>
 __global__ void __launch_bounds__(kThreads)
     cache_read_kernel(const CacheView c, __nv_bfloat16* __restrict__ k_out,
                       __nv_bfloat16* __restrict__ v_out) {
-  constexpr int kBatch = 8;
+  constexpr int kBatch = 4;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= c.T) return;
   const int n = find_request(c.row_off, c.R, t);
