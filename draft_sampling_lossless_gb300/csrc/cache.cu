@@ -9,10 +9,10 @@
 // lane leave room for fewer warps and are slower (eight, in blocks of eight warps:
 // 79 us for 68 below).
 //
-// Measured (8 heads of 128): nine prompts of 1500 to 6000 rows written as e4m3 68 us,
-// 5.3 TB/s (78% of the measured copy rate: the conversions and the exponents, single
-// bytes, come on top); 24 prefixes of 500 to 8000 rows of bf16 read 120 us, 6.5 TB/s
-// (96%); 64 requests' 1 to 8 rows of bf16 written 6.2 us, latency.
+// Measured (8 heads of 128): nine prompts of 1500 to 6000 rows written as e4m3 and read
+// back 68 us, 5.3 TB/s (78% of the measured copy rate: the conversions and the exponents,
+// single bytes, come on top); 24 prefixes of 500 to 8000 rows of bf16 read 120 us,
+// 6.5 TB/s (96%); 64 requests' 1 to 8 rows of bf16 written 6.2 us, latency.
 #include "cache.cuh"
 
 namespace dspark {

@@ -428,7 +428,7 @@ int dspark_check_wait_timeout(int limit_us, void* ws, size_t ws_bytes, void* str
  *
  * Limits: D a multiple of 16, 16 <= D <= 128; page a power of two, 16 <= page
  * <= 1024; n_pages * Hkv * page < 2^31; 1 <= R <= 2^20; 0 <= T <= 2^24 rows (T
- * = 0 does nothing); max_pages * page < 2^30.
+ * = 0 does nothing); max_pages * page < 2^30; T * Hq / Hkv <= 2^30.
  *
  * dspark_cache (host memory, the caller's) describes the pools: fill it once
  * with dspark_cache_init and pass it to every call; it may be copied.  It
