@@ -9,7 +9,7 @@ using namespace attend;
 // are the N side of the products, as far as its two terms of P and S's columns go; more
 // are their M side.  With 32 the first kernel is still ahead: 64 requests of 1 to 8
 // rows of a group of 4 take 184 us (the other 222), over e4m3 188 us (344); single
-// tokens over e4m3 127 us (363), one token 12 us (17).
+// tokens over e4m3 127 us (363), one token 14 us (19), each in a graph.
 static bool few(int max_rows, int group) { return (int64_t)max_rows * group <= 32; }
 
 size_t attend_workspace_bytes(int T, int group, int D) {

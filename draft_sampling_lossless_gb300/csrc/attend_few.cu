@@ -39,14 +39,14 @@
 // the split of the work.
 //
 // Measured (32 query heads over 8 of 128, of the measured copy rate):
-//   64 requests of 1 to 8 rows, 500 to 8000 positions  184 us, 6.2 TB/s, 92%
-//   3 of 5 to 8 rows, 90 to 180 thousand positions     227 us, 6.6 TB/s, 98%
-//   the first, e4m3: 188 us, 3.1 TB/s, 46%; 256 single tokens, e4m3: 127 us, 4.5 TB/s,
-//     66%: the softmax threads' instructions (P's four terms take half of them) and
+//   64 requests of 1 to 8 rows, 500 to 8000 positions  180 us, 6.3 TB/s, 93%
+//   3 of 5 to 8 rows, 90 to 180 thousand positions     221 us, 6.8 TB/s, 100%
+//   the first, e4m3: 186 us, 3.2 TB/s, 47%; 256 single tokens, e4m3: 125 us, 4.5 TB/s,
+//     67%: the softmax threads' instructions (P's four terms take half of them) and
 //     the moves of references bound it
-//   64 drafter's blocks of 7 rows, 16 heads over 8 of 64: 62 us, 4.6 TB/s, 68%: the
+//   64 drafter's blocks of 7 rows, 16 heads over 8 of 64: 60 us, 4.9 TB/s, 72%: the
 //     ends of items
-//   one token, 700 positions: 12 us, latency: the plan of the work (2 us), the first
+//   one token, 700 positions: 11 us, latency: the plan of the work (2 us), the first
 //     loads (2 us), six tiles, the join
 #include "attend.cuh"
 
@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     tmem_relinquish();
     tc_fence_before();
   }
+  grid_dependency_wait();  // row_off, ctx, the pages
   const Range rg = plan<32, F::kThreads>(p, ms->sum, ms->found);
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
@@ -817,8 +818,9 @@ cudaError_t launch_one(const AttendArgs& a, const Params& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
   DSPARK_LAUNCH(kKindAttend, st,
-                kernel<<<grid, F::kThreads, F::kTotal, st>>>(a.desc->tm_k, a.desc->tm_v, p));
-  return cudaGetLastError();
+                e = launch_pdl(kernel, dim3(grid), dim3(F::kThreads), F::kTotal, st, a.desc->tm_k,
+                               a.desc->tm_v, p));
+  return e;
 }
 
 template <int DP, bool E4M3>

@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
     mbar_init(b_drain, 1);
     fence_mbar_init();
   }
+  grid_dependency_wait();  // row_off, ctx, the pages
   const Range rg = plan<kRows, F::kThreads>(p, ms->sum, ms->found);
   if (rg.u0 >= rg.u1) return;  // no tiles for this block
   if (warp == kWarpMma) {
@@ -751,8 +752,9 @@ cudaError_t launch_one(const AttendArgs& a, const Params& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
   DSPARK_LAUNCH(kKindAttend, st,
-                kernel<<<grid, F::kThreads, F::kTotal, st>>>(a.desc->tm_k, a.desc->tm_v, p));
-  return cudaGetLastError();
+                e = launch_pdl(kernel, dim3(grid), dim3(F::kThreads), F::kTotal, st, a.desc->tm_k,
+                               a.desc->tm_v, p));
+  return e;
 }
 
 }  // namespace

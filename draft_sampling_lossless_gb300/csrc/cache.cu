@@ -10,9 +10,9 @@
 // 79 us for 68 below).
 //
 // Measured (8 heads of 128): nine prompts of 1500 to 6000 rows written as e4m3 and read
-// back 68 us, 5.3 TB/s (78% of the measured copy rate: the conversions and the exponents,
-// single bytes, come on top); 24 prefixes of 500 to 8000 rows of bf16 read 120 us,
-// 6.5 TB/s (96%); 64 requests' 1 to 8 rows of bf16 written 6.2 us, latency.
+// back 66 us, 5.4 TB/s (80% of the measured copy rate: the conversions and the exponents,
+// single bytes, come on top); 24 prefixes of 500 to 8000 rows of bf16 read 118 us,
+// 6.7 TB/s (99%); 64 requests' 1 to 8 rows of bf16 written 6.2 us, latency.
 #include "cache.cuh"
 
 namespace dspark {
@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kThreads)
     cache_append_kernel(const CacheView c, const __nv_bfloat16* __restrict__ k, int64_t k_stride,
                         const __nv_bfloat16* __restrict__ v, int64_t v_stride) {
   constexpr int kBatch = 4;
+  grid_dependency_wait();  // the rows, the tables, the pools
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= c.T) return;
   const int steps = (2 * c.Hkv * LP + 31) / 32;
@@ -151,6 +152,7 @@ __global__ void __launch_bounds__(kThreads)
     cache_read_kernel(const CacheView c, __nv_bfloat16* __restrict__ k_out,
                       __nv_bfloat16* __restrict__ v_out) {
   constexpr int kBatch = 4;
+  grid_dependency_wait();  // the rows, the tables, the pools
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= c.T) return;
   const int n = find_request(c.row_off, c.R, t);
@@ -207,21 +209,24 @@ cudaError_t launch_cache_append(const CacheView& c, bool e4m3, const void* k, in
                                 const void* v, int64_t v_stride, cudaStream_t st) {
   auto kernel = c.D > 64 ? (e4m3 ? cache_append_kernel<true, 16> : cache_append_kernel<false, 16>)
                          : (e4m3 ? cache_append_kernel<true, 8> : cache_append_kernel<false, 8>);
+  cudaError_t e;
   DSPARK_LAUNCH(kKindCacheAppend, st,
-                kernel<<<(c.T + kWarps - 1) / kWarps, kThreads, 0, st>>>(
-                    c, static_cast<const __nv_bfloat16*>(k), k_stride,
-                    static_cast<const __nv_bfloat16*>(v), v_stride));
-  return cudaGetLastError();
+                e = launch_pdl(kernel, dim3((c.T + kWarps - 1) / kWarps), dim3(kThreads), 0, st, c,
+                               static_cast<const __nv_bfloat16*>(k), k_stride,
+                               static_cast<const __nv_bfloat16*>(v), v_stride));
+  return e;
 }
 
 cudaError_t launch_cache_read(const CacheView& c, bool e4m3, void* k_out, void* v_out,
                               cudaStream_t st) {
   auto kernel = c.D > 64 ? (e4m3 ? cache_read_kernel<true, 16> : cache_read_kernel<false, 16>)
                          : (e4m3 ? cache_read_kernel<true, 8> : cache_read_kernel<false, 8>);
+  cudaError_t e;
   DSPARK_LAUNCH(kKindCacheRead, st,
-                kernel<<<(c.T + kWarps - 1) / kWarps, kThreads, 0, st>>>(
-                    c, static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out)));
-  return cudaGetLastError();
+                e = launch_pdl(kernel, dim3((c.T + kWarps - 1) / kWarps), dim3(kThreads), 0, st, c,
+                               static_cast<__nv_bfloat16*>(k_out),
+                               static_cast<__nv_bfloat16*>(v_out)));
+  return e;
 }
 
 }  // namespace dspark
