@@ -25,12 +25,12 @@
 //     shrinks with the rows, and no warp waits for another's maximum.  The copies
 //     and the two streams are joined once, at the end.
 //
-// e4m3 caches: four more warps turn the codes into bf16 tiles, scaled (exact: the
+// e4m3 caches: eight more warps turn the codes into bf16 tiles, scaled (exact: the
 // scales are powers of two), between the loads and the products.
 //
 // Roles: warps 0-7 the two softmax warpgroups (they also load Q and store), warp 8
 // issues the MMAs, warps 9 and 10 the TMA loads of K and V (11 completes the
-// warpgroup), warps 12-15 convert.  Every wait is bounded; a timeout sets
+// warpgroup), warps 12-19 convert.  Every wait is bounded; a timeout sets
 // DSPARK_DEVFLAG_TIMEOUT and ends the kernel.  See attend.cuh for the split of the work.
 //
 // What bounds it: a stream's chain of scores (8 MMAs of 96 cycles: both operands come
@@ -42,8 +42,9 @@
 // 515 us for 478; loops of 16 took 499, loads one chunk ahead 507, two threads a row 542.
 // Measured (32 query heads over 8 of 128): two chunks of 2000 rows after 1000 to 7000
 // positions 478 us, 938 TFLOP/s of visible products (49% of the measured matrix rate);
-// three of 700 to 1500, 40 heads, window 2048, e4m3 241 us, 453 TFLOP/s: tiles at the
-// edges of the windows are computed whole, and the codes' conversion comes on top.
+// three of 700 to 1500, 40 heads, window 2048, e4m3 236 us, 464 TFLOP/s: tiles at the
+// edges of the windows are computed whole, an item has a dozen tiles, and the codes'
+// conversion takes as many instructions as the softmax (four warps for it: 242 us).
 #include "attend.cuh"
 
 namespace dspark {
@@ -62,7 +63,7 @@ constexpr float kGrow = 8.0f;    // log2 growth of a maximum that moves the refe
 
 template <int DP, bool E4M3>
 struct Many {
-  static constexpr int kThreads = E4M3 ? 512 : 384;
+  static constexpr int kThreads = E4M3 ? 640 : 384;
   static constexpr uint32_t kTile = kHalf * (DP / 64);  // a K, V or Q tile of bf16
   // Q of both streams; at an item's end 32 KB to join through and the streams' (m, l)
   static constexpr uint32_t kXch = 32768;
@@ -81,7 +82,7 @@ struct Many {
 };
 
 struct Misc {  // shared words
-  int64_t sum[16];
+  int64_t sum[32];
   Found found[2];
   Segment seg[kSegDepth];
   uint64_t bars[2 * 12 + 2 * 4 + 2 * kSegDepth + 8];
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
     *s_abort = 0;
 #pragma unroll 1
     for (int i = 0; i < NS; ++i) {
-      mbar_init(b_full + 8 * i, E4M3 ? 128 : 1);
+      mbar_init(b_full + 8 * i, E4M3 ? 8 : 1);
       mbar_init(b_empty + 8 * i, 1);
     }
     for (int i = 0; i < F::kRawSlots; ++i) {
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
     }
     for (int i = 0; i < kSegDepth; ++i) {
       mbar_init(b_segFull + 8 * i, 1);
-      mbar_init(b_segEmpty + 8 * i, E4M3 ? 14 : 10);  // the MMA thread and the other warps
+      mbar_init(b_segEmpty + 8 * i, E4M3 ? 18 : 10);  // the MMA thread and the other warps
     }
     mbar_init(b_q, kSoftThreads);
     for (int i = 0; i < 2; ++i) {
@@ -286,9 +287,10 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
   const uint32_t tmem = ms->tmem;
 
   // bf16: 384 threads of 168 registers become 256 x 208 and 128 x 88;
-  // e4m3: 512 of 128 become 256 x 168 and 256 x 88
+  // e4m3: 640 of 96 become 256 x 128 and 384 x 72
   if (warp == kWarpTma || warp == kWarpTma + 1) {
-    reg_dec<88>();
+    if (E4M3) reg_dec<72>();
+    else reg_dec<88>();
     // ------------------------------------------------------------ loads
     const int kv = warp - kWarpTma;  // warp 9 K, warp 10 V
     const CUtensorMap* map = kv ? &tm_v : &tm_k;
@@ -346,7 +348,8 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
         if ((i & 1) == kv) mbar_wait(full0 + 8 * (i % kRing), (i / kRing) & 1);
     }
   } else if (warp == kWarpMma) {
-    reg_dec<88>();
+    if (E4M3) reg_dec<72>();
+    else reg_dec<88>();
     // ------------------------------------------------------------ products
     if (elect_one()) {
       constexpr uint32_t kIdS = idesc_bf16_f32(128, kBN);
@@ -459,7 +462,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp < 8) {
-    if (E4M3) reg_inc<168>();
+    if (E4M3) reg_inc<128>();
     else reg_inc<208>();
     // ------------------------------------------------------------ softmax
     const int s = warp >> 2;  // the stream
@@ -680,16 +683,17 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
       tc_fence_before();
     }
   } else if (warp < 12) {
-    reg_dec<88>();  // completes the warpgroup
+    if (E4M3) reg_dec<72>();
+    else reg_dec<88>();  // completes the warpgroup
   } else if (E4M3) {
-    reg_dec<88>();
+    reg_dec<72>();
     // ------------------------------------------------------------ codes to bf16
     const int ct = tid - 384, c = ct & 7;  // 8 lanes a row of 128 codes, 16 codes a lane
     uint32_t e = 0;
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth;
       const bool got = wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort);
-      if (group_any(4, 128, !got)) break;
+      if (group_any(4, 256, !got)) break;
       const int nt = ms->seg[ss].ntiles, tile0 = ms->seg[ss].tile0;
       const int lo = ms->seg[ss].lo, hi = ms->seg[ss].hi;
       __syncwarp();
@@ -706,8 +710,8 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
         const uint8_t* exps = smem + F::kExpOff + raw * 128;
         uint8_t* dst = s_kv + slot * F::kTile;
 #pragma unroll 2
-        for (int k = 0; k < 8; ++k) {
-          const int row = k * 16 + (ct >> 3);
+        for (int k = 0; k < 4; ++k) {
+          const int row = k * 32 + (ct >> 3);
           const uint4 v = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
           uint32_t w[4] = {v.x, v.y, v.z, v.w}, h[8];
           // positions that no row sees are zeros: 0 * NaN must not reach a sum
@@ -729,8 +733,9 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(b_full + 8 * slot);
-        group_sync(4, 128);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_full + 8 * slot);
+        group_sync(4, 256);
         if (ct == 0) mbar_arrive(b_rawEmpty + 8 * raw);
       }
     }
