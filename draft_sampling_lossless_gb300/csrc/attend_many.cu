@@ -42,9 +42,9 @@
 // 515 us for 478; loops of 16 took 499, loads one chunk ahead 507, two threads a row 542.
 // Measured (32 query heads over 8 of 128): two chunks of 2000 rows after 1000 to 7000
 // positions 478 us, 938 TFLOP/s of visible products (49% of the measured matrix rate);
-// three of 700 to 1500, 40 heads, window 2048, e4m3 236 us, 464 TFLOP/s: tiles at the
+// three of 700 to 1500, 40 heads, window 2048, e4m3 233 us, 470 TFLOP/s: tiles at the
 // edges of the windows are computed whole, an item has a dozen tiles, and the codes'
-// conversion takes as many instructions as the softmax (four warps for it: 242 us).
+// conversion takes as many instructions as the softmax (four warps for it: 6 us more).
 #include "attend.cuh"
 
 namespace dspark {
@@ -214,8 +214,9 @@ __device__ __forceinline__ void codes_to_bf16(const uint32_t (&w)[4], uint32_t f
     nan |= (w[j] & 0x7f7f7f7fu) + 0x01010101u;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const uint32_t t = __byte_perm(w[j], 0, k ? 0x3424 : 0x1404);
-      const uint32_t u = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
+      uint32_t u;  // two codes with their signs over the bytes above, four bits up
+      asm("prmt.b32 %0, %1, 0, %2;" : "=r"(u) : "r"(w[j]), "r"(k ? 0xb3a2 : 0x9180));
+      u = (u << 4) & 0x87f087f0u;
       __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u),
                                  *reinterpret_cast<const __nv_bfloat162*>(&f));
       if (two) x = __hmul2(x, *reinterpret_cast<const __nv_bfloat162*>(&g));
