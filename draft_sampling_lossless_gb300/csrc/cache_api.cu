@@ -240,7 +240,10 @@ int dspark_attend(const dspark_cache* cache, int R, int T, int Hq, int max_rows,
   a.Hq = Hq;
   a.max_rows = max_rows == 0 || max_rows > T ? T : max_rows;
   a.causal = causal != 0;
-  a.window = window;
+  // No position reaches 2^30 + 2^24 (pages, then rows): a larger window is the same one, and
+  // the kernels' 32-bit differences of positions and windows hold.
+  constexpr int kWidest = (1 << 30) + (1 << 24);
+  a.window = window < kWidest ? window : kWidest;
   a.scale = scale;
   a.q = q;
   a.q_stride = q_stride;
