@@ -12,8 +12,10 @@
 // sums its own exponentials, joined over the positions once, at the end.
 // P = 2^(s - m) against a reference m of each row, the maximum of the first tile of
 // the row's part.  Any reference gives the same quotient as long as P stays in
-// range; where a score passes it by 64 powers of two (8 in e4m3, which has less
+// range; where a score passes it by 24 powers of two (8 in e4m3, which has less
 // range), the row's reference moves to the tile's maximum, O and the sum with it.
+// (24 and not the 64 that sums of P alone would allow: a value up to 2^80 times such a P
+// still leaves O finite over 2^24 positions.)
 //
 // bf16: P enters its product as two bf16 terms, its rounding and the rounding of the
 // rest (columns of N side by side; a row that one position dominates would
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   constexpr int NS = F::kSlots, NK = F::kSlotsK, NV = F::kSlotsV, NH = F::kNH, SB = F::kSBufs;
   // P's largest exponent (e4m3 ends at 448); rows above half of it move along with one
   // that passed it
-  constexpr float kLimit = E4M3 ? 8.f : 64.f;
+  constexpr float kLimit = E4M3 ? 8.f : 24.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc* ms = reinterpret_cast<Misc*>(smem + F::kMiscOff);
   const uint32_t b_full = smem_u32(ms->bars), b_empty = b_full + 8 * NS;
