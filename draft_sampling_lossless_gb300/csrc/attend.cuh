@@ -188,6 +188,95 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// 16 e4m3 codes as packed bf16 times 2^(byte - 127), exact but for what falls below
+// bf16's range.  Code s eeee mmm moved to s 0000eeee mmm0000 is its value times 2^-120: the
+// factor 2^(byte - 7) makes up for that, in two steps where it passes bf16's range.
+__device__ __forceinline__ void codes_to_bf16(const uint32_t (&w)[4], uint32_t byte,
+                                              uint32_t (&out)[8]) {
+  byte = min(byte, 253u);
+  const uint32_t e = min(byte + 120u, 254u), f = (e << 7) | (e << 23);
+  uint32_t nan = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    nan |= (w[j] & 0x7f7f7f7fu) + 0x01010101u;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t u;  // two codes with their signs over the bytes above, four bits up
+      asm("prmt.b32 %0, %1, 0, %2;" : "=r"(u) : "r"(w[j]), "r"(k ? 0xb3a2 : 0x9180));
+      u = (u << 4) & 0x87f087f0u;
+      const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&f));
+      out[2 * j + k] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+  }
+  if (byte > 134u) {
+    const uint32_t g = (byte - 7u) * 0x00800080u;  // 2^(byte - 134), both halves
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(out + j),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&g));
+      out[j] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+  }
+  if (nan & 0x80808080u) {  // a code without a value
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t t = (w[j] & 0x7f7f7f7fu) + 0x01010101u;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t u;  // the bytes' top bits over two bytes each
+        asm("prmt.b32 %0, %1, 0, %2;" : "=r"(u) : "r"(t), "r"(k ? 0xbbaa : 0x9988));
+        out[2 * j + k] |= u & 0x7fff7fffu;
+      }
+    }
+  }
+}
+
+// Turns tiles of codes (128 bytes a row, as the TMA swizzles them) into bf16 tiles.  Eight
+// lanes that access shared memory together take four chunks of 16 codes of two rows, r and
+// r ^ 5 of a group of eight: their reads, and the even and the odd halves of their writes,
+// fall in different banks.
+template <int DP, int WARPS>
+struct Converter {
+  static constexpr int kStep = (DP > 64 ? 4 : 8) * WARPS;  // rows a step
+  int row;            // of the first step
+  uint32_t from, to;  // its codes, its first 8 values (the others 16 bytes ^ on)
+  __device__ __forceinline__ Converter(int warp, int lane) {
+    const int c = ((lane >> 1) & 3) | (DP > 64 ? (lane >> 1) & 4 : 0);
+    const int p = DP > 64 ? (lane >> 4) | ((warp & 1) << 1) : lane >> 3;
+    const int r = lane & 1 ? p ^ 5 : p;
+    row = (DP > 64 ? warp >> 1 : warp) * 8 + r;
+    from = row * 128 + ((c ^ r) << 4);
+    to = (c >> 2) * kHalf + row * 128 + ((((c & 3) * 2) ^ r) << 4);
+  }
+  // `lo`, `hi`: rows outside become zeros (0 * NaN must not reach a sum).
+  __device__ __forceinline__ void operator()(const uint8_t* src, const uint8_t* exps,
+                                             uint8_t* dst, int lo, int hi) const {
+    const bool edge = lo > 0 || hi < kBN;
+    src += from;
+    exps += row;
+    uint4 next = *reinterpret_cast<const uint4*>(src);
+    uint32_t byte = *exps;
+#pragma unroll 1
+    for (int k = 0; k < kBN / kStep; ++k) {
+      uint32_t w[4] = {next.x, next.y, next.z, next.w}, h[8];
+      const uint32_t b = byte;
+      src += kStep * 128;
+      exps += kStep;
+      if (k + 1 < kBN / kStep) {
+        next = *reinterpret_cast<const uint4*>(src);
+        byte = *exps;
+      }
+      const int r = row + k * kStep;
+      if (edge && (r < lo || r >= hi)) w[0] = w[1] = w[2] = w[3] = 0;
+      codes_to_bf16(w, b, h);
+      *reinterpret_cast<uint4*>(dst + to) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(dst + (to ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+      dst += kStep * 128;
+    }
+  }
+};
+
 // Blocks 0 .. ctas-1 take `each` units (tiles and items' costs), the first `extra` of
 // them one more.
 struct Found {  // the request that holds a unit, from the thread that finds it

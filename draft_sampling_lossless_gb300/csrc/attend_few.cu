@@ -12,28 +12,32 @@
 // sums its own exponentials, joined over the positions once, at the end.
 // P = 2^(s - m) against a reference m of each row, the maximum of the first tile of
 // the row's part.  Any reference gives the same quotient as long as P stays in
-// range; where a score passes it by 24 powers of two (8 in e4m3, which has less
-// range), the row's reference moves to the tile's maximum, O and the sum with it.
+// range; where a score passes it by 24 powers of two, the row's reference moves to the
+// tile's maximum, O and the sum with it.
 // (24 and not the 64 that sums of P alone would allow: a value up to 2^80 times such a P
 // still leaves O finite over 2^24 positions.)
 //
-// bf16: P enters its product as two bf16 terms, its rounding and the rounding of the
-// rest (columns of N side by side; a row that one position dominates would
-// otherwise carry that rounding straight into the result).
+// P enters its product as two bf16 terms, its rounding and the rounding of the rest
+// (columns of N side by side): 16 bits of it however small it is.  A row that one position
+// dominates would otherwise carry that rounding straight into the result, and a long
+// context beside one dominant position is a sum of small P.
 //
-// e4m3: the codes are multiplied as they are stored.  Q comes as two e4m3 terms,
-// q 2^-a = q1 + q2 / 16, which hold a bf16's eight bits exactly (down to
-// 2^-13 of the row's largest; below, to 2^-21 of it), P as four, each the
-// rounding of what the ones before left, times 16 (16 bits; all of it down to 2^-21).
-// A position's scales are its thread's own: K's a factor of the scores; V's, with
-// exponent e, goes into P = 2^(s + e - m), and l sums 2^-e P.
+// e4m3: K's codes are multiplied as they are stored.  Q comes as two e4m3 terms,
+// q 2^-a = q1 + q2 / 16, which hold a bf16's eight bits exactly (down to 2^-13 of the row's
+// largest; below, to 2^-21 of it); a position's scale is its thread's own, a factor of
+// the scores.  V's codes become bf16 on the way, scales and all (exact).  P as e4m3 terms
+// over V's codes (four of them) was as fast over 32 rows and took 124 us for 256 single
+// tokens instead of 150, but its range ends at 2^-22 of the reference: what lies below was
+// in l and not in O.
 //
 // Two streams, each a warpgroup with its own P, O and m, take alternate tiles.
 // Roles: warps 0-7 softmax, one warp issues the MMAs of the scores (as many tiles ahead
 // as S has buffers, over the ends of items too), two load K and V through a ring each,
-// one fetches the next item's Q and the scales, one issues the MMAs of O.  One thread
-// for both products was not enough: its MMAs (64 cycles each), commits and waits took
-// as long as a tile of e4m3 does (8 verified rows of bf16: 191 us, with two 184).
+// one fetches the next item's Q and the scales, one issues the MMAs of O; e4m3: eight
+// convert V into a ring of three tiles (four warps: 184 us for single tokens; two tiles:
+// 159).  One thread for both products was not enough: its MMAs (64 cycles each), commits
+// and waits took as long as a tile of e4m3 does (8 verified rows of bf16: 191 us, with two
+// 184, at the time).
 // What a tile costs besides the loads is fetching instructions: with the loops over
 // rows unrolled, the blocks' roles asked for more than the instruction caches give
 // (23% of the fetches missed the SM's, the next level ran at 90% of its rate), and
@@ -43,9 +47,9 @@
 // Measured (32 query heads over 8 of 128, of the measured copy rate):
 //   64 requests of 1 to 8 rows, 500 to 8000 positions  180 us, 6.3 TB/s, 93%
 //   3 of 5 to 8 rows, 90 to 180 thousand positions     221 us, 6.8 TB/s, 100%
-//   the first, e4m3: 186 us, 3.2 TB/s, 47%; 256 single tokens, e4m3: 125 us, 4.5 TB/s,
-//     67%: the softmax threads' instructions (P's four terms take half of them) and
-//     the moves of references bound it
+//   the first, e4m3: 184 us, 3.2 TB/s, 48%; 256 single tokens, e4m3: 150 us, 3.8 TB/s,
+//     56%: the softmax threads' chains of instructions, which the converting warps'
+//     instructions stretch (half of all issue slots are taken)
 //   64 drafter's blocks of 7 rows, 16 heads over 8 of 64: 60 us, 4.9 TB/s, 72%: the
 //     ends of items
 //   one token, 700 positions: 11 us, latency: the plan of the work (2 us), the first
@@ -65,29 +69,32 @@ template <int DP, int NR, bool E4M3>
 struct Few {
   static constexpr int kSoft = 256;  // softmax threads, two warpgroups; then five warps
   static constexpr int kWarpS = kSoft / 32, kWarpTma = kWarpS + 1, kWarpO = kWarpS + 4;
-  static constexpr int kThreads = kSoft + 160;
+  static constexpr int kConv = E4M3 ? 8 : 0;  // warps that convert V
+  static constexpr int kThreads = kSoft + 160 + 32 * kConv;
   static constexpr int kNH = DP / 64;
-  static constexpr int kParts = E4M3 ? 4 : 2;                         // terms of P
-  static constexpr int kPN = (kParts * NR + 15) / 16 * 16;            // N of the products
+  static constexpr int kPN = 2 * NR;                                  // N of the products
   static constexpr int kQRows = E4M3 ? 2 * NR : (NR < 16 ? 16 : NR);  // N of the scores
-  static constexpr int kSBufs = E4M3 ? 3 : 4;  // tiles of scores ahead
+  static constexpr int kSBufs = 4;  // tiles of scores ahead
   // tensor memory: S, 64 columns each, then O of the streams, then the positions' own
   // sums, l
-  static constexpr uint32_t kColO = 64 * kSBufs, kOCols = E4M3 ? 128 : 64;
+  static constexpr uint32_t kColO = 64 * kSBufs, kOCols = 64;
   static constexpr uint32_t kColL = kColO + 2 * kOCols;
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kSlot = E4M3 ? kHalf : kHalf * kNH;       // a tile
+  static constexpr uint32_t kTile = kHalf * kNH;                      // a tile of bf16
+  static constexpr uint32_t kSlot = E4M3 ? kHalf : kTile;             // a tile as loaded
+  static constexpr int kConvSlots = E4M3 ? (kNH > 1 ? 3 : 4) : 0;     // tiles converted
   static constexpr uint32_t kQHalf = kQRows * 128;
   static constexpr uint32_t kQBytes = kQHalf * (E4M3 ? 1 : kNH);
   static constexpr uint32_t kExp = E4M3 ? kExpDepth * 256 : 0;
   static constexpr uint32_t kMisc = 4096;
   static constexpr int kFit =
-      (int)((kMaxSmem - 2 * kHalf - 2 * kQBytes - kExp - kMisc) / kSlot);
+      (int)((kMaxSmem - 2 * kHalf - kConvSlots * kTile - 2 * kQBytes - kExp - kMisc) / kSlot);
   static constexpr int kSlots = kFit > 12 ? 12 : kFit;
   static constexpr int kSlotsK = kSlots / 2, kSlotsV = kSlots - kSlotsK;
   // P of each stream (at an item's end its O, then the join's buffer)
   static constexpr uint32_t kPOff = kSlots * kSlot;
-  static constexpr uint32_t kQOff = kPOff + 2 * kHalf;
+  static constexpr uint32_t kConvOff = kPOff + 2 * kHalf;
+  static constexpr uint32_t kQOff = kConvOff + kConvSlots * kTile;
   static constexpr uint32_t kExpOff = kQOff + 2 * kQBytes;
   static constexpr uint32_t kMiscOff = kExpOff + kExp;
   static constexpr uint32_t kTotal = kMiscOff + kMisc;
@@ -102,7 +109,7 @@ struct Misc {  // shared words
   int64_t sum[32];
   Found found[2];
   Segment seg[kSegDepth];
-  uint64_t bars[2 * 12 + 2 * kSegDepth + 4 + 4 + 8 + 2 * kExpDepth + 2];
+  uint64_t bars[2 * 12 + 2 * kSegDepth + 4 + 8 + 4 + 2 * kExpDepth + 2 * 4 + 2];
   int abort_flag, last;
   uint32_t tmem;
 };
@@ -127,29 +134,17 @@ __device__ __forceinline__ float reduce_rows(float (&v)[NR], Op op) {
   return v[0];
 }
 
-// Two values as four e4m3 terms each: v = t0 + t1 / 16 + t2 / 256 + t3 / 4096.
-__device__ __forceinline__ void e4m3_terms(float a, float b, uint32_t (&t)[4]) {
-  const unsigned long long up = pack2(16.f, 16.f), down = pack2(-16.f, -16.f);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    t[k] = e4m3x2(a, b);
-    if (k == 3) break;
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)t[k]));
-    const float2 g = __half22float2(*reinterpret_cast<__half2*>(&h));
-    unpack2(fma2(pack2(g.x, g.y), down, mul2(pack2(a, b), up)), a, b);
-  }
-}
-
 template <int DP, int NR, bool E4M3>
 __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     attend_few_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
   using F = Few<DP, NR, E4M3>;
   constexpr int NS = F::kSlots, NK = F::kSlotsK, NV = F::kSlotsV, NH = F::kNH, SB = F::kSBufs;
-  // P's largest exponent (e4m3 ends at 448); rows above half of it move along with one
-  // that passed it
-  constexpr float kLimit = E4M3 ? 8.f : 24.f;
+  // V as it is multiplied: as loaded, or converted
+  constexpr int NM = E4M3 ? F::kConvSlots : NV;
+  constexpr uint32_t kVOff = E4M3 ? F::kConvOff : NK * F::kSlot;
+  // P's largest exponent; rows above half of it move along with one that passed it
+  constexpr float kLimit = 24.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc* ms = reinterpret_cast<Misc*>(smem + F::kMiscOff);
   const uint32_t b_full = smem_u32(ms->bars), b_empty = b_full + 8 * NS;
@@ -157,7 +152,11 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   const uint32_t b_qFull = b_segEmpty + 8 * kSegDepth, b_qEmpty = b_qFull + 16;
   const uint32_t b_s = b_qEmpty + 16, b_sFree = b_s + 32, b_p = b_sFree + 32, b_o = b_p + 16;
   const uint32_t b_expFull = b_o + 16, b_expEmpty = b_expFull + 8 * kExpDepth;
-  const uint32_t b_drain = b_expEmpty + 8 * kExpDepth;
+  const uint32_t b_conv = b_expEmpty + 8 * kExpDepth, b_convFree = b_conv + 8 * F::kConvSlots;
+  const uint32_t b_drain = b_convFree + 8 * F::kConvSlots;
+  // V's tiles: ready for the product, and no longer read by it
+  const uint32_t b_v = E4M3 ? b_conv : b_full + 8 * NK;
+  const uint32_t b_vFree = E4M3 ? b_convFree : b_empty + 8 * NK;
   volatile int* s_abort = &ms->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023) return;  // never: the declared alignment, which the swizzle needs
@@ -166,12 +165,15 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   if (warp == F::kWarpS) {
     for (uint32_t bar = b_full + 8 * lane; bar <= b_drain + 8; bar += 8 * 32) {
       uint32_t n = 1;
-      if (bar >= b_segEmpty && bar < b_qFull) n = 4 + F::kSoft / 32;  // all but the warp that fills
+      if (E4M3 && bar >= b_empty + 8 * NK && bar < b_segFull) n = F::kConv;
+      else if (bar >= b_segEmpty && bar < b_qFull)
+        n = 4 + F::kConv + F::kSoft / 32;  // all but the warp that fills
       else if (bar >= b_qFull && bar < b_qEmpty) n = 32;
       else if (E4M3 && bar >= b_qEmpty && bar < b_s) n = 1 + F::kSoft / 32;  // a's readers
       else if (bar >= b_sFree && bar < b_o) n = F::kSoft / 64;  // a stream's warps
       else if (bar >= b_expFull && bar < b_expEmpty) n = 32;
-      else if (bar >= b_expEmpty && bar < b_drain) n = F::kSoft / 64;
+      else if (bar >= b_expEmpty && bar < b_conv) n = F::kSoft / 64 + F::kConv;
+      else if (bar >= b_conv && bar < b_convFree) n = F::kConv;
       mbar_init(bar, n);
     }
     if (lane == 0) *s_abort = 0;
@@ -289,10 +291,9 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
     // ------------------------------------------------------------ outputs
     if (elect_one()) {
       constexpr uint32_t kIdO =
-          (E4M3 ? idesc_0_f32(128, F::kPN) : idesc_bf16_f32(128, F::kPN)) | kIdescTransposeA |
-          kIdescTransposeB;
+          idesc_bf16_f32(128, F::kPN) | kIdescTransposeA | kIdescTransposeB;
       // D = 64: both groups of 64 MMA rows read the same values
-      const uint64_t v0 = desc_mnmajor_sw128(smem_u32(smem) + NK * F::kSlot, NH > 1 ? kHalf : 0);
+      const uint64_t v0 = desc_mnmajor_sw128(smem_u32(smem) + kVOff, NH > 1 ? kHalf : 0);
       const uint64_t p0 = desc_mnmajor_sw128(smem_u32(smem) + F::kPOff, 0);
       uint32_t at = 0, parity = 0, ph_p = 0;
       bool ok = true;
@@ -307,26 +308,22 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
           const int s = i & 1;
-          ok = wait_bar(b_full + 8 * (NK + at), parity, s_abort) &&
+          ok = wait_bar(b_v + 8 * at, parity, s_abort) &&
                wait_bar(b_p + 8 * s, (ph_p >> s) & 1, s_abort);
           if (!ok) break;
           ph_p ^= 1u << s;
           tc_fence_after();
-          uint64_t a = v0 + at * (F::kSlot >> 4), b = p0 + s * (kHalf >> 4);
+          uint64_t a = v0 + at * (F::kTile >> 4), b = p0 + s * (kHalf >> 4);
           const uint32_t o = tmem + F::kColO + s * F::kOCols;
-          constexpr int kSteps = kBN / (E4M3 ? 32 : 16);  // of 4096 or 2048 bytes
 #pragma unroll 2
-          for (int k = 0; k < kSteps; ++k) {
-            if constexpr (E4M3)
-              mma_e4m3(o, a, b, kIdO, i >= 2 || k > 0);
-            else
-              mma_bf16(o, a, b, kIdO, i >= 2 || k > 0);
-            a += kHalf / kSteps >> 4;
-            b += kHalf / kSteps >> 4;
+          for (int k = 0; k < kBN / 16; ++k) {  // steps of 16 positions, 2048 bytes
+            mma_bf16(o, a, b, kIdO, i >= 2 || k > 0);
+            a += 2048 >> 4;
+            b += 2048 >> 4;
           }
-          mma_commit(b_empty + 8 * (NK + at));
+          mma_commit(b_vFree + 8 * at);
           mma_commit(b_o + 8 * s);
-          if (++at == NV) {
+          if (++at == NM) {
             at = 0;
             parity ^= 1;
           }
@@ -394,18 +391,15 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
 #pragma unroll 1
       for (int i = s; i < sg.ntiles; i += 2) {
         const int t0 = (sg.tile0 + i) * kBN;
-        float ck = 0.f, ev = 0.f, un = 1.f;
+        float ck = 0.f;
         if constexpr (E4M3) {
-          // scales of this thread's position (any byte gives finite factors)
+          // the scale of this thread's key (any byte gives a finite factor)
           const uint32_t q = (base + i) % kExpDepth;
           wait_bar(b_expFull + 8 * q, ((base + i) / kExpDepth) & 1, s_abort);
-          const uint8_t* ex = smem + F::kExpOff + q * 256 + pt;
-          const int ek = min(max((int)ex[0], 1), 254), ee = min(max((int)ex[128], 1), 253);
+          const int ek = min(max((int)smem[F::kExpOff + q * 256 + pt], 1), 254);
           __syncwarp();
           if (lane == 0) mbar_arrive(b_expEmpty + 8 * q);
           ck = __uint_as_float((uint32_t)ek << 23);
-          ev = (float)(ee - 127);
-          un = __uint_as_float((uint32_t)(254 - ee) << 23);
         }
         const uint32_t sb = (base + i) % SB, t_s = tmem + lanes + sb * 64;
         wait_bar(b_s + 8 * sb, ((base + i) / SB) & 1, s_abort);
@@ -427,9 +421,9 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
             }
           }
         }
-        // The logarithms to base 2 of the rows' exponentials (e4m3: times 2^e of the
-        // value's exponent e), back to S, and whether one passes its reference by too
-        // much.  Eights of rows that the item does not have are left out throughout.
+        // The logarithms to base 2 of the rows' exponentials, back to S, and whether one
+        // passes its reference by too much.  Eights of rows that the item does not have are
+        // left out throughout.
         float top = -INFINITY;
 #pragma unroll 1
         for (int r0 = 0; r0 < sg.nrows; r0 += 8) {
@@ -447,7 +441,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
                   fma2(pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
                        pack2(0.0625f, 0.0625f),
                        pack2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])));
-              unpack2(fma2(mul2(x, pack2(a.x, a.y)), pack2(ck, ck), pack2(ev, ev)), y[k], y[k + 1]);
+              unpack2(mul2(mul2(x, pack2(a.x, a.y)), pack2(ck, ck)), y[k], y[k + 1]);
             }
           } else {
             tmem_wait_ld_regs(u);
@@ -520,7 +514,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
               for (int k = 0; k < 8; ++k) v[k] *= w[k];
               store_l(r0, v);
 #pragma unroll 1
-              for (int q = 0; q < F::kParts; ++q) {
+              for (int q = 0; q < 2; ++q) {
                 uint32_t o[8];
                 tmem_ld_32x32b_x8(t_o + q * NR + r0, o);
                 tmem_wait_ld_regs(o);
@@ -543,44 +537,24 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             u[k] = __float_as_uint(ex2_approx(__uint_as_float(u[k]) + nm[r0 + k]));
-          if constexpr (E4M3) {
-            uint32_t t[4][4];
+          uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float a = __uint_as_float(u[2 * k]), b = __uint_as_float(u[2 * k + 1]);
-              l[2 * k] = fmaf(a, un, l[2 * k]);
-              l[2 * k + 1] = fmaf(b, un, l[2 * k + 1]);
-              uint32_t c[4];
-              e4m3_terms(a, b, c);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) t[q][k] = c[q];
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int at = q * NR + r0;
-              *reinterpret_cast<uint2*>(my_p + (((at >> 4) ^ (pt & 7)) << 4) + (at & 8)) =
-                  make_uint2(t[q][0] | (t[q][1] << 16), t[q][2] | (t[q][3] << 16));
-            }
-          } else {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float a = __uint_as_float(u[2 * k]), b = __uint_as_float(u[2 * k + 1]);
-              l[2 * k] += a;
-              l[2 * k + 1] += b;
-              hi[k] = pack_bf16(a, b);
-              lo[k] = pack_bf16(a - __uint_as_float(hi[k] << 16),
-                                b - __uint_as_float(hi[k] & 0xffff0000u));
-            }
-            *reinterpret_cast<uint4*>(my_p + (((r0 >> 3) ^ (pt & 7)) << 4)) =
-                make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(my_p + ((((NR + r0) >> 3) ^ (pt & 7)) << 4)) =
-                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          for (int k = 0; k < 4; ++k) {
+            const float a = __uint_as_float(u[2 * k]), b = __uint_as_float(u[2 * k + 1]);
+            l[2 * k] += a;
+            l[2 * k + 1] += b;
+            hi[k] = pack_bf16(a, b);
+            lo[k] = pack_bf16(a - __uint_as_float(hi[k] << 16),
+                              b - __uint_as_float(hi[k] & 0xffff0000u));
           }
+          *reinterpret_cast<uint4*>(my_p + (((r0 >> 3) ^ (pt & 7)) << 4)) =
+              make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(my_p + ((((NR + r0) >> 3) ^ (pt & 7)) << 4)) =
+              make_uint4(lo[0], lo[1], lo[2], lo[3]);
           store_l(r0, l);
         }
-        // values that no row sees: 0 * NaN must not reach a sum
-        if (t0 < sg.lo || t0 + kBN > sg.hi) {
+        // values that no row sees: 0 * NaN must not reach a sum (e4m3: converted to zeros)
+        if (!E4M3 && (t0 < sg.lo || t0 + kBN > sg.hi)) {
           const uint32_t slot = NK + (base + i) % NV;
           wait_bar(b_full + 8 * slot, ((base + i) / NV) & 1, s_abort);
           if (t0 + pt < sg.lo || t0 + pt >= sg.hi) {
@@ -621,20 +595,14 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         const float sum = reduce_rows<8>(v, [](float a, float b) { return a + b; });
         if (lane % 4 == 0) ms->wm[s][warp & 3][r0 + lane / 4] = sum;
         if (has) {
-          uint32_t u[F::kParts][8];
+          uint32_t hi[8], lo[8];
+          tmem_ld_32x32b_x8(t_o + r0, hi);
+          tmem_ld_32x32b_x8(t_o + NR + r0, lo);
+          tmem_wait_ld_regs(hi, lo);
+          if (pt < DP)
 #pragma unroll
-          for (int q = 0; q < F::kParts; ++q) tmem_ld_32x32b_x8(t_o + q * NR + r0, u[q]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float x = 0.f;
-#pragma unroll
-            for (int q = F::kParts - 1; q >= 0; --q) {
-              asm volatile("" : "+r"(u[q][k]));
-              x = fmaf(x, E4M3 ? 0.0625f : 1.f, __uint_as_float(u[q][k]));
-            }
-            if (pt < DP) o_s[(r0 + k) * DP + pt] = x;
-          }
+            for (int k = 0; k < 8; ++k)
+              o_s[(r0 + k) * DP + pt] = __uint_as_float(hi[k]) + __uint_as_float(lo[k]);
         }
       }
       group_sync(1, F::kSoft);
@@ -693,6 +661,44 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         finish_split<DP, 32, F::kSoft, false>(p, sg, &ms->last,
                                               reinterpret_cast<float2*>(smem + F::kPOff));
       tc_fence_before();
+    }
+  } else if (E4M3 && warp > F::kWarpO) {
+    // ------------------------------------------------------------ V's codes to bf16
+    const Converter<DP, F::kConv ? F::kConv : 4> convert(warp - F::kWarpO - 1, lane);
+    uint32_t t = 0, at = 0, parity = 0;  // tiles so far, the ring's slot
+    bool ok = true;
+#pragma unroll 1
+    for (int sn = 0; ok; ++sn) {
+      const int ss = sn % kSegDepth;
+      ok = __all_sync(0xffffffffu, wait_bar(b_segFull + 8 * ss, (sn / kSegDepth) & 1, s_abort));
+      if (!ok) break;
+      const int nt = ms->seg[ss].ntiles, lo = ms->seg[ss].lo, hi = ms->seg[ss].hi;
+      int t0 = ms->seg[ss].tile0 * kBN;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_segEmpty + 8 * ss);
+      if (nt == 0) break;
+#pragma unroll 1
+      for (int i = 0; i < nt; ++i, ++t, t0 += kBN) {
+        const uint32_t q = t % kExpDepth, to = t % NM;
+        ok = wait_bar(b_full + 8 * (NK + at), parity, s_abort) &&
+             wait_bar(b_expFull + 8 * q, (t / kExpDepth) & 1, s_abort) &&
+             wait_bar(b_convFree + 8 * to, ((t / NM) & 1) ^ 1, s_abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        convert(smem + (NK + at) * F::kSlot, smem + F::kExpOff + q * 256 + 128,
+                smem + F::kConvOff + to * F::kTile, lo - t0, hi - t0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(b_conv + 8 * to);
+          mbar_arrive(b_empty + 8 * (NK + at));
+          mbar_arrive(b_expEmpty + 8 * q);
+        }
+        if (++at == NV) {
+          at = 0;
+          parity ^= 1;
+        }
+      }
     }
   } else {
     // ------------------------------------------------------------ Q, e4m3's scales
@@ -775,8 +781,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
       mbar_arrive(b_qFull + 8 * qb);
       if constexpr (!E4M3) continue;
       // the exponent bytes of K and V, four positions a lane; a tile's are loaded while
-      // those of the one before wait for room.  Where no row looks, any scale does, but
-      // not one that moves the references.
+      // those of the one before wait for room.  Where no row looks, any scale does.
       const int log_page = p.c.log_page, end_pos = min(sg.hi, p.c.max_pages << log_page);
       const int32_t* table = p.c.pages + (int64_t)sg.n * p.c.max_pages;
       auto page = [&](int pos) {

@@ -203,34 +203,6 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int to, int t
           make_uint4(0, 0, 0, 0);
 }
 
-// 16 e4m3 codes as packed bf16 times f (and times g where more than f's range is
-// needed): code s eeee mmm moved to s 0000eeee mmm0000 is the value times 2^-120,
-// which f makes up for.
-__device__ __forceinline__ void codes_to_bf16(const uint32_t (&w)[4], uint32_t f, bool two,
-                                              uint32_t g, uint32_t (&out)[8]) {
-  uint32_t nan = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    nan |= (w[j] & 0x7f7f7f7fu) + 0x01010101u;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint32_t u;  // two codes with their signs over the bytes above, four bits up
-      asm("prmt.b32 %0, %1, 0, %2;" : "=r"(u) : "r"(w[j]), "r"(k ? 0xb3a2 : 0x9180));
-      u = (u << 4) & 0x87f087f0u;
-      __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u),
-                                 *reinterpret_cast<const __nv_bfloat162*>(&f));
-      if (two) x = __hmul2(x, *reinterpret_cast<const __nv_bfloat162*>(&g));
-      out[2 * j + k] = *reinterpret_cast<const uint32_t*>(&x);
-    }
-  }
-  if (nan & 0x80808080u) {  // a code without a value
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (((w[j >> 2] >> (8 * (j & 3))) & 0x7fu) == 0x7fu)
-        out[j >> 1] |= 0x7fffu << (16 * (j & 1));
-  }
-}
-
 template <int DP, bool E4M3>
 __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
     attend_many_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -689,7 +661,8 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
   } else if (E4M3) {
     reg_dec<72>();
     // ------------------------------------------------------------ codes to bf16
-    const int ct = tid - 384, c = ct & 7;  // 8 lanes a row of 128 codes, 16 codes a lane
+    const int ct = tid - 384;
+    const Converter<DP, 8> convert(ct >> 5, lane);
     uint32_t e = 0;
     for (int sn = 0;; ++sn) {
       const int ss = sn % kSegDepth;
@@ -704,35 +677,10 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
       for (int i = 0; i < 2 * nt; ++i, ++e) {
         const uint32_t raw = e % NRAW, slot = e % NS;
         const int t0 = (tile0 + (i >> 1)) * kBN;
-        const bool edge = t0 < lo || t0 + kBN > hi;
         wait_bar(b_rawFull + 8 * raw, (e / NRAW) & 1, s_abort);
         wait_bar(b_empty + 8 * slot, ((e / NS) & 1) ^ 1, s_abort);
-        const uint8_t* src = smem + F::kRawOff + raw * kHalf;
-        const uint8_t* exps = smem + F::kExpOff + raw * 128;
-        uint8_t* dst = s_kv + slot * F::kTile;
-#pragma unroll 2
-        for (int k = 0; k < 4; ++k) {
-          const int row = k * 32 + (ct >> 3);
-          const uint4 v = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
-          uint32_t w[4] = {v.x, v.y, v.z, v.w}, h[8];
-          // positions that no row sees are zeros: 0 * NaN must not reach a sum
-          if (edge && (t0 + row < lo || t0 + row >= hi)) w[0] = w[1] = w[2] = w[3] = 0;
-          // 2^(byte - 127 + 120), as two factors past bf16's range
-          const uint32_t byte = min((uint32_t)exps[row], 253u);
-          const uint32_t f = min(byte + 120u, 254u), g = byte + 247u - f;
-          codes_to_bf16(w, (f << 7) | (f << 23), byte > 134, (g << 7) | (g << 23), h);
-          if (c < DP / 16) {
-            // lanes 0-3 and 4-7 of a row write chunks of the two halves of D: even ones
-            // and odd ones first, so that the eight fall in different banks
-            uint8_t* to = dst + (c >> 2) * kHalf + row * 128;
-            const int first = 2 * (c & 3) + (c >> 2), second = first ^ 1;
-            const bool odd = c >> 2;
-            *reinterpret_cast<uint4*>(to + ((first ^ (row & 7)) << 4)) =
-                odd ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(to + ((second ^ (row & 7)) << 4)) =
-                odd ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
-          }
-        }
+        convert(smem + F::kRawOff + raw * kHalf, smem + F::kExpOff + raw * 128,
+                s_kv + slot * F::kTile, lo - t0, hi - t0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_full + 8 * slot);

@@ -512,8 +512,10 @@ int dspark_cache_read(const dspark_cache* cache, int R, int T, const int32_t* ro
  *         DSPARK_DEVFLAG_ROW_RANGE.
  *   scale finite and > 0
  * Products are exact, sums and softmax statistics fp32.  A probability has 16
- * bits in the product with v (two bf16 terms; over e4m3 in up to 32 rows of a
- * group four e4m3 terms, and there q has two); the result is rounded once to bf16.
+ * bits in the product with v (two bf16 terms), however small it is; the result is
+ * rounded once to bf16.  Over e4m3, where max_rows * Hq / Hkv <= 32, q enters its
+ * products as two e4m3 terms: what a row's values have below 2^-21 of its largest
+ * is rounded away.
  * Positions that no row of the request sees are never part of a sum, whatever
  * is stored there.  A NaN or infinity stored at a visible position may also
  * reach those rows of the same request that do not see it yet.  Results are
