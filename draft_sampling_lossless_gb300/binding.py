@@ -340,6 +340,13 @@ def dspark_check_wait_timeout(limit_us, ws, stream=None):
            lib().dspark_check_wait_timeout(int(limit_us), _p(ws), ws.numel(), _stream(stream)))
 
 
+def _on_gpu(t):
+    """t's address; the kernels follow whatever they are given."""
+    if not t.is_cuda:
+        raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
+    return t.data_ptr()
+
+
 def _rows(t, Hx, D):
     """Pointer and row stride of a [T, Hx, D] bf16 tensor whose rows are packed
     heads and may lie apart (a slice of one projection's output)."""
@@ -348,13 +355,20 @@ def _rows(t, Hx, D):
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != D and Hx > 1):
         raise ValueError("the heads of a row must be contiguous")
-    return t.data_ptr(), (s0 if t.shape[0] > 1 else Hx * D)
+    return _on_gpu(t), (s0 if t.shape[0] > 1 else Hx * D)
 
 
 def _i32(t, n, what):
     if t.dtype != torch.int32 or not t.is_contiguous() or t.shape[0] != n:
         raise ValueError(f"{what} must be a contiguous int32 tensor with {n} entries")
-    return t.data_ptr()
+    return _on_gpu(t)
+
+
+def _ws(ws):
+    """Address and bytes of a workspace."""
+    if not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return _on_gpu(ws), ws.numel() * ws.element_size()
 
 
 def cache_init(k, v, k_exp=None, v_exp=None) -> KVCache:
@@ -369,6 +383,8 @@ def cache_init(k, v, k_exp=None, v_exp=None) -> KVCache:
         for t in (k_exp, v_exp):
             if t is None or t.dtype != torch.uint8 or t.shape != k.shape[:3]:
                 raise ValueError("k_exp and v_exp must be uint8 [n_pages, Hkv, page]")
+    for t in (k, v, k_exp, v_exp) if e4m3 else (k, v):
+        _on_gpu(t)
     n_pages, Hkv, page, D = k.shape
     c = KVCache()
     _check("dspark_cache_init", lib().dspark_cache_init(
@@ -389,7 +405,7 @@ def dspark_cache_append(cache, Hkv, D, k, v, row_off, ctx, pages, ws, stream=Non
     vp, vs = _rows(v, Hkv, D)
     _check("dspark_cache_append", lib().dspark_cache_append(
         cache, R, T, kp, ks, vp, vs, _i32(row_off, R + 1, "row_off"), _i32(ctx, R, "ctx"),
-        _i32(pages, R, "pages"), pages.shape[1], ws.data_ptr(), ws.numel(), _raw_stream(stream)))
+        _i32(pages, R, "pages"), pages.shape[1], *_ws(ws), _raw_stream(stream)))
 
 
 def dspark_cache_read(cache, Hkv, D, row_off, start, pages, k_out, v_out, ws, stream=None):
@@ -399,8 +415,8 @@ def dspark_cache_read(cache, Hkv, D, row_off, start, pages, k_out, v_out, ws, st
             raise ValueError(f"k_out and v_out must be contiguous bf16 tensors [T, {Hkv}, {D}]")
     _check("dspark_cache_read", lib().dspark_cache_read(
         cache, R, T, _i32(row_off, R + 1, "row_off"), _i32(start, R, "start"),
-        _i32(pages, R, "pages"), pages.shape[1], k_out.data_ptr(), v_out.data_ptr(),
-        ws.data_ptr(), ws.numel(), _raw_stream(stream)))
+        _i32(pages, R, "pages"), pages.shape[1], _on_gpu(k_out), _on_gpu(v_out), *_ws(ws),
+        _raw_stream(stream)))
 
 
 def dspark_attend(cache, D, q, row_off, ctx, pages, out, lse, scale, causal, window, max_rows, ws,
@@ -415,5 +431,5 @@ def dspark_attend(cache, D, q, row_off, ctx, pages, out, lse, scale, causal, win
         raise ValueError("lse must be a contiguous fp32 tensor [T, Hq]")
     _check("dspark_attend", lib().dspark_attend(
         cache, R, T, Hq, max_rows, scale, causal, window, qp, qs, _i32(row_off, R + 1, "row_off"),
-        _i32(ctx, R, "ctx"), _i32(pages, R, "pages"), pages.shape[1], out.data_ptr(),
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream)))
+        _i32(ctx, R, "ctx"), _i32(pages, R, "pages"), pages.shape[1], _on_gpu(out),
+        None if lse is None else _on_gpu(lse), *_ws(ws), _raw_stream(stream)))
