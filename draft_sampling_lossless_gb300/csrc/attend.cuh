@@ -31,7 +31,9 @@ constexpr int kMaxSmem = 232448;
 constexpr uint32_t kHalf = kBN * 128;  // bytes of 128 rows of 128 bytes
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWaitTries = 1 << 22;
+// A role may wait for another's whole part of an item, longer than the library's usual
+// second in the largest calls.
+constexpr uint32_t kWaitLimitNs = 4000000000u;
 constexpr uint32_t kCounterOffset = 256;  // workspace: status word, counters, partials
 constexpr uint32_t kPartOffset = 4096;
 constexpr int kItemCost = 2;  // in tiles: Q, the final sums and the store of an item
@@ -134,20 +136,9 @@ struct Segment {  // part of an item that this block computes
 };
 static_assert(sizeof(Segment) == 64, "a segment's words");
 
-// Waits for a phase; gives up when another role has, or after kWaitTries tries (each
-// suspended for a while by the hardware), and tells the others; the block reports
-// that at its end.  Short: it is inlined in every role's loop, and the loops of a
-// block's roles share the instruction caches.
+// A wait that has run out shows in the block's flag; the block reports it at its end.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  int tries = kWaitTries;
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    if (--tries == 0 || *abort_flag) {
-      *abort_flag = 1;
-      return false;
-    }
-  }
-  return true;
+  return mbar_wait_or_abort(bar, parity, abort_flag, kWaitLimitNs);
 }
 
 // Registers a thread after the roles part.

@@ -88,8 +88,23 @@ struct Misc {  // shared words
   uint64_t bars[2 * 12 + 2 * 4 + 2 * kSegDepth + 8];
   int abort_flag, last;
   uint32_t tmem;
+  uint32_t issued[2];  // where each loading warp stopped: its next ring entry
 };
 static_assert(sizeof(Misc) <= 1024, "shared words");
+
+// The last entry of a ring of n slots that was loaded into slot i, where the even entries
+// (K) below k and the odd ones (V) below v were issued; none: a negative number.  In a ring
+// of an odd number of slots K and V take turns in each.
+__host__ __device__ constexpr int last_entry(int i, int n, int k, int v) {
+  const int top = k > v ? k : v;
+  int e = i + (top - i + n - 1) / n * n;
+  while (e >= 0 && e >= (e & 1 ? v : k)) e -= n;
+  return e;
+}
+static_assert(last_entry(0, 5, 0, 1) < 0 && last_entry(0, 5, 2, 1) == 0, "");
+static_assert(last_entry(1, 5, 8, 7) == 6 && last_entry(1, 5, 6, 7) == 1, "K in V's slot or not");
+static_assert(last_entry(4, 5, 10, 7) == 4 && last_entry(3, 5, 10, 9) == 8, "");
+static_assert(last_entry(2, 12, 40, 27) == 38 && last_entry(3, 12, 40, 27) == 15, "");
 
 __device__ __forceinline__ void mask_chunk(uint32_t (&v)[32], int col, int lo, int hi) {
 #pragma unroll
@@ -315,11 +330,7 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
     };
     load_all<kRows>(p, rg, kv == 0, ms->found, ms->seg, b_segFull, b_segEmpty, s_abort, issue,
                     flush);
-    if (*s_abort) {
-      // the copies in flight land before the block's shared memory goes
-      for (uint32_t i = e > kRing ? e - kRing : kv; i < e; ++i)
-        if ((i & 1) == kv) mbar_wait(full0 + 8 * (i % kRing), (i / kRing) & 1);
-    }
+    ms->issued[kv] = e;
   } else if (warp == kWarpMma) {
     if (E4M3) reg_dec<72>();
     else reg_dec<88>();
@@ -691,7 +702,15 @@ __global__ void __launch_bounds__(Many<DP, E4M3>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *s_abort) set_flag(p.c.status, kFlagWaitTimeout);
+  if (tid == 0 && *s_abort) {
+    set_flag(p.c.status, kFlagWaitTimeout);
+    // the copies in flight land before the block's shared memory goes
+    constexpr int kRing = E4M3 ? NRAW : NS;
+    for (int i = 0; i < kRing; ++i) {
+      const int e = last_entry(i, kRing, (int)ms->issued[0], (int)ms->issued[1]);
+      if (e >= 0) mbar_wait((E4M3 ? b_rawFull : b_full) + 8 * i, (e / kRing) & 1);
+    }
+  }
   if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);

@@ -836,7 +836,8 @@ __device__ __forceinline__ void grid_sync(unsigned* ctr, unsigned target, volati
 // towards, each with a short limit.  Both waits must give up, set the
 // timeout bit and let the kernel return; the counter is put back to zero.
 // out[0] = 1 if the mbarrier wait reported success (it must not),
-// out[1] = the abort flag after the grid wait (it must be set).
+// out[1] = the abort flag after the grid wait (it must be set),
+// out[2], out[3] = the same two of the attention kernels' wait.
 __global__ void wait_check_kernel(uint64_t limit_ns, unsigned* ctr, uint32_t* status, int* out) {
   __shared__ __align__(8) uint64_t bar;
   __shared__ int abort_flag;
@@ -853,6 +854,9 @@ __global__ void wait_check_kernel(uint64_t limit_ns, unsigned* ctr, uint32_t* st
     out[0] = ok ? 1 : 0;
     out[1] = abort_flag;
     atomicExch(ctr, 0u);
+    abort_flag = 0;
+    out[2] = mbar_wait_or_abort(smem_u32(&bar), 0, &abort_flag, (uint32_t)limit_ns) ? 1 : 0;
+    out[3] = abort_flag;
   }
 }
 

@@ -388,13 +388,15 @@ int dspark_schedule_noalloc(int R, int gamma, const float* a, const float* sps, 
  * persistent draft's grid barrier) gives up after a time limit, ORs
  * DSPARK_DEVFLAG_TIMEOUT into the status word and lets the kernel return, so
  * a stalled pipeline never leaves the GPU hung.  This call runs those same
- * two waits in a one-block kernel against barriers that nothing completes,
+ * waits (the attention kernels have one of their own) in a one-block kernel
+ * against barriers that nothing completes,
  * each with a limit of limit_us microseconds (1 .. 10^6).  Once the stream
  * reaches it, the status word has DSPARK_DEVFLAG_TIMEOUT set and the device
  * stays usable.  It uses the first 256 bytes of `ws` (at least 256 bytes,
  * 256-byte aligned): the status word at byte 0, a counter at byte 64 that it
- * leaves at zero, and at byte 128 two int32 results (1 if the mbarrier wait
- * claimed success -- it must not -- and 1 if the grid wait gave up).
+ * leaves at zero, and at byte 128 four int32 results (1 if the mbarrier wait
+ * claimed success -- it must not -- and 1 if the grid wait gave up; 1 if the
+ * attention's wait claimed success, and 1 if it told its block to stop).
  * Errors: DSPARK_ERR_INVALID_ARG (limit out of range, NULL or misaligned
  * ws), DSPARK_ERR_WORKSPACE, DSPARK_ERR_CUDA.
  */
