@@ -184,7 +184,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // factor 2^(byte - 7) makes up for that, in two steps where it passes bf16's range.
 __device__ __forceinline__ void codes_to_bf16(const uint32_t (&w)[4], uint32_t byte,
                                               uint32_t (&out)[8]) {
-  byte = min(byte, 253u);
+  byte = exponent_byte(byte);
   const uint32_t e = min(byte + 120u, 254u), f = (e << 7) | (e << 23);
   uint32_t nan = 0;
 #pragma unroll

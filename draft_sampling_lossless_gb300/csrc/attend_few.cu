@@ -393,13 +393,13 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
         const int t0 = (sg.tile0 + i) * kBN;
         float ck = 0.f;
         if constexpr (E4M3) {
-          // the scale of this thread's key (any byte gives a finite factor)
+          // the scale of this thread's key
           const uint32_t q = (base + i) % kExpDepth;
           wait_bar(b_expFull + 8 * q, ((base + i) / kExpDepth) & 1, s_abort);
-          const int ek = min(max((int)smem[F::kExpOff + q * 256 + pt], 1), 254);
+          const uint32_t ek = exponent_byte(smem[F::kExpOff + q * 256 + pt]);
           __syncwarp();
           if (lane == 0) mbar_arrive(b_expEmpty + 8 * q);
-          ck = __uint_as_float((uint32_t)ek << 23);
+          ck = __uint_as_float(ek << 23);
         }
         const uint32_t sb = (base + i) % SB, t_s = tmem + lanes + sb * 64;
         wait_bar(b_s + 8 * sb, ((base + i) / SB) & 1, s_abort);

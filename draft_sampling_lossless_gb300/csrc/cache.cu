@@ -190,8 +190,7 @@ __global__ void __launch_bounds__(kThreads)
       if (!p.ok) continue;
       uint4 y = x[i];
       if constexpr (E4M3) {
-        // 2^(byte - 127); a byte of 0 or 255 is never written, its float is still defined
-        const float f = __uint_as_float((uint32_t)e[i] << 23);
+        const float f = __uint_as_float(exponent_byte(e[i]) << 23);  // 2^(byte - 127)
         y = make_uint4(e4m3x2_to_bf16x2(x[i].x & 0xffffu, f), e4m3x2_to_bf16x2(x[i].x >> 16, f),
                        e4m3x2_to_bf16x2(x[i].y & 0xffffu, f), e4m3x2_to_bf16x2(x[i].y >> 16, f));
       }

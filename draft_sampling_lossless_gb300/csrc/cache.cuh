@@ -70,6 +70,10 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return d;
 }
 
+// An exponent byte as it counts: 0, 254 and 255 are never written, and their powers of two
+// are no normal floats of bf16's or fp32's (or leave no room for a code).
+__device__ __forceinline__ uint32_t exponent_byte(uint32_t b) { return min(max(b, 1u), 253u); }
+
 // The launchers: enqueue on `st`.
 cudaError_t launch_cache_append(const CacheView& c, bool e4m3, const void* k, int64_t k_stride,
                                 const void* v, int64_t v_stride, cudaStream_t st);

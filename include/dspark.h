@@ -414,7 +414,8 @@ int dspark_check_wait_timeout(int limit_us, void* ws, size_t ws_bytes, void* str
  *   Two pools, k and v, [n_pages][Hkv][page][D], either bf16
  *   (DSPARK_CACHE_BF16) or e4m3 codes (DSPARK_CACHE_E4M3) with one exponent
  *   byte for each (page, head, slot) in k_exp, v_exp [n_pages][Hkv][page].
- *   A code c stands for c * 2^(byte - 127).
+ *   A code c stands for c * 2^(byte - 127), 1 <= byte <= 253 (bytes outside, which
+ *   dspark_cache_append never writes, count as the nearest).
  *   Request n's position p is in slot p % page of page pages[n][p / page]
  *   (pages [R][max_pages] int32, any page ids; entries past the last used
  *   position are not read).
