@@ -8,8 +8,10 @@ using namespace attend;
 // Up to 32 packed rows a head (max_rows is the host's bound of a request's rows)
 // are the N side of the products, as far as its two terms of P and S's columns go; more
 // are their M side.  With 32 the first kernel is still ahead: 64 requests of 1 to 8
-// rows of a group of 4 take 184 us (the other 222), over e4m3 188 us (344); single
-// tokens over e4m3 127 us (363), one token 14 us (19), each in a graph.
+// rows of a group of 4 take 184 us (the other 218), over e4m3 184 us (274), of 8 rows each
+// 193 us (217) and 204 us (289); single tokens over e4m3 150 us (287), one token 12.7 us
+// (16.8), each in a graph.  Past 32 there is the second kernel only: requests of 1 to 9
+// rows 179 us, 78% of the measured copy rate, over e4m3 319 us, 29%.
 static bool few(int max_rows, int group) { return (int64_t)max_rows * group <= 32; }
 
 size_t attend_workspace_bytes(int T, int group, int D) {

@@ -550,8 +550,9 @@ __device__ __forceinline__ void load_all(const Params& p, const Range& rg, bool 
 // Joins the partial results of an item's blocks (the THREADS softmax threads, warps 0
 // on, of the last one to finish).  `buf`, 32 KB of shared memory: the blocks' (m, l) of a
 // group of rows, then their weights 2^(m - M) / L; the sums run over the blocks in
-// order, eight values a thread.  About 3000 cycles for 32 rows of two or three blocks.  kLanesOnRows: records hold O as [DP / 4][ROWS][4],
-// else [ROWS][DP]; a warp's loads are contiguous either way.
+// order, eight values a thread.  About 3000 cycles for 32 rows of two or three blocks.
+// kLanesOnRows: records hold O as [DP / 4][ROWS][4], else [ROWS][DP]; a warp's loads are
+// contiguous either way.
 template <int DP, int ROWS, int THREADS, bool kLanesOnRows>
 __device__ __forceinline__ void join(const Params& p, const Segment& sg, float2* buf) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

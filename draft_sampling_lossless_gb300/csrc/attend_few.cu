@@ -27,7 +27,7 @@
 // largest; below, to 2^-21 of it); a position's scale is its thread's own, a factor of
 // the scores.  V's codes become bf16 on the way, scales and all (exact).  P as e4m3 terms
 // over V's codes (four of them) was as fast over 32 rows and took 124 us for 256 single
-// tokens instead of 150, but its range ends at 2^-22 of the reference: what lies below was
+// tokens instead of 147, but its range ends at 2^-22 of the reference: what lies below was
 // in l and not in O.
 //
 // Two streams, each a warpgroup with its own P, O and m, take alternate tiles.
@@ -44,15 +44,15 @@
 // that, not the arithmetic, set the pace.  Every wait is bounded.  See attend.cuh for
 // the split of the work.
 //
-// Measured (32 query heads over 8 of 128, of the measured copy rate):
-//   64 requests of 1 to 8 rows, 500 to 8000 positions  180 us, 6.3 TB/s, 93%
-//   3 of 5 to 8 rows, 90 to 180 thousand positions     221 us, 6.8 TB/s, 100%
-//   the first, e4m3: 184 us, 3.2 TB/s, 48%; 256 single tokens, e4m3: 150 us, 3.8 TB/s,
-//     56%: the softmax threads' chains of instructions, which the converting warps'
-//     instructions stretch (half of all issue slots are taken)
-//   64 drafter's blocks of 7 rows, 16 heads over 8 of 64: 60 us, 4.9 TB/s, 72%: the
+// Measured among other calls (32 query heads over 8 of 128, of the measured copy rate):
+//   64 requests of 1 to 8 rows, 500 to 8000 positions  181 us, 6.3 TB/s, 93%
+//   3 of 5 to 8 rows, 90 to 180 thousand positions     224 us, 6.7 TB/s, 99%
+//   the first, e4m3: 182 us, 3.3 TB/s, 48%; 256 single tokens, e4m3: 147 us, 3.9 TB/s,
+//     57%: the softmax threads' chains of instructions, which the converting warps'
+//     instructions stretch (58% of the issue slots are taken)
+//   64 drafter's blocks of 7 rows, 16 heads over 8 of 64: 59 us, 4.9 TB/s, 73%: the
 //     ends of items
-//   one token, 700 positions: 11 us, latency: the plan of the work (2 us), the first
+//   one token, 700 positions: 10.5 us, latency: the plan of the work (2 us), the first
 //     loads (2 us), six tiles, the join
 #include "attend.cuh"
 
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
   } else if (warp == F::kWarpS) {
     // ------------------------------------------------------------ scores
     if (elect_one()) {
-      constexpr uint32_t kIdS = E4M3 ? idesc_0_f32(128, F::kQRows) : idesc_bf16_f32(128, F::kQRows);
+      constexpr uint32_t kIdS = E4M3 ? idesc_e4m3_f32(128, F::kQRows) : idesc_bf16_f32(128, F::kQRows);
       const int ksteps = E4M3 ? (p.c.D + 31) / 32 : p.c.D / 16;
       const uint64_t k0 = desc_kmajor_sw128(smem_u32(smem));
       const uint64_t q0 = desc_kmajor_sw128(smem_u32(smem) + F::kQOff);

@@ -38,13 +38,15 @@
 // the softmax is the longest: 256 rows by 128 positions take about 5200 cycles, their
 // MMAs 3600 of those.
 // The softmax in loops of 32 positions, read twice, is what the instruction caches
-// hold: unrolled over the tile, with a copy for each number of row copies, it took
-// 515 us for 478; loops of 16 took 499, loads one chunk ahead 507, two threads a row 542.
-// Measured (32 query heads over 8 of 128): two chunks of 2000 rows after 1000 to 7000
-// positions 478 us, 938 TFLOP/s of visible products (49% of the measured matrix rate);
-// three of 700 to 1500, 40 heads, window 2048, e4m3 233 us, 470 TFLOP/s: tiles at the
-// edges of the windows are computed whole, an item has a dozen tiles, and the codes'
-// conversion takes as many instructions as the softmax (four warps for it: 6 us more).
+// hold: unrolled over the tile, with a copy for each number of row copies, the chunks
+// below took 515 us for 478 (alone in a graph, at the time); loops of 16 took 499, loads
+// one chunk ahead 507, two threads a row 542.
+// Measured (32 query heads over 8 of 128), among other calls: two chunks of 2000 rows
+// after 1000 to 7000 positions 491 us, 913 TFLOP/s of visible products (47% of the
+// measured matrix rate; alone in a graph 475 us); three of 700 to 1500, 40 heads, window
+// 2048, e4m3 223 us, 491 TFLOP/s: tiles at the edges of the windows are computed whole,
+// an item has a dozen tiles, and every row tile converts its K and V again (four warps
+// for it: 6 us more).
 #include "attend.cuh"
 
 namespace dspark {

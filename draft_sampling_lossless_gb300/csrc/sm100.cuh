@@ -241,8 +241,7 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
-// The same on e4m3 operands (K = 32 a step), and on halves: kind::f16 with an
-// instruction descriptor of halves.
+// The same on e4m3 operands (K = 32 a step).
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                          uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -375,9 +374,8 @@ __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t 
 constexpr uint32_t kIdescTransposeA = 1u << 15;  // A is MN-major
 constexpr uint32_t kIdescTransposeB = 1u << 16;  // B is MN-major
 
-// Instruction descriptor with format 0 operands: halves for kind::f16, e4m3 for
-// kind::f8f6f4.
-__host__ __device__ constexpr uint32_t idesc_0_f32(int M, int N) {
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator, e4m3 A and B (format 0).
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 

@@ -423,7 +423,8 @@ int dspark_check_wait_timeout(int limit_us, void* ws, size_t ws_bytes, void* str
  *   row_off[n] .. row_off[n+1]-1 (row_off [R+1] int32, row_off[0] >= 0), its row j at
  *   position ctx[n] + j, ctx[n] (int32) the number of positions cached before
  *   the call.  A request may have no rows.  A row at a negative position
- *   (ctx[n] < 0) is padding: it is not stored and sees nothing.  Rows of the
+ *   (ctx[n] < 0) is padding: it is not stored and, under a causal mask, sees
+ *   nothing (a block's rows all see the same).  Rows of the
  *   batch past row_off[R] are left as they are.
  *
  * Rejected rows need no undoing: the next step's ctx[n] is this step's plus
@@ -518,7 +519,7 @@ int dspark_cache_read(const dspark_cache* cache, int R, int T, const int32_t* ro
  * bits in the product with v (two bf16 terms), however small it is; the result is
  * rounded once to bf16.  Over e4m3, where max_rows * Hq / Hkv <= 32, q enters its
  * products as two e4m3 terms: what a row's values have below 2^-21 of its largest
- * is rounded away.
+ * is rounded away.  Sums stay finite for values up to 2^80 in size.
  * Positions that no row of the request sees are never part of a sum, whatever
  * is stored there.  A NaN or infinity stored at a visible position may also
  * reach those rows of the same request that do not see it yet.  Results are
