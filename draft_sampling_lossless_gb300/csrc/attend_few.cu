@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(Few<DP, NR, E4M3>::kThreads, 1)
             for (int o = 8; o > 0; o >>= 1)
               amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o, 16));
             // q 2^-a within the codes' range
-            const int a = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -100), 120);
+            const int a = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -126), 120);
             const float inv = __uint_as_float((uint32_t)(127 - a) << 23);
             uint32_t hi[4], lo[4];
 #pragma unroll
