@@ -47,11 +47,21 @@ SYMBOLS = (
     "dspark_cache_append",
     "dspark_cache_read",
     "dspark_attend",
+    "dspark_weights4_bytes",
+    "dspark_weights4_init",
+    "dspark_weights4_load",
+    "dspark_weights4_quantize",
+    "dspark_linear4_workspace_bytes",
+    "dspark_linear4",
+    "dspark_gated4",
+    "dspark_norm",
 )
 
 
 DSPARK_CACHE_BF16 = 0
 DSPARK_CACHE_E4M3 = 1
+
+ACTIVATIONS = {"silu": 0, "gelu": 1}
 
 DEVFLAG_NONFINITE = 0x2
 DEVFLAG_ROW_RANGE = 0x4
@@ -61,6 +71,12 @@ DEVFLAG_PAGE_RANGE = 0x20
 
 class KVCache(ctypes.Structure):
     """dspark_cache: the host description of a layer's key/value pools."""
+
+    _fields_ = [("opaque", ctypes.c_uint64 * 64)]
+
+
+class Weights4Desc(ctypes.Structure):
+    """dspark_weights4: the host description of a 4-bit matrix."""
 
     _fields_ = [("opaque", ctypes.c_uint64 * 64)]
 
@@ -135,6 +151,24 @@ def lib() -> ctypes.CDLL:
         L.dspark_attend.restype = c_int
         L.dspark_attend.argtypes = [cache, c_int, c_int, c_int, c_int, c_float, c_int, c_int, vp,
                                     c_i64, vp, vp, vp, c_int, vp, vp, vp, c_size, vp]
+        w4 = ctypes.POINTER(Weights4Desc)
+        L.dspark_weights4_bytes.restype = c_size
+        L.dspark_weights4_bytes.argtypes = [c_int, c_int]
+        L.dspark_weights4_init.restype = c_int
+        L.dspark_weights4_init.argtypes = [w4, c_int, c_int, vp]
+        L.dspark_weights4_load.restype = c_int
+        L.dspark_weights4_load.argtypes = [w4, vp, vp, vp]
+        L.dspark_weights4_quantize.restype = c_int
+        L.dspark_weights4_quantize.argtypes = [w4, vp, c_int, c_i64, vp]
+        L.dspark_linear4_workspace_bytes.restype = c_size
+        L.dspark_linear4_workspace_bytes.argtypes = [c_int, c_int]
+        L.dspark_linear4.restype = c_int
+        L.dspark_linear4.argtypes = [w4, c_int, vp, c_i64, vp, c_i64, vp, c_size, vp]
+        L.dspark_gated4.restype = c_int
+        L.dspark_gated4.argtypes = [w4, w4, c_int, c_int, vp, c_i64, vp, c_i64, vp, c_size, vp]
+        L.dspark_norm.restype = c_int
+        L.dspark_norm.argtypes = [c_int, c_int, c_int, vp, c_i64, vp, c_i64, vp, vp, c_i64,
+                                  c_float, vp, c_float, vp, c_i64, vp, c_i64, vp]
         L.dspark_check_wait_timeout.restype = c_int
         L.dspark_check_wait_timeout.argtypes = [c_int, vp, c_size, vp]
         L.dspark_launch_count.restype = ctypes.c_longlong
@@ -433,3 +467,102 @@ def dspark_attend(cache, D, q, row_off, ctx, pages, out, lse, scale, causal, win
         cache, R, T, Hq, max_rows, scale, causal, window, qp, qs, _i32(row_off, R + 1, "row_off"),
         _i32(ctx, R, "ctx"), _i32(pages, R, "pages"), pages.shape[1], _on_gpu(out),
         None if lse is None else _on_gpu(lse), *_ws(ws), _raw_stream(stream)))
+
+
+def weights4_init(N, K, store) -> Weights4Desc:
+    """The host description of a matrix [N, K] in `store` (uint8, at least
+    weights4_bytes(N, K)); the caller keeps the tensor alive."""
+    if store.dtype != torch.uint8 or not store.is_contiguous() or (
+            store.numel() < weights4_bytes(N, K)):
+        raise ValueError("the store must be a contiguous uint8 tensor of weights4_bytes(N, K)")
+    d = Weights4Desc()
+    _check("dspark_weights4_init",
+           lib().dspark_weights4_init(ctypes.byref(d), N, K, _on_gpu(store)))
+    return d
+
+
+def weights4_bytes(N, K) -> int:
+    return int(lib().dspark_weights4_bytes(N, K))
+
+
+def dspark_weights4_load(w, N, K, codes, scales, stream=None):
+    for t, cols, what in ((codes, K // 2, "codes"), (scales, K // 32, "scales")):
+        if t.dtype != torch.uint8 or t.shape != (N, cols) or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous uint8 tensor [{N}, {cols}]")
+    _same_device(codes, scales)
+    _check("dspark_weights4_load", lib().dspark_weights4_load(
+        w, _on_gpu(codes), _on_gpu(scales), _raw_stream(stream)))
+
+
+def dspark_weights4_quantize(w, N, K, src, stream=None):
+    dt = _dt(src)
+    p, stride = _matrix(src, N, K, src.dtype, "the matrix")
+    _check("dspark_weights4_quantize",
+           lib().dspark_weights4_quantize(w, p, dt, stride, _raw_stream(stream)))
+
+
+def linear4_workspace_bytes(T, K) -> int:
+    return int(lib().dspark_linear4_workspace_bytes(T, K))
+
+
+def _matrix(t, T, cols, dtype, what):
+    """Pointer and row stride of a [T, cols] tensor whose rows may lie apart."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != T or t.shape[1] != cols:
+        raise ValueError(f"{what} must be {dtype} [{T}, {cols}], got {t.dtype} {tuple(t.shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"the columns of {what} must be contiguous")
+    return _on_gpu(t), (s0 if T > 1 else cols)
+
+
+def _vector(t, d, what):
+    if t.dtype != torch.float32 or t.shape != (d,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous fp32 tensor [{d}]")
+    return _on_gpu(t)
+
+
+def _same_device(*tensors):
+    """The kernels run on the current device: every tensor has to be there."""
+    at = torch.cuda.current_device()
+    for t in tensors:
+        if t.get_device() != at:
+            raise ValueError(f"expected CUDA tensors on the current device ({at}), "
+                             f"got one on {t.device}")
+
+
+def dspark_linear4(w, N, K, x, out, ws, stream=None):
+    T = x.shape[0]
+    xp, xs = _matrix(x, T, K, torch.bfloat16, "x")
+    op, os_ = _matrix(out, T, N, torch.bfloat16, "out")
+    _check("dspark_linear4", lib().dspark_linear4(
+        w, T, xp, xs, op, os_, *_ws(ws), _raw_stream(stream)))
+
+
+def dspark_gated4(gate, up, N, K, act, x, out, ws, stream=None):
+    T = x.shape[0]
+    xp, xs = _matrix(x, T, K, torch.bfloat16, "x")
+    op, os_ = _matrix(out, T, N, torch.bfloat16, "out")
+    _check("dspark_gated4", lib().dspark_gated4(
+        gate, up, act, T, xp, xs, op, os_, *_ws(ws), _raw_stream(stream)))
+
+
+def dspark_norm(x, y, post, gate, alpha, pre, eps, x_out, h, stream=None):
+    T, d = x.shape
+    dt = _dt(x)
+    xp, xs = _matrix(x, T, d, x.dtype, "x")
+    yp = gp = op = hp = None
+    ys = gs = os_ = hs = 0
+    if y is not None:
+        yp, ys = _matrix(y, T, d, torch.bfloat16, "y")
+    if gate is not None:
+        rows = T if gate.shape[0] == T else 1
+        gp, gs = _matrix(gate, rows, d, torch.bfloat16, "gate")
+        gs = gs if rows > 1 else 0
+    if x_out is not None:
+        op, os_ = _matrix(x_out, T, d, x.dtype, "x_out")
+    if h is not None:
+        hp, hs = _matrix(h, T, d, torch.bfloat16, "h")
+    _check("dspark_norm", lib().dspark_norm(
+        T, d, dt, xp, xs, yp, ys, None if post is None else _vector(post, d, "post"), gp, gs,
+        alpha, None if pre is None else _vector(pre, d, "pre"), eps, op, os_, hp, hs,
+        _raw_stream(stream)))

@@ -208,6 +208,9 @@ enum KernelKind {
   kKindCacheAppend,
   kKindCacheRead,
   kKindAttend,
+  kKindWeights4,
+  kKindLinear4,
+  kKindNorm,
   kKindCount
 };
 

@@ -1,0 +1,70 @@
+// The target's layers around its attention: the host description of 4-bit weights,
+// what their kernels share, and the launchers.
+#pragma once
+
+#include <cuda.h>
+
+#include "common.cuh"
+
+namespace dspark {
+
+// What the opaque words of a dspark_weights4 hold.  The store: codes [N][Kp / 2], Kp = K
+// rounded up to 128, then the scales in blocks of 128 rows and 128 columns (scale_at).
+struct Weights4Desc {
+  uint64_t magic;
+  int N, K, Kp, pad;
+  uint8_t *codes, *scales;
+  CUtensorMap tm;  // boxes of 128 rows by 128 codes, spread to a byte each
+};
+constexpr uint64_t kWeights4Magic = 0x6473706b77347834ull;
+
+__host__ __device__ constexpr int padded_k(int K) { return (K + 127) / 128 * 128; }
+constexpr size_t codes_bytes(int N, int K) {
+  return ((size_t)N * (padded_k(K) / 2) + 511) / 512 * 512;
+}
+constexpr size_t scales_bytes(int N, int K) {
+  return (size_t)((N + 127) / 128) * (padded_k(K) / 128) * 512;
+}
+// Where the scale of row n, columns 32 g .. 32 g + 31 is: a block of 128 rows and four
+// groups is 512 bytes, [n % 32][n / 32 % 4][g % 4], as tcgen05.cp spreads it over tensor
+// memory's lanes (32 of them) and columns.
+__host__ __device__ constexpr size_t scale_at(int n, int g, int Kp) {
+  return ((size_t)(n >> 7) * (Kp >> 7) + (g >> 2)) * 512 + (n & 31) * 16 + ((n >> 5) & 3) * 4 +
+         (g & 3);
+}
+
+// out[t][n] = x[t] . W[n], or act(x[t] . G[n]) * (x[t] . U[n]).
+struct Linear4Args {
+  const Weights4Desc *w, *up;  // up: the second matrix of a gated product, else null
+  int act;                     // DSPARK_ACT_*
+  int T;
+  const __nv_bfloat16* x;
+  int64_t x_stride;
+  __nv_bfloat16* out;
+  int64_t out_stride;
+  void* ws;
+};
+size_t linear4_workspace_bytes(int T, int K);
+cudaError_t launch_linear4(const Linear4Args& a, cudaStream_t st);
+
+cudaError_t launch_weights4_load(const Weights4Desc& d, const uint8_t* codes,
+                                 const uint8_t* scales, cudaStream_t st);
+cudaError_t launch_weights4_quantize(const Weights4Desc& d, const void* src, int dt,
+                                     int64_t stride, cudaStream_t st);
+
+struct NormArgs {
+  int T, d, dt;
+  float alpha, eps;
+  const void* x;
+  int64_t x_stride;
+  const __nv_bfloat16 *y, *gate;
+  int64_t y_stride, gate_stride;
+  const float *post, *pre;
+  void* x_out;
+  int64_t x_out_stride;
+  __nv_bfloat16* h;
+  int64_t h_stride;
+};
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
+
+}  // namespace dspark

@@ -22,6 +22,15 @@
  *   dspark_attend        the rows' attention over each request's pages
  *   dspark_cache_read    a range of cached positions read back
  *
+ * The rest of the target's layers, between its attentions:
+ *
+ *   dspark_norm          a block's output into the stream (its norm, gate and
+ *                        scale), and the next block's norm of the stream
+ *   dspark_linear4       a product with 4-bit weights
+ *   dspark_gated4        the gated product of a feed-forward block, 4-bit weights
+ *   dspark_weights4_load, dspark_weights4_quantize
+ *                        4-bit weights laid out for them, once
+ *
  * Conventions shared by every call
  * --------------------------------
  * - Every array argument is a DEVICE pointer owned by the caller, row-major,
@@ -530,6 +539,127 @@ int dspark_attend(const dspark_cache* cache, int R, int T, int Hq, int max_rows,
                   int causal, int window, const void* q, int64_t q_stride,
                   const int32_t* row_off, const int32_t* ctx, const int32_t* pages, int max_pages,
                   void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * 4-bit weights.
+ *
+ * The projections of the target's layers (news article, figure 1: the target
+ * verifies the scheduled prefix of every request in one batch) read all their
+ * weights for a few rows, so the weights' bytes are their time.  The pages give
+ * no format; this library takes the open microscaling one of 4 bits: W [N][K], a
+ * code of 4 bits for each value, one scale byte for 32 consecutive columns of a
+ * row.
+ *
+ *   A code is a sign bit over two bits of exponent and one of fraction:
+ *   magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.  A scale byte b stands for
+ *   2^(b - 127), 1 <= b <= 254 (bytes outside count as the nearest).
+ *   W[n][k] = code * scale: 4.25 bits a value.
+ *
+ * dspark_weights4 (host memory, the caller's) describes one matrix in a store
+ * of dspark_weights4_bytes(N, K) bytes of device memory, 256-byte aligned, that
+ * dspark_weights4_load or dspark_weights4_quantize fills once.  It holds the
+ * store's address and a tensor map, nothing else; it may be copied and needs no
+ * release.
+ *
+ * Limits: 1 <= N <= 2^24; K a multiple of 32, 32 <= K <= 65536; 0 <= T <= 2^24
+ * rows (T = 0 does nothing).
+ */
+typedef struct dspark_weights4 {
+  uint64_t opaque[64];
+} dspark_weights4;
+
+typedef enum { DSPARK_ACT_SILU = 0, DSPARK_ACT_GELU = 1 } dspark_act;
+
+/* Bytes of a matrix's store; 0 if the sizes are out of range. */
+size_t dspark_weights4_bytes(int N, int K);
+
+/* DSPARK_ERR_INVALID_ARG, or DSPARK_ERR_CUDA where the driver's tensor-map
+ * encoder is missing or refuses. */
+int dspark_weights4_init(dspark_weights4* w, int N, int K, void* store);
+
+/*
+ * dspark_weights4_load -- fills the store from codes and scales as checkpoints
+ * hold them.
+ *
+ *   codes   [N][K / 2]   two codes a byte, the even column in the low half;
+ *                        16-byte aligned
+ *   scales  [N][K / 32]  scale bytes
+ */
+int dspark_weights4_load(const dspark_weights4* w, const uint8_t* codes, const uint8_t* scales,
+                         void* stream);
+
+/*
+ * dspark_weights4_quantize -- fills the store from a matrix in bf16 or fp32.
+ *
+ * For each group of 32 columns of a row,
+ *   e    = the smallest integer >= -100 with max |w| <= 6 * 2^e
+ *   code = w * 2^-e rounded to a code (to nearest, ties to the even code)
+ * and the scale byte is e + 127.  The maximum is over the finite values; an
+ * infinity becomes +-6 * 2^e, a NaN zero.
+ *
+ *   src   [N][K] dt (DSPARK_BF16 or DSPARK_F32), rows `stride` elements apart (a
+ *         multiple of 8, at least K), 16-byte aligned
+ */
+int dspark_weights4_quantize(const dspark_weights4* w, const void* src, int dt, int64_t stride,
+                             void* stream);
+
+/* Workspace bytes that cover dspark_linear4 and dspark_gated4 with up to T rows
+ * of K columns or fewer.  Returns 0 if the sizes are out of range.  The rules of
+ * every workspace hold (256-byte aligned, zeroed once, the status word first). */
+size_t dspark_linear4_workspace_bytes(int T, int K);
+
+/*
+ * dspark_linear4 -- out = x W^T.
+ *
+ *   x     [T][K] bf16, rows x_stride elements apart (a multiple of 8, at least
+ *         K), 16-byte aligned
+ *   out   [T][N] bf16, rows out_stride elements apart (at least N)
+ * What lies between the rows of out is left as it is.  out must not overlap x.
+ * Products are exact but for what a row's values have below 2^-21 of the largest
+ * of their 32 columns (which may be rounded away, as may values below 2^-118);
+ * sums are fp32, the result is rounded once.  A row of x with a NaN or an
+ * infinity gives NaN or infinities in its own row of out, and only there.
+ * Results are bit-reproducible.
+ */
+int dspark_linear4(const dspark_weights4* w, int T, const void* x, int64_t x_stride, void* out,
+                   int64_t out_stride, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * dspark_gated4 -- out = act(x G^T) * (x U^T), the first half of a gated
+ * feed-forward block in one call (dspark_linear4 is the second).
+ *
+ *   gate, up   two matrices of one shape [N][K]
+ *   act        DSPARK_ACT_SILU: a / (1 + exp(-a));  DSPARK_ACT_GELU:
+ *              0.5 a (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3)))
+ *   the rest as in dspark_linear4; neither product is rounded before act
+ */
+int dspark_gated4(const dspark_weights4* gate, const dspark_weights4* up, int act, int T,
+                  const void* x, int64_t x_stride, void* out, int64_t out_stride, void* ws,
+                  size_t ws_bytes, void* stream);
+
+/*
+ * dspark_norm -- the norms between two blocks: a block's output y through its
+ * own norm, gate and scale into the stream x, and the next block's norm of it.
+ *
+ *   rms(v) = v / sqrt(mean v^2 + eps)
+ *   u  = rms(y) * post        (post NULL: u = y)
+ *   x' = x + alpha * gate * u (gate NULL: 1; y NULL: x' = x)
+ *   x_out = x',  h = rms(x') * pre, each rounded once (h from x' unrounded)
+ *
+ *   x, x_out   [T][d] dt (DSPARK_BF16 or DSPARK_F32)
+ *   y, h       [T][d] bf16
+ *   gate       [T][d] bf16, or one row for all where gate_stride is 0
+ *   post, pre  [d] f32
+ * y NULL: no post, gate or x_out.  x_out NULL: x' is not stored.  h NULL: no pre,
+ * and x_out must be there.  Rows are *_stride elements apart (multiples of 8, at
+ * least d), all pointers 16-byte aligned; d a multiple of 8, 8 <= d <= 32768.
+ * x_out may be x, and h may be y, with the same strides; no other outputs may overlap
+ * inputs.  Sums are fp32.  A NaN or an infinity stays in its row.
+ */
+int dspark_norm(int T, int d, int dt, const void* x, int64_t x_stride, const void* y,
+                int64_t y_stride, const float* post, const void* gate, int64_t gate_stride,
+                float alpha, const float* pre, float eps, void* x_out, int64_t x_out_stride,
+                void* h, int64_t h_stride, void* stream);
 
 /*
  * Launch counting and kernel tracing (measurement support; no counterpart on
