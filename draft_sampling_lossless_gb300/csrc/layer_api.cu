@@ -93,6 +93,8 @@ int run_linear4(const char* name, const Weights4Desc& w, const Weights4Desc* up,
                 size_t ws_bytes, void* stream) {
   if (T < 0 || T > kMaxT)
     return fail(DSPARK_ERR_INVALID_ARG, "T out of range (%d; need 0 <= T <= 2^24)", T);
+  if ((int64_t)T * w.N > (1ll << 38))
+    return fail(DSPARK_ERR_INVALID_ARG, "T * N must be at most 2^38");
   REQUIRE_ALIGNED(ws, 256);
   const size_t need = linear4_workspace_bytes(T, w.K);
   if (ws_bytes < need)

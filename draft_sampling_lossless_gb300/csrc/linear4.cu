@@ -1,6 +1,5 @@
 // Products with 4-bit weights: x W^T, and act(x G^T) * (x U^T).
-#include "dspark.h"
-#include "layer.cuh"
+#include "linear4.cuh"
 
 namespace dspark {
 
@@ -12,11 +11,6 @@ __device__ __forceinline__ float code_value(uint32_t c) {
   const uint32_t e = (c >> 1) & 3, f = c & 1;
   const float v = e == 0 ? 0.5f * f : (1.f + 0.5f * f) * (float)(1u << (e - 1));
   return c & 8 ? -v : v;
-}
-
-__device__ __forceinline__ float activation(int act, float a) {
-  if (act == DSPARK_ACT_SILU) return a / (1.f + expf(-a));
-  return 0.5f * a * (1.f + tanhf(0.7978845608028654f * fmaf(0.044715f * a * a, a, a)));
 }
 
 // A warp a feature and kTokens tokens, a lane a group of 32 columns.
@@ -54,9 +48,10 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 }  // namespace
 
-size_t linear4_workspace_bytes(int T, int K) { return 256 + 0 * (size_t)T * K; }
+size_t linear4_workspace_bytes(int T, int K) { return linear4_tile_workspace_bytes(T, K); }
 
 cudaError_t launch_linear4(const Linear4Args& a, cudaStream_t st) {
+  if (a.T > 16) return launch_linear4_tile(a, st);
   const int per = 65535 * kTokens;  // the grid's second dimension
   cudaError_t e = cudaSuccess;
   for (int t = 0; t < a.T && e == cudaSuccess; t += per) {

@@ -1,0 +1,531 @@
+// Products with 4-bit weights on the tensor cores: x W^T, and act(x G^T) * (x U^T).
+//
+// Block-scaled MMAs (kind mxf8f6f4) take the codes and scales of W as they are stored, so
+// nothing is unpacked: A is 128 rows of W, a code in each byte (the TMA load spreads
+// them), its scales beside the accumulators in tensor memory.  B is the rows of x.  Its
+// e4m3 has 4 significant bits, bf16 has 8: x is two e4m3 terms, exactly,
+//
+//   x = 2^e (hi + 2^-4 lo),  |hi| <= 448,  e for each row and 32 columns,
+//
+// but for what lies below 2^-22 of a group's largest (lo ends at 2^-9 of its scale), so
+// each step of K runs two MMAs, on hi and on lo, into one accumulator.  That is the rate of
+// bf16 MMAs, for a quarter of the weights' bytes and no conversions.
+//
+// A first kernel writes hi, lo and their exponents in tiles that one bulk copy brings in,
+// swizzled as the MMA reads them; the second starts under it and already loads weights.
+#include "linear4.cuh"
+#include "sm100.cuh"
+
+namespace dspark {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kMaxTokens = 192;   // rows of x a tile
+constexpr int kThreads = 192;     // load, MMA, four warps of results
+constexpr int kMaxSmem = 232448;
+constexpr int kSfCol = 384;       // tensor memory: accumulators below, scales above
+constexpr int kMaxSplit = 8;
+constexpr uint32_t kStatusBytes = 1024;
+constexpr uint32_t kWaitNs = 2000000000u;
+
+// Bytes of the tile of `tokens` rows and 128 columns of x: hi, lo, their exponents in
+// blocks of 128 rows as tcgen05.cp takes them.
+__host__ __device__ constexpr uint32_t exp_blocks(int tokens) { return (tokens + 127) / 128; }
+__host__ __device__ constexpr uint32_t tile_bytes(int tokens) {
+  return (uint32_t)tokens * 256 + exp_blocks(tokens) * 1024;
+}
+
+// ---------------------------------------------------------------- x in two terms
+
+// The smallest e >= -118 with amax <= 448 * 2^e (448 = 1.75 * 2^8).
+__device__ __forceinline__ int group_exponent(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = (int)(b >> 23) - 127 - ((b & 0x7fffffu) <= 0x600000u ? 8 : 7);
+  return max(e, -118);
+}
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+constexpr int kSplitThreads = 256;
+
+// Four lanes a group of 32 columns, eight values each; 16 lanes a row's 128 columns.
+// Rows past T stay as they are: they reach only columns of the product that are not stored.
+__global__ void __launch_bounds__(kSplitThreads)
+    split_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride, int T, int K, int KB,
+                 int tokens, uint8_t* __restrict__ out) {
+  grid_dependency_wait();
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int64_t i = ((int64_t)blockIdx.x * kSplitThreads + threadIdx.x) >> 4;
+  const int lane = threadIdx.x & 15;
+  const int64_t t = i / KB;
+  const int kb = (int)(i - t * KB), col = kb * 128 + lane * 8;
+  uint4 raw = make_uint4(0, 0, 0, 0);
+  if (t < T && col < K) raw = __ldg(reinterpret_cast<const uint4*>(x + t * x_stride + col));
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  float v[8], amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float a = fabsf(v[j]);
+    if (a < INFINITY) amax = fmaxf(amax, a);
+    else v[j] = NAN;  // its row's results are not finite
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const int e = group_exponent(amax);
+  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+  uint32_t hi[2], lo[2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float a = v[2 * j] * f, b = v[2 * j + 1] * f;
+    const uint32_t h = to_e4m3x2(a, b);
+    const float2 c = from_e4m3x2(h);
+    const uint32_t l = to_e4m3x2((a - c.x) * 16.f, (b - c.y) * 16.f);
+    if (j & 1) hi[j >> 1] |= h << 16, lo[j >> 1] |= l << 16;
+    else hi[j >> 1] = h, lo[j >> 1] = l;
+  }
+  // the row's four exponent bytes, in the first of its 16 lanes
+  uint32_t exps = 0;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    exps |= (uint32_t)(__shfl_sync(0xffffffffu, e, (threadIdx.x & 16) + g * 4) + 127) << (8 * g);
+  if (t >= T) return;
+  const int64_t tile = t / tokens;
+  const int r = (int)(t - tile * tokens);
+  uint8_t* dst = out + (tile * KB + kb) * tile_bytes(tokens);
+  const uint32_t at = r * 128 + (((lane >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
+  *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0], hi[1]);
+  *reinterpret_cast<uint2*>(dst + tokens * 128 + at) = make_uint2(lo[0], lo[1]);
+  if (lane == 0) {
+    uint8_t* s = dst + tokens * 256 + (r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+    *reinterpret_cast<uint32_t*>(s) = exps;
+    *reinterpret_cast<uint32_t*>(s + exp_blocks(tokens) * 512) = exps - 0x04040404u;
+  }
+}
+
+// ---------------------------------------------------------------- the product
+
+struct Params {
+  const uint8_t *sw, *su;  // scales of the matrices
+  const uint8_t* xq;       // tiles of x
+  int N, T, KB, tokens, feature_tiles, tiles, split, stages, act;
+  __nv_bfloat16* out;
+  int64_t out_stride;
+  uint32_t* status;
+};
+
+struct Small {  // at the end of shared memory
+  uint64_t full[12], empty[12], acc_full[2], acc_empty[2], drain;
+  uint32_t tmem;
+  int abort_flag, issued;
+};
+
+// kind mxf8f6f4: A e2m1 (5), B e4m3 (0), scales powers of two, both K-major, M = 128; `j`:
+// which byte of the scales' columns.
+__device__ __forceinline__ uint32_t idesc_mx(int N, int j) {
+  return (5u << 7) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (8u << 24) |
+         (static_cast<uint32_t>(j) << 4) | (static_cast<uint32_t>(j) << 29);
+}
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+// 512 bytes (32 rows of 16) over the 32 lanes and 4 columns at `taddr`, in each quarter of the
+// lanes; in order with this thread's MMAs.
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(128 >> 4) << 16;
+  d |= static_cast<uint64_t>(128 >> 4) << 32;  // from 8 rows to the next 8
+  d |= static_cast<uint64_t>(1) << 46;
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+        "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+// Untiled copy, 16-byte aligned, completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\t"
+      "barrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, int rank, float v) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(addr),
+      "r"(rank), "f"(v)
+      : "memory");
+}
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_wait_or_abort(bar, parity, abort_flag, kWaitNs);
+}
+
+// MATS: 1, or 2 for the gated product (both accumulators in the same lanes).
+template <int MATS>
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_u,
+                const Params p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t x_bytes = tile_bytes(p.tokens);
+  // a stage: codes (16 KB a matrix), x's tile, the codes' scales (512 bytes a matrix)
+  const uint32_t stage_bytes = (MATS * (16384 + 512) + x_bytes + 1023) & ~1023u;
+  const uint32_t s0 = smem_u32(smem);
+  Small* ms = reinterpret_cast<Small*>(smem + (size_t)p.stages * stage_bytes);
+  const uint32_t b_full = smem_u32(ms->full), b_empty = smem_u32(ms->empty);
+  const uint32_t b_accFull = smem_u32(ms->acc_full), b_accEmpty = smem_u32(ms->acc_empty);
+  const uint32_t b_drain = smem_u32(&ms->drain);
+  volatile int* s_abort = &ms->abort_flag;
+
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ms->tmem), 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(b_full + 8 * i, 1);
+      mbar_init(b_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_accFull + 8 * i, 1);
+      mbar_init(b_accEmpty + 8 * i, 4);
+    }
+    mbar_init(b_drain, 1);
+    fence_mbar_init();
+    ms->abort_flag = 0;
+    ms->issued = 0;
+    tma_prefetch(&tm_w);
+    if (MATS == 2) tma_prefetch(&tm_u);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem;
+
+  // Tiles: `split` blocks (a cluster) share one, each a range of K; or a block takes every
+  // gridDim.x-th.
+  const int rank = p.split > 1 ? (int)(blockIdx.x % p.split) : 0;
+  const int first = blockIdx.x / p.split, step = gridDim.x / p.split;
+  const int k0 = (int)((int64_t)p.KB * rank / p.split);
+  const int k1 = (int)((int64_t)p.KB * (rank + 1) / p.split);
+
+  if (warp == 0) {
+    if (elect_one()) {
+      const uint32_t tx = MATS * (8192 + 512) + x_bytes;
+      auto load_w = [&](int s, int tile, int kb) {
+        const int ft = tile % p.feature_tiles;
+        const uint32_t bar = b_full + 8 * s, dst = s0 + s * stage_bytes;
+        mbar_arrive_expect_tx(bar, tx);
+        tma_load_2d(dst, &tm_w, bar, kb * 128, ft * 128);
+        if (MATS == 2) tma_load_2d(dst + 16384, &tm_u, bar, kb * 128, ft * 128);
+        const size_t at = ((size_t)ft * p.KB + kb) * 512;
+        bulk_load(dst + MATS * 16384 + x_bytes, p.sw + at, 512, bar);
+        if (MATS == 2) bulk_load(dst + MATS * 16384 + x_bytes + 512, p.su + at, 512, bar);
+      };
+      auto load_x = [&](int s, int tile, int kb) {
+        const int tt = tile / p.feature_tiles;
+        bulk_load(s0 + s * stage_bytes + MATS * 16384,
+                  p.xq + ((size_t)tt * p.KB + kb) * x_bytes, x_bytes, b_full + 8 * s);
+      };
+      // the first stages' weights, before the kernel that writes x's tiles has ended
+      int e = 0;
+      const int here = min(p.stages, k1 - k0);
+      if (first < p.tiles) {
+        for (; e < here; ++e) load_w(e, first, k0 + e);
+        grid_dependency_wait();
+        for (int i = 0; i < here; ++i) load_x(i, first, k0 + i);
+      }
+      bool ok = true;
+      for (int tile = first; tile < p.tiles && ok; tile += step) {
+        for (int kb = tile == first ? k0 + here : k0; kb < k1 && ok; ++kb, ++e) {
+          const int s = e % p.stages;
+          ok = wait_bar(b_empty + 8 * s, ((e / p.stages) & 1) ^ 1, s_abort);
+          if (!ok) break;
+          load_w(s, tile, kb);
+          load_x(s, tile, kb);
+        }
+      }
+      ms->issued = e;
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      const uint32_t nb = exp_blocks(p.tokens);
+      int e = 0, n = 0;
+      bool ok = true;
+      for (int tile = first; tile < p.tiles && ok; tile += step, ++n) {
+        const int buf = n & 1;
+        ok = wait_bar(b_accEmpty + 8 * buf, ((n >> 1) & 1) ^ 1, s_abort);
+        tc_fence_after();
+        const uint32_t acc = tmem + buf * MATS * p.tokens;
+        for (int kb = k0; kb < k1 && ok; ++kb, ++e) {
+          const int s = e % p.stages;
+          ok = wait_bar(b_full + 8 * s, (e / p.stages) & 1, s_abort);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = s0 + s * stage_bytes, at_x = at + MATS * 16384;
+          const uint32_t at_e = at_x + p.tokens * 256, at_s = at_x + x_bytes;
+          // the scales' columns: W (4 a matrix), hi's, lo's; two sets in turn
+          const uint32_t t_w = tmem + kSfCol + (e & 1) * 32, t_hi = t_w + 4 * MATS;
+          const uint32_t t_lo = t_hi + 4 * nb;
+#pragma unroll
+          for (int m = 0; m < MATS; ++m) scales_to_tmem(t_w + 4 * m, at_s + 512 * m);
+          for (uint32_t i = 0; i < nb; ++i) {
+            scales_to_tmem(t_hi + 4 * i, at_e + 512 * i);
+            scales_to_tmem(t_lo + 4 * i, at_e + 512 * (nb + i));
+          }
+          const uint64_t d_w = desc_kmajor_sw128(at), d_hi = desc_kmajor_sw128(at_x);
+          const uint64_t d_lo = desc_kmajor_sw128(at_x + p.tokens * 128);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t id = idesc_mx(p.tokens, j);
+#pragma unroll
+            for (int m = 0; m < MATS; ++m) {
+              const uint64_t d_a = d_w + m * (16384 >> 4) + 2 * j;
+              mma_mx(acc + m * p.tokens, d_a, d_hi + 2 * j, id, t_w + 4 * m, t_hi,
+                     kb > k0 || j > 0);
+              mma_mx(acc + m * p.tokens, d_a, d_lo + 2 * j, id, t_w + 4 * m, t_lo, 1);
+            }
+          }
+          mma_commit(b_empty + 8 * s);
+        }
+        mma_commit(b_accFull + 8 * buf);
+      }
+      if (*s_abort) {  // what was issued ends before tensor memory goes
+        mma_commit(b_drain);
+        mbar_wait(b_drain, 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ results
+    grid_dependency_wait();
+    const int quad = warp & 3;
+    const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
+    int n = 0;
+    for (int tile = first; tile < p.tiles; tile += step, ++n) {
+      const int buf = n & 1, ft = tile % p.feature_tiles, tt = tile / p.feature_tiles;
+      const bool ok = wait_bar(b_accFull + 8 * buf, (n >> 1) & 1, s_abort);
+      if (__any_sync(0xffffffffu, !ok)) break;
+      if (p.split > 1) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + t_lane + buf * MATS * p.tokens;
+      const int f = ft * 128 + quad * 32 + lane, t0 = tt * p.tokens;
+      __nv_bfloat16* out = p.out + (int64_t)t0 * p.out_stride + f;
+      const int rows = min(p.tokens, p.T - t0);
+#pragma unroll 1
+      for (int c = 0; c < rows; c += 16) {
+        uint32_t a[16], b[16];
+        tmem_ld_x16(acc + c, a);
+        if (MATS == 2) {
+          tmem_ld_x16(acc + p.tokens + c, b);
+          tmem_wait_ld_regs(a, b);
+        } else {
+          tmem_wait_ld_regs(a);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float v = __uint_as_float(a[i]);
+          if (MATS == 2) v = activation(p.act, v) * __uint_as_float(b[i]);
+          if (f < p.N && c + i < rows) out[(c + i) * p.out_stride] = __float2bfloat16(v);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_accEmpty + 8 * buf);
+    }
+  }
+
+  if (p.split > 1) {
+    // Each block of the cluster sums some columns (rows of x) of the tile over all of them, in
+    // the order of their ranges of K.  The partial sums go to their block's shared memory,
+    // where the stages were: no MMA of the cluster reads them any more.
+    __syncthreads();
+    __syncwarp();
+    cluster_sync_all();
+    const int cols = p.tokens / p.split, quad = warp & 3;
+    float* part = reinterpret_cast<float*>(smem);  // [split][MATS][cols][128]
+    const int ft = first % p.feature_tiles, tt = first / p.feature_tiles;
+    if (warp >= 2) {
+      tc_fence_after();
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < MATS * p.tokens; c += 16) {
+        uint32_t a[16];
+        tmem_ld_x16(acc + c, a);
+        tmem_wait_ld_regs(a);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int m = MATS == 2 && c + i >= p.tokens, col = c + i - m * p.tokens;
+          const int to = col / cols;
+          store_cluster(smem_u32(part + ((rank * MATS + m) * cols + col - to * cols) * 128 +
+                                 quad * 32 + lane),
+                        to, __uint_as_float(a[i]));
+        }
+      }
+      tc_fence_before();
+    }
+    __syncthreads();
+    __syncwarp();
+    cluster_sync_all();
+    const int t0 = tt * p.tokens + rank * cols;
+    for (int i = tid; i < cols * 128; i += kThreads) {
+      const int col = i >> 7, f = i & 127;
+      float v[MATS];
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) {
+        v[m] = 0.f;
+        for (int r = 0; r < p.split; ++r) v[m] += part[((r * MATS + m) * cols + col) * 128 + f];
+      }
+      float o = v[0];
+      if (MATS == 2) o = activation(p.act, o) * v[MATS - 1];
+      if (t0 + col < p.T && ft * 128 + f < p.N)
+        p.out[(int64_t)(t0 + col) * p.out_stride + ft * 128 + f] = __float2bfloat16(o);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *s_abort) {
+    set_flag(p.status, kFlagWaitTimeout);
+    // the copies in flight land before the block's shared memory goes
+    const int n = ms->issued;
+    for (int i = max(0, n - p.stages); i < n; ++i)
+      mbar_wait(b_full + 8 * (i % p.stages), (i / p.stages) & 1);
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// How a product is cut: rows of x a tile, and blocks that share a tile's K.
+struct Cut {
+  int tokens, split;
+};
+
+// The time of the busiest block in cycles of the MMAs: one of 128 x N x 32 takes N / 2, and
+// 32 at least (A's 4 KB from shared memory).  `split` blocks that share a tile exchange
+// their sums.
+Cut choose(int N, int T, int KB, int mats, int sms) {
+  const int ft = (N + 127) / 128, most = kMaxTokens / mats;
+  Cut best = {16, 1};
+  int64_t least = INT64_MAX;
+  for (int tokens = 16; tokens <= most; tokens += 16) {
+    const int64_t tiles = (int64_t)ft * ((T + tokens - 1) / tokens);
+    const int64_t block = 8 * mats * (int64_t)(tokens / 2 > 32 ? tokens / 2 : 32);
+    for (int split = 1; split <= kMaxSplit; split *= 2) {
+      if (split > 1 && (tiles * split > sms || KB < 2 * split)) break;
+      const int64_t waves = split > 1 ? 1 : (tiles + sms - 1) / sms;
+      const int64_t time = waves * ((KB + split - 1) / split) * block +
+                           (split > 1 ? 2000 + 8 * tokens * mats : 4 * tokens * mats);
+      if (time < least) least = time, best = {tokens, split};
+    }
+  }
+  return best;
+}
+
+template <int MATS>
+cudaError_t launch(const Linear4Args& a, const Cut& cut, cudaStream_t st) {
+  auto kernel = tile_kernel<MATS>;
+  Params p;
+  p.sw = a.w->scales;
+  p.su = a.up ? a.up->scales : nullptr;
+  p.xq = static_cast<const uint8_t*>(a.ws) + kStatusBytes;
+  p.N = a.w->N;
+  p.T = a.T;
+  p.KB = a.w->Kp / 128;
+  p.tokens = cut.tokens;
+  p.feature_tiles = (p.N + 127) / 128;
+  p.tiles = p.feature_tiles * ((a.T + cut.tokens - 1) / cut.tokens);
+  p.split = cut.split;
+  p.act = a.act;
+  p.out = a.out;
+  p.out_stride = a.out_stride;
+  p.status = static_cast<uint32_t*>(a.ws);
+  const uint32_t stage = (MATS * (16384 + 512) + tile_bytes(cut.tokens) + 1023) & ~1023u;
+  p.stages = (int)((kMaxSmem - 1024 - sizeof(Small)) / stage);
+  if (p.stages > 12) p.stages = 12;
+  cudaError_t e = ensure_smem_attr((const void*)kernel, kMaxSmem);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cut.split > 1 ? p.tiles * cut.split : p.tiles < sms ? p.tiles : sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kMaxSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cut.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cut.split > 1 ? 2 : 1;
+  DSPARK_LAUNCH(kKindLinear4, st,
+                e = cudaLaunchKernelEx(&cfg, kernel, a.w->tm, a.up ? a.up->tm : a.w->tm, p));
+  return e;
+}
+
+}  // namespace
+
+size_t linear4_tile_workspace_bytes(int T, int K) {
+  size_t most = 0;
+  for (int tokens = 16; tokens <= kMaxTokens; tokens += 16) {
+    const size_t n = (size_t)((T + tokens - 1) / tokens) * tile_bytes(tokens);
+    if (n > most) most = n;
+  }
+  return kStatusBytes + most * (padded_k(K) / 128);
+}
+
+cudaError_t launch_linear4_tile(const Linear4Args& a, cudaStream_t st) {
+  const int KB = a.w->Kp / 128;
+  const Cut cut = choose(a.w->N, a.T, KB, a.up ? 2 : 1, sm_count());
+  const int64_t threads = (int64_t)a.T * KB * 16;
+  cudaError_t e;
+  DSPARK_LAUNCH(kKindLinear4, st,
+                e = launch_pdl(split_kernel, dim3((unsigned)((threads + 255) / 256)),
+                               dim3(kSplitThreads), 0, st, a.x, a.x_stride, a.T, a.w->K, KB,
+                               cut.tokens, static_cast<uint8_t*>(a.ws) + kStatusBytes));
+  if (e != cudaSuccess) return e;
+  return a.up ? launch<2>(a, cut, st) : launch<1>(a, cut, st);
+}
+
+}  // namespace dspark

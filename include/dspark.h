@@ -562,7 +562,7 @@ int dspark_attend(const dspark_cache* cache, int R, int T, int Hq, int max_rows,
  * release.
  *
  * Limits: 1 <= N <= 2^24; K a multiple of 32, 32 <= K <= 65536; 0 <= T <= 2^24
- * rows (T = 0 does nothing).
+ * rows (T = 0 does nothing), T * N <= 2^38.
  */
 typedef struct dspark_weights4 {
   uint64_t opaque[64];
