@@ -17,4 +17,8 @@ __device__ __forceinline__ float activation(int act, float a) {
 size_t linear4_tile_workspace_bytes(int T, int K);
 cudaError_t launch_linear4_tile(const Linear4Args& a, cudaStream_t st);
 
+// The kernel of a few rows (linear4_rows.cu): up to 16, as many as fit in shared memory.
+bool linear4_rows_fits(int T, int Kp);
+cudaError_t launch_linear4_rows(const Linear4Args& a, cudaStream_t st);
+
 }  // namespace dspark

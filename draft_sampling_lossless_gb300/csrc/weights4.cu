@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kThreads)
     reinterpret_cast<uint4*>(d.codes)[n * groups + g] = c;
   }
   const int b = in ? __ldg(scales + n * used + g) : 127;
-  d.scales[scale_at((int)n, g, d.Kp)] = (uint8_t)min(max(b, 1), 254);
+  d.scales[scale_at((int)n, g, d.Kp)] = (uint8_t)min(max(b, 1), 252);
 }
 
 __device__ __forceinline__ float finite_abs(float v) {
@@ -62,7 +62,8 @@ __global__ void __launch_bounds__(kThreads)
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   const uint32_t b = __float_as_uint(amax);
-  const int e = max((int)(b >> 23) - 127 - ((b & 0x7fffffu) <= 0x400000u ? 2 : 1), -100);
+  const int e =
+      min(max((int)(b >> 23) - 127 - ((b & 0x7fffffu) <= 0x400000u ? 2 : 1), -100), 125);
   const float f = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = v[j] == v[j] ? v[j] * f : 0.f;

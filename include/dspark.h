@@ -552,7 +552,8 @@ int dspark_attend(const dspark_cache* cache, int R, int T, int Hq, int max_rows,
  *
  *   A code is a sign bit over two bits of exponent and one of fraction:
  *   magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.  A scale byte b stands for
- *   2^(b - 127), 1 <= b <= 254 (bytes outside count as the nearest).
+ *   2^(b - 127), 1 <= b <= 252 (bytes outside count as the nearest: every value is a
+ *   normal or subnormal of fp32 and bf16).
  *   W[n][k] = code * scale: 4.25 bits a value.
  *
  * dspark_weights4 (host memory, the caller's) describes one matrix in a store
@@ -592,7 +593,7 @@ int dspark_weights4_load(const dspark_weights4* w, const uint8_t* codes, const u
  * dspark_weights4_quantize -- fills the store from a matrix in bf16 or fp32.
  *
  * For each group of 32 columns of a row,
- *   e    = the smallest integer >= -100 with max |w| <= 6 * 2^e
+ *   e    = the smallest integer >= -100 with max |w| <= 6 * 2^e, at most 125
  *   code = w * 2^-e rounded to a code (to nearest, ties to the even code)
  * and the scale byte is e + 127.  The maximum is over the finite values; an
  * infinity becomes +-6 * 2^e, a NaN zero.
