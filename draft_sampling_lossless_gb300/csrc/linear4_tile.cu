@@ -134,11 +134,10 @@ struct Small {  // at the end of shared memory
   int abort_flag, issued;
 };
 
-// kind mxf8f6f4: A e2m1 (5), B e4m3 (0), scales powers of two, both K-major, M = 128; `j`:
-// which byte of the scales' columns.
-__device__ __forceinline__ uint32_t idesc_mx(int N, int j) {
-  return (5u << 7) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (8u << 24) |
-         (static_cast<uint32_t>(j) << 4) | (static_cast<uint32_t>(j) << 29);
+// kind mxf8f6f4: A e2m1 (5), B e4m3 (0), scales powers of two, both K-major, M = 128, the
+// first byte of the scales' columns (byte j: j << 4 for B's, j << 29 for A's).
+__device__ __forceinline__ uint32_t idesc_mx(int N) {
+  return (5u << 7) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (8u << 24);
 }
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t sa, uint32_t sb, uint32_t accumulate) {
@@ -152,12 +151,15 @@ __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint3
 }
 // 512 bytes (32 rows of 16) over the 32 lanes and 4 columns at `taddr`, in each quarter of the
 // lanes; in order with this thread's MMAs.
-__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t saddr) {
+__device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
   d |= static_cast<uint64_t>(128 >> 4) << 16;
   d |= static_cast<uint64_t>(128 >> 4) << 32;  // from 8 rows to the next 8
   d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t d) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d)
                : "memory");
 }
@@ -249,12 +251,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int k0 = (int)((int64_t)p.KB * rank / p.split);
   const int k1 = (int)((int64_t)p.KB * (rank + 1) / p.split);
 
+  // Places in the ring of stages and phases are counted, not divided out: a division by a
+  // number that only the launch knows costs the one issuing thread 200 cycles a step.
   if (warp == 0) {
     if (elect_one()) {
       const uint32_t tx = MATS * (8192 + 512) + x_bytes;
-      auto load_w = [&](int s, int tile, int kb) {
-        const int ft = tile % p.feature_tiles;
-        const uint32_t bar = b_full + 8 * s, dst = s0 + s * stage_bytes;
+      const int tt_step = step / p.feature_tiles, ft_step = step - tt_step * p.feature_tiles;
+      int tt = first / p.feature_tiles, ft = first - tt * p.feature_tiles;
+      auto load_w = [&](uint32_t bar, uint32_t dst, int kb) {
         mbar_arrive_expect_tx(bar, tx);
         tma_load_2d(dst, &tm_w, bar, kb * 128, ft * 128);
         if (MATS == 2) tma_load_2d(dst + 16384, &tm_u, bar, kb * 128, ft * 128);
@@ -262,73 +266,96 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk_load(dst + MATS * 16384 + x_bytes, p.sw + at, 512, bar);
         if (MATS == 2) bulk_load(dst + MATS * 16384 + x_bytes + 512, p.su + at, 512, bar);
       };
-      auto load_x = [&](int s, int tile, int kb) {
-        const int tt = tile / p.feature_tiles;
-        bulk_load(s0 + s * stage_bytes + MATS * 16384,
-                  p.xq + ((size_t)tt * p.KB + kb) * x_bytes, x_bytes, b_full + 8 * s);
+      auto load_x = [&](uint32_t bar, uint32_t dst, int kb) {
+        bulk_load(dst + MATS * 16384, p.xq + ((size_t)tt * p.KB + kb) * x_bytes, x_bytes, bar);
       };
       // the first stages' weights, before the kernel that writes x's tiles has ended
-      int e = 0;
       const int here = min(p.stages, k1 - k0);
-      if (first < p.tiles) {
-        for (; e < here; ++e) load_w(e, first, k0 + e);
-        grid_dependency_wait();
-        for (int i = 0; i < here; ++i) load_x(i, first, k0 + i);
-      }
+      for (int i = 0; i < here; ++i) load_w(b_full + 8 * i, s0 + i * stage_bytes, k0 + i);
+      grid_dependency_wait();
+      for (int i = 0; i < here; ++i) load_x(b_full + 8 * i, s0 + i * stage_bytes, k0 + i);
+      int issued = here, s = here, kb = k0 + here;
+      uint32_t free_parity = 1;  // of the ring's round: the first finds every stage free
       bool ok = true;
-      for (int tile = first; tile < p.tiles && ok; tile += step) {
-        for (int kb = tile == first ? k0 + here : k0; kb < k1 && ok; ++kb, ++e) {
-          const int s = e % p.stages;
-          ok = wait_bar(b_empty + 8 * s, ((e / p.stages) & 1) ^ 1, s_abort);
+      for (int tile = first; ok;) {
+        for (; kb < k1; ++kb, ++s, ++issued) {
+          if (s == p.stages) {
+            s = 0;
+            free_parity ^= 1;
+          }
+          ok = wait_bar(b_empty + 8 * s, free_parity, s_abort);
           if (!ok) break;
-          load_w(s, tile, kb);
-          load_x(s, tile, kb);
+          load_w(b_full + 8 * s, s0 + s * stage_bytes, kb);
+          load_x(b_full + 8 * s, s0 + s * stage_bytes, kb);
+        }
+        tile += step;
+        if (tile >= p.tiles) break;
+        kb = k0;
+        tt += tt_step;
+        ft += ft_step;
+        if (ft >= p.feature_tiles) {
+          ft -= p.feature_tiles;
+          ++tt;
         }
       }
-      ms->issued = e;
+      ms->issued = issued;
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      const uint32_t nb = exp_blocks(p.tokens);
-      int e = 0, n = 0;
+      const uint32_t nb = exp_blocks(p.tokens), id0 = idesc_mx(p.tokens);
+      const uint32_t stage_desc = stage_bytes >> 4;
+      const uint64_t d_w0 = desc_kmajor_sw128(s0);
+      const uint64_t d_x0 = d_w0 + MATS * (16384 >> 4);
+      const uint64_t d_e0 = desc_scales(s0 + MATS * 16384 + p.tokens * 256);
+      const uint64_t d_s0 = desc_scales(s0 + MATS * 16384 + x_bytes);
+      const uint32_t lo_off = p.tokens * 128 >> 4;
+      int s = 0, buf = 0;
+      uint32_t full_parity = 0, acc_parity = 1, set = 0, at = 0;
       bool ok = true;
-      for (int tile = first; tile < p.tiles && ok; tile += step, ++n) {
-        const int buf = n & 1;
-        ok = wait_bar(b_accEmpty + 8 * buf, ((n >> 1) & 1) ^ 1, s_abort);
+      for (int tile = first; tile < p.tiles && ok; tile += step) {
+        ok = wait_bar(b_accEmpty + 8 * buf, acc_parity, s_abort);
         tc_fence_after();
         const uint32_t acc = tmem + buf * MATS * p.tokens;
-        for (int kb = k0; kb < k1 && ok; ++kb, ++e) {
-          const int s = e % p.stages;
-          ok = wait_bar(b_full + 8 * s, (e / p.stages) & 1, s_abort);
+        uint32_t add = 0;
+        for (int kb = k0; kb < k1 && ok; ++kb) {
+          ok = wait_bar(b_full + 8 * s, full_parity, s_abort);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t at = s0 + s * stage_bytes, at_x = at + MATS * 16384;
-          const uint32_t at_e = at_x + p.tokens * 256, at_s = at_x + x_bytes;
           // the scales' columns: W (4 a matrix), hi's, lo's; two sets in turn
-          const uint32_t t_w = tmem + kSfCol + (e & 1) * 32, t_hi = t_w + 4 * MATS;
+          const uint32_t t_w = tmem + kSfCol + set, t_hi = t_w + 4 * MATS;
           const uint32_t t_lo = t_hi + 4 * nb;
 #pragma unroll
-          for (int m = 0; m < MATS; ++m) scales_to_tmem(t_w + 4 * m, at_s + 512 * m);
-          for (uint32_t i = 0; i < nb; ++i) {
-            scales_to_tmem(t_hi + 4 * i, at_e + 512 * i);
-            scales_to_tmem(t_lo + 4 * i, at_e + 512 * (nb + i));
+          for (int m = 0; m < MATS; ++m) scales_to_tmem(t_w + 4 * m, d_s0 + at + 32 * m);
+          scales_to_tmem(t_hi, d_e0 + at);
+          scales_to_tmem(t_lo, d_e0 + at + 32 * nb);
+          if (nb > 1) {
+            scales_to_tmem(t_hi + 4, d_e0 + at + 32);
+            scales_to_tmem(t_lo + 4, d_e0 + at + 96);
           }
-          const uint64_t d_w = desc_kmajor_sw128(at), d_hi = desc_kmajor_sw128(at_x);
-          const uint64_t d_lo = desc_kmajor_sw128(at_x + p.tokens * 128);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t id = idesc_mx(p.tokens, j);
+            const uint32_t id = id0 + j * ((1u << 4) + (1u << 29));
 #pragma unroll
             for (int m = 0; m < MATS; ++m) {
-              const uint64_t d_a = d_w + m * (16384 >> 4) + 2 * j;
-              mma_mx(acc + m * p.tokens, d_a, d_hi + 2 * j, id, t_w + 4 * m, t_hi,
-                     kb > k0 || j > 0);
-              mma_mx(acc + m * p.tokens, d_a, d_lo + 2 * j, id, t_w + 4 * m, t_lo, 1);
+              const uint64_t d_a = d_w0 + at + m * (16384 >> 4) + 2 * j;
+              const uint64_t d_b = d_x0 + at + 2 * j;
+              mma_mx(acc + m * p.tokens, d_a, d_b, id, t_w + 4 * m, t_hi, j > 0 ? 1 : add);
+              mma_mx(acc + m * p.tokens, d_a, d_b + lo_off, id, t_w + 4 * m, t_lo, 1);
             }
           }
           mma_commit(b_empty + 8 * s);
+          add = 1;
+          set ^= 32;
+          at += stage_desc;
+          if (++s == p.stages) {
+            s = 0;
+            at = 0;
+            full_parity ^= 1;
+          }
         }
         mma_commit(b_accFull + 8 * buf);
+        buf ^= 1;
+        if (buf == 0) acc_parity ^= 1;
       }
       if (*s_abort) {  // what was issued ends before tensor memory goes
         mma_commit(b_drain);
@@ -441,16 +468,18 @@ struct Cut {
   int tokens, split;
 };
 
-// The time of the busiest block in cycles of the MMAs: one of 128 x N x 32 takes N / 2, and
-// 32 at least (A's 4 KB from shared memory).  `split` blocks that share a tile exchange
-// their sums.
+// The time of the busiest block in cycles: an MMA of 128 x N x 32 takes N / 2, and 32 at least
+// (A's 4 KB from shared memory); the stage's bytes come at some 45 a cycle.  `split` blocks that
+// share a tile exchange their sums.
 Cut choose(int N, int T, int KB, int mats, int sms) {
   const int ft = (N + 127) / 128, most = kMaxTokens / mats;
   Cut best = {16, 1};
   int64_t least = INT64_MAX;
   for (int tokens = 16; tokens <= most; tokens += 16) {
     const int64_t tiles = (int64_t)ft * ((T + tokens - 1) / tokens);
-    const int64_t block = 8 * mats * (int64_t)(tokens / 2 > 32 ? tokens / 2 : 32);
+    const int64_t mma = 8 * mats * (tokens / 2 > 32 ? tokens / 2 : 32);
+    const int64_t fill = (8704 * mats + (int64_t)tile_bytes(tokens)) / 45;
+    const int64_t block = mma > fill ? mma : fill;
     for (int split = 1; split <= kMaxSplit; split *= 2) {
       if (split > 1 && (tiles * split > sms || KB < 2 * split)) break;
       const int64_t waves = split > 1 ? 1 : (tiles + sms - 1) / sms;
