@@ -3,14 +3,18 @@
 
 #include "dspark.h"
 #include "layer.cuh"
+#include "sm100.cuh"
 
 namespace dspark {
 
-// silu, or gelu's tanh form.  exp and tanh in full fp32: their errors stay far below the
-// result's rounding.
+// silu(a) = a s(a); gelu's tanh form, 0.5 a (1 + tanh y) = a s(2 y), with s(v) = 1 / (1 +
+// exp(-v)).  ex2.approx and the quick division are off by 2^-21 or so (2^-24 |v| in the exponent
+// on top), far below the result's rounding.  exp(-v) past 2^126 gives 0.
 __device__ __forceinline__ float activation(int act, float a) {
-  if (act == DSPARK_ACT_SILU) return a / (1.f + expf(-a));
-  return 0.5f * a * (1.f + tanhf(0.7978845608028654f * fmaf(0.044715f * a * a, a, a)));
+  float v = a;
+  if (act != DSPARK_ACT_SILU) v = 1.5957691216057308f * fmaf(0.044715f * a * a, a, a);
+  const float d = 1.f + sm100::ex2_approx(-1.4426950408889634f * v);
+  return __fdividef(a, d);
 }
 
 // The kernel on the tensor cores (linear4_tile.cu).

@@ -23,18 +23,26 @@ using namespace sm100;
 namespace {
 
 constexpr int kMaxTokens = 192;   // rows of x a tile
-constexpr int kThreads = 192;     // load, MMA, four warps of results
+constexpr int kThreads = 320;     // load, MMA, eight warps of results
 constexpr int kMaxSmem = 232448;
 constexpr int kSfCol = 384;       // tensor memory: accumulators below, scales above
 constexpr int kMaxSplit = 8;
 constexpr uint32_t kStatusBytes = 1024;
 constexpr uint32_t kWaitNs = 2000000000u;
 
-// Bytes of the tile of `tokens` rows and 128 columns of x: hi, lo, their exponents in
-// blocks of 128 rows as tcgen05.cp takes them.
-__host__ __device__ constexpr uint32_t exp_blocks(int tokens) { return (tokens + 127) / 128; }
-__host__ __device__ constexpr uint32_t tile_bytes(int tokens) {
-  return (uint32_t)tokens * 256 + exp_blocks(tokens) * 1024;
+// How a product is cut.  `tokens`: rows of x a tile; `wide`: hi and lo as 2 * tokens columns
+// of one MMA, else an MMA each; `split`: blocks that share a tile's K.
+struct Cut {
+  int mats, tokens, wide, split;
+};
+
+// The tile of `tokens` rows and 128 columns of x: hi, lo, their exponents in blocks of 512
+// bytes for 128 MMA columns, as tcgen05.cp takes them (hi's then lo's).
+__host__ __device__ constexpr uint32_t exp_blocks(int tokens, int wide) {
+  return wide ? (2 * tokens + 127) / 128 : 2 * ((tokens + 127) / 128);
+}
+__host__ __device__ constexpr uint32_t tile_bytes(int tokens, int wide) {
+  return (uint32_t)tokens * 256 + exp_blocks(tokens, wide) * 512;
 }
 
 // ---------------------------------------------------------------- x in two terms
@@ -62,7 +70,7 @@ constexpr int kSplitThreads = 256;
 // Rows past T stay as they are: they reach only columns of the product that are not stored.
 __global__ void __launch_bounds__(kSplitThreads)
     split_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride, int T, int K, int KB,
-                 int tokens, uint8_t* __restrict__ out) {
+                 int tokens, int wide, uint8_t* __restrict__ out) {
   grid_dependency_wait();
   asm volatile("griddepcontrol.launch_dependents;");
   const int64_t i = ((int64_t)blockIdx.x * kSplitThreads + threadIdx.x) >> 4;
@@ -106,14 +114,14 @@ __global__ void __launch_bounds__(kSplitThreads)
   if (t >= T) return;
   const int64_t tile = t / tokens;
   const int r = (int)(t - tile * tokens);
-  uint8_t* dst = out + (tile * KB + kb) * tile_bytes(tokens);
+  uint8_t* dst = out + (tile * KB + kb) * tile_bytes(tokens, wide);
   const uint32_t at = r * 128 + (((lane >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
   *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0], hi[1]);
   *reinterpret_cast<uint2*>(dst + tokens * 128 + at) = make_uint2(lo[0], lo[1]);
-  if (lane == 0) {
-    uint8_t* s = dst + tokens * 256 + (r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
-    *reinterpret_cast<uint32_t*>(s) = exps;
-    *reinterpret_cast<uint32_t*>(s + exp_blocks(tokens) * 512) = exps - 0x04040404u;
+  if (lane < 2) {  // an MMA column's exponents: lane n % 32 of tensor memory, column n / 32
+    const int n = lane == 0 ? r : wide ? tokens + r : (tokens + 127) / 128 * 128 + r;
+    *reinterpret_cast<uint32_t*>(dst + tokens * 256 + (n >> 7) * 512 + (n & 31) * 16 +
+                                 ((n >> 5) & 3) * 4) = exps - lane * 0x04040404u;
   }
 }
 
@@ -122,7 +130,8 @@ __global__ void __launch_bounds__(kSplitThreads)
 struct Params {
   const uint8_t *sw, *su;  // scales of the matrices
   const uint8_t* xq;       // tiles of x
-  int N, T, KB, tokens, feature_tiles, tiles, split, stages, act;
+  int N, T, KB, row_blocks, tokens, wide, feature_tiles, tiles, split, stages, buffers, act;
+  bool vector;  // rows of out are 16-byte aligned
   __nv_bfloat16* out;
   int64_t out_stride;
   uint32_t* status;
@@ -187,12 +196,12 @@ __device__ __forceinline__ void cluster_sync_all() {
       "barrier.cluster.wait.acquire.aligned;" ::
           : "memory");
 }
-__device__ __forceinline__ void store_cluster(uint32_t addr, int rank, float v) {
+__device__ __forceinline__ void store_cluster(uint32_t addr, int rank, const float (&v)[4]) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\t"
       "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(addr),
-      "r"(rank), "f"(v)
+      "st.shared::cluster.v4.f32 [a], {%2, %3, %4, %5};\n\t}" ::"r"(addr),
+      "r"(rank), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
       : "memory");
 }
 
@@ -200,8 +209,77 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   return mbar_wait_or_abort(bar, parity, abort_flag, kWaitNs);
 }
 
-// MATS: 1, or 2 for the gated product (both accumulators in the same lanes).
-template <int MATS>
+// 16 rows of x of an accumulator at `taddr`, hi's and lo's sums added.
+__device__ __forceinline__ void load_sums(uint32_t taddr, const Params& p, float (&v)[16]) {
+  uint32_t a[16], b[16];
+  tmem_ld_x16(taddr, a);
+  if (p.wide) {
+    tmem_ld_x16(taddr + p.tokens, b);
+    tmem_wait_ld_regs(a, b);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
+  } else {
+    tmem_wait_ld_regs(a);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// A warp's 16 rows of x by 32 features, a feature a lane, rounded and turned in three exchanges
+// so that a lane has 8 neighbouring features of two rows: two 16-byte stores for 16 of two
+// bytes (whose 64 bytes a warp took 9 cycles each).  `out`: the first row and feature.
+__device__ __forceinline__ void store_rows(const float (&v)[16], const Params& p,
+                                           __nv_bfloat16* out, int rows, int features) {
+  const uint32_t lane = threadIdx.x & 31;
+  const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+  uint32_t x[8];  // rows 2 j and 2 j + 1, then row 2 j + b0 of two features
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+  const uint32_t give = b0 ? 0x5410u : 0x7632u;
+  const uint32_t first = b0 ? 0x3254u : 0x5410u, second = b0 ? 0x3276u : 0x7610u;
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const uint32_t r = __shfl_xor_sync(0xffffffffu, __byte_perm(x[j], x[j + 1], give), 1);
+    x[j] = __byte_perm(x[j], r, first);
+    x[j + 1] = __byte_perm(x[j + 1], r, second);
+  }
+  uint2 y[4];  // row 4 i + 2 b1 + b0 of four features
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t keep = b1 ? x[2 * i + 1] : x[2 * i];
+    const uint32_t r = __shfl_xor_sync(0xffffffffu, b1 ? x[2 * i] : x[2 * i + 1], 2);
+    y[i] = b1 ? make_uint2(r, keep) : make_uint2(keep, r);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint2 keep = b2 ? y[2 * k + 1] : y[2 * k], send = b2 ? y[2 * k] : y[2 * k + 1];
+    uint2 r;
+    r.x = __shfl_xor_sync(0xffffffffu, send.x, 4);
+    r.y = __shfl_xor_sync(0xffffffffu, send.y, 4);
+    const uint4 z = b2 ? make_uint4(r.x, r.y, keep.x, keep.y) : make_uint4(keep.x, keep.y, r.x, r.y);
+    const int row = 8 * k + (lane & 7), f = lane & ~7u;
+    if (row >= rows || f >= features) continue;
+    __nv_bfloat16* dst = out + row * p.out_stride + f;
+    if (p.vector && f + 8 <= features) {
+      *reinterpret_cast<uint4*>(dst) = z;
+    } else {
+      const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (f + i < features)
+          reinterpret_cast<uint16_t*>(dst)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+
+// MATS row tiles of 128 share a block's x: two of one matrix, or (GATED) one of each.
+template <int MATS, bool GATED>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_u,
                 const Params p) {
@@ -209,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t x_bytes = tile_bytes(p.tokens);
+  const uint32_t x_bytes = tile_bytes(p.tokens, p.wide);
   // a stage: codes (16 KB a matrix), x's tile, the codes' scales (512 bytes a matrix)
   const uint32_t stage_bytes = (MATS * (16384 + 512) + x_bytes + 1023) & ~1023u;
   const uint32_t s0 = smem_u32(smem);
@@ -230,14 +308,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_accFull + 8 * i, 1);
-      mbar_init(b_accEmpty + 8 * i, 4);
+      mbar_init(b_accEmpty + 8 * i, 8);
     }
     mbar_init(b_drain, 1);
     fence_mbar_init();
     ms->abort_flag = 0;
     ms->issued = 0;
     tma_prefetch(&tm_w);
-    if (MATS == 2) tma_prefetch(&tm_u);
+    if (GATED) tma_prefetch(&tm_u);
   }
   tc_fence_before();
   __syncthreads();
@@ -260,11 +338,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tt = first / p.feature_tiles, ft = first - tt * p.feature_tiles;
       auto load_w = [&](uint32_t bar, uint32_t dst, int kb) {
         mbar_arrive_expect_tx(bar, tx);
-        tma_load_2d(dst, &tm_w, bar, kb * 128, ft * 128);
-        if (MATS == 2) tma_load_2d(dst + 16384, &tm_u, bar, kb * 128, ft * 128);
-        const size_t at = ((size_t)ft * p.KB + kb) * 512;
-        bulk_load(dst + MATS * 16384 + x_bytes, p.sw + at, 512, bar);
-        if (MATS == 2) bulk_load(dst + MATS * 16384 + x_bytes + 512, p.su + at, 512, bar);
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+          const int row = GATED || MATS == 1 ? ft : ft * 2 + m;  // in blocks of 128
+          tma_load_2d(dst + m * 16384, GATED && m ? &tm_u : &tm_w, bar, kb * 128, row * 128);
+          // (the second tile of an odd number reads zeros, with the last tile's scales)
+          const int in = GATED || MATS == 1 ? row : min(row, p.row_blocks - 1);
+          bulk_load(dst + MATS * 16384 + x_bytes + m * 512,
+                    (GATED && m ? p.su : p.sw) + ((size_t)in * p.KB + kb) * 512, 512, bar);
+        }
       };
       auto load_x = [&](uint32_t bar, uint32_t dst, int kb) {
         bulk_load(dst + MATS * 16384, p.xq + ((size_t)tt * p.KB + kb) * x_bytes, x_bytes, bar);
@@ -302,7 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      const uint32_t nb = exp_blocks(p.tokens), id0 = idesc_mx(p.tokens);
+      const uint32_t nb = exp_blocks(p.tokens, p.wide), acc_cols = p.tokens << p.wide;
+      const uint32_t id0 = idesc_mx(acc_cols);
       const uint32_t stage_desc = stage_bytes >> 4;
       const uint64_t d_w0 = desc_kmajor_sw128(s0);
       const uint64_t d_x0 = d_w0 + MATS * (16384 >> 4);
@@ -315,32 +398,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int tile = first; tile < p.tiles && ok; tile += step) {
         ok = wait_bar(b_accEmpty + 8 * buf, acc_parity, s_abort);
         tc_fence_after();
-        const uint32_t acc = tmem + buf * MATS * p.tokens;
+        const uint32_t acc = tmem + buf * MATS * acc_cols;
         uint32_t add = 0;
         for (int kb = k0; kb < k1 && ok; ++kb) {
           ok = wait_bar(b_full + 8 * s, full_parity, s_abort);
           if (!ok) break;
           tc_fence_after();
-          // the scales' columns: W (4 a matrix), hi's, lo's; two sets in turn
-          const uint32_t t_w = tmem + kSfCol + set, t_hi = t_w + 4 * MATS;
-          const uint32_t t_lo = t_hi + 4 * nb;
+          // the scales' columns: W (4 a tile), hi's, lo's; two sets in turn
+          const uint32_t t_w = tmem + kSfCol + set, t_x = t_w + 4 * MATS;
 #pragma unroll
           for (int m = 0; m < MATS; ++m) scales_to_tmem(t_w + 4 * m, d_s0 + at + 32 * m);
-          scales_to_tmem(t_hi, d_e0 + at);
-          scales_to_tmem(t_lo, d_e0 + at + 32 * nb);
-          if (nb > 1) {
-            scales_to_tmem(t_hi + 4, d_e0 + at + 32);
-            scales_to_tmem(t_lo + 4, d_e0 + at + 96);
+          scales_to_tmem(t_x, d_e0 + at);
+          if (nb > 1) scales_to_tmem(t_x + 4, d_e0 + at + 32);
+          if (nb > 2) {
+            scales_to_tmem(t_x + 8, d_e0 + at + 64);
+            scales_to_tmem(t_x + 12, d_e0 + at + 96);
           }
+          if (p.wide) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t id = id0 + j * ((1u << 4) + (1u << 29));
+            for (int j = 0; j < 4; ++j) {
 #pragma unroll
-            for (int m = 0; m < MATS; ++m) {
-              const uint64_t d_a = d_w0 + at + m * (16384 >> 4) + 2 * j;
-              const uint64_t d_b = d_x0 + at + 2 * j;
-              mma_mx(acc + m * p.tokens, d_a, d_b, id, t_w + 4 * m, t_hi, j > 0 ? 1 : add);
-              mma_mx(acc + m * p.tokens, d_a, d_b + lo_off, id, t_w + 4 * m, t_lo, 1);
+              for (int m = 0; m < MATS; ++m)
+                mma_mx(acc + m * acc_cols, d_w0 + at + m * (16384 >> 4) + 2 * j, d_x0 + at + 2 * j,
+                       id0 + j * ((1u << 4) + (1u << 29)), t_w + 4 * m, t_x, j > 0 ? 1 : add);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+              for (int m = 0; m < MATS; ++m) {
+                const uint32_t id = id0 + j * ((1u << 4) + (1u << 29));
+                const uint64_t d_a = d_w0 + at + m * (16384 >> 4) + 2 * j;
+                const uint64_t d_b = d_x0 + at + 2 * j;
+                mma_mx(acc + m * acc_cols, d_a, d_b, id, t_w + 4 * m, t_x, j > 0 ? 1 : add);
+                mma_mx(acc + m * acc_cols, d_a, d_b + lo_off, id, t_w + 4 * m, t_x + 2 * nb, 1);
+              }
             }
           }
           mma_commit(b_empty + 8 * s);
@@ -354,8 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         mma_commit(b_accFull + 8 * buf);
-        buf ^= 1;
-        if (buf == 0) acc_parity ^= 1;
+        if (++buf == p.buffers) {
+          buf = 0;
+          acc_parity ^= 1;
+        }
       }
       if (*s_abort) {  // what was issued ends before tensor memory goes
         mma_commit(b_drain);
@@ -364,40 +458,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ results
+    // Two warps a quarter of the lanes, every second 16 rows of x each.
     grid_dependency_wait();
-    const int quad = warp & 3;
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t acc_cols = p.tokens << p.wide;
     const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
-    int n = 0;
-    for (int tile = first; tile < p.tiles; tile += step, ++n) {
-      const int buf = n & 1, ft = tile % p.feature_tiles, tt = tile / p.feature_tiles;
-      const bool ok = wait_bar(b_accFull + 8 * buf, (n >> 1) & 1, s_abort);
+    int buf = 0;
+    uint32_t acc_parity = 0;
+    for (int tile = first; tile < p.tiles; tile += step) {
+      const int tt = tile / p.feature_tiles, ft = tile - tt * p.feature_tiles;
+      const bool ok = wait_bar(b_accFull + 8 * buf, acc_parity, s_abort);
       if (__any_sync(0xffffffffu, !ok)) break;
       if (p.split > 1) break;
       tc_fence_after();
-      const uint32_t acc = tmem + t_lane + buf * MATS * p.tokens;
-      const int f = ft * 128 + quad * 32 + lane, t0 = tt * p.tokens;
-      __nv_bfloat16* out = p.out + (int64_t)t0 * p.out_stride + f;
-      const int rows = min(p.tokens, p.T - t0);
+      const uint32_t acc = tmem + t_lane + buf * MATS * acc_cols;
+      const int t0 = tt * p.tokens, rows = min(p.tokens, p.T - t0);
+      const int f0 = ft * (GATED ? 128 : 128 * MATS) + quad * 32;
 #pragma unroll 1
-      for (int c = 0; c < rows; c += 16) {
-        uint32_t a[16], b[16];
-        tmem_ld_x16(acc + c, a);
-        if (MATS == 2) {
-          tmem_ld_x16(acc + p.tokens + c, b);
-          tmem_wait_ld_regs(a, b);
-        } else {
-          tmem_wait_ld_regs(a);
-        }
+      for (int c = half * 16; c < rows; c += 32) {
+        __nv_bfloat16* out = p.out + (int64_t)(t0 + c) * p.out_stride + f0;
+#pragma unroll 1
+        for (int m = 0; m < (GATED ? 1 : MATS); ++m) {
+          float a[16];
+          load_sums(acc + m * acc_cols + c, p, a);
+          if (GATED) {
+            float b[16];
+            load_sums(acc + acc_cols + c, p, b);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float v = __uint_as_float(a[i]);
-          if (MATS == 2) v = activation(p.act, v) * __uint_as_float(b[i]);
-          if (f < p.N && c + i < rows) out[(c + i) * p.out_stride] = __float2bfloat16(v);
+            for (int i = 0; i < 16; ++i) a[i] = activation(p.act, a[i]) * b[i];
+          }
+          store_rows(a, p, out + m * 128, rows - c, p.N - f0 - m * 128);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_accEmpty + 8 * buf);
+      if (++buf == p.buffers) {
+        buf = 0;
+        acc_parity ^= 1;
+      }
     }
   }
 
@@ -408,24 +507,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     __syncwarp();
     cluster_sync_all();
-    const int cols = p.tokens / p.split, quad = warp & 3;
-    float* part = reinterpret_cast<float*>(smem);  // [split][MATS][cols][128]
-    const int ft = first % p.feature_tiles, tt = first / p.feature_tiles;
+    const int cols = p.tokens / p.split;  // a multiple of 4
+    float4* part = reinterpret_cast<float4*>(smem);  // [split][MATS][cols / 4][128]
     if (warp >= 2) {
       tc_fence_after();
-      const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+      const int quad = warp & 3, half = (warp - 2) >> 2, f = quad * 32 + lane;
+      const uint32_t acc_cols = p.tokens << p.wide;
 #pragma unroll 1
-      for (int c = 0; c < MATS * p.tokens; c += 16) {
-        uint32_t a[16];
-        tmem_ld_x16(acc + c, a);
-        tmem_wait_ld_regs(a);
+      for (int m = 0; m < MATS; ++m) {
+        const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + m * acc_cols;
+#pragma unroll 1
+        for (int c = half * 16; c < p.tokens; c += 32) {
+          float a[16];
+          load_sums(acc + c, p, a);
+          int to = c / cols, at = (c - to * cols) >> 2;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int m = MATS == 2 && c + i >= p.tokens, col = c + i - m * p.tokens;
-          const int to = col / cols;
-          store_cluster(smem_u32(part + ((rank * MATS + m) * cols + col - to * cols) * 128 +
-                                 quad * 32 + lane),
-                        to, __uint_as_float(a[i]));
+          for (int i = 0; i < 16; i += 4) {
+            const float v[4] = {a[i], a[i + 1], a[i + 2], a[i + 3]};
+            store_cluster(smem_u32(part + ((rank * MATS + m) * (cols >> 2) + at) * 128 + f), to, v);
+            if (++at == cols >> 2) at = 0, ++to;
+          }
         }
       }
       tc_fence_before();
@@ -433,19 +534,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     __syncwarp();
     cluster_sync_all();
+    const int tt = first / p.feature_tiles, ft = first - tt * p.feature_tiles;
     const int t0 = tt * p.tokens + rank * cols;
-    for (int i = tid; i < cols * 128; i += kThreads) {
-      const int col = i >> 7, f = i & 127;
-      float v[MATS];
+    for (int i = tid; i < cols * 32; i += kThreads) {  // four rows of x, one feature
+      const int c = i >> 7, f = i & 127;
+      float4 v[MATS];
 #pragma unroll
       for (int m = 0; m < MATS; ++m) {
-        v[m] = 0.f;
-        for (int r = 0; r < p.split; ++r) v[m] += part[((r * MATS + m) * cols + col) * 128 + f];
+        v[m] = part[(m * (cols >> 2) + c) * 128 + f];
+        for (int r = 1; r < p.split; ++r) {
+          const float4 x = part[((r * MATS + m) * (cols >> 2) + c) * 128 + f];
+          v[m].x += x.x;
+          v[m].y += x.y;
+          v[m].z += x.z;
+          v[m].w += x.w;
+        }
       }
-      float o = v[0];
-      if (MATS == 2) o = activation(p.act, o) * v[MATS - 1];
-      if (t0 + col < p.T && ft * 128 + f < p.N)
-        p.out[(int64_t)(t0 + col) * p.out_stride + ft * 128 + f] = __float2bfloat16(o);
+#pragma unroll
+      for (int m = 0; m < (GATED ? 1 : MATS); ++m) {
+        const int n = ft * (GATED ? 128 : 128 * MATS) + m * 128 + f;
+        if (n >= p.N) continue;
+        float o[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
+        if (GATED) {
+          const float4 u = v[MATS - 1];
+          o[0] = activation(p.act, o[0]) * u.x;
+          o[1] = activation(p.act, o[1]) * u.y;
+          o[2] = activation(p.act, o[2]) * u.z;
+          o[3] = activation(p.act, o[3]) * u.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (t0 + c * 4 + j < p.T)
+            p.out[(int64_t)(t0 + c * 4 + j) * p.out_stride + n] = __float2bfloat16(o[j]);
+      }
     }
   }
   tc_fence_before();
@@ -463,37 +584,53 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// How a product is cut: rows of x a tile, and blocks that share a tile's K.
-struct Cut {
-  int tokens, split;
-};
+constexpr uint32_t stage_bytes_of(const Cut& c) {
+  return (c.mats * (16384 + 512) + tile_bytes(c.tokens, c.wide) + 1023) & ~1023u;
+}
+int stages_of(const Cut& c) {
+  const int n = (int)((kMaxSmem - 1024 - sizeof(Small)) / stage_bytes_of(c));
+  return n < 12 ? n : 12;
+}
+int acc_cols_of(const Cut& c) { return c.mats * (c.tokens << c.wide); }
 
-// The time of the busiest block in cycles: an MMA of 128 x N x 32 takes N / 2, and 32 at least
-// (A's 4 KB from shared memory); the stage's bytes come at some 45 a cycle.  `split` blocks that
-// share a tile exchange their sums.
-Cut choose(int N, int T, int KB, int mats, int sms) {
-  const int ft = (N + 127) / 128, most = kMaxTokens / mats;
-  Cut best = {16, 1};
+// The cut with the least time of the busiest block, in cycles.  An MMA of 128 x N x 32 takes
+// N / 2, and 64 at least (A's 4 KB from shared memory); a stage's bytes come at some 60 a cycle.
+// Two accumulators hide the results' way out behind the next tile.  `split` blocks exchange
+// their sums.
+Cut choose(int N, int T, int KB, bool gated, int sms) {
+  const int blocks = (N + 127) / 128;
+  Cut best = {gated ? 2 : 1, 16, 1, 1};
   int64_t least = INT64_MAX;
-  for (int tokens = 16; tokens <= most; tokens += 16) {
-    const int64_t tiles = (int64_t)ft * ((T + tokens - 1) / tokens);
-    const int64_t mma = 8 * mats * (tokens / 2 > 32 ? tokens / 2 : 32);
-    const int64_t fill = (8704 * mats + (int64_t)tile_bytes(tokens)) / 45;
-    const int64_t block = mma > fill ? mma : fill;
-    for (int split = 1; split <= kMaxSplit; split *= 2) {
-      if (split > 1 && (tiles * split > sms || KB < 2 * split)) break;
-      const int64_t waves = split > 1 ? 1 : (tiles + sms - 1) / sms;
-      const int64_t time = waves * ((KB + split - 1) / split) * block +
-                           (split > 1 ? 2000 + 8 * tokens * mats : 4 * tokens * mats);
-      if (time < least) least = time, best = {tokens, split};
-    }
-  }
+  Cut c;
+  for (c.mats = gated ? 2 : 1; c.mats <= 2; ++c.mats)
+    for (c.wide = 0; c.wide < 2; ++c.wide)
+      for (c.tokens = 16; c.tokens <= (c.wide ? kMaxTokens / 2 : kMaxTokens); c.tokens += 16) {
+        if (acc_cols_of(c) > kSfCol || stages_of(c) < 3) break;
+        const int64_t ft = gated ? blocks : (blocks + c.mats - 1) / c.mats;
+        const int64_t tiles = ft * ((T + c.tokens - 1) / c.tokens);
+        const int n2 = c.wide ? c.tokens : c.tokens / 2;  // half of an MMA's N
+        const int64_t mma = (c.wide ? 4 : 8) * c.mats * (n2 > 64 ? n2 : 64);
+        const int64_t fill = (8704 * c.mats + (int64_t)tile_bytes(c.tokens, c.wide)) / 60;
+        const int64_t step = (mma > fill ? mma : fill) + 50;
+        const int64_t out = 500 + (gated ? 12 : 6 * c.mats) * c.tokens;
+        for (c.split = 1; c.split <= kMaxSplit; c.split *= 2) {
+          if (c.split > 1 &&
+              (tiles * c.split > sms || KB < 2 * c.split || c.tokens % (4 * c.split) != 0))
+            break;
+          const int64_t waves = c.split > 1 ? 1 : (tiles + sms - 1) / sms;
+          const int64_t hidden = 2 * acc_cols_of(c) <= kSfCol;
+          const int64_t time =
+              waves * ((KB + c.split - 1) / c.split) * step + (hidden ? 1 : waves) * out +
+              (c.split > 1 ? 2500 : 0);
+          if (time < least) least = time, best = c;
+        }
+      }
   return best;
 }
 
-template <int MATS>
+template <int MATS, bool GATED>
 cudaError_t launch(const Linear4Args& a, const Cut& cut, cudaStream_t st) {
-  auto kernel = tile_kernel<MATS>;
+  auto kernel = tile_kernel<MATS, GATED>;
   Params p;
   p.sw = a.w->scales;
   p.su = a.up ? a.up->scales : nullptr;
@@ -501,17 +638,19 @@ cudaError_t launch(const Linear4Args& a, const Cut& cut, cudaStream_t st) {
   p.N = a.w->N;
   p.T = a.T;
   p.KB = a.w->Kp / 128;
+  p.row_blocks = (p.N + 127) / 128;
   p.tokens = cut.tokens;
-  p.feature_tiles = (p.N + 127) / 128;
+  p.wide = cut.wide;
+  p.feature_tiles = GATED ? p.row_blocks : (p.row_blocks + MATS - 1) / MATS;
   p.tiles = p.feature_tiles * ((a.T + cut.tokens - 1) / cut.tokens);
   p.split = cut.split;
   p.act = a.act;
   p.out = a.out;
   p.out_stride = a.out_stride;
   p.status = static_cast<uint32_t*>(a.ws);
-  const uint32_t stage = (MATS * (16384 + 512) + tile_bytes(cut.tokens) + 1023) & ~1023u;
-  p.stages = (int)((kMaxSmem - 1024 - sizeof(Small)) / stage);
-  if (p.stages > 12) p.stages = 12;
+  p.vector = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.out_stride % 8 == 0;
+  p.stages = stages_of(cut);
+  p.buffers = 2 * acc_cols_of(cut) <= kSfCol ? 2 : 1;
   cudaError_t e = ensure_smem_attr((const void*)kernel, kMaxSmem);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
@@ -537,24 +676,27 @@ cudaError_t launch(const Linear4Args& a, const Cut& cut, cudaStream_t st) {
 
 size_t linear4_tile_workspace_bytes(int T, int K) {
   size_t most = 0;
-  for (int tokens = 16; tokens <= kMaxTokens; tokens += 16) {
-    const size_t n = (size_t)((T + tokens - 1) / tokens) * tile_bytes(tokens);
-    if (n > most) most = n;
-  }
+  for (int wide = 0; wide < 2; ++wide)
+    for (int tokens = 16; tokens <= kMaxTokens; tokens += 16) {
+      const size_t n = (size_t)((T + tokens - 1) / tokens) * tile_bytes(tokens, wide);
+      if (n > most) most = n;
+    }
   return kStatusBytes + most * (padded_k(K) / 128);
 }
 
 cudaError_t launch_linear4_tile(const Linear4Args& a, cudaStream_t st) {
   const int KB = a.w->Kp / 128;
-  const Cut cut = choose(a.w->N, a.T, KB, a.up ? 2 : 1, sm_count());
+  const Cut cut = choose(a.w->N, a.T, KB, a.up != nullptr, sm_count());
   const int64_t threads = (int64_t)a.T * KB * 16;
   cudaError_t e;
   DSPARK_LAUNCH(kKindLinear4, st,
                 e = launch_pdl(split_kernel, dim3((unsigned)((threads + 255) / 256)),
                                dim3(kSplitThreads), 0, st, a.x, a.x_stride, a.T, a.w->K, KB,
-                               cut.tokens, static_cast<uint8_t*>(a.ws) + kStatusBytes));
+                               cut.tokens, cut.wide, static_cast<uint8_t*>(a.ws) + kStatusBytes));
   if (e != cudaSuccess) return e;
-  return a.up ? launch<2>(a, cut, st) : launch<1>(a, cut, st);
+  return a.up            ? launch<2, true>(a, cut, st)
+         : cut.mats == 2 ? launch<2, false>(a, cut, st)
+                         : launch<1, false>(a, cut, st);
 }
 
 }  // namespace dspark

@@ -68,7 +68,8 @@ def check_linear(x, w, got):
 def act64(name, a):
     if name == "silu":
         return a * torch.sigmoid(a)
-    return 0.5 * a * (1 + torch.tanh(math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3)))
+    # 0.5 (1 + tanh y) = 1 / (1 + exp(-2 y)), which 64 bits hold where 1 + tanh y cancels
+    return a * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3))
 
 
 def check_gated(x, g, u, act, got):
