@@ -23,9 +23,12 @@ using namespace sm100;
 namespace {
 
 constexpr int kMaxTokens = 192;   // rows of x a tile
-constexpr int kThreads = 320;     // load, MMA, eight warps of results
+constexpr int kOutWarps = 16;     // warps of results, a quarter of them for 32 lanes each
+constexpr int kTurns = kOutWarps / 4;
+constexpr int kThreads = 64 + kOutWarps * 32;  // one that loads, one that issues MMAs, results
 constexpr int kMaxSmem = 232448;
-constexpr int kSfCol = 384;       // tensor memory: accumulators below, scales above
+constexpr int kSfCol = 480;       // tensor memory: accumulators below, scales above
+constexpr int kMaxSlots = 8;
 constexpr int kMaxSplit = 8;
 constexpr uint32_t kStatusBytes = 1024;
 constexpr uint32_t kWaitNs = 2000000000u;
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(kSplitThreads)
 struct Params {
   const uint8_t *sw, *su;  // scales of the matrices
   const uint8_t* xq;       // tiles of x
-  int N, T, KB, row_blocks, tokens, wide, feature_tiles, tiles, split, stages, buffers, act;
+  int N, T, KB, row_blocks, tokens, wide, feature_tiles, tiles, split, stages, slots, act;
   bool vector;  // rows of out are 16-byte aligned
   __nv_bfloat16* out;
   int64_t out_stride;
@@ -138,7 +141,7 @@ struct Params {
 };
 
 struct Small {  // at the end of shared memory
-  uint64_t full[12], empty[12], acc_full[2], acc_empty[2], drain;
+  uint64_t full[12], empty[12], acc_full[kMaxSlots], acc_empty[kMaxSlots], drain;
   uint32_t tmem;
   int abort_flag, issued;
 };
@@ -172,15 +175,6 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t d) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d)
                : "memory");
 }
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
-        "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr));
-}
 // Untiled copy, 16-byte aligned, completing on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -209,19 +203,19 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   return mbar_wait_or_abort(bar, parity, abort_flag, kWaitNs);
 }
 
-// 16 rows of x of an accumulator at `taddr`, hi's and lo's sums added.
-__device__ __forceinline__ void load_sums(uint32_t taddr, const Params& p, float (&v)[16]) {
-  uint32_t a[16], b[16];
-  tmem_ld_x16(taddr, a);
+// Eight rows of x of an accumulator at `taddr`, hi's and lo's sums added.
+__device__ __forceinline__ void load_sums(uint32_t taddr, const Params& p, float (&v)[8]) {
+  uint32_t a[8], b[8];
+  tmem_ld_32x32b_x8(taddr, a);
   if (p.wide) {
-    tmem_ld_x16(taddr + p.tokens, b);
+    tmem_ld_32x32b_x8(taddr + p.tokens, b);
     tmem_wait_ld_regs(a, b);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
   } else {
     tmem_wait_ld_regs(a);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]);
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(a[i]);
   }
 }
 
@@ -231,50 +225,47 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return d;
 }
 
-// A warp's 16 rows of x by 32 features, a feature a lane, rounded and turned in three exchanges
-// so that a lane has 8 neighbouring features of two rows: two 16-byte stores for 16 of two
-// bytes (whose 64 bytes a warp took 9 cycles each).  `out`: the first row and feature.
-__device__ __forceinline__ void store_rows(const float (&v)[16], const Params& p,
+// A warp's 8 rows of x by 32 features, a feature a lane (v[0..3]: pairs of rows in bf16), turned
+// in three exchanges so that a lane has 8 neighbouring features of a row: one 16-byte store
+// for 8 of two bytes.  `out`: the first row and feature.
+__device__ __forceinline__ void store_rows(const uint32_t* v, const Params& p,
                                            __nv_bfloat16* out, int rows, int features) {
   const uint32_t lane = threadIdx.x & 31;
   const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
-  uint32_t x[8];  // rows 2 j and 2 j + 1, then row 2 j + b0 of two features
+  uint32_t x[4];  // rows 2 j and 2 j + 1, then row 2 j + b0 of two features
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+  for (int j = 0; j < 4; ++j) x[j] = v[j];
   const uint32_t give = b0 ? 0x5410u : 0x7632u;
   const uint32_t first = b0 ? 0x3254u : 0x5410u, second = b0 ? 0x3276u : 0x7610u;
 #pragma unroll
-  for (int j = 0; j < 8; j += 2) {
+  for (int j = 0; j < 4; j += 2) {
     const uint32_t r = __shfl_xor_sync(0xffffffffu, __byte_perm(x[j], x[j + 1], give), 1);
     x[j] = __byte_perm(x[j], r, first);
     x[j + 1] = __byte_perm(x[j + 1], r, second);
   }
-  uint2 y[4];  // row 4 i + 2 b1 + b0 of four features
+  uint2 y[2];  // row 4 i + 2 b1 + b0 of four features
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const uint32_t keep = b1 ? x[2 * i + 1] : x[2 * i];
     const uint32_t r = __shfl_xor_sync(0xffffffffu, b1 ? x[2 * i] : x[2 * i + 1], 2);
     y[i] = b1 ? make_uint2(r, keep) : make_uint2(keep, r);
   }
+  const uint2 keep = b2 ? y[1] : y[0], send = b2 ? y[0] : y[1];
+  uint2 r;
+  r.x = __shfl_xor_sync(0xffffffffu, send.x, 4);
+  r.y = __shfl_xor_sync(0xffffffffu, send.y, 4);
+  const uint4 z = b2 ? make_uint4(r.x, r.y, keep.x, keep.y) : make_uint4(keep.x, keep.y, r.x, r.y);
+  const int row = lane & 7, f = lane & ~7u;
+  if (row >= rows || f >= features) return;
+  __nv_bfloat16* dst = out + row * p.out_stride + f;
+  if (p.vector && f + 8 <= features) {
+    *reinterpret_cast<uint4*>(dst) = z;
+  } else {
+    const uint32_t w[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint2 keep = b2 ? y[2 * k + 1] : y[2 * k], send = b2 ? y[2 * k] : y[2 * k + 1];
-    uint2 r;
-    r.x = __shfl_xor_sync(0xffffffffu, send.x, 4);
-    r.y = __shfl_xor_sync(0xffffffffu, send.y, 4);
-    const uint4 z = b2 ? make_uint4(r.x, r.y, keep.x, keep.y) : make_uint4(keep.x, keep.y, r.x, r.y);
-    const int row = 8 * k + (lane & 7), f = lane & ~7u;
-    if (row >= rows || f >= features) continue;
-    __nv_bfloat16* dst = out + row * p.out_stride + f;
-    if (p.vector && f + 8 <= features) {
-      *reinterpret_cast<uint4*>(dst) = z;
-    } else {
-      const uint32_t w[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (f + i < features)
-          reinterpret_cast<uint16_t*>(dst)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-    }
+    for (int i = 0; i < 8; ++i)
+      if (f + i < features)
+        reinterpret_cast<uint16_t*>(dst)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
   }
 }
 
@@ -306,9 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(b_full + 8 * i, 1);
       mbar_init(b_empty + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(b_accFull + 8 * i, 1);
-      mbar_init(b_accEmpty + 8 * i, 8);
+      mbar_init(b_accEmpty + 8 * i, kOutWarps);
     }
     mbar_init(b_drain, 1);
     fence_mbar_init();
@@ -392,20 +383,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t d_e0 = desc_scales(s0 + MATS * 16384 + p.tokens * 256);
       const uint64_t d_s0 = desc_scales(s0 + MATS * 16384 + x_bytes);
       const uint32_t lo_off = p.tokens * 128 >> 4;
-      int s = 0, buf = 0;
-      uint32_t full_parity = 0, acc_parity = 1, set = 0, at = 0;
+      // Accumulators are a ring of `slots`, MATS of them a tile: three slots for two matrices let
+      // the next tile start when the first matrix's sums have left.
+      int s = 0, slot = 0;
+      uint32_t full_parity = 0, acc_parity = 1, at = 0;
       bool ok = true;
       for (int tile = first; tile < p.tiles && ok; tile += step) {
-        ok = wait_bar(b_accEmpty + 8 * buf, acc_parity, s_abort);
+        uint32_t acc[MATS], b_done[MATS];
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+          ok = ok && wait_bar(b_accEmpty + 8 * slot, acc_parity, s_abort);
+          acc[m] = tmem + slot * acc_cols;
+          b_done[m] = b_accFull + 8 * slot;
+          if (++slot == p.slots) {
+            slot = 0;
+            acc_parity ^= 1;
+          }
+        }
         tc_fence_after();
-        const uint32_t acc = tmem + buf * MATS * acc_cols;
         uint32_t add = 0;
         for (int kb = k0; kb < k1 && ok; ++kb) {
           ok = wait_bar(b_full + 8 * s, full_parity, s_abort);
           if (!ok) break;
           tc_fence_after();
-          // the scales' columns: W (4 a tile), hi's, lo's; two sets in turn
-          const uint32_t t_w = tmem + kSfCol + set, t_x = t_w + 4 * MATS;
+          // the scales' columns: W (4 a tile), hi's, lo's (copies and MMAs run in order)
+          const uint32_t t_w = tmem + kSfCol, t_x = t_w + 4 * MATS;
 #pragma unroll
           for (int m = 0; m < MATS; ++m) scales_to_tmem(t_w + 4 * m, d_s0 + at + 32 * m);
           scales_to_tmem(t_x, d_e0 + at);
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4; ++j) {
 #pragma unroll
               for (int m = 0; m < MATS; ++m)
-                mma_mx(acc + m * acc_cols, d_w0 + at + m * (16384 >> 4) + 2 * j, d_x0 + at + 2 * j,
+                mma_mx(acc[m], d_w0 + at + m * (16384 >> 4) + 2 * j, d_x0 + at + 2 * j,
                        id0 + j * ((1u << 4) + (1u << 29)), t_w + 4 * m, t_x, j > 0 ? 1 : add);
             }
           } else {
@@ -430,14 +432,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t id = id0 + j * ((1u << 4) + (1u << 29));
                 const uint64_t d_a = d_w0 + at + m * (16384 >> 4) + 2 * j;
                 const uint64_t d_b = d_x0 + at + 2 * j;
-                mma_mx(acc + m * acc_cols, d_a, d_b, id, t_w + 4 * m, t_x, j > 0 ? 1 : add);
-                mma_mx(acc + m * acc_cols, d_a, d_b + lo_off, id, t_w + 4 * m, t_x + 2 * nb, 1);
+                mma_mx(acc[m], d_a, d_b, id, t_w + 4 * m, t_x, j > 0 ? 1 : add);
+                mma_mx(acc[m], d_a, d_b + lo_off, id, t_w + 4 * m, t_x + 2 * nb, 1);
               }
             }
           }
           mma_commit(b_empty + 8 * s);
           add = 1;
-          set ^= 32;
           at += stage_desc;
           if (++s == p.stages) {
             s = 0;
@@ -445,11 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             full_parity ^= 1;
           }
         }
-        mma_commit(b_accFull + 8 * buf);
-        if (++buf == p.buffers) {
-          buf = 0;
-          acc_parity ^= 1;
-        }
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) mma_commit(b_done[m]);
       }
       if (*s_abort) {  // what was issued ends before tensor memory goes
         mma_commit(b_drain);
@@ -458,45 +456,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ results
-    // Two warps a quarter of the lanes, every second 16 rows of x each.
+    // Each of the warps that share a quarter of the lanes takes 8 rows of x in turn.
     grid_dependency_wait();
-    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const int quad = warp & 3, turn = (warp - 2) >> 2;
     const uint32_t acc_cols = p.tokens << p.wide;
     const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
-    int buf = 0;
+    int slot = 0;
     uint32_t acc_parity = 0;
-    for (int tile = first; tile < p.tiles; tile += step) {
-      const int tt = tile / p.feature_tiles, ft = tile - tt * p.feature_tiles;
-      const bool ok = wait_bar(b_accFull + 8 * buf, acc_parity, s_abort);
-      if (__any_sync(0xffffffffu, !ok)) break;
-      if (p.split > 1) break;
+    bool ok = true;
+    auto wait_slot = [&]() {
+      ok = wait_bar(b_accFull + 8 * slot, acc_parity, s_abort);
+      ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      const uint32_t acc = tmem + t_lane + buf * MATS * acc_cols;
-      const int t0 = tt * p.tokens, rows = min(p.tokens, p.T - t0);
-      const int f0 = ft * (GATED ? 128 : 128 * MATS) + quad * 32;
-#pragma unroll 1
-      for (int c = half * 16; c < rows; c += 32) {
-        __nv_bfloat16* out = p.out + (int64_t)(t0 + c) * p.out_stride + f0;
-#pragma unroll 1
-        for (int m = 0; m < (GATED ? 1 : MATS); ++m) {
-          float a[16];
-          load_sums(acc + m * acc_cols + c, p, a);
-          if (GATED) {
-            float b[16];
-            load_sums(acc + acc_cols + c, p, b);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) a[i] = activation(p.act, a[i]) * b[i];
-          }
-          store_rows(a, p, out + m * 128, rows - c, p.N - f0 - m * 128);
-        }
-      }
+      return tmem + t_lane + slot * acc_cols;
+    };
+    auto free_slot = [&]() {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_accEmpty + 8 * buf);
-      if (++buf == p.buffers) {
-        buf = 0;
+      if (lane == 0) mbar_arrive(b_accEmpty + 8 * slot);
+      if (++slot == p.slots) {
+        slot = 0;
         acc_parity ^= 1;
       }
+    };
+    for (int tile = first; tile < p.tiles; tile += step) {
+      const int tt = tile / p.feature_tiles, ft = tile - tt * p.feature_tiles;
+      const int t0 = tt * p.tokens, rows = min(p.tokens, p.T - t0);
+      const int f0 = ft * (GATED ? 128 : 128 * MATS) + quad * 32;
+      // The sums leave tensor memory before the activation and the stores (which go out at some 2
+      // TB/s where all blocks store at once): the first matrix's in fp32 where the second
+      // belongs to it, else rounded.
+      constexpr int kRounds = (MATS == 2 ? 160 : 192) / (8 * kTurns);
+      uint32_t v[kRounds][GATED ? 8 : 4 * MATS];
+#pragma unroll
+      for (int m = 0; m < (GATED ? 1 : MATS); ++m) {
+        const uint32_t acc = wait_slot();
+        if (!ok || p.split > 1) break;
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+          const int c = (i * kTurns + turn) * 8;
+          if (c < rows) {
+            float a[8];
+            load_sums(acc + c, p, a);
+#pragma unroll
+            for (int j = 0; j < (GATED ? 8 : 4); ++j)
+              v[i][4 * m + j] = GATED ? __float_as_uint(a[j]) : pack_bf16(a[2 * j & 7], a[2 * j + 1 & 7]);
+          }
+        }
+        free_slot();
+      }
+      if (!ok || p.split > 1) break;
+      uint32_t acc = 0;
+      if (GATED) {
+        acc = wait_slot();
+        if (!ok) break;
+      }
+      __nv_bfloat16* out = p.out + (int64_t)(t0 + turn * 8) * p.out_stride + f0;
+#pragma unroll
+      for (int i = 0; i < kRounds; ++i) {
+        const int c = (i * kTurns + turn) * 8;
+        if (c < rows) {
+          if (GATED) {
+            float b[8];
+            load_sums(acc + c, p, b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[j] *= activation(p.act, __uint_as_float(v[i][j]));
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = pack_bf16(b[2 * j], b[2 * j + 1]);
+            store_rows(o, p, out, rows - c, p.N - f0);
+          } else {
+#pragma unroll
+            for (int m = 0; m < MATS; ++m)
+              store_rows(&v[i][4 * m], p, out + m * 128, rows - c, p.N - f0 - m * 128);
+          }
+        }
+        out += (int64_t)kTurns * 8 * p.out_stride;
+      }
+      if (GATED) free_slot();
     }
   }
 
@@ -511,18 +548,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     float4* part = reinterpret_cast<float4*>(smem);  // [split][MATS][cols / 4][128]
     if (warp >= 2) {
       tc_fence_after();
-      const int quad = warp & 3, half = (warp - 2) >> 2, f = quad * 32 + lane;
+      const int quad = warp & 3, turn = (warp - 2) >> 2, f = quad * 32 + lane;
       const uint32_t acc_cols = p.tokens << p.wide;
 #pragma unroll 1
       for (int m = 0; m < MATS; ++m) {
         const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + m * acc_cols;
 #pragma unroll 1
-        for (int c = half * 16; c < p.tokens; c += 32) {
-          float a[16];
+        for (int c = turn * 8; c < p.tokens; c += kTurns * 8) {
+          float a[8];
           load_sums(acc + c, p, a);
           int to = c / cols, at = (c - to * cols) >> 2;
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
+          for (int i = 0; i < 8; i += 4) {
             const float v[4] = {a[i], a[i + 1], a[i + 2], a[i + 3]};
             store_cluster(smem_u32(part + ((rank * MATS + m) * (cols >> 2) + at) * 128 + f), to, v);
             if (++at == cols >> 2) at = 0, ++to;
@@ -591,12 +628,15 @@ int stages_of(const Cut& c) {
   const int n = (int)((kMaxSmem - 1024 - sizeof(Small)) / stage_bytes_of(c));
   return n < 12 ? n : 12;
 }
-int acc_cols_of(const Cut& c) { return c.mats * (c.tokens << c.wide); }
+int slots_of(const Cut& c) {
+  const int n = kSfCol / (c.tokens << c.wide);
+  return n < kMaxSlots ? n : kMaxSlots;
+}
 
-// The cut with the least time of the busiest block, in cycles.  An MMA of 128 x N x 32 takes
-// N / 2, and 64 at least (A's 4 KB from shared memory); a stage's bytes come at some 60 a cycle.
-// Two accumulators hide the results' way out behind the next tile.  `split` blocks exchange
-// their sums.
+// The cut with the least time of the busiest block, in cycles.  An MMA of 128 x N x 32 was
+// measured to take 70 (N = 96; A's 4 KB from shared memory), 76 (128), 80 (144), 86 (160), 101
+// (192); a stage's bytes come at some 55 a cycle.  Between two tiles the MMAs pause, longer
+// with one accumulator than with two.  `split` blocks exchange their sums.
 Cut choose(int N, int T, int KB, bool gated, int sms) {
   const int blocks = (N + 127) / 128;
   Cut best = {gated ? 2 : 1, 16, 1, 1};
@@ -605,23 +645,22 @@ Cut choose(int N, int T, int KB, bool gated, int sms) {
   for (c.mats = gated ? 2 : 1; c.mats <= 2; ++c.mats)
     for (c.wide = 0; c.wide < 2; ++c.wide)
       for (c.tokens = 16; c.tokens <= (c.wide ? kMaxTokens / 2 : kMaxTokens); c.tokens += 16) {
-        if (acc_cols_of(c) > kSfCol || stages_of(c) < 3) break;
+        if (stages_of(c) < 3 || c.tokens > (c.mats == 2 ? 160 : 192)) break;
         const int64_t ft = gated ? blocks : (blocks + c.mats - 1) / c.mats;
         const int64_t tiles = ft * ((T + c.tokens - 1) / c.tokens);
-        const int n2 = c.wide ? c.tokens : c.tokens / 2;  // half of an MMA's N
-        const int64_t mma = (c.wide ? 4 : 8) * c.mats * (n2 > 64 ? n2 : 64);
-        const int64_t fill = (8704 * c.mats + (int64_t)tile_bytes(c.tokens, c.wide)) / 60;
-        const int64_t step = (mma > fill ? mma : fill) + 50;
-        const int64_t out = 500 + (gated ? 12 : 6 * c.mats) * c.tokens;
+        const int n = c.tokens << c.wide, by_n = n / 2 + 5, by_a = 58 + n / 8;
+        const int64_t mma = (c.wide ? 4 : 8) * c.mats * (by_n > by_a ? by_n : by_a);
+        const int64_t fill = (8704 * c.mats + (int64_t)tile_bytes(c.tokens, c.wide)) / 55;
+        const int64_t step = (mma > fill ? mma : fill) + 20;
+        const int64_t pause = slots_of(c) >= 2 * c.mats ? 350 : slots_of(c) > c.mats ? 1000 : gated ? 4000 : 1500;
+        const int64_t out = 500 + (gated ? 40 : 24 * c.mats) * c.tokens;
         for (c.split = 1; c.split <= kMaxSplit; c.split *= 2) {
           if (c.split > 1 &&
               (tiles * c.split > sms || KB < 2 * c.split || c.tokens % (4 * c.split) != 0))
             break;
           const int64_t waves = c.split > 1 ? 1 : (tiles + sms - 1) / sms;
-          const int64_t hidden = 2 * acc_cols_of(c) <= kSfCol;
-          const int64_t time =
-              waves * ((KB + c.split - 1) / c.split) * step + (hidden ? 1 : waves) * out +
-              (c.split > 1 ? 2500 : 0);
+          const int64_t time = waves * (((KB + c.split - 1) / c.split) * step + pause) +
+                               (c.split > 1 ? 3000 + 8 * c.mats * c.tokens : out);
           if (time < least) least = time, best = c;
         }
       }
@@ -650,7 +689,7 @@ cudaError_t launch(const Linear4Args& a, const Cut& cut, cudaStream_t st) {
   p.status = static_cast<uint32_t*>(a.ws);
   p.vector = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.out_stride % 8 == 0;
   p.stages = stages_of(cut);
-  p.buffers = 2 * acc_cols_of(cut) <= kSfCol ? 2 : 1;
+  p.slots = slots_of(cut);
   cudaError_t e = ensure_smem_attr((const void*)kernel, kMaxSmem);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
