@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxRows = 16;
+constexpr int kMaxRows = 64;
 constexpr size_t kMaxSmemX = 196608;  // x's bytes in shared memory
 
 // Row m (of 16) of row tile j (of 8) of a block of 128: four neighbours from each quarter, whose
@@ -79,131 +79,164 @@ struct Slot {
   uint32_t s0, s1;
 };
 
-// A pair's A fragments of rows g and g + 8: the values, times 2^126 2^(b - 127) in one step, or in
-// two where that passes bf16's range.
-struct Scale {
-  uint32_t f, g;
-  __device__ __forceinline__ explicit Scale(uint32_t b) {
-    f = min(b + 126u, 254u) * 0x00800080u;
-    g = b > 128u ? (b - 1u) * 0x00800080u : 0x3f803f80u;
-  }
-};
-
+// NT: eights of rows of x; DEPTH: steps whose loads are in flight.
 template <int MATS, int NT, int DEPTH>
 __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Params p) {
-  extern __shared__ uint4 s_x[];  // [KB][4][T][4]: step, word, row, lane's t
-  __shared__ float4 red[kWarps][MATS][NT][32];
+  constexpr int kRedNT = NT < 2 ? NT : 2;  // eights of rows that are added up at a time
+  extern __shared__ uint4 s_x[];           // [KB][4][T][4]: step, word, row, lane's t
+  __shared__ float4 red[kWarps][MATS][kRedNT][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   grid_dependency_wait();
 
   // `splits` warps share a row tile, each a range of K; the groups of warps take tiles in
   // turn, neighbouring tiles in different blocks.
-  const int group = warp / p.splits, ks = warp - group * p.splits;
-  const int first = group * gridDim.x + blockIdx.x, stride = gridDim.x * (kWarps / p.splits);
+  const int group = warp / p.splits, ks = warp - group * p.splits, groups = kWarps / p.splits;
+  const int first = group * gridDim.x + blockIdx.x, stride = gridDim.x * groups;
   const int k0 = p.KB * ks / p.splits, k1 = p.KB * (ks + 1) / p.splits, steps = k1 - k0;
-  const int mine = first < p.tiles ? (p.tiles - first + stride - 1) / stride : 0;
+  const int mine = group < groups && first < p.tiles ? (p.tiles - first + stride - 1) / stride : 0;
   const int items = mine * steps;
 
   Slot ring[DEPTH][MATS];
-  int at_tile = first, at_step = k0, loaded = 0;  // what is loaded next
+  int at_tile = first, left = steps, loaded = 0;  // what is loaded next
+  int64_t c0 = 0, c1 = 0, sc = 0;
+  auto place = [&]() {  // rows past N take the last one's codes: their sums are not stored
+    const int n0 = min(row_of(at_tile, g), p.N - 1), n1 = min(row_of(at_tile, g + 8), p.N - 1);
+    c0 = (int64_t)n0 * (p.Kp >> 1) + k0 * 64 + t * 16;
+    c1 = c0 + (int64_t)(n1 - n0) * (p.Kp >> 1);
+    sc = ((int64_t)(at_tile >> 3) * p.KB + k0) * 512 + (at_tile & 7) * 64 + (g & 3) * 16 +
+         (g >> 2) * 4 + t;
+  };
+  if (items > 0) place();
   auto load = [&](Slot (&s)[MATS]) {
     if (loaded >= items) return;
     ++loaded;
-    const int n0 = row_of(at_tile, g), n1 = row_of(at_tile, g + 8);
-    const int64_t col = (int64_t)at_step * 64 + t * 16;
 #pragma unroll
     for (int m = 0; m < MATS; ++m) {
-      const uint8_t* c = m ? p.cu : p.cw;
-      const uint8_t* sc = (m ? p.su : p.sw) +
-                          ((size_t)(at_tile >> 3) * p.KB + at_step) * 512 + (at_tile & 7) * 64 + t;
-      s[m].c0 = n0 < p.N ? load_codes(c + (int64_t)n0 * (p.Kp >> 1) + col) : make_uint4(0, 0, 0, 0);
-      s[m].c1 = n1 < p.N ? load_codes(c + (int64_t)n1 * (p.Kp >> 1) + col) : make_uint4(0, 0, 0, 0);
-      s[m].s0 = __ldg(sc + (g & 3) * 16 + (g >> 2) * 4);
-      s[m].s1 = __ldg(sc + (g & 3) * 16 + (g >> 2) * 4 + 8);
+      s[m].c0 = load_codes((m ? p.cu : p.cw) + c0);
+      s[m].c1 = load_codes((m ? p.cu : p.cw) + c1);
+      s[m].s0 = __ldg((m ? p.su : p.sw) + sc);
+      s[m].s1 = __ldg((m ? p.su : p.sw) + sc + 8);
     }
-    if (++at_step == k1) {
-      at_step = k0;
+    c0 += 64;
+    c1 += 64;
+    sc += 512;
+    if (--left == 0) {
+      left = steps;
       at_tile += stride;
+      if (at_tile < p.tiles) place();
     }
   };
 #pragma unroll
   for (int i = 0; i < DEPTH; ++i) load(ring[i]);
 
   // x in the lanes' order, the columns of eight as (0, 4, 1, 5, 2, 6, 3, 7); zeros past K
-  const int chunks = p.Kp >> 3;
-  for (int i = tid; i < p.T * chunks; i += kThreads) {
-    const int r = i / chunks, c = i - r * chunks;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (c * 8 < p.K) v = __ldg(reinterpret_cast<const uint4*>(p.x + r * p.x_stride + c * 8));
-    s_x[(((c >> 4) * 4 + (c & 3)) * p.T + r) * 4 + ((c >> 2) & 3)] =
-        make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                   __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+  const int chunks = p.Kp >> 3, all = p.T * chunks;
+  constexpr int kBatch = 8;  // loads in flight
+  for (int i0 = tid; i0 < all; i0 += kThreads * kBatch) {
+    uint4 v[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * kThreads, r = i / chunks, c = i - r * chunks;
+      v[b] = make_uint4(0, 0, 0, 0);
+      if (i < all && c * 8 < p.K)
+        v[b] = __ldg(reinterpret_cast<const uint4*>(p.x + r * p.x_stride + c * 8));
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * kThreads, r = i / chunks, c = i - r * chunks;
+      if (i < all)
+        s_x[(((c >> 4) * 4 + (c & 3)) * p.T + r) * 4 + ((c >> 2) & 3)] = make_uint4(
+            __byte_perm(v[b].x, v[b].z, 0x5410), __byte_perm(v[b].x, v[b].z, 0x7632),
+            __byte_perm(v[b].y, v[b].w, 0x5410), __byte_perm(v[b].y, v[b].w, 0x7632));
+    }
   }
   __syncthreads();
 
   float d[MATS][NT][4] = {};
-  int tile = first, step = k0;
+  int tile = first, step = 0;
+  const int x_word = p.T * 4;
+  const int x_first = k0 * 4 * x_word + t;
+  int x_at = x_first;
+  // columns of the products past T take the last row of x: they are not stored
+  auto x_of = [&](int nt) { return s_x[x_at + min(g + 8 * nt, p.T - 1) * 4]; };
   auto use = [&](const Slot (&s)[MATS]) {
+    // a group's power of two, times 2^126 for the codes' bits, in one factor or (scales above 2) two
+    uint32_t f0[MATS], f1[MATS];
+    bool big = false;
+#pragma unroll
+    for (int m = 0; m < MATS; ++m) {
+      f0[m] = min(s[m].s0 + 126u, 254u) * 0x00800080u;
+      f1[m] = min(s[m].s1 + 126u, 254u) * 0x00800080u;
+      big |= s[m].s0 > 128u || s[m].s1 > 128u;
+    }
+    big = __any_sync(0xffffffffu, big);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      uint4 b[NT];
+      uint4 b[NT];  // (NT > 2: read again for the second matrix)
+      if (NT <= 2) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        b[nt] = make_uint4(0, 0, 0, 0);
-        if (g + 8 * nt < p.T) b[nt] = s_x[((step * 4 + w) * p.T + g + 8 * nt) * 4 + t];
+        for (int nt = 0; nt < NT; ++nt) b[nt] = x_of(nt);
       }
 #pragma unroll
       for (int m = 0; m < MATS; ++m) {
-        const Scale a0(s[m].s0), a1(s[m].s1);
         const uint32_t w0 = w == 0 ? s[m].c0.x : w == 1 ? s[m].c0.y : w == 2 ? s[m].c0.z : s[m].c0.w;
         const uint32_t w1 = w == 0 ? s[m].c1.x : w == 1 ? s[m].c1.y : w == 2 ? s[m].c1.z : s[m].c1.w;
-        uint32_t lo[4] = {mul_bf16x2(pair_bits<0>(w0), a0.f), mul_bf16x2(pair_bits<0>(w1), a1.f),
-                          mul_bf16x2(pair_bits<1>(w0), a0.f), mul_bf16x2(pair_bits<1>(w1), a1.f)};
-        uint32_t hi[4] = {mul_bf16x2(pair_bits<2>(w0), a0.f), mul_bf16x2(pair_bits<2>(w1), a1.f),
-                          mul_bf16x2(pair_bits<3>(w0), a0.f), mul_bf16x2(pair_bits<3>(w1), a1.f)};
-        if (s[m].s0 > 128u || s[m].s1 > 128u) {
+        uint32_t lo[4] = {mul_bf16x2(pair_bits<0>(w0), f0[m]), mul_bf16x2(pair_bits<0>(w1), f1[m]),
+                          mul_bf16x2(pair_bits<1>(w0), f0[m]), mul_bf16x2(pair_bits<1>(w1), f1[m])};
+        uint32_t hi[4] = {mul_bf16x2(pair_bits<2>(w0), f0[m]), mul_bf16x2(pair_bits<2>(w1), f1[m]),
+                          mul_bf16x2(pair_bits<3>(w0), f0[m]), mul_bf16x2(pair_bits<3>(w1), f1[m])};
+        if (big) {
+          const uint32_t h0 = s[m].s0 > 128u ? (s[m].s0 - 1u) * 0x00800080u : 0x3f803f80u;
+          const uint32_t h1 = s[m].s1 > 128u ? (s[m].s1 - 1u) * 0x00800080u : 0x3f803f80u;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            lo[i] = mul_bf16x2(lo[i], i & 1 ? a1.g : a0.g);
-            hi[i] = mul_bf16x2(hi[i], i & 1 ? a1.g : a0.g);
+            lo[i] = mul_bf16x2(lo[i], i & 1 ? h1 : h0);
+            hi[i] = mul_bf16x2(hi[i], i & 1 ? h1 : h0);
           }
         }
-        __syncwarp();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          if (NT > 2) b[nt] = x_of(nt);
           mma_16816(d[m][nt], lo, b[nt].x, b[nt].y);
           mma_16816(d[m][nt], hi, b[nt].z, b[nt].w);
         }
       }
+      x_at += x_word;
     }
-    if (++step < k1) return;
+    if (++step < steps) return;
     // the tile's end: the group's partial sums, added in the order of their ranges
-    step = k0;
-#pragma unroll
-    for (int m = 0; m < MATS; ++m)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        red[warp][m][nt][lane] = make_float4(d[m][nt][0], d[m][nt][1], d[m][nt][2], d[m][nt][3]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) d[m][nt][j] = 0.f;
-      }
+    step = 0;
+    x_at = x_first;
     const int n_threads = p.splits * 32;
-    group_sync(group, n_threads);
-    for (int e = tid - group * n_threads; e < NT * 128; e += n_threads) {
-      const int nt = e >> 7, l = (e >> 2) & 31, j = e & 3;
-      float v[MATS];
 #pragma unroll
-      for (int m = 0; m < MATS; ++m) {
-        v[m] = 0.f;
-        for (int k = 0; k < p.splits; ++k)
-          v[m] += reinterpret_cast<const float*>(&red[group * p.splits + k][m][nt][l])[j];
+    for (int n0 = 0; n0 < NT; n0 += kRedNT) {
+#pragma unroll
+      for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int k = 0; k < kRedNT; ++k) {
+          float(&v)[4] = d[m][n0 + k];
+          red[warp][m][k][lane] = make_float4(v[0], v[1], v[2], v[3]);
+          v[0] = v[1] = v[2] = v[3] = 0.f;
+        }
+      group_sync(group, n_threads);
+      for (int e = tid - group * n_threads; e < kRedNT * 128; e += n_threads) {
+        // neighbouring threads take neighbouring features: e = (row of x, feature of the tile)
+        const int k = e >> 7, c = (e >> 4) & 7, row = e & 15;
+        const int l = (row & 7) * 4 + (c >> 1), j = (row >> 3) * 2 + (c & 1);
+        float v[MATS];
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+          v[m] = 0.f;
+          for (int q = 0; q < p.splits; ++q)
+            v[m] += reinterpret_cast<const float*>(&red[group * p.splits + q][m][k][l])[j];
+        }
+        float o = v[0];
+        if (MATS == 2) o = activation(p.act, o) * v[MATS - 1];
+        const int n = row_of(tile, row), r = (n0 + k) * 8 + c;
+        if (n < p.N && r < p.T) p.out[r * p.out_stride + n] = __float2bfloat16(o);
       }
-      float o = v[0];
-      if (MATS == 2) o = activation(p.act, o) * v[MATS - 1];
-      const int n = row_of(tile, (l >> 2) + (j >> 1) * 8), r = nt * 8 + (l & 3) * 2 + (j & 1);
-      if (n < p.N && r < p.T) p.out[r * p.out_stride + n] = __float2bfloat16(o);
+      group_sync(group, n_threads);
     }
-    group_sync(group, n_threads);
     tile += stride;
   };
 #pragma unroll 1
@@ -218,9 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Params p) {
   }
 }
 
-template <int MATS, int NT>
+template <int MATS, int NT, int DEPTH>
 cudaError_t launch(const Linear4Args& a, cudaStream_t st) {
-  auto kernel = rows_kernel<MATS, NT, MATS == 2 ? 3 : 5>;
+  auto kernel = rows_kernel<MATS, NT, DEPTH>;
   Params p;
   p.cw = a.w->codes;
   p.sw = a.w->scales;
@@ -241,11 +274,12 @@ cudaError_t launch(const Linear4Args& a, cudaStream_t st) {
   cudaError_t e = ensure_smem_attr((const void*)kernel, (int)kMaxSmemX);
   if (e != cudaSuccess) return e;
   const int grid = sm_count();
-  // the warps that share a tile: as many steps as the busiest warp has, the fewest
+  // the warps that share a tile: the fewest steps of the busiest warp (a tile's end counts as
+  // one more)
   int64_t least = INT64_MAX;
-  for (int s = 1; s <= kWarps && s <= p.KB; s *= 2) {
+  for (int s = 1; s <= kWarps && s <= p.KB; ++s) {
     const int64_t slots = (int64_t)grid * (kWarps / s);
-    const int64_t steps = (p.tiles + slots - 1) / slots * ((p.KB + s - 1) / s);
+    const int64_t steps = (p.tiles + slots - 1) / slots * ((p.KB + s - 1) / s + 1);
     if (steps < least) least = steps, p.splits = s;
   }
   DSPARK_LAUNCH(kKindLinear4, st,
@@ -260,8 +294,10 @@ bool linear4_rows_fits(int T, int Kp) {
 }
 
 cudaError_t launch_linear4_rows(const Linear4Args& a, cudaStream_t st) {
-  if (a.T <= 8) return a.up ? launch<2, 1>(a, st) : launch<1, 1>(a, st);
-  return a.up ? launch<2, 2>(a, st) : launch<1, 2>(a, st);
+  if (a.T <= 8) return a.up ? launch<2, 1, 3>(a, st) : launch<1, 1, 5>(a, st);
+  if (a.T <= 16) return a.up ? launch<2, 2, 3>(a, st) : launch<1, 2, 5>(a, st);
+  if (a.T <= 32) return a.up ? launch<2, 4, 2>(a, st) : launch<1, 4, 4>(a, st);
+  return a.up ? launch<2, 8, 1>(a, st) : launch<1, 8, 3>(a, st);
 }
 
 }  // namespace dspark
