@@ -25,6 +25,8 @@ namespace {
 constexpr int kMaxTokens = 192;   // rows of x a tile
 constexpr int kOutWarps = 16;     // warps of results, a quarter of them for 32 lanes each
 constexpr int kTurns = kOutWarps / 4;
+constexpr int kPass = kOutWarps * 2;  // rows of x that they split at a time
+constexpr int kMaxPasses = 3;
 constexpr int kThreads = 64 + kOutWarps * 32;  // one that loads, one that issues MMAs, results
 constexpr int kMaxSmem = 232448;
 constexpr int kSfCol = 480;       // tensor memory: accumulators below, scales above
@@ -37,6 +39,7 @@ constexpr uint32_t kWaitNs = 2000000000u;
 // of one MMA, else an MMA each; `split`: blocks that share a tile's K.
 struct Cut {
   int mats, tokens, wide, split;
+  bool own;  // the blocks split x themselves (one tile each), no kernel before
 };
 
 // The tile of `tokens` rows and 128 columns of x: hi, lo, their exponents in blocks of 512
@@ -67,9 +70,65 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
+// Eight values of a row's 128 columns by each of 16 lanes, four lanes a group of 32: the codes of
+// hi and lo; returns the row's four exponent bytes (in every lane).
+__device__ __forceinline__ uint32_t split8(uint4 raw, uint2& hi, uint2& lo) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  // bf16 magnitudes order as whole numbers; past 0x7f80 a NaN
+  uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                          __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+  top = max(top & 0xffffu, top >> 16);
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  }
+  if (top >= 0x7f80u) {  // the maximum is over what is finite; the rest makes its row's results NaN
+    top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = fabsf(v[j]);
+      if (a < INFINITY) top = max(top, __float_as_uint(a) >> 16);
+      else v[j] = NAN;
+    }
+  }
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const int e = group_exponent(__uint_as_float(top << 16));
+  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float a = v[2 * j] * f, b = v[2 * j + 1] * f;
+    h[j] = to_e4m3x2(a, b);
+    const float2 c = from_e4m3x2(h[j]);
+    l[j] = to_e4m3x2((a - c.x) * 16.f, (b - c.y) * 16.f);
+  }
+  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+  uint32_t exps = 0;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    exps |= (uint32_t)(__shfl_sync(0xffffffffu, e, (threadIdx.x & 16) + g * 4) + 127) << (8 * g);
+  return exps;
+}
+
+// Where they go in the tile at `dst`: row r, its lane of 16.
+__device__ __forceinline__ void put8(uint8_t* dst, int tokens, int wide, int r, int lane, uint2 hi,
+                                     uint2 lo, uint32_t exps) {
+  const uint32_t at = r * 128 + (((lane >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
+  *reinterpret_cast<uint2*>(dst + at) = hi;
+  *reinterpret_cast<uint2*>(dst + tokens * 128 + at) = lo;
+  if (lane < 2) {  // an MMA column's exponents: lane n % 32 of tensor memory, column n / 32
+    const int n = lane == 0 ? r : wide ? tokens + r : (tokens + 127) / 128 * 128 + r;
+    *reinterpret_cast<uint32_t*>(dst + tokens * 256 + (n >> 7) * 512 + (n & 31) * 16 +
+                                 ((n >> 5) & 3) * 4) = exps - lane * 0x04040404u;
+  }
+}
+
 constexpr int kSplitThreads = 256;
 
-// Four lanes a group of 32 columns, eight values each; 16 lanes a row's 128 columns.
 // Rows past T stay as they are: they reach only columns of the product that are not stored.
 __global__ void __launch_bounds__(kSplitThreads)
     split_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride, int T, int K, int KB,
@@ -82,58 +141,22 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int kb = (int)(i - t * KB), col = kb * 128 + lane * 8;
   uint4 raw = make_uint4(0, 0, 0, 0);
   if (t < T && col < K) raw = __ldg(reinterpret_cast<const uint4*>(x + t * x_stride + col));
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  float v[8], amax = 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = __uint_as_float(w[j] << 16);
-    v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float a = fabsf(v[j]);
-    if (a < INFINITY) amax = fmaxf(amax, a);
-    else v[j] = NAN;  // its row's results are not finite
-  }
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  const int e = group_exponent(amax);
-  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-  uint32_t hi[2], lo[2];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float a = v[2 * j] * f, b = v[2 * j + 1] * f;
-    const uint32_t h = to_e4m3x2(a, b);
-    const float2 c = from_e4m3x2(h);
-    const uint32_t l = to_e4m3x2((a - c.x) * 16.f, (b - c.y) * 16.f);
-    if (j & 1) hi[j >> 1] |= h << 16, lo[j >> 1] |= l << 16;
-    else hi[j >> 1] = h, lo[j >> 1] = l;
-  }
-  // the row's four exponent bytes, in the first of its 16 lanes
-  uint32_t exps = 0;
-#pragma unroll
-  for (int g = 0; g < 4; ++g)
-    exps |= (uint32_t)(__shfl_sync(0xffffffffu, e, (threadIdx.x & 16) + g * 4) + 127) << (8 * g);
+  uint2 hi, lo;
+  const uint32_t exps = split8(raw, hi, lo);
   if (t >= T) return;
   const int64_t tile = t / tokens;
-  const int r = (int)(t - tile * tokens);
-  uint8_t* dst = out + (tile * KB + kb) * tile_bytes(tokens, wide);
-  const uint32_t at = r * 128 + (((lane >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
-  *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0], hi[1]);
-  *reinterpret_cast<uint2*>(dst + tokens * 128 + at) = make_uint2(lo[0], lo[1]);
-  if (lane < 2) {  // an MMA column's exponents: lane n % 32 of tensor memory, column n / 32
-    const int n = lane == 0 ? r : wide ? tokens + r : (tokens + 127) / 128 * 128 + r;
-    *reinterpret_cast<uint32_t*>(dst + tokens * 256 + (n >> 7) * 512 + (n & 31) * 16 +
-                                 ((n >> 5) & 3) * 4) = exps - lane * 0x04040404u;
-  }
+  put8(out + (tile * KB + kb) * tile_bytes(tokens, wide), tokens, wide, (int)(t - tile * tokens),
+       lane, hi, lo, exps);
 }
 
 // ---------------------------------------------------------------- the product
 
 struct Params {
   const uint8_t *sw, *su;  // scales of the matrices
-  const uint8_t* xq;       // tiles of x
-  int N, T, KB, row_blocks, tokens, wide, feature_tiles, tiles, split, stages, slots, act;
+  const uint8_t* xq;       // tiles of x, or null: the blocks make their own
+  const __nv_bfloat16* x;
+  int64_t x_stride;
+  int N, T, K, KB, row_blocks, tokens, wide, feature_tiles, tiles, split, stages, slots, act;
   bool vector;  // rows of out are 16-byte aligned
   __nv_bfloat16* out;
   int64_t out_stride;
@@ -294,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(b_full + 8 * i, 1);
+      mbar_init(b_full + 8 * i, p.xq ? 1 : 1 + kOutWarps);
       mbar_init(b_empty + 8 * i, 1);
     }
     for (int i = 0; i < kMaxSlots; ++i) {
@@ -324,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // number that only the launch knows costs the one issuing thread 200 cycles a step.
   if (warp == 0) {
     if (elect_one()) {
-      const uint32_t tx = MATS * (8192 + 512) + x_bytes;
+      const uint32_t tx = MATS * (8192 + 512) + (p.xq ? x_bytes : 0);
       const int tt_step = step / p.feature_tiles, ft_step = step - tt_step * p.feature_tiles;
       int tt = first / p.feature_tiles, ft = first - tt * p.feature_tiles;
       auto load_w = [&](uint32_t bar, uint32_t dst, int kb) {
@@ -340,9 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto load_x = [&](uint32_t bar, uint32_t dst, int kb) {
-        bulk_load(dst + MATS * 16384, p.xq + ((size_t)tt * p.KB + kb) * x_bytes, x_bytes, bar);
+        if (p.xq)
+          bulk_load(dst + MATS * 16384, p.xq + ((size_t)tt * p.KB + kb) * x_bytes, x_bytes, bar);
       };
-      // the first stages' weights, before the kernel that writes x's tiles has ended
+      // the first stages' weights, before the kernel that writes x's tiles has ended (without
+      // that, the kernel before this one may have written the weights)
+      if (!p.xq) grid_dependency_wait();
       const int here = min(p.stages, k1 - k0);
       for (int i = 0; i < here; ++i) load_w(b_full + 8 * i, s0 + i * stage_bytes, k0 + i);
       grid_dependency_wait();
@@ -464,6 +490,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     int slot = 0;
     uint32_t acc_parity = 0;
     bool ok = true;
+    if (!p.xq) {
+      // x's tiles first, 16 lanes a row, the next one's loads under this one's conversion
+      const int tt = first / p.feature_tiles, t0 = tt * p.tokens;
+      const int l16 = tid & 15, r0 = (tid - 64) >> 4;
+      uint4 next[kMaxPasses];
+      auto fetch = [&](int kb) {
+#pragma unroll
+        for (int i = 0; i < kMaxPasses; ++i) {
+          const int r = r0 + i * kPass, col = kb * 128 + l16 * 8;
+          next[i] = make_uint4(0, 0, 0, 0);
+          if (r < p.tokens && t0 + r < p.T && col < p.K)
+            next[i] = __ldg(reinterpret_cast<const uint4*>(p.x + (t0 + r) * p.x_stride + col));
+        }
+      };
+      fetch(k0);
+      int s = 0;
+      uint32_t free_parity = 1;
+      for (int kb = k0; kb < k1 && ok; ++kb) {
+        ok = wait_bar(b_empty + 8 * s, free_parity, s_abort);
+        ok = __all_sync(0xffffffffu, ok);
+        uint4 now[kMaxPasses];
+#pragma unroll
+        for (int i = 0; i < kMaxPasses; ++i) now[i] = next[i];
+        if (kb + 1 < k1) fetch(kb + 1);
+        uint8_t* dst = smem + (size_t)s * stage_bytes + MATS * 16384;
+#pragma unroll
+        for (int i = 0; i < kMaxPasses; ++i) {
+          const int r = r0 + i * kPass;
+          if ((i * kPass + ((warp - 2) << 1)) >= p.tokens) break;  // (a warp has two rows)
+          uint2 hi, lo;
+          const uint32_t exps = split8(now[i], hi, lo);
+          put8(dst, p.tokens, p.wide, r, l16, hi, lo, exps);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_full + 8 * s);
+        if (++s == p.stages) {
+          s = 0;
+          free_parity ^= 1;
+        }
+      }
+    }
     auto wait_slot = [&]() {
       ok = wait_bar(b_accFull + 8 * slot, acc_parity, s_abort);
       ok = __all_sync(0xffffffffu, ok);
@@ -639,7 +707,7 @@ int slots_of(const Cut& c) {
 // with one accumulator than with two.  `split` blocks exchange their sums.
 Cut choose(int N, int T, int KB, bool gated, int sms) {
   const int blocks = (N + 127) / 128;
-  Cut best = {gated ? 2 : 1, 16, 1, 1};
+  Cut best = {gated ? 2 : 1, 16, 1, 1, false};
   int64_t least = INT64_MAX;
   Cut c;
   for (c.mats = gated ? 2 : 1; c.mats <= 2; ++c.mats)
@@ -659,9 +727,15 @@ Cut choose(int N, int T, int KB, bool gated, int sms) {
               (tiles * c.split > sms || KB < 2 * c.split || c.tokens % (4 * c.split) != 0))
             break;
           const int64_t waves = c.split > 1 ? 1 : (tiles + sms - 1) / sms;
-          const int64_t time = waves * (((KB + c.split - 1) / c.split) * step + pause) +
-                               (c.split > 1 ? 3000 + 8 * c.mats * c.tokens : out);
-          if (time < least) least = time, best = c;
+          for (int own = 0; own < 2; ++own) {
+            c.own = own;
+            if (own && (waves > 1 || c.tokens > kMaxPasses * kPass)) break;
+            const int64_t own_step = own ? 12 * (int64_t)c.tokens + 100 : 0;
+            const int64_t time =
+                waves * (((KB + c.split - 1) / c.split) * (step > own_step ? step : own_step) + pause) +
+                (c.split > 1 ? 6000 + 8 * c.mats * c.tokens : out) + (own ? 0 : 4000);
+            if (time < least) least = time, best = c;
+          }
         }
       }
   return best;
@@ -673,7 +747,10 @@ cudaError_t launch(const Linear4Args& a, const Cut& cut, cudaStream_t st) {
   Params p;
   p.sw = a.w->scales;
   p.su = a.up ? a.up->scales : nullptr;
-  p.xq = static_cast<const uint8_t*>(a.ws) + kStatusBytes;
+  p.xq = cut.own ? nullptr : static_cast<const uint8_t*>(a.ws) + kStatusBytes;
+  p.x = a.x;
+  p.x_stride = a.x_stride;
+  p.K = a.w->K;
   p.N = a.w->N;
   p.T = a.T;
   p.KB = a.w->Kp / 128;
@@ -726,13 +803,16 @@ size_t linear4_tile_workspace_bytes(int T, int K) {
 cudaError_t launch_linear4_tile(const Linear4Args& a, cudaStream_t st) {
   const int KB = a.w->Kp / 128;
   const Cut cut = choose(a.w->N, a.T, KB, a.up != nullptr, sm_count());
-  const int64_t threads = (int64_t)a.T * KB * 16;
-  cudaError_t e;
-  DSPARK_LAUNCH(kKindLinear4, st,
-                e = launch_pdl(split_kernel, dim3((unsigned)((threads + 255) / 256)),
-                               dim3(kSplitThreads), 0, st, a.x, a.x_stride, a.T, a.w->K, KB,
-                               cut.tokens, cut.wide, static_cast<uint8_t*>(a.ws) + kStatusBytes));
-  if (e != cudaSuccess) return e;
+  if (!cut.own) {
+    const int64_t threads = (int64_t)a.T * KB * 16;
+    cudaError_t e;
+    DSPARK_LAUNCH(kKindLinear4, st,
+                  e = launch_pdl(split_kernel, dim3((unsigned)((threads + 255) / 256)),
+                                 dim3(kSplitThreads), 0, st, a.x, a.x_stride, a.T, a.w->K, KB,
+                                 cut.tokens, cut.wide,
+                                 static_cast<uint8_t*>(a.ws) + kStatusBytes));
+    if (e != cudaSuccess) return e;
+  }
   return a.up            ? launch<2, true>(a, cut, st)
          : cut.mats == 2 ? launch<2, false>(a, cut, st)
                          : launch<1, false>(a, cut, st);
