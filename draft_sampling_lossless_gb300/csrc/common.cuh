@@ -254,6 +254,8 @@ cudaError_t ensure_smem_attr(const void* func, int bytes);
 // `threads` threads and `dyn_smem` bytes of dynamic shared memory, cached per
 // (device, func, threads, dyn_smem); 0 if the query fails.
 int blocks_per_sm(const void* func, int threads, size_t dyn_smem);
+// Clusters of `blocks` blocks of `func` that the current device holds at a time, cached alike.
+int resident_clusters(const void* func, int threads, size_t dyn_smem, int blocks);
 
 // Every kernel launch: counted, and bracketed by trace events when tracing.
 #define DSPARK_LAUNCH(kind, st, ...)   \

@@ -18,6 +18,7 @@ std::mutex g_mu;
 std::map<int, int> g_sms;                                        // device -> SMs
 std::map<std::pair<int, const void*>, int> g_smem;               // (device, func) -> bytes set
 std::map<std::tuple<int, const void*, int, size_t>, int> g_occ;  // -> blocks per SM
+std::map<std::tuple<int, const void*, int, size_t, int>, int> g_clusters;  // -> resident clusters
 
 int current_device() {
   int dev = 0;
@@ -62,6 +63,28 @@ int blocks_per_sm(const void* func, int threads, size_t dyn_smem) {
       n < 1)
     return 0;  // not cached: asked again next time
   g_occ[key] = n;
+  return n;
+}
+
+int resident_clusters(const void* func, int threads, size_t dyn_smem, int blocks) {
+  const int dev = current_device();
+  std::lock_guard<std::mutex> lk(g_mu);
+  auto key = std::make_tuple(dev, func, threads, dyn_smem, blocks);
+  auto it = g_clusters.find(key);
+  if (it != g_clusters.end()) return it->second;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = dyn_smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = blocks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, func, &cfg) != cudaSuccess || n < 0) return 0;
+  g_clusters[key] = n;
   return n;
 }
 

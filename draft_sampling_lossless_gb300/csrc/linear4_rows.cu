@@ -130,25 +130,32 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Params p) {
   for (int i = 0; i < DEPTH; ++i) load(ring[i]);
 
   // x in the lanes' order, the columns of eight as (0, 4, 1, 5, 2, 6, 3, 7); zeros past K
-  const int chunks = p.Kp >> 3, all = p.T * chunks;
+  const int chunks = p.Kp >> 3;
   constexpr int kBatch = 8;  // loads in flight
-  for (int i0 = tid; i0 < all; i0 += kThreads * kBatch) {
+  const int r_step = kThreads / chunks, c_step = kThreads - r_step * chunks;
+  int r = tid / chunks, c = tid - r * chunks;
+  while (r < p.T) {
     uint4 v[kBatch];
+    int at[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + b * kThreads, r = i / chunks, c = i - r * chunks;
       v[b] = make_uint4(0, 0, 0, 0);
-      if (i < all && c * 8 < p.K)
+      at[b] = r < p.T ? (((c >> 4) * 4 + (c & 3)) * p.T + r) * 4 + ((c >> 2) & 3) : -1;
+      if (r < p.T && c * 8 < p.K)
         v[b] = __ldg(reinterpret_cast<const uint4*>(p.x + r * p.x_stride + c * 8));
+      r += r_step;
+      c += c_step;
+      if (c >= chunks) {
+        c -= chunks;
+        ++r;
+      }
     }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + b * kThreads, r = i / chunks, c = i - r * chunks;
-      if (i < all)
-        s_x[(((c >> 4) * 4 + (c & 3)) * p.T + r) * 4 + ((c >> 2) & 3)] = make_uint4(
+    for (int b = 0; b < kBatch; ++b)
+      if (at[b] >= 0)
+        s_x[at[b]] = make_uint4(
             __byte_perm(v[b].x, v[b].z, 0x5410), __byte_perm(v[b].x, v[b].z, 0x7632),
             __byte_perm(v[b].y, v[b].w, 0x5410), __byte_perm(v[b].y, v[b].w, 0x7632));
-    }
   }
   __syncthreads();
 
@@ -291,6 +298,16 @@ cudaError_t launch(const Linear4Args& a, cudaStream_t st) {
 
 bool linear4_rows_fits(int T, int Kp) {
   return T <= kMaxRows && (size_t)T * Kp * 2 <= kMaxSmemX;
+}
+
+// Its time but for what every call takes: the values of the SM with the most row tiles, at 21 a
+// cycle with up to 8 rows (the conversions bound it), 15, 9 and 5.3 with up to 16, 32 and 64,
+// and x's way into shared memory.
+int64_t linear4_rows_cycles(const Linear4Args& a) {
+  const int tiles = (a.w->N + 127) / 128 * 8, sms = sm_count();
+  const int64_t values = (int64_t)((tiles + sms - 1) / sms) * 16 * a.w->Kp * (a.up ? 2 : 1);
+  const int64_t rate = a.T <= 8 ? 210 : a.T <= 16 ? 150 : a.T <= 32 ? 90 : 53;
+  return values * 10 / rate + (int64_t)a.T * a.w->Kp * 2 / 40;
 }
 
 cudaError_t launch_linear4_rows(const Linear4Args& a, cudaStream_t st) {

@@ -25,8 +25,6 @@ namespace {
 constexpr int kMaxTokens = 192;   // rows of x a tile
 constexpr int kOutWarps = 16;     // warps of results, a quarter of them for 32 lanes each
 constexpr int kTurns = kOutWarps / 4;
-constexpr int kPass = kOutWarps * 2;  // rows of x that they split at a time
-constexpr int kMaxPasses = 3;
 constexpr int kThreads = 64 + kOutWarps * 32;  // one that loads, one that issues MMAs, results
 constexpr int kMaxSmem = 232448;
 constexpr int kSfCol = 480;       // tensor memory: accumulators below, scales above
@@ -35,12 +33,7 @@ constexpr int kMaxSplit = 8;
 constexpr uint32_t kStatusBytes = 1024;
 constexpr uint32_t kWaitNs = 2000000000u;
 
-// How a product is cut.  `tokens`: rows of x a tile; `wide`: hi and lo as 2 * tokens columns
-// of one MMA, else an MMA each; `split`: blocks that share a tile's K.
-struct Cut {
-  int mats, tokens, wide, split;
-  bool own;  // the blocks split x themselves (one tile each), no kernel before
-};
+using Cut = TileCut;
 
 // The tile of `tokens` rows and 128 columns of x: hi, lo, their exponents in blocks of 512
 // bytes for 128 MMA columns, as tcgen05.cp takes them (hi's then lo's).
@@ -316,8 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if (tid == 0) {
+    const int t0 = blockIdx.x / p.split / p.feature_tiles * p.tokens;
+    const int quads = (min(p.tokens, p.T - t0) + 3) >> 2;  // arrivals of who splits x
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(b_full + 8 * i, p.xq ? 1 : 1 + kOutWarps);
+      mbar_init(b_full + 8 * i, p.xq ? 1 : 1 + quads);
       mbar_init(b_empty + 8 * i, 1);
     }
     for (int i = 0; i < kMaxSlots; ++i) {
@@ -491,45 +486,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_parity = 0;
     bool ok = true;
     if (!p.xq) {
-      // x's tiles first, 16 lanes a row, the next one's loads under this one's conversion
-      const int tt = first / p.feature_tiles, t0 = tt * p.tokens;
-      const int l16 = tid & 15, r0 = (tid - 64) >> 4;
-      uint4 next[kMaxPasses];
-      auto fetch = [&](int kb) {
+      // x's tiles first.  A task is four rows of 128 columns, 16 lanes a row; it takes a warp some
+      // 1000 cycles from end to end, so the warps take tasks in turn, several tiles at a time.
+      const int t0 = first / p.feature_tiles * p.tokens, rows = min(p.tokens, p.T - t0);
+      const int quads = (rows + 3) >> 2, l16 = lane & 15;
+      // (No more warps than tasks of a ring of stages: then the tile one round before a warp's
+      // next has been waited for, and a phase's parity tells the two rounds apart.)
+      const int takers = min(kOutWarps, p.stages * quads);
+      const int kb_step = takers / quads, q_step = takers - kb_step * quads;
+      int kb = warp - 2 < takers ? k0 + (warp - 2) / quads : k1, q = (warp - 2) % quads;
+      const __nv_bfloat16* x = p.x + (int64_t)t0 * p.x_stride + l16 * 8;
+      auto fetch = [&](uint4 (&v)[2], int kb, int q) {
 #pragma unroll
-        for (int i = 0; i < kMaxPasses; ++i) {
-          const int r = r0 + i * kPass, col = kb * 128 + l16 * 8;
-          next[i] = make_uint4(0, 0, 0, 0);
-          if (r < p.tokens && t0 + r < p.T && col < p.K)
-            next[i] = __ldg(reinterpret_cast<const uint4*>(p.x + (t0 + r) * p.x_stride + col));
+        for (int i = 0; i < 2; ++i) {
+          const int r = q * 4 + i * 2 + (lane >> 4);
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (kb < k1 && r < rows && kb * 128 + l16 * 8 < p.K)
+            v[i] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)r * p.x_stride + kb * 128));
         }
       };
-      fetch(k0);
-      int s = 0;
+      uint4 next[2];
+      fetch(next, kb, q);
+      int s = kb - k0;  // its place in the ring of stages
       uint32_t free_parity = 1;
-      for (int kb = k0; kb < k1 && ok; ++kb) {
-        ok = wait_bar(b_empty + 8 * s, free_parity, s_abort);
-        ok = __all_sync(0xffffffffu, ok);
-        uint4 now[kMaxPasses];
-#pragma unroll
-        for (int i = 0; i < kMaxPasses; ++i) now[i] = next[i];
-        if (kb + 1 < k1) fetch(kb + 1);
-        uint8_t* dst = smem + (size_t)s * stage_bytes + MATS * 16384;
-#pragma unroll
-        for (int i = 0; i < kMaxPasses; ++i) {
-          const int r = r0 + i * kPass;
-          if ((i * kPass + ((warp - 2) << 1)) >= p.tokens) break;  // (a warp has two rows)
-          uint2 hi, lo;
-          const uint32_t exps = split8(now[i], hi, lo);
-          put8(dst, p.tokens, p.wide, r, l16, hi, lo, exps);
+      while (kb < k1) {
+        for (; s >= p.stages; s -= p.stages) free_parity ^= 1;
+        const uint4 now[2] = {next[0], next[1]};
+        const int q_now = q, s_now = s;
+        kb += kb_step;
+        s += kb_step;
+        q += q_step;
+        if (q >= quads) {
+          q -= quads;
+          ++kb;
+          ++s;
         }
+        fetch(next, kb, q);
+        ok = wait_bar(b_empty + 8 * s_now, free_parity, s_abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t* dst = smem + (size_t)s_now * stage_bytes + MATS * 16384;
+        uint2 hi[2], lo[2];
+        uint32_t exps[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) exps[i] = split8(now[i], hi[i], lo[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)  // (the tile has a multiple of 16 rows)
+          put8(dst, p.tokens, p.wide, q_now * 4 + i * 2 + (lane >> 4), l16, hi[i], lo[i], exps[i]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_full + 8 * s);
-        if (++s == p.stages) {
-          s = 0;
-          free_parity ^= 1;
-        }
+        if (lane == 0) mbar_arrive(b_full + 8 * s_now);
       }
     }
     auto wait_slot = [&]() {
@@ -701,43 +707,68 @@ int slots_of(const Cut& c) {
   return n < kMaxSlots ? n : kMaxSlots;
 }
 
-// The cut with the least time of the busiest block, in cycles.  An MMA of 128 x N x 32 was
-// measured to take 70 (N = 96; A's 4 KB from shared memory), 76 (128), 80 (144), 86 (160), 101
-// (192); a stage's bytes come at some 55 a cycle.  Between two tiles the MMAs pause, longer
-// with one accumulator than with two.  `split` blocks exchange their sums.
-Cut choose(int N, int T, int KB, bool gated, int sms) {
-  const int blocks = (N + 127) / 128;
-  Cut best = {gated ? 2 : 1, 16, 1, 1, false};
+const void* kernel_of(bool gated, int mats) {
+  return gated ? (const void*)tile_kernel<2, true>
+               : mats == 2 ? (const void*)tile_kernel<2, false> : (const void*)tile_kernel<1, false>;
+}
+
+// Cycles of a step of 128 columns.  An MMA of 128 x N x 32 was measured to take 70 (N = 96; A's
+// 4 KB from shared memory), 76 (128), 80 (144), 86 (160), 101 (192); the issuing thread takes 45
+// an MMA and 210 a step; a stage's bytes come at some 55 a cycle.
+int64_t step_cycles(const Cut& c) {
+  const int n = c.tokens << c.wide, by_n = n / 2 + 5, by_a = 58 + n / 8;
+  const int count = (c.wide ? 4 : 8) * c.mats;
+  const int64_t mma = count * (by_n > by_a ? by_n : by_a) + 20;
+  const int64_t fill = (8704 * c.mats + (int64_t)tile_bytes(c.tokens, c.wide)) / 55;
+  const int64_t issue = 210 + 45 * count;
+  return mma > fill ? (mma > issue ? mma : issue) : (fill > issue ? fill : issue);
+}
+
+// The cut with the least time of the busiest block, in cycles.  Between two tiles the MMAs
+// pause, the longer the fewer accumulators there are; blocks that share a tile exchange sums in
+// some 2400; a row of x that a block splits takes it 38 a step, a kernel before it 3000, most of
+// that the host's (one token by 10240 x 2560 gated: 10.3 us own, 10.6 us with a kernel before;
+// 16 rows 11.7 and 10.7 us; 10 us of the host's time instead of 6).
+Cut choose(int N, int T, int KB, bool gated) {
+  const int sms = sm_count(), blocks = (N + 127) / 128;
+  Cut best = {gated ? 2 : 1, 16, 1, 1, false, 0};
   int64_t least = INT64_MAX;
   Cut c;
   for (c.mats = gated ? 2 : 1; c.mats <= 2; ++c.mats)
     for (c.wide = 0; c.wide < 2; ++c.wide)
       for (c.tokens = 16; c.tokens <= (c.wide ? kMaxTokens / 2 : kMaxTokens); c.tokens += 16) {
         if (stages_of(c) < 3 || c.tokens > (c.mats == 2 ? 160 : 192)) break;
+        if (c.tokens - 16 >= T) break;
         const int64_t ft = gated ? blocks : (blocks + c.mats - 1) / c.mats;
         const int64_t tiles = ft * ((T + c.tokens - 1) / c.tokens);
-        const int n = c.tokens << c.wide, by_n = n / 2 + 5, by_a = 58 + n / 8;
-        const int64_t mma = (c.wide ? 4 : 8) * c.mats * (by_n > by_a ? by_n : by_a);
-        const int64_t fill = (8704 * c.mats + (int64_t)tile_bytes(c.tokens, c.wide)) / 55;
-        const int64_t step = (mma > fill ? mma : fill) + 20;
-        const int64_t pause = slots_of(c) >= 2 * c.mats ? 350 : slots_of(c) > c.mats ? 1000 : gated ? 4000 : 1500;
+        const int64_t step = step_cycles(c);
+        const int64_t split_x = 38 * (int64_t)(c.tokens < T ? c.tokens : T);
+        const int slots = slots_of(c);
+        const int64_t pause = slots >= 2 * c.mats ? 350 : slots > c.mats ? 1500 : gated ? 4000 : 2000;
         const int64_t out = 500 + (gated ? 40 : 24 * c.mats) * c.tokens;
         for (c.split = 1; c.split <= kMaxSplit; c.split *= 2) {
           if (c.split > 1 &&
               (tiles * c.split > sms || KB < 2 * c.split || c.tokens % (4 * c.split) != 0))
             break;
           const int64_t waves = c.split > 1 ? 1 : (tiles + sms - 1) / sms;
+          const int64_t steps = (KB + c.split - 1) / c.split;
           for (int own = 0; own < 2; ++own) {
             c.own = own;
-            if (own && (waves > 1 || c.tokens > kMaxPasses * kPass)) break;
-            const int64_t own_step = own ? 12 * (int64_t)c.tokens + 100 : 0;
-            const int64_t time =
-                waves * (((KB + c.split - 1) / c.split) * (step > own_step ? step : own_step) + pause) +
-                (c.split > 1 ? 6000 + 8 * c.mats * c.tokens : out) + (own ? 0 : 4000);
-            if (time < least) least = time, best = c;
+            if (own && waves > 1) break;
+            const int64_t time = waves * (steps * (own && split_x > step ? split_x : step) + pause) +
+                                 (c.split > 1 ? 2400 + 8 * c.mats * c.tokens : out) +
+                                 (own ? 0 : 3000);
+            if (time >= least) continue;
+            // (fewer clusters fit than blocks: those of a GPC)
+            if (c.split > 1 && tiles > resident_clusters(kernel_of(gated, c.mats), kThreads,
+                                                         kMaxSmem, c.split))
+              continue;
+            least = time;
+            best = c;
           }
         }
       }
+  best.cycles = least;
   return best;
 }
 
@@ -767,8 +798,7 @@ cudaError_t launch(const Linear4Args& a, const Cut& cut, cudaStream_t st) {
   p.vector = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.out_stride % 8 == 0;
   p.stages = stages_of(cut);
   p.slots = slots_of(cut);
-  cudaError_t e = ensure_smem_attr((const void*)kernel, kMaxSmem);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   const int sms = sm_count();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cut.split > 1 ? p.tiles * cut.split : p.tiles < sms ? p.tiles : sms);
@@ -800,12 +830,11 @@ size_t linear4_tile_workspace_bytes(int T, int K) {
   return kStatusBytes + most * (padded_k(K) / 128);
 }
 
-cudaError_t launch_linear4_tile(const Linear4Args& a, cudaStream_t st) {
+cudaError_t launch_linear4_tile(const Linear4Args& a, const TileCut& cut, cudaStream_t st) {
   const int KB = a.w->Kp / 128;
-  const Cut cut = choose(a.w->N, a.T, KB, a.up != nullptr, sm_count());
+  cudaError_t e;
   if (!cut.own) {
     const int64_t threads = (int64_t)a.T * KB * 16;
-    cudaError_t e;
     DSPARK_LAUNCH(kKindLinear4, st,
                   e = launch_pdl(split_kernel, dim3((unsigned)((threads + 255) / 256)),
                                  dim3(kSplitThreads), 0, st, a.x, a.x_stride, a.T, a.w->K, KB,
@@ -816,6 +845,15 @@ cudaError_t launch_linear4_tile(const Linear4Args& a, cudaStream_t st) {
   return a.up            ? launch<2, true>(a, cut, st)
          : cut.mats == 2 ? launch<2, false>(a, cut, st)
                          : launch<1, false>(a, cut, st);
+}
+
+cudaError_t linear4_tile_cut(const Linear4Args& a, TileCut* t) {
+  for (int mats = a.up ? 2 : 1; mats <= 2; ++mats) {
+    const cudaError_t e = ensure_smem_attr(kernel_of(a.up != nullptr, mats), kMaxSmem);
+    if (e != cudaSuccess) return e;
+  }
+  *t = choose(a.w->N, a.T, a.w->Kp / 128, a.up != nullptr);
+  return cudaSuccess;
 }
 
 }  // namespace dspark
