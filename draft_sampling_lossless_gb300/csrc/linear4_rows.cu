@@ -1,4 +1,4 @@
-// Products of a few rows with 4-bit weights: x W^T, and act(x G^T) * (x U^T), T <= 16.
+// Products of a few rows with 4-bit weights: x W^T, and act(x G^T) * (x U^T), T <= 32.
 //
 // The weights' bytes are all the time there is (4.25 bits a value), so a warp takes them
 // from memory into registers, several loads ahead, and the values never stop in shared
@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxRows = 64;
+constexpr int kMaxRows = 32;
 constexpr size_t kMaxSmemX = 196608;  // x's bytes in shared memory
 
 // Row m (of 16) of row tile j (of 8) of a block of 128: four neighbours from each quarter, whose
@@ -301,20 +301,19 @@ bool linear4_rows_fits(int T, int Kp) {
 }
 
 // Its time but for what every call takes: the values of the SM with the most row tiles, at 21 a
-// cycle with up to 8 rows (the conversions bound it), 15, 9 and 5.3 with up to 16, 32 and 64,
-// and x's way into shared memory.
+// cycle with up to 8 rows (the conversions bound it), 15 and 9 with up to 16 and 32, and x's way
+// into shared memory.
 int64_t linear4_rows_cycles(const Linear4Args& a) {
   const int tiles = (a.w->N + 127) / 128 * 8, sms = sm_count();
   const int64_t values = (int64_t)((tiles + sms - 1) / sms) * 16 * a.w->Kp * (a.up ? 2 : 1);
-  const int64_t rate = a.T <= 8 ? 210 : a.T <= 16 ? 150 : a.T <= 32 ? 90 : 53;
+  const int64_t rate = a.T <= 8 ? 210 : a.T <= 16 ? 150 : 90;
   return values * 10 / rate + (int64_t)a.T * a.w->Kp * 2 / 40;
 }
 
 cudaError_t launch_linear4_rows(const Linear4Args& a, cudaStream_t st) {
   if (a.T <= 8) return a.up ? launch<2, 1, 3>(a, st) : launch<1, 1, 5>(a, st);
   if (a.T <= 16) return a.up ? launch<2, 2, 3>(a, st) : launch<1, 2, 5>(a, st);
-  if (a.T <= 32) return a.up ? launch<2, 4, 2>(a, st) : launch<1, 4, 4>(a, st);
-  return a.up ? launch<2, 8, 1>(a, st) : launch<1, 8, 3>(a, st);
+  return a.up ? launch<2, 4, 2>(a, st) : launch<1, 4, 4>(a, st);
 }
 
 }  // namespace dspark
