@@ -489,80 +489,107 @@ def dspark_weights4_load(w, N, K, codes, scales, stream=None):
     for t, cols, what in ((codes, K // 2, "codes"), (scales, K // 32, "scales")):
         if t.dtype != torch.uint8 or t.shape != (N, cols) or not t.is_contiguous():
             raise ValueError(f"{what} must be a contiguous uint8 tensor [{N}, {cols}]")
-    _same_device(codes, scales)
+    at = codes.get_device()
+    if scales.get_device() != at or at < 0:
+        raise _elsewhere(scales if at >= 0 else codes, at)
     _check("dspark_weights4_load", lib().dspark_weights4_load(
-        w, _on_gpu(codes), _on_gpu(scales), _raw_stream(stream)))
+        w, codes.data_ptr(), scales.data_ptr(), _stream_on(at, stream)))
 
 
 def dspark_weights4_quantize(w, N, K, src, stream=None):
-    dt = _dt(src)
-    p, stride = _matrix(src, N, K, src.dtype, "the matrix")
-    _check("dspark_weights4_quantize",
-           lib().dspark_weights4_quantize(w, p, dt, stride, _raw_stream(stream)))
+    dt, at = _dt(src), src.get_device()
+    p, stride = _matrix(src, (N, K), src.dtype, at, "the matrix")
+    _check("dspark_weights4_quantize", lib().dspark_weights4_quantize(
+        w, p, dt, stride, _stream_on(at, stream)))
 
 
 def linear4_workspace_bytes(T, K) -> int:
     return int(lib().dspark_linear4_workspace_bytes(T, K))
 
 
-def _matrix(t, T, cols, dtype, what):
-    """Pointer and row stride of a [T, cols] tensor whose rows may lie apart."""
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != T or t.shape[1] != cols:
-        raise ValueError(f"{what} must be {dtype} [{T}, {cols}], got {t.dtype} {tuple(t.shape)}")
+def _elsewhere(t, at):
+    return ValueError(f"expected a CUDA tensor, got one on {t.device}" if t.get_device() < 0 else
+                      f"expected the tensors on one device ({at}), got one on {t.device}")
+
+
+def _matrix(t, shape, dtype, at, what):
+    """Pointer and row stride of a matrix on device `at` whose rows may lie apart."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     s0, s1 = t.stride()
-    if s1 != 1 and cols > 1:
+    if s1 != 1 and shape[1] > 1:
         raise ValueError(f"the columns of {what} must be contiguous")
-    return _on_gpu(t), (s0 if T > 1 else cols)
+    if t.get_device() != at or at < 0:
+        raise _elsewhere(t, at)
+    return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
 
 
-def _vector(t, d, what):
-    if t.dtype != torch.float32 or t.shape != (d,) or not t.is_contiguous():
+def _vector(t, d, at, what):
+    if t.dtype is not torch.float32 or t.shape != (d,) or t.stride(0) != 1:
         raise ValueError(f"{what} must be a contiguous fp32 tensor [{d}]")
-    return _on_gpu(t)
+    if t.get_device() != at:
+        raise _elsewhere(t, at)
+    return t.data_ptr()
 
 
-def _same_device(*tensors):
-    """The kernels run on the current device: every tensor has to be there."""
-    at = torch.cuda.current_device()
-    for t in tensors:
-        if t.get_device() != at:
-            raise ValueError(f"expected CUDA tensors on the current device ({at}), "
-                             f"got one on {t.device}")
+def _stream_on(at, stream):
+    """The stream's handle, the current one's when None; the kernels run on the current
+    device, where the tensors (on device `at`) have to be."""
+    if torch._C._cuda_getDevice() != at:
+        raise ValueError(f"the tensors are on device {at}, which is not the current one")
+    return torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream
 
 
-def dspark_linear4(w, N, K, x, out, ws, stream=None):
-    T = x.shape[0]
-    xp, xs = _matrix(x, T, K, torch.bfloat16, "x")
-    op, os_ = _matrix(out, T, N, torch.bfloat16, "out")
-    _check("dspark_linear4", lib().dspark_linear4(
-        w, T, xp, xs, op, os_, *_ws(ws), _raw_stream(stream)))
+def _products(x, out, ws, N, K, stream, devices):
+    """What the two products' calls take of their tensors."""
+    T, at = x.shape[0], x.get_device()
+    xp, xs = _matrix(x, (T, K), torch.bfloat16, at, "x")
+    op, os_ = _matrix(out, (T, N), torch.bfloat16, at, "out")
+    if ws.get_device() != at:
+        raise _elsewhere(ws, at)
+    for d in devices:
+        if d != at:
+            raise ValueError(f"the weights are on device {d}, x is on {at}")
+    if not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return T, xp, xs, op, os_, ws.data_ptr(), ws.nbytes, _stream_on(at, stream)
 
 
-def dspark_gated4(gate, up, N, K, act, x, out, ws, stream=None):
-    T = x.shape[0]
-    xp, xs = _matrix(x, T, K, torch.bfloat16, "x")
-    op, os_ = _matrix(out, T, N, torch.bfloat16, "out")
-    _check("dspark_gated4", lib().dspark_gated4(
-        gate, up, act, T, xp, xs, op, os_, *_ws(ws), _raw_stream(stream)))
+def dspark_linear4(w, N, K, x, out, ws, stream=None, devices=()):
+    """devices: that of the weights' store."""
+    _check("dspark_linear4",
+           lib().dspark_linear4(w, *_products(x, out, ws, N, K, stream, devices)))
+
+
+def dspark_gated4(gate, up, N, K, act, x, out, ws, stream=None, devices=()):
+    """devices: those of the weights' stores."""
+    _check("dspark_gated4",
+           lib().dspark_gated4(gate, up, act, *_products(x, out, ws, N, K, stream, devices)))
 
 
 def dspark_norm(x, y, post, gate, alpha, pre, eps, x_out, h, stream=None):
-    T, d = x.shape
-    dt = _dt(x)
-    xp, xs = _matrix(x, T, d, x.dtype, "x")
-    yp = gp = op = hp = None
+    shape, dt, at, bf16 = x.shape, _dt(x), x.get_device(), torch.bfloat16
+    if len(shape) != 2:
+        raise ValueError(f"x must be a matrix [T, d], got {list(shape)}")
+    T, d = shape
+    xp, xs = _matrix(x, shape, x.dtype, at, "x")
+    yp = gp = op = hp = postp = prep = None
     ys = gs = os_ = hs = 0
     if y is not None:
-        yp, ys = _matrix(y, T, d, torch.bfloat16, "y")
+        yp, ys = _matrix(y, shape, bf16, at, "y")
     if gate is not None:
-        rows = T if gate.shape[0] == T else 1
-        gp, gs = _matrix(gate, rows, d, torch.bfloat16, "gate")
-        gs = gs if rows > 1 else 0
+        if T > 1 and gate.shape == shape:
+            gp, gs = _matrix(gate, shape, bf16, at, "gate")
+        else:  # one row for all
+            gp, _ = _matrix(gate, (1, d), bf16, at, "gate")
+    if post is not None:
+        postp = _vector(post, d, at, "post")
+    if pre is not None:
+        prep = _vector(pre, d, at, "pre")
     if x_out is not None:
-        op, os_ = _matrix(x_out, T, d, x.dtype, "x_out")
+        op, os_ = _matrix(x_out, shape, x.dtype, at, "x_out")
     if h is not None:
-        hp, hs = _matrix(h, T, d, torch.bfloat16, "h")
+        hp, hs = _matrix(h, shape, bf16, at, "h")
     _check("dspark_norm", lib().dspark_norm(
-        T, d, dt, xp, xs, yp, ys, None if post is None else _vector(post, d, "post"), gp, gs,
-        alpha, None if pre is None else _vector(pre, d, "pre"), eps, op, os_, hp, hs,
-        _raw_stream(stream)))
+        T, d, dt, xp, xs, yp, ys, postp, gp, gs, alpha, prep, eps, op, os_, hp, hs,
+        _stream_on(at, stream)))

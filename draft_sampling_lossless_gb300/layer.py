@@ -26,6 +26,7 @@ class Weights4:
         self.store = torch.empty(n, dtype=torch.uint8, device=device)
         self.desc = B.weights4_init(N, K, self.store)
         self._ref = ctypes.byref(self.desc)
+        self._on = (self.store.get_device(),)
 
     @classmethod
     def load(cls, codes, scales, stream=None):
@@ -55,7 +56,7 @@ def workspace(T, K, device="cuda"):
 
 def linear4(x, w, out, ws, stream=None):
     """out = x w^T: x [T, K], out [T, N] bf16."""
-    B.dspark_linear4(w._ref, w.N, w.K, x, out, ws, stream)
+    B.dspark_linear4(w._ref, w.N, w.K, x, out, ws, stream, w._on)
 
 
 def gated4(x, gate, up, out, ws, act="silu", stream=None):
@@ -65,7 +66,8 @@ def gated4(x, gate, up, out, ws, act="silu", stream=None):
         raise ValueError(f"act must be one of {sorted(B.ACTIVATIONS)}, got {act!r}")
     if (up.N, up.K) != (gate.N, gate.K):
         raise ValueError("gate and up differ in shape")
-    B.dspark_gated4(gate._ref, up._ref, gate.N, gate.K, B.ACTIVATIONS[act], x, out, ws, stream)
+    B.dspark_gated4(gate._ref, up._ref, gate.N, gate.K, B.ACTIVATIONS[act], x, out, ws, stream,
+                    (*gate._on, *up._on))
 
 
 def norm(x, h=None, pre=None, y=None, x_out=None, post=None, gate=None, alpha=1.0, eps=1e-6,
