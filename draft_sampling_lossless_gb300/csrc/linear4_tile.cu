@@ -714,12 +714,12 @@ const void* kernel_of(bool gated, int mats) {
 
 // Cycles of a step of 128 columns.  An MMA of 128 x N x 32 was measured to take 70 (N = 96; A's
 // 4 KB from shared memory), 76 (128), 80 (144), 86 (160), 101 (192); the issuing thread takes 45
-// an MMA and 210 a step; a stage's bytes come at some 55 a cycle.
+// an MMA and 210 a step; a stage's bytes come at some 80 a cycle.
 int64_t step_cycles(const Cut& c) {
   const int n = c.tokens << c.wide, by_n = n / 2 + 5, by_a = 58 + n / 8;
   const int count = (c.wide ? 4 : 8) * c.mats;
   const int64_t mma = count * (by_n > by_a ? by_n : by_a) + 20;
-  const int64_t fill = (8704 * c.mats + (int64_t)tile_bytes(c.tokens, c.wide)) / 55;
+  const int64_t fill = (8704 * c.mats + (int64_t)tile_bytes(c.tokens, c.wide)) / 80;
   const int64_t issue = 210 + 45 * count;
   return mma > fill ? (mma > issue ? mma : issue) : (fill > issue ? fill : issue);
 }
