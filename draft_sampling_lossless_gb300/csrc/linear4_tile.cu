@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ms->issued = issued;
     }
   } else if (warp == 1) {
+    grid_dependency_wait();  // so that the waits' limits do not count what ran before
     if (elect_one()) {
       const uint32_t nb = exp_blocks(p.tokens, p.wide), acc_cols = p.tokens << p.wide;
       const uint32_t id0 = idesc_mx(acc_cols);
@@ -686,8 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     set_flag(p.status, kFlagWaitTimeout);
     // the copies in flight land before the block's shared memory goes
     const int n = ms->issued;
+    // (a wait that runs out, where x's part never came, has been long enough for all of them)
     for (int i = max(0, n - p.stages); i < n; ++i)
-      mbar_wait(b_full + 8 * (i % p.stages), (i / p.stages) & 1);
+      if (!mbar_wait(b_full + 8 * (i % p.stages), (i / p.stages) & 1)) break;
   }
   if (warp == 1) {
     tc_fence_after();

@@ -10,19 +10,22 @@ append), say from bf16 to e4m3.
 
 The target is synthetic: random embeddings, a few attention layers on top of
 them, an output table.  The drafter is the Markov head alone on the same two
-tables, so that it agrees with the target most of the time.  The projections are
-plain fp32 torch products; the attention, the cache and the four stages run in
-the CUDA library.
+tables, so that it agrees with the target most of the time.  `Target`'s projections
+are plain fp32 torch products; the attention, the cache and the four stages run in
+the CUDA library.  `Target4` has 4-bit projections, a gated feed-forward block in
+each layer and the norms between blocks, all of them in the library too.
 
-    python -m draft_sampling_lossless_gb300.decode
+    python -m draft_sampling_lossless_gb300.decode [--four-bit]
 """
 
 from __future__ import annotations
 
 import math
+import sys
 
 import torch
 
+from . import layer
 from .cache import PagedCache
 from .pipeline import DSparkStep
 
@@ -58,6 +61,61 @@ class Target:
         for i in range(len(self.wqkv)):
             x = x + attention(i, *self.qkv(i, x)).reshape(len(tokens), -1).float() @ self.wo[i]
         return self.norm(x) @ self.unemb.T
+
+    def status(self) -> int:
+        """Device status bits of the forward pass's own calls."""
+        return 0
+
+
+class Target4(Target):
+    """The same with 4-bit weights and F-wide feed-forward blocks: per layer
+    x += wo attention(norm(x) wqkv), x += down(silu(gate h) * up h) with h = norm(x),
+    the stream x in fp32, everything between in bf16."""
+
+    def __init__(self, V=512, d=64, Hq=8, Hkv=2, D=32, layers=2, window=0, F=256, device="cuda",
+                 seed=0):
+        super().__init__(V, d, Hq, Hkv, D, layers, window, device, seed)
+        g = torch.Generator(device="cpu").manual_seed(seed + 1)
+
+        def w(n, k, std):
+            return layer.Weights4.quantize((torch.randn((n, k), generator=g) * std).to(device))
+
+        self.F = F
+        self.qkv4 = [layer.Weights4.quantize(m.T.contiguous()) for m in self.wqkv]
+        self.wo4 = [layer.Weights4.quantize(m.T.contiguous()) for m in self.wo]
+        self.gate4 = [w(F, d, 1.0 / math.sqrt(d)) for _ in range(layers)]
+        self.up4 = [w(F, d, 1.0 / math.sqrt(d)) for _ in range(layers)]
+        self.down4 = [w(d, F, 0.7 / math.sqrt(F)) for _ in range(layers)]
+        self.unemb4 = layer.Weights4.quantize(self.unemb)
+        self.ones = torch.ones(d, device=device)
+        self.ws = None
+
+    def forward(self, tokens, attention):
+        T, dev = len(tokens), self.emb.device
+        widest = max(self.d, self.Hq * self.D, self.F)
+        if self.ws is None or self.ws.numel() < layer.workspace_bytes(T, widest):
+            self.ws = layer.workspace(T, widest, dev)
+
+        def rows(n):
+            return torch.empty((T, n), dtype=torch.bfloat16, device=dev)
+
+        x, h, y = self.emb[tokens], rows(self.d), rows(self.d)
+        layer.norm(x, h, self.ones)
+        for i, (gate, up, down) in enumerate(zip(self.gate4, self.up4, self.down4)):
+            qkv, m = rows((self.Hq + 2 * self.Hkv) * self.D), rows(self.F)
+            layer.linear4(h, self.qkv4[i], qkv, self.ws)
+            o = attention(i, *qkv.view(T, -1, self.D).split([self.Hq, self.Hkv, self.Hkv], dim=1))
+            layer.linear4(o.reshape(T, -1), self.wo4[i], y, self.ws)
+            layer.norm(x, h, self.ones, y=y, x_out=x)
+            layer.gated4(h, gate, up, m, self.ws)
+            layer.linear4(m, down, y, self.ws)
+            layer.norm(x, h, self.ones, y=y, x_out=x)
+        logits = rows(self.V)
+        layer.linear4(h, self.unemb4, logits, self.ws)
+        return logits.float()
+
+    def status(self) -> int:
+        return 0 if self.ws is None else layer.status(self.ws)
 
 
 class Decoder:
@@ -158,7 +216,8 @@ class Decoder:
             raise RuntimeError(f"device status {a.status(ws):#x}")
 
     def check(self):
-        for word in [self.step_.status()] + [self.caches[0].status(w) for w in self.ws.values()]:
+        words = [self.step_.status(), self.t.status()]
+        for word in words + [self.caches[0].status(w) for w in self.ws.values()]:
             if word != 0:
                 raise RuntimeError(f"device status {word:#x}")
 
@@ -166,7 +225,7 @@ class Decoder:
 def main():
     g = torch.Generator().manual_seed(2)
     prompts = [torch.randint(0, 512, (n,), generator=g).tolist() for n in (1, 5, 40, 150)]
-    d = Decoder(Target(), prompts)
+    d = Decoder(Target4() if "--four-bit" in sys.argv[1:] else Target(), prompts)
     steps = 24
     for i in range(steps):
         if i == steps // 2:

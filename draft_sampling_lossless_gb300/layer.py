@@ -45,13 +45,18 @@ class Weights4:
         return w
 
 
-def workspace(T, K, device="cuda"):
-    """A zeroed workspace (uint8) for products of up to T rows of up to K columns;
-    calls in flight at the same time need one each."""
+def workspace_bytes(T, K) -> int:
+    """Bytes of a workspace for products of up to T rows of up to K columns."""
     n = B.linear4_workspace_bytes(T, K)
     if n == 0:
         raise ValueError("sizes out of range")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return n
+
+
+def workspace(T, K, device="cuda"):
+    """A zeroed workspace (uint8) for products of up to T rows of up to K columns;
+    calls in flight at the same time need one each."""
+    return torch.zeros(workspace_bytes(T, K), dtype=torch.uint8, device=device)
 
 
 def linear4(x, w, out, ws, stream=None):

@@ -516,3 +516,132 @@ def test_refusals_that_need_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         layer.norm(x, out[:, :1].expand(300, 96).contiguous().cpu(), torch.ones(96, device=DEV))
     assert B.launch_count() - n == 2  # the two matrices loaded in between
+
+
+# ---------------------------------------------------------------- large sizes, first calls
+
+
+@pytest.mark.parametrize("T,N,K", ((64, 151936, 2560), (4100, 6144, 2560), (1500, 2560, 10240),
+                                   (9, 32000, 2560), (33, 151936, 640)))
+def test_large_sizes(T, N, K):
+    """Against the 64-bit form in some of the columns; every value is finite."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    q = layer.Weights4.quantize(torch.randn((N, K), generator=g, device=DEV).bfloat16())
+    x = (torch.randn((T, K), generator=g, device=DEV) * 2).bfloat16()
+    got = run_linear(x, q)
+    assert got.isfinite().all()
+    # the matrix's values: unit rows of some columns' groups would need K rows; take the
+    # columns' codes back through a product with whole blocks of unit rows
+    cols = torch.randint(0, N, (40,), generator=torch.Generator().manual_seed(1)).to(DEV)
+    m = torch.empty(len(cols), K, dtype=torch.float64, device=DEV)
+    for k in range(0, K, 640):
+        unit = torch.zeros(640, K, dtype=torch.bfloat16, device=DEV)
+        unit[torch.arange(640), torch.arange(k, k + 640)] = 1.0
+        m[:, k:k + 640] = run_linear(unit, q)[:, cols].double().T
+
+    class W:
+        pass
+
+    w = W()
+    w.K, w.m = K, m
+    check_linear(x, w, got[:, cols])
+
+
+def test_gated_prompts():
+    T, N, K = 2300, 10240, 640
+    g = torch.Generator(device=DEV).manual_seed(2)
+    ws = [torch.randn((N, K), generator=g, device=DEV).mul_(0.05) for _ in range(2)]
+    qs = [layer.Weights4.quantize(w) for w in ws]
+    x = torch.randn((T, K), generator=g, device=DEV).bfloat16()
+    got = run_gated(x, *qs, "silu")
+    cols = torch.randint(0, N, (64,), generator=torch.Generator().manual_seed(1)).to(DEV)
+    unit = torch.eye(K, dtype=torch.bfloat16, device=DEV)
+    mats = []
+    for q in qs:
+        w = type("W", (), {})()
+        w.K, w.m = K, run_linear(unit, q)[:, cols].double().T
+        mats.append(w)
+    check_gated(x, *mats, "silu", got[:, cols])
+
+
+FIRST = """
+import torch
+from draft_sampling_lossless_gb300 import layer
+x = torch.randn({T}, 512, device="cuda").bfloat16()
+q = layer.Weights4.quantize(torch.randn(300, 512, device="cuda"))
+h, pre = torch.empty_like(x), torch.ones(512, device="cuda")
+out = torch.zeros({T}, 300, dtype=torch.bfloat16, device="cuda")
+ws = layer.workspace({T}, 512)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    layer.norm(x, h, pre)
+    layer.linear4(h, q, out, ws)
+g.replay()
+a = out.clone()
+layer.linear4(h, q, out, ws)
+assert torch.equal(a, out) and a.abs().max() > 0
+print("same")
+"""
+
+
+@pytest.mark.parametrize("T", (2, 60, 300))
+def test_first_call_of_a_process_may_be_captured(T):
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(T=T)], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-800:]
+
+
+def test_two_graphs_one_after_the_other_may_share_a_workspace():
+    w = Matrix(260, 384)
+    q = w.load()
+    xs = [activations(T, 384) for T in (40, 300)]
+    want = [run_linear(x, q).clone() for x in xs]
+    ws = layer.workspace(300, 384)
+    outs = [torch.empty_like(o) for o in want]
+    graphs = []
+    for x, o in zip(xs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer.linear4(x, q, o, ws)
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for o, r in zip(outs, want):
+        assert torch.equal(o, r)
+    assert layer.status(ws) == 0
+
+
+def test_one_matrix_for_gate_and_up_and_outputs_into_a_wider_buffer():
+    w = Matrix(96, 64, lo=120, hi=123)
+    q = w.load()
+    for T in (5, 50, 200):
+        x = activations(T, 64)
+        wide = torch.full((T, 300), 3.0, dtype=torch.bfloat16, device=DEV)
+        layer.gated4(x, q, q, wide[:, 101:197], layer.workspace(T, 64))
+        check_gated(x, w, w, "silu", wide[:, 101:197])
+        assert (wide[:, :101] == 3).all() and (wide[:, 197:] == 3).all()
+
+
+def test_devices_and_streams():
+    """Tensors of a call are on one device, the current one; a call given a stream runs there."""
+    w = Matrix(64, 96)
+    q = w.load()
+    x = activations(7, 96)
+    want = run_linear(x, q)
+    out = torch.zeros_like(want)
+    ws = layer.workspace(7, 96)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    layer.linear4(x, q, out, ws, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(out, want)
+    with pytest.raises(ValueError, match="device"):
+        B.dspark_linear4(q._ref, 64, 96, x, out, ws, None, (1,))
