@@ -728,7 +728,7 @@ int64_t step_cycles(const Cut& c) {
 
 // The cut with the least time of the busiest block, in cycles.  Between two tiles the MMAs
 // pause, the longer the fewer accumulators there are; blocks that share a tile exchange sums in
-// some 2400; a row of x that a block splits takes it 38 a step, a kernel before it 3000, most of
+// some 3000 to 6000; a row of x that a block splits takes it 43 a step, a kernel before it 3000, most of
 // that the host's (one token by 10240 x 2560 gated: 10.3 us own, 10.6 us with a kernel before;
 // 16 rows 11.7 and 10.7 us; 10 us of the host's time instead of 6).
 Cut choose(int N, int T, int KB, bool gated) {
@@ -744,7 +744,7 @@ Cut choose(int N, int T, int KB, bool gated) {
         const int64_t ft = gated ? blocks : (blocks + c.mats - 1) / c.mats;
         const int64_t tiles = ft * ((T + c.tokens - 1) / c.tokens);
         const int64_t step = step_cycles(c);
-        const int64_t split_x = 38 * (int64_t)(c.tokens < T ? c.tokens : T);
+        const int64_t split_x = 43 * (int64_t)(c.tokens < T ? c.tokens : T);
         const int slots = slots_of(c);
         const int64_t pause = slots >= 2 * c.mats ? 350 : slots > c.mats ? 1500 : gated ? 4000 : 2000;
         const int64_t out = 500 + (gated ? 40 : 24 * c.mats) * c.tokens;
@@ -758,7 +758,7 @@ Cut choose(int N, int T, int KB, bool gated) {
             c.own = own;
             if (own && waves > 1) break;
             const int64_t time = waves * (steps * (own && split_x > step ? split_x : step) + pause) +
-                                 (c.split > 1 ? 2400 + 8 * c.mats * c.tokens : out) +
+                                 (c.split > 1 ? 1500 + 600 * c.split + 14 * c.mats * c.tokens : out) +
                                  (own ? 0 : 3000);
             if (time >= least) continue;
             // (fewer clusters fit than blocks: those of a GPC)
