@@ -63,21 +63,19 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-// Eight values of a row's 128 columns by each of 16 lanes, four lanes a group of 32: the codes of
-// hi and lo; returns the row's four exponent bytes (in every lane).
-__device__ __forceinline__ uint32_t split8(uint4 raw, uint2& hi, uint2& lo) {
+// The largest finite magnitude of eight values, as bf16 bits (magnitudes order as whole numbers,
+// past 0x7f80 a NaN).  What is not finite becomes NaN in v: its row's results are not finite.
+__device__ __forceinline__ uint32_t top_of8(uint4 raw, float (&v)[8]) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  // bf16 magnitudes order as whole numbers; past 0x7f80 a NaN
   uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
                           __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
   top = max(top & 0xffffu, top >> 16);
-  float v[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     v[2 * j] = __uint_as_float(w[j] << 16);
     v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
   }
-  if (top >= 0x7f80u) {  // the maximum is over what is finite; the rest makes its row's results NaN
+  if (top >= 0x7f80u) {
     top = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -86,10 +84,10 @@ __device__ __forceinline__ uint32_t split8(uint4 raw, uint2& hi, uint2& lo) {
       else v[j] = NAN;
     }
   }
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const int e = group_exponent(__uint_as_float(top << 16));
-  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+  return top;
+}
+// Their codes of hi and lo for the group's factor f = 2^-e.
+__device__ __forceinline__ void codes_of8(const float (&v)[8], float f, uint2& hi, uint2& lo) {
   uint32_t h[4], l[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -100,46 +98,74 @@ __device__ __forceinline__ uint32_t split8(uint4 raw, uint2& hi, uint2& lo) {
   }
   hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
   lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+// A row's exponents go to the place of its MMA column n: lane n % 32 of tensor memory, column
+// n / 32; hi's and lo's (`term` 0 and 1).
+__device__ __forceinline__ void put_exps(uint8_t* dst, int tokens, int wide, int r, int term,
+                                         uint32_t exps) {
+  const int n = term == 0 ? r : wide ? tokens + r : (tokens + 127) / 128 * 128 + r;
+  *reinterpret_cast<uint32_t*>(dst + tokens * 256 + (n >> 7) * 512 + (n & 31) * 16 +
+                               ((n >> 5) & 3) * 4) = exps - term * 0x04040404u;
+}
+
+// Eight values of a row's 128 columns by each of 16 lanes, into row r of the tile at `dst`.
+__device__ __forceinline__ void split8(uint4 raw, uint8_t* dst, int tokens, int wide, int r) {
+  const int lane = threadIdx.x & 15;
+  float v[8];
+  uint32_t top = top_of8(raw, v);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const int e = group_exponent(__uint_as_float(top << 16));
+  uint2 hi, lo;
+  codes_of8(v, __uint_as_float((uint32_t)(127 - e) << 23), hi, lo);
   uint32_t exps = 0;
 #pragma unroll
   for (int g = 0; g < 4; ++g)
     exps |= (uint32_t)(__shfl_sync(0xffffffffu, e, (threadIdx.x & 16) + g * 4) + 127) << (8 * g);
-  return exps;
-}
-
-// Where they go in the tile at `dst`: row r, its lane of 16.
-__device__ __forceinline__ void put8(uint8_t* dst, int tokens, int wide, int r, int lane, uint2 hi,
-                                     uint2 lo, uint32_t exps) {
   const uint32_t at = r * 128 + (((lane >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
   *reinterpret_cast<uint2*>(dst + at) = hi;
   *reinterpret_cast<uint2*>(dst + tokens * 128 + at) = lo;
-  if (lane < 2) {  // an MMA column's exponents: lane n % 32 of tensor memory, column n / 32
-    const int n = lane == 0 ? r : wide ? tokens + r : (tokens + 127) / 128 * 128 + r;
-    *reinterpret_cast<uint32_t*>(dst + tokens * 256 + (n >> 7) * 512 + (n & 31) * 16 +
-                                 ((n >> 5) & 3) * 4) = exps - lane * 0x04040404u;
-  }
+  if (lane < 2) put_exps(dst, tokens, wide, r, lane, exps);
 }
 
-constexpr int kSplitThreads = 256;
+// A warp a row's four tiles of 128 columns, 16 values a lane.  Rows past T stay as they are:
+// they reach only columns of the product that are not stored.
+constexpr int kSplitWarps = 8;
 
-// Rows past T stay as they are: they reach only columns of the product that are not stored.
-__global__ void __launch_bounds__(kSplitThreads)
+__global__ void __launch_bounds__(kSplitWarps * 32)
     split_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride, int T, int K, int KB,
                  int tokens, int wide, uint8_t* __restrict__ out) {
   grid_dependency_wait();
   asm volatile("griddepcontrol.launch_dependents;");
-  const int64_t i = ((int64_t)blockIdx.x * kSplitThreads + threadIdx.x) >> 4;
-  const int lane = threadIdx.x & 15;
-  const int64_t t = i / KB;
-  const int kb = (int)(i - t * KB), col = kb * 128 + lane * 8;
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (t < T && col < K) raw = __ldg(reinterpret_cast<const uint4*>(x + t * x_stride + col));
-  uint2 hi, lo;
-  const uint32_t exps = split8(raw, hi, lo);
-  if (t >= T) return;
-  const int64_t tile = t / tokens;
-  put8(out + (tile * KB + kb) * tile_bytes(tokens, wide), tokens, wide, (int)(t - tile * tokens),
-       lane, hi, lo, exps);
+  const int t = blockIdx.x * kSplitWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int kb = blockIdx.y * 4 + (lane >> 3), l8 = lane & 7, col = kb * 128 + l8 * 16;
+  if (t >= T) return;  // (whole warps)
+  uint4 raw[2] = {};
+  if (col < K) {  // K is a multiple of 32
+    const uint4* p = reinterpret_cast<const uint4*>(x + t * x_stride + col);
+    raw[0] = __ldg(p);
+    raw[1] = __ldg(p + 1);
+  }
+  float v[2][8];
+  uint32_t top = max(top_of8(raw[0], v[0]), top_of8(raw[1], v[1]));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const int e = group_exponent(__uint_as_float(top << 16));
+  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+  uint2 hi[2], lo[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) codes_of8(v[i], f, hi[i], lo[i]);
+  uint32_t exps = 0;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    exps |= (uint32_t)(__shfl_sync(0xffffffffu, e, (lane & 24) + g * 2) + 127) << (8 * g);
+  if (kb >= KB) return;
+  const int tile = t / tokens, r = t - tile * tokens;
+  uint8_t* dst = out + ((size_t)tile * KB + kb) * tile_bytes(tokens, wide);
+  const uint32_t at = r * 128 + ((l8 ^ (r & 7)) << 4);
+  *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0].x, hi[0].y, hi[1].x, hi[1].y);
+  *reinterpret_cast<uint4*>(dst + tokens * 128 + at) =
+      make_uint4(lo[0].x, lo[0].y, lo[1].x, lo[1].y);
+  if (l8 < 2) put_exps(dst, tokens, wide, r, l8, exps);
 }
 
 // ---------------------------------------------------------------- the product
@@ -527,13 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         uint8_t* dst = smem + (size_t)s_now * stage_bytes + MATS * 16384;
-        uint2 hi[2], lo[2];
-        uint32_t exps[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) exps[i] = split8(now[i], hi[i], lo[i]);
 #pragma unroll
         for (int i = 0; i < 2; ++i)  // (the tile has a multiple of 16 rows)
-          put8(dst, p.tokens, p.wide, q_now * 4 + i * 2 + (lane >> 4), l16, hi[i], lo[i], exps[i]);
+          split8(now[i], dst, p.tokens, p.wide, q_now * 4 + i * 2 + (lane >> 4));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_full + 8 * s_now);
@@ -836,10 +858,10 @@ cudaError_t launch_linear4_tile(const Linear4Args& a, const TileCut& cut, cudaSt
   const int KB = a.w->Kp / 128;
   cudaError_t e;
   if (!cut.own) {
-    const int64_t threads = (int64_t)a.T * KB * 16;
     DSPARK_LAUNCH(kKindLinear4, st,
-                  e = launch_pdl(split_kernel, dim3((unsigned)((threads + 255) / 256)),
-                                 dim3(kSplitThreads), 0, st, a.x, a.x_stride, a.T, a.w->K, KB,
+                  e = launch_pdl(split_kernel,
+                                 dim3((a.T + kSplitWarps - 1) / kSplitWarps, (KB + 3) / 4),
+                                 dim3(kSplitWarps * 32), 0, st, a.x, a.x_stride, a.T, a.w->K, KB,
                                  cut.tokens, cut.wide,
                                  static_cast<uint8_t*>(a.ws) + kStatusBytes));
     if (e != cudaSuccess) return e;
