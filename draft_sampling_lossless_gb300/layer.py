@@ -32,7 +32,8 @@ class Weights4:
     def load(cls, codes, scales, stream=None):
         """From codes [N, K / 2] (two a byte, the even column in the low half) and
         scale bytes [N, K / 32] (b for 2^(b - 127)), uint8."""
-        w = cls(codes.shape[0], 2 * codes.shape[1], codes.device)
+        with torch.cuda.stream(stream):  # the store's memory is that stream's
+            w = cls(codes.shape[0], 2 * codes.shape[1], codes.device)
         B.dspark_weights4_load(w._ref, w.N, w.K, codes, scales, stream)
         return w
 
@@ -40,7 +41,8 @@ class Weights4:
     def quantize(cls, src, stream=None):
         """From a bf16 or fp32 matrix [N, K]: to nearest, scales that hold each
         group's largest value."""
-        w = cls(src.shape[0], src.shape[1], src.device)
+        with torch.cuda.stream(stream):
+            w = cls(src.shape[0], src.shape[1], src.device)
         B.dspark_weights4_quantize(w._ref, w.N, w.K, src, stream)
         return w
 

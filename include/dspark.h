@@ -620,7 +620,7 @@ size_t dspark_linear4_workspace_bytes(int T, int K);
  * of their 32 columns (which may be rounded away, as may values below 2^-118);
  * sums are fp32, the result is rounded once.  A row of x with a NaN or an
  * infinity gives NaN or infinities in its own row of out, and only there.
- * Results are bit-reproducible.
+ * Results are bit-reproducible (for the same T, N and K).
  */
 int dspark_linear4(const dspark_weights4* w, int T, const void* x, int64_t x_stride, void* out,
                    int64_t out_stride, void* ws, size_t ws_bytes, void* stream);

@@ -522,7 +522,8 @@ def test_refusals_that_need_tensors():
 
 
 @pytest.mark.parametrize("T,N,K", ((64, 151936, 2560), (4100, 6144, 2560), (1500, 2560, 10240),
-                                   (9, 32000, 2560), (33, 151936, 640)))
+                                   (9, 32000, 2560), (33, 151936, 640), (5, 130, 65280),
+                                   (40, 130, 65280), (200, 130, 65280)))
 def test_large_sizes(T, N, K):
     """Against the 64-bit form in some of the columns; every value is finite."""
     g = torch.Generator(device=DEV).manual_seed(T)
@@ -645,3 +646,44 @@ def test_devices_and_streams():
     assert torch.equal(out, want)
     with pytest.raises(ValueError, match="device"):
         B.dspark_linear4(q._ref, 64, 96, x, out, ws, None, (1,))
+
+
+@pytest.mark.parametrize("T", (3, 40, 200))
+def test_the_longest_rows(T):
+    """K = 65536, whole numbers: every partial sum is a whole number of halves below 2^23."""
+    K = 65536
+    g = torch.Generator().manual_seed(T)
+    x = torch.randint(-3, 4, (T, K), generator=g).float().bfloat16().to(DEV)
+    w = Matrix(150, K, lo=127, hi=127)
+    got = run_linear(x, w.load())
+    assert torch.equal(got, (x.double() @ w.m.T).float().bfloat16())
+
+
+def test_weights_made_on_another_stream():
+    s = torch.cuda.Stream()
+    m = Matrix(200, 320)
+    codes, scales = m.codes.to(DEV), m.scales.to(DEV)
+    torch.cuda.synchronize()
+    q = layer.Weights4.load(codes, scales, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    for T in (4, 100):
+        x = activations(T, 320)
+        check_linear(x, m, run_linear(x, q))
+
+
+def test_weights_written_just_before_they_are_used():
+    """A product queued behind the call that writes its weights uses the new ones."""
+    a, b = Matrix(300, 640), Matrix(300, 640, seed=8)
+    q = a.load()
+    cb = b.codes.to(DEV), b.scales.to(DEV)
+    for T in (2, 50, 300):
+        x = activations(T, 640)
+        ws = layer.workspace(T, 640)
+        outs = [torch.empty(T, 300, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        ca = a.codes.to(DEV), a.scales.to(DEV)
+        torch.cuda.synchronize()
+        for (c, s), o in ((ca, outs[0]), (cb, outs[1])):
+            B.dspark_weights4_load(q._ref, 300, 640, c, s)
+            layer.linear4(x, q, o, ws)
+        check_linear(x, a, outs[0])
+        check_linear(x, b, outs[1])
