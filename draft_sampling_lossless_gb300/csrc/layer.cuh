@@ -8,29 +8,32 @@
 
 namespace dspark {
 
-// What the opaque words of a dspark_weights4 hold.  The store: codes [N][Kp / 2], Kp = K
-// rounded up to 128, then the scales in blocks of 128 rows and 128 columns (scale_at).
+// What the opaque words of a dspark_weights4 hold.  The store: tiles of 128 rows by 128 columns,
+// [ceil(N / 128)][Kp / 128], Kp = K rounded up to 128, each its codes [128][64 bytes] and then
+// its scales, one run of 8704 bytes.  (With codes in rows of K, 4100 rows of
+// x gated by 2 x 10240 x 2560 took 235 us for 231, one by 6144 x 2560 5.6 us for 5.45.)
 struct Weights4Desc {
   uint64_t magic;
   int N, K, Kp, pad;
-  uint8_t *codes, *scales;
-  CUtensorMap tm;  // boxes of 128 rows by 128 codes, spread to a byte each
+  uint8_t* store;
+  CUtensorMap tm;  // boxes of a tile's codes, spread to a byte each
 };
 constexpr uint64_t kWeights4Magic = 0x6473706b77347834ull;
+constexpr int kTileCodes = 8192, kTileBytes = kTileCodes + 512;
 
 __host__ __device__ constexpr int padded_k(int K) { return (K + 127) / 128 * 128; }
-constexpr size_t codes_bytes(int N, int K) {
-  return ((size_t)N * (padded_k(K) / 2) + 511) / 512 * 512;
+constexpr size_t weights4_bytes(int N, int K) {
+  return (size_t)((N + 127) / 128) * (padded_k(K) / 128) * kTileBytes;
 }
-constexpr size_t scales_bytes(int N, int K) {
-  return (size_t)((N + 127) / 128) * (padded_k(K) / 128) * 512;
+// The tile of row n, columns 32 g .. 32 g + 31; in it, their 16 bytes of codes, and their scale:
+// [n % 32][n / 32 % 4][g % 4], as tcgen05.cp spreads 512 bytes over tensor memory's lanes (32 of
+// them) and columns.
+__host__ __device__ constexpr size_t tile_at(int n, int g, int Kp) {
+  return ((size_t)(n >> 7) * (Kp >> 7) + (g >> 2)) * kTileBytes;
 }
-// Where the scale of row n, columns 32 g .. 32 g + 31 is: a block of 128 rows and four
-// groups is 512 bytes, [n % 32][n / 32 % 4][g % 4], as tcgen05.cp spreads it over tensor
-// memory's lanes (32 of them) and columns.
-__host__ __device__ constexpr size_t scale_at(int n, int g, int Kp) {
-  return ((size_t)(n >> 7) * (Kp >> 7) + (g >> 2)) * 512 + (n & 31) * 16 + ((n >> 5) & 3) * 4 +
-         (g & 3);
+__host__ __device__ constexpr int code_in_tile(int n, int g) { return (n & 127) * 64 + (g & 3) * 16; }
+__host__ __device__ constexpr int scale_in_tile(int n, int g) {
+  return kTileCodes + (n & 31) * 16 + ((n >> 5) & 3) * 4 + (g & 3);
 }
 
 // out[t][n] = x[t] . W[n], or act(x[t] . G[n]) * (x[t] . U[n]).

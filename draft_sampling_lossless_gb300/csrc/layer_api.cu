@@ -62,8 +62,9 @@ int load_desc(const char* what, const dspark_weights4* w, Weights4Desc& d) {
   return DSPARK_OK;
 }
 
-// Boxes of 128 codes of 128 rows, each code spread to a byte's place (16 codes in 8 bytes,
-// 8 bytes apart) and swizzled as the MMA operand that they land in; rows past N read as zeros.
+// Boxes of a tile's codes, 128 rows of 128, each code spread to a byte's place (16 codes in 8
+// bytes, 8 bytes apart) and swizzled as the MMA operand that they land in; tiles past the last
+// read as zeros.
 cudaError_t encode_codes(Weights4Desc& d) {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() {
     void* f = nullptr;
@@ -75,11 +76,11 @@ cudaError_t encode_codes(Weights4Desc& d) {
     return (PFN_cuTensorMapEncodeTiled_v12000) nullptr;
   }();
   if (fn == nullptr) return cudaErrorNotSupported;
-  cuuint64_t dims[2] = {(cuuint64_t)d.Kp, (cuuint64_t)d.N};
-  cuuint64_t strides[1] = {(cuuint64_t)d.Kp / 2};
-  cuuint32_t box[2] = {128, 128};
-  cuuint32_t es[2] = {1, 1};
-  return fn(&d.tm, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, d.codes, dims, strides, box, es,
+  cuuint64_t dims[3] = {128, 128, (cuuint64_t)((d.N + 127) / 128) * (d.Kp / 128)};
+  cuuint64_t strides[2] = {64, kTileBytes};
+  cuuint32_t box[3] = {128, 128, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(&d.tm, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, d.store, dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
@@ -127,7 +128,7 @@ int run_linear4(const char* name, const Weights4Desc& w, const Weights4Desc* up,
 extern "C" {
 
 size_t dspark_weights4_bytes(int N, int K) {
-  return shape_ok(N, K) ? codes_bytes(N, K) + scales_bytes(N, K) : 0;
+  return shape_ok(N, K) ? weights4_bytes(N, K) : 0;
 }
 
 int dspark_weights4_init(dspark_weights4* w, int N, int K, void* store) {
@@ -142,8 +143,7 @@ int dspark_weights4_init(dspark_weights4* w, int N, int K, void* store) {
   d.N = N;
   d.K = K;
   d.Kp = padded_k(K);
-  d.codes = static_cast<uint8_t*>(store);
-  d.scales = d.codes + codes_bytes(N, K);
+  d.store = static_cast<uint8_t*>(store);
   const cudaError_t e = encode_codes(d);
   if (e != cudaSuccess) return cuda_fail(e, "dspark_weights4_init");
   d.magic = kWeights4Magic;

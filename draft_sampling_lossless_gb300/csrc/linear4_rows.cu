@@ -72,7 +72,7 @@ __device__ __forceinline__ void group_sync(int group, int threads) {
 }
 
 struct Params {
-  const uint8_t *cw, *sw, *cu, *su;
+  const uint8_t *w, *u;  // the matrices' tiles
   int N, T, K, Kp, KB, tiles, splits, act;
   const __nv_bfloat16* x;
   int64_t x_stride;
@@ -105,13 +105,12 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Params p) {
 
   Slot ring[DEPTH][MATS];
   int at_tile = first, left = steps, loaded = 0;  // what is loaded next
-  int64_t c0 = 0, c1 = 0, sc = 0;
-  auto place = [&]() {  // rows past N take the last one's codes: their sums are not stored
-    const int n0 = min(row_of(at_tile, g), p.N - 1), n1 = min(row_of(at_tile, g + 8), p.N - 1);
-    c0 = (int64_t)n0 * (p.Kp >> 1) + k0 * 64 + t * 16;
-    c1 = c0 + (int64_t)(n1 - n0) * (p.Kp >> 1);
-    sc = ((int64_t)(at_tile >> 3) * p.KB + k0) * 512 + (at_tile & 7) * 64 + (g & 3) * 16 +
-         (g >> 2) * 4 + t;
+  // the codes of rows g and g + 8 (64 rows on in the tile), their scales
+  const int local = (g >> 2) * 32 + (g & 3), c_lane = local * 64 + t * 16;
+  const int s_lane = kTileCodes + (g & 3) * 16 + (g >> 2) * 4 + t;
+  int64_t at_c = 0;
+  auto place = [&]() {  // (rows past N have zero codes)
+    at_c = ((int64_t)(at_tile >> 3) * p.KB + k0) * kTileBytes;
   };
   if (items > 0) place();
   auto load = [&](Slot (&s)[MATS]) {
@@ -119,14 +118,15 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const Params p) {
     ++loaded;
 #pragma unroll
     for (int m = 0; m < MATS; ++m) {
-      s[m].c0 = load_codes((m ? p.cu : p.cw) + c0);
-      s[m].c1 = load_codes((m ? p.cu : p.cw) + c1);
-      s[m].s0 = __ldg((m ? p.su : p.sw) + sc);
-      s[m].s1 = __ldg((m ? p.su : p.sw) + sc + 8);
+      const uint8_t* tile = (m ? p.u : p.w) + at_c;
+      const uint8_t* c = tile + (at_tile & 7) * 256 + c_lane;
+      const uint8_t* sc = tile + (at_tile & 7) * 64 + s_lane;
+      s[m].c0 = load_codes(c);
+      s[m].c1 = load_codes(c + 4096);
+      s[m].s0 = __ldg(sc);
+      s[m].s1 = __ldg(sc + 8);
     }
-    c0 += 64;
-    c1 += 64;
-    sc += 512;
+    at_c += kTileBytes;
     if (--left == 0) {
       left = steps;
       at_tile += stride;
@@ -269,10 +269,8 @@ template <int MATS, int NT, int DEPTH>
 cudaError_t launch(const Linear4Args& a, cudaStream_t st) {
   auto kernel = rows_kernel<MATS, NT, DEPTH>;
   Params p;
-  p.cw = a.w->codes;
-  p.sw = a.w->scales;
-  p.cu = a.up ? a.up->codes : nullptr;
-  p.su = a.up ? a.up->scales : nullptr;
+  p.w = a.w->store;
+  p.u = a.up ? a.up->store : nullptr;
   p.N = a.w->N;
   p.T = a.T;
   p.K = a.w->K;

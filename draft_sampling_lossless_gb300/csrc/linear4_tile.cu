@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32)
 // ---------------------------------------------------------------- the product
 
 struct Params {
-  const uint8_t *sw, *su;  // scales of the matrices
+  const uint8_t *w, *u;    // the matrices' tiles
   const uint8_t* xq;       // tiles of x, or null: the blocks make their own
   const __nv_bfloat16* x;
   int64_t x_stride;
@@ -386,11 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int m = 0; m < MATS; ++m) {
           const int row = GATED || MATS == 1 ? ft : ft * 2 + m;  // in blocks of 128
-          tma_load_2d(dst + m * 16384, GATED && m ? &tm_u : &tm_w, bar, kb * 128, row * 128);
+          tma_load_3d(dst + m * 16384, GATED && m ? &tm_u : &tm_w, bar, 0, 0, row * p.KB + kb);
           // (the second tile of an odd number reads zeros, with the last tile's scales)
           const int in = GATED || MATS == 1 ? row : min(row, p.row_blocks - 1);
           bulk_load(dst + MATS * 16384 + x_bytes + m * 512,
-                    (GATED && m ? p.su : p.sw) + ((size_t)in * p.KB + kb) * 512, 512, bar);
+                    (GATED && m ? p.u : p.w) + ((size_t)in * p.KB + kb) * kTileBytes + kTileCodes,
+                    512, bar);
         }
       };
       auto load_x = [&](uint32_t bar, uint32_t dst, int kb) {
@@ -810,8 +811,8 @@ template <int MATS, bool GATED>
 cudaError_t launch(const Linear4Args& a, const Cut& cut, cudaStream_t st) {
   auto kernel = tile_kernel<MATS, GATED>;
   Params p;
-  p.sw = a.w->scales;
-  p.su = a.up ? a.up->scales : nullptr;
+  p.w = a.w->store;
+  p.u = a.up ? a.up->store : nullptr;
   p.xq = cut.own ? nullptr : static_cast<const uint8_t*>(a.ws) + kStatusBytes;
   p.x = a.x;
   p.x_stride = a.x_stride;

@@ -21,13 +21,15 @@ __global__ void __launch_bounds__(kThreads)
   const int g = (int)(i - n * groups);
   if (n >= (d.N + 127) / 128 * 128) return;
   const bool in = n < d.N && g < used;
-  if (n < d.N) {
-    uint4 c = make_uint4(0, 0, 0, 0);
-    if (in) c = __ldg(reinterpret_cast<const uint4*>(codes) + n * used + g);
-    reinterpret_cast<uint4*>(d.codes)[n * groups + g] = c;
+  uint4 c = make_uint4(0, 0, 0, 0);
+  int b = 127;
+  if (in) {
+    c = __ldg(reinterpret_cast<const uint4*>(codes) + n * used + g);
+    b = __ldg(scales + n * used + g);
   }
-  const int b = in ? __ldg(scales + n * used + g) : 127;
-  d.scales[scale_at((int)n, g, d.Kp)] = (uint8_t)min(max(b, 1), 252);
+  uint8_t* tile = d.store + tile_at((int)n, g, d.Kp);
+  *reinterpret_cast<uint4*>(tile + code_in_tile((int)n, g)) = c;
+  tile[scale_in_tile((int)n, g)] = (uint8_t)min(max(b, 1), 252);
 }
 
 __device__ __forceinline__ float finite_abs(float v) {
@@ -77,8 +79,9 @@ __global__ void __launch_bounds__(kThreads)
       : "=r"(c)
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   if (n >= (d.N + 127) / 128 * 128) return;
-  if (n < d.N) reinterpret_cast<uint32_t*>(d.codes)[(n * groups + g) * 4 + q] = in ? c : 0u;
-  if (q == 0) d.scales[scale_at((int)n, g, d.Kp)] = (uint8_t)(in ? e + 127 : 127);
+  uint8_t* tile = d.store + tile_at((int)n, g, d.Kp);
+  *reinterpret_cast<uint32_t*>(tile + code_in_tile((int)n, g) + q * 4) = in ? c : 0u;
+  if (q == 0) tile[scale_in_tile((int)n, g)] = (uint8_t)(in ? e + 127 : 127);
 }
 
 int64_t blocks_for(const Weights4Desc& d, int lanes) {

@@ -145,11 +145,7 @@ def test_quantize_and_load_agree_with_a_search():
         code = code + 8 * torch.signbit(w).long().view(N, K)
         ref = Matrix(N, K, codes=code, scales=(e + 127).to(torch.uint8))
         a, b = ref.load(), layer.Weights4.quantize(w.to(DEV))
-        used = B.weights4_bytes(N, K)
-        codes_end = N * (-(-K // 128) * 64)
-        assert torch.equal(a.store[:codes_end], b.store[:codes_end]), (N, K)
-        s0 = (codes_end + 511) // 512 * 512
-        assert torch.equal(a.store[s0:used], b.store[s0:used]), (N, K)
+        assert torch.equal(a.store, b.store), (N, K)
 
 
 def test_quantize_takes_what_is_not_finite():

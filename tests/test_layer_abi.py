@@ -11,9 +11,9 @@ WS = 1 << 30
 
 
 def test_store_sizes(lib):
-    # codes in rows padded to 128 columns, rounded up to 512; scales of 128 x 128 blocks
-    assert lib.weights4_bytes(1, 32) == 512 + 512
-    assert lib.weights4_bytes(129, 2560) == 129 * 1280 + 2 * 20 * 512 + (-129 * 1280) % 512
+    # tiles of 128 x 128: 64 bytes of codes a row, 512 bytes of scales
+    assert lib.weights4_bytes(1, 32) == 128 * 64 + 512
+    assert lib.weights4_bytes(129, 2560) == 2 * 20 * (128 * 64 + 512)
     for N, K in ((0, 32), (-1, 32), (1, 0), (1, 16), (1, 33), (1, 1 << 17), ((1 << 24) + 1, 32)):
         assert lib.weights4_bytes(N, K) == 0, (N, K)
 
@@ -81,7 +81,7 @@ def test_the_python_calls_refuse_host_tensors_and_wrong_types(lib):
     with pytest.raises(ValueError, match="CUDA"):
         lib.dspark_norm(x, None, None, None, 1.0, torch.ones(64), 1e-6, None, x.clone(), stream=0)
     with pytest.raises(ValueError, match="CUDA"):
-        lib.weights4_init(8, 64, torch.zeros(4096, dtype=torch.uint8))
+        lib.weights4_init(8, 64, torch.zeros(16384, dtype=torch.uint8))
     with pytest.raises(ValueError, match="store"):
         lib.weights4_init(8, 64, torch.zeros(16, dtype=torch.uint8))
     for bad in (x.float(), x[:, :32], x[0], x.T.contiguous().T):
