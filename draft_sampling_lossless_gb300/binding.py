@@ -540,11 +540,19 @@ def _stream_on(at, stream):
     return torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream
 
 
+# The calls of a layer are a few microseconds each on the GPU, and so is a call's marshalling:
+# below, one test a tensor lets the usual ones pass, and _matrix says what is wrong with another.
+
+_BF16 = torch.bfloat16
+
+
 def _products(x, out, ws, N, K, stream, devices):
     """What the two products' calls take of their tensors."""
     T, at = x.shape[0], x.get_device()
-    xp, xs = _matrix(x, (T, K), torch.bfloat16, at, "x")
-    op, os_ = _matrix(out, (T, N), torch.bfloat16, at, "out")
+    if x.dtype is not _BF16 or x.shape != (T, K) or at < 0:
+        _matrix(x, (T, K), _BF16, at, "x")
+    if out.dtype is not _BF16 or out.shape != (T, N) or out.get_device() != at:
+        _matrix(out, (T, N), _BF16, at, "out")
     if ws.get_device() != at:
         raise _elsewhere(ws, at)
     for d in devices:
@@ -552,44 +560,74 @@ def _products(x, out, ws, N, K, stream, devices):
             raise ValueError(f"the weights are on device {d}, x is on {at}")
     if not ws.is_contiguous():
         raise ValueError("the workspace must be contiguous")
-    return T, xp, xs, op, os_, ws.data_ptr(), ws.nbytes, _stream_on(at, stream)
+    xs, x1 = x.stride()
+    os_, o1 = out.stride()
+    if x1 != 1 or (o1 != 1 and N > 1):
+        raise ValueError("the columns of x and out must be contiguous")
+    if T == 1:
+        xs, os_ = K, N
+    return (T, x.data_ptr(), xs, out.data_ptr(), os_, ws.data_ptr(), ws.nbytes,
+            _stream_on(at, stream))
 
 
 def dspark_linear4(w, N, K, x, out, ws, stream=None, devices=()):
     """devices: that of the weights' store."""
-    _check("dspark_linear4",
-           lib().dspark_linear4(w, *_products(x, out, ws, N, K, stream, devices)))
+    code = lib().dspark_linear4(w, *_products(x, out, ws, N, K, stream, devices))
+    if code:
+        _check("dspark_linear4", code)
 
 
 def dspark_gated4(gate, up, N, K, act, x, out, ws, stream=None, devices=()):
     """devices: those of the weights' stores."""
-    _check("dspark_gated4",
-           lib().dspark_gated4(gate, up, act, *_products(x, out, ws, N, K, stream, devices)))
+    code = lib().dspark_gated4(gate, up, act, *_products(x, out, ws, N, K, stream, devices))
+    if code:
+        _check("dspark_gated4", code)
 
 
 def dspark_norm(x, y, post, gate, alpha, pre, eps, x_out, h, stream=None):
-    shape, dt, at, bf16 = x.shape, _dt(x), x.get_device(), torch.bfloat16
+    shape, xt, at = x.shape, x.dtype, x.get_device()
+    dt = DSPARK_BF16 if xt is _BF16 else _dt(x)
     if len(shape) != 2:
         raise ValueError(f"x must be a matrix [T, d], got {list(shape)}")
+    if at < 0:
+        raise _elsewhere(x, at)
     T, d = shape
-    xp, xs = _matrix(x, shape, x.dtype, at, "x")
+    xs, c = x.stride()
     yp = gp = op = hp = postp = prep = None
     ys = gs = os_ = hs = 0
+    c1 = c2 = c3 = c4 = 1  # the columns' strides
     if y is not None:
-        yp, ys = _matrix(y, shape, bf16, at, "y")
+        if y.dtype is not _BF16 or y.shape != shape or y.get_device() != at:
+            _matrix(y, shape, _BF16, at, "y")
+        ys, c1 = y.stride()
+        yp = y.data_ptr()
     if gate is not None:
-        if T > 1 and gate.shape == shape:
-            gp, gs = _matrix(gate, shape, bf16, at, "gate")
-        else:  # one row for all
-            gp, _ = _matrix(gate, (1, d), bf16, at, "gate")
+        if gate.dtype is not _BF16 or gate.get_device() != at or (
+                gate.shape != shape and gate.shape != (1, d)):
+            _matrix(gate, shape, _BF16, at, "gate")
+        gs, c2 = gate.stride()
+        gp = gate.data_ptr()
+        if T == 1 or gate.shape[0] == 1:
+            gs = 0  # one row for all
+    if x_out is not None:
+        if x_out.dtype is not xt or x_out.shape != shape or x_out.get_device() != at:
+            _matrix(x_out, shape, xt, at, "x_out")
+        os_, c3 = x_out.stride()
+        op = x_out.data_ptr()
+    if h is not None:
+        if h.dtype is not _BF16 or h.shape != shape or h.get_device() != at:
+            _matrix(h, shape, _BF16, at, "h")
+        hs, c4 = h.stride()
+        hp = h.data_ptr()
+    if not c == c1 == c2 == c3 == c4 == 1 and d > 1:
+        raise ValueError("the columns of the matrices must be contiguous")
     if post is not None:
         postp = _vector(post, d, at, "post")
     if pre is not None:
-        prep = _vector(pre, d, at, "pre")
-    if x_out is not None:
-        op, os_ = _matrix(x_out, shape, x.dtype, at, "x_out")
-    if h is not None:
-        hp, hs = _matrix(h, shape, bf16, at, "h")
-    _check("dspark_norm", lib().dspark_norm(
-        T, d, dt, xp, xs, yp, ys, postp, gp, gs, alpha, prep, eps, op, os_, hp, hs,
-        _stream_on(at, stream)))
+        prep = postp if pre is post else _vector(pre, d, at, "pre")
+    if T == 1:
+        xs = ys = os_ = hs = d
+    code = lib().dspark_norm(T, d, dt, x.data_ptr(), xs, yp, ys, postp, gp, gs, alpha, prep, eps,
+                             op, os_, hp, hs, _stream_on(at, stream))
+    if code:
+        _check("dspark_norm", code)
