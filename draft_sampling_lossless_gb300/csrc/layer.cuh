@@ -57,7 +57,7 @@ cudaError_t launch_weights4_quantize(const Weights4Desc& d, const void* src, int
 
 struct NormArgs {
   int T, d, dt;
-  float alpha, eps;
+  float alpha, eps, inv_d;
   const void* x;
   int64_t x_stride;
   const __nv_bfloat16 *y, *gate;

@@ -248,6 +248,7 @@ int dspark_norm(int T, int d, int dt, const void* x, int64_t x_stride, const voi
   a.dt = dt;
   a.alpha = alpha;
   a.eps = eps;
+  a.inv_d = 1.f / (float)d;
   a.x = x;
   a.x_stride = x_stride;
   a.y = static_cast<const __nv_bfloat16*>(y);

@@ -20,8 +20,8 @@
 // the same 62 cycles, on as many SMs as there are tiles; with a large vocabulary HBM.  Measured
 // among calls in a graph: 4100 rows gated by 2 x 10240 x 2560 235 us, 1.83 PFLOP/s (95% of
 // cuBLAS's measured bf16 rate), tensor pipe 76% busy at 2100 rows; 4100 rows by 6144 x 2560 83
-// us, 1.55 PFLOP/s, 10 of them the first kernel; 64 rows by 151936 x 2560 46.7 us, 4.8 TB/s; 122
-// rows by 2560 x 4096 10.6 us, gated by 2 x 10240 x 2560 19.5 us (80 tiles on 152 SMs, or 240 in
+// us, 1.55 PFLOP/s, 10 of them the first kernel; 64 rows by 151936 x 2560 47.2 us, 4.8 TB/s; 122
+// rows by 2560 x 4096 10.7 us, gated by 2 x 10240 x 2560 18.8 us (80 tiles on 152 SMs, or 240 in
 // two rounds); one row gated by the same 10.3 us.
 #include "linear4.cuh"
 #include "sm100.cuh"

@@ -8,7 +8,7 @@
 // issued together.  h comes from x' before its rounding, so that each output is rounded once.
 //
 // Measured: 16000 rows of 2560, fp32 stream, norms on both sides and one gate 72.2 us, 6.8
-// TB/s (100% of the measured copy rate); 16000 of 7168, bf16 stream, a gate a row 191 us, 6.0
+// TB/s (100% of the measured copy rate); 16000 of 7168, bf16 stream, a gate a row 190 us, 6.0
 // TB/s; 300 of those 4.3 us; one row of 2560 1.9 us, latency (among calls in a graph).
 #include "dspark.h"
 #include "layer.cuh"
@@ -69,11 +69,29 @@ __device__ __forceinline__ float row_sum(float v, float* sh) {
   return warp_sum(lane < (int)(blockDim.x >> 5) ? sh[lane] : 0.f);
 }
 
+// 1 / sqrt(mean + eps) of a row from its values' sum of squares.  Where that left fp32's range
+// (values past 2^56 or so; where eps leaves it to them, below 2^-48) it is taken again of the
+// values times a power of two; each(f) calls f for each of this thread's values.
+template <class Each>
+__device__ __forceinline__ float row_factor(float sum, float inv_d, float eps, float* sh,
+                                            Each&& each) {
+  if (sum <= 0x1p112f && (sum >= 0x1p-96f || eps >= 0x1p-80f))  // (the same in every thread)
+    return __frsqrt_rn(fmaf(sum, inv_d, eps));
+  const float s = sum < 1.f ? 0x1p64f : 0x1p-75f;
+  float again = 0.f;
+  each([&](float v) {
+    v *= s;
+    again = fmaf(v, v, again);
+  });
+  return s * __frsqrt_rn(fmaf(row_sum(again, sh), inv_d, eps * s * s));
+}
+
 // A block a row, V pieces of eight values a thread.  All of a row's loads are issued before
-// the first sum.
+// the first sum.  (Up to 1024 threads with one piece, 512 with more; with two, 56 registers
+// leave room for seven blocks of rows of 2560.)
 template <typename T, int V>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 512) norm_kernel(const NormArgs a) {
-  __shared__ float sh[2][32];
+__global__ void __maxnreg__(V == 1 ? 64 : V == 2 ? 56 : 128) norm_kernel(const NormArgs a) {
+  __shared__ float sh[2][64];
   grid_dependency_wait();
   const int64_t t = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
@@ -113,7 +131,16 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512) norm_kernel(const NormArg
 #pragma unroll
           for (int j = 0; j < 8; ++j) sum = fmaf(u[j], u[j], sum);
         }
-      r *= 1.f / sqrtf(row_sum(sum, sh[0]) / a.d + a.eps);
+      r *= row_factor(row_sum(sum, sh[0]), a.inv_d, a.eps, sh[0] + 32, [&](auto&& f) {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (i0 + k * step < a.d) {
+            float u[8];
+            ry[k].get(u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f(u[j]);
+          }
+      });
     }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -145,7 +172,12 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512) norm_kernel(const NormArg
   for (int k = 0; k < V; ++k)
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = fmaf(v[k][j], v[k][j], sum);
-  const float r = 1.f / sqrtf(row_sum(sum, sh[1]) / a.d + a.eps);
+  const float r = row_factor(row_sum(sum, sh[1]), a.inv_d, a.eps, sh[1] + 32, [&](auto&& f) {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f(v[k][j]);
+  });
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int i = i0 + k * step;

@@ -683,3 +683,30 @@ def test_weights_written_just_before_they_are_used():
             layer.linear4(x, q, o, ws)
         check_linear(x, a, outs[0])
         check_linear(x, b, outs[1])
+
+
+@pytest.mark.parametrize("d", (64, 2560, 12000))
+@pytest.mark.parametrize("size,eps", ((2.0 ** 100, 1e-6), (2.0 ** 126, 1e-6), (2.0 ** 66, 0.0),
+                                      (2.0 ** -70, 0.0), (2.0 ** -120, 0.0), (2.0 ** -20, 0.0),
+                                      (2.0 ** -70, 1e-6)))
+def test_norm_of_far_values(d, size, eps):
+    """Rows whose squares leave fp32's range are normed like others (as in test_norm_sizes: the
+    sum, a root, a quotient and products in fp32, bf16's rounding)."""
+    for T in (3, 200):
+        g = torch.Generator().manual_seed(d + T)
+        x = (torch.rand(T, d, generator=g) + 0.5).mul(size).to(DEV)
+        x[1] = torch.rand(d, generator=g).to(DEV)  # an ordinary row among them
+        pre = (1 + 0.3 * torch.randn(d, generator=g)).to(DEV)
+        h = torch.empty(T, d, dtype=torch.bfloat16, device=DEV)
+        layer.norm(x, h, pre, eps=eps)
+        _, want = norm64(x, None, None, None, 1.0, pre, eps)
+        rel = 8 * 2.0 ** -24 + (d / 8 + 16) * 2.0 ** -24 + 2.0 ** -8
+        assert ((h.double() - want).abs() <= rel * want.abs() + 1e-38).all()
+        y = x.bfloat16()  # the block's own norm brings its output back to ordinary sizes
+        s = torch.ones(T, d, device=DEV)
+        xo = torch.empty_like(s)
+        layer.norm(s, h, pre, y=y, x_out=xo, post=pre, eps=eps)
+        want_x, _ = norm64(s, y, pre, None, 1.0, None, eps)
+        err = (want_x - 1).abs() * (16 * 2.0 ** -24 + (d / 8 + 16) * 2.0 ** -24) + 2.0 ** -23 * (
+            want_x.abs() + 1)
+        assert ((xo.double() - want_x).abs() <= err).all()
