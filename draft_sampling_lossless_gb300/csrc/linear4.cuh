@@ -30,7 +30,7 @@ size_t linear4_tile_workspace_bytes(int T, int K);
 cudaError_t linear4_tile_cut(const Linear4Args& a, TileCut* cut);
 cudaError_t launch_linear4_tile(const Linear4Args& a, const TileCut& cut, cudaStream_t st);
 
-// The kernel of a few rows (linear4_rows.cu): up to 64, as many as fit in shared memory.
+// The kernel of a few rows (linear4_rows.cu): up to 32, as many as fit in shared memory.
 bool linear4_rows_fits(int T, int Kp);
 int64_t linear4_rows_cycles(const Linear4Args& a);
 cudaError_t launch_linear4_rows(const Linear4Args& a, cudaStream_t st);
