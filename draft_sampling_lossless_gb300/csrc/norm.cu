@@ -8,8 +8,10 @@
 // issued together.  h comes from x' before its rounding, so that each output is rounded once.
 //
 // Measured: 16000 rows of 2560, fp32 stream, norms on both sides and one gate 72.2 us, 6.8
-// TB/s (100% of the measured copy rate); 16000 of 7168, bf16 stream, a gate a row 190 us, 6.0
+// TB/s (100% of the measured copy rate); 16000 of 7168, bf16 stream, a gate a row 191 us, 6.0
 // TB/s; 300 of those 4.3 us; one row of 2560 1.9 us, latency (among calls in a graph).
+#include <type_traits>
+
 #include "dspark.h"
 #include "layer.cuh"
 
@@ -69,21 +71,26 @@ __device__ __forceinline__ float row_sum(float v, float* sh) {
   return warp_sum(lane < (int)(blockDim.x >> 5) ? sh[lane] : 0.f);
 }
 
-// 1 / sqrt(mean + eps) of a row from its values' sum of squares.  Where that left fp32's range
-// (values past 2^56 or so; where eps leaves it to them, below 2^-48) it is taken again of the
-// values times a power of two; each(f) calls f for each of this thread's values.
+// rms(v) = (v * s) * q, from the sum of a row's squares.  Where that left fp32's range (values
+// past 2^56 or so; where eps leaves it to them, below 2^-48) it is taken again of the values
+// times s, a power of two; else s is 1.  Two factors, since their product may be past 2^128 (a
+// row of subnormals); 2^100 times the largest of the small rows still has its square in range, and
+// so has 2^100 times the smallest subnormal.  each(f) calls f for each of this thread's values.
+struct Factor {
+  float s, q;
+};
 template <class Each>
-__device__ __forceinline__ float row_factor(float sum, float inv_d, float eps, float* sh,
-                                            Each&& each) {
+__device__ __forceinline__ Factor row_factor(float sum, float inv_d, float eps, float* sh,
+                                             Each&& each) {
   if (sum <= 0x1p112f && (sum >= 0x1p-96f || eps >= 0x1p-80f))  // (the same in every thread)
-    return __frsqrt_rn(fmaf(sum, inv_d, eps));
-  const float s = sum < 1.f ? 0x1p64f : 0x1p-75f;
+    return {1.f, __frsqrt_rn(fmaf(sum, inv_d, eps))};
+  const float s = sum < 1.f ? 0x1p100f : 0x1p-75f;
   float again = 0.f;
   each([&](float v) {
     v *= s;
     again = fmaf(v, v, again);
   });
-  return s * __frsqrt_rn(fmaf(row_sum(again, sh), inv_d, eps * s * s));
+  return {s, __frsqrt_rn(fmaf(row_sum(again, sh), inv_d, eps * s * s))};
 }
 
 // A block a row, V pieces of eight values a thread.  All of a row's loads are issued before
@@ -120,7 +127,7 @@ __global__ void __maxnreg__(V == 1 ? 64 : V == 2 ? 56 : 128) norm_kernel(const N
     }
   }
   if (y != nullptr) {
-    float r = a.alpha;
+    Factor r = {1.f, 1.f};
     if (a.post != nullptr) {
       float sum = 0.f;
 #pragma unroll
@@ -131,7 +138,7 @@ __global__ void __maxnreg__(V == 1 ? 64 : V == 2 ? 56 : 128) norm_kernel(const N
 #pragma unroll
           for (int j = 0; j < 8; ++j) sum = fmaf(u[j], u[j], sum);
         }
-      r *= row_factor(row_sum(sum, sh[0]), a.inv_d, a.eps, sh[0] + 32, [&](auto&& f) {
+      r = row_factor(row_sum(sum, sh[0]), a.inv_d, a.eps, sh[0] + 32, [&](auto&& f) {
 #pragma unroll
         for (int k = 0; k < V; ++k)
           if (i0 + k * step < a.d) {
@@ -142,29 +149,35 @@ __global__ void __maxnreg__(V == 1 ? 64 : V == 2 ? 56 : 128) norm_kernel(const N
           }
       });
     }
+    // In the formula's order, so that what it has in range stays there: y normed before post,
+    // alpha by the gate before either meets u.
+    auto add = [&](auto scaled) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int i = i0 + k * step;
-      if (i < a.d) {
-        float u[8], g[8];
-        ry[k].get(u);
-        if (a.post != nullptr) {
-          Raw8<float> w;
-          w.load(a.post + i);
-          w.get(g);
+      for (int k = 0; k < V; ++k) {
+        const int i = i0 + k * step;
+        if (i < a.d) {
+          float u[8], g[8];
+          ry[k].get(u);
+          if (a.post != nullptr) {
+            Raw8<float> w;
+            w.load(a.post + i);
+            w.get(g);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) u[j] *= g[j];
+            for (int j = 0; j < 8; ++j) u[j] = (scaled ? u[j] * r.s : u[j]) * r.q * g[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] = 1.f;
+          if (gate != nullptr) rg[k].get(g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[k][j] = fmaf(a.alpha * g[j], u[j], v[k][j]);
+          if (a.x_out != nullptr) store8(static_cast<T*>(a.x_out) + t * a.x_out_stride + i, v[k]);
         }
-        if (gate != nullptr) {
-          rg[k].get(g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u[j] *= g[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] = fmaf(r, u[j], v[k][j]);
-        if (a.x_out != nullptr) store8(static_cast<T*>(a.x_out) + t * a.x_out_stride + i, v[k]);
       }
-    }
+    };
+    // (A second copy of the loop saves a product: 2000 rows of 2560 7.45 us for 7.6.  With eight
+    // pieces it costs registers: 1000 rows of 32768, fp32 stream, 107 us for 103, bf16 77.6 for 78.3.)
+    if (V < 8 && r.s == 1.f) add(std::false_type());
+    else add(std::true_type());
   }
   if (a.h == nullptr) return;
   float sum = 0.f;
@@ -172,7 +185,7 @@ __global__ void __maxnreg__(V == 1 ? 64 : V == 2 ? 56 : 128) norm_kernel(const N
   for (int k = 0; k < V; ++k)
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = fmaf(v[k][j], v[k][j], sum);
-  const float r = row_factor(row_sum(sum, sh[1]), a.inv_d, a.eps, sh[1] + 32, [&](auto&& f) {
+  const Factor r = row_factor(row_sum(sum, sh[1]), a.inv_d, a.eps, sh[1] + 32, [&](auto&& f) {
 #pragma unroll
     for (int k = 0; k < V; ++k)
 #pragma unroll
@@ -187,7 +200,7 @@ __global__ void __maxnreg__(V == 1 ? 64 : V == 2 ? 56 : 128) norm_kernel(const N
       w.load(a.pre + i);
       w.get(g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * r * g[j];
+      for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * r.s * r.q * g[j];
       store8(a.h + t * a.h_stride + i, v[k]);
     }
   }

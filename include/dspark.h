@@ -655,8 +655,9 @@ int dspark_gated4(const dspark_weights4* gate, const dspark_weights4* up, int ac
  * and x_out must be there.  Rows are *_stride elements apart (multiples of 8, at
  * least d), all pointers 16-byte aligned; d a multiple of 8, 8 <= d <= 32768.
  * x_out may be x, and h may be y, with the same strides; no other outputs may overlap
- * inputs.  Sums are fp32, taken again with a power of two where the squares leave its range.  A
- * NaN or an infinity stays in its row.
+ * inputs.  Sums are fp32, taken again with a power of two where the squares leave its range;
+ * products are fp32 in the formulas' order: rms(y), times post; alpha * gate, times that.  A NaN
+ * or an infinity stays in its row.
  */
 int dspark_norm(int T, int d, int dt, const void* x, int64_t x_stride, const void* y,
                 int64_t y_stride, const float* post, const void* gate, int64_t gate_stride,
