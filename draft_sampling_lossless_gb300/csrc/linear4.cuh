@@ -7,14 +7,20 @@
 
 namespace dspark {
 
-// silu(a) = a s(a); gelu's tanh form, 0.5 a (1 + tanh y) = a s(2 y), with s(v) = 1 / (1 +
-// exp(-v)).  ex2.approx and the quick division are off by 2^-21 or so (2^-24 |v| in the exponent
-// on top), far below the result's rounding.  exp(-v) past 2^126 gives 0.
+// silu(a) = a s(a); gelu's tanh form, 0.5 a (1 + tanh y) = a s(2 y), with s(v) = g / (g + 1 / g),
+// g = exp(v / 2): v / 2, so that s is right down to the subnormals, where silu(-88) lies (times a
+// large second factor an ordinary number; 1 / (1 + exp(-v)) ends at exp(-v) = 2^126, for
+// 18.9 us instead of 19.0 with 122 rows gated by 2 x 10240 x 2560).  Above 2 ln 2^120 s is 1.
+// ex2.approx and rcp.approx are off by 2^-21 or so together (2^-24 |v| in the exponent on top),
+// far below the result's rounding.  A NaN stays one by the factor a.
 __device__ __forceinline__ float activation(int act, float a) {
   float v = a;
   if (act != DSPARK_ACT_SILU) v = 1.5957691216057308f * fmaf(0.044715f * a * a, a, a);
-  const float d = 1.f + sm100::ex2_approx(-1.4426950408889634f * v);
-  return __fdividef(a, d);
+  const float t = fminf(0.72134752044448170f * v, 120.f);
+  const float g = sm100::ex2_approx(t);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(g + sm100::ex2_approx(-t)));
+  return a * (g * r);
 }
 
 // The kernel on the tensor cores (linear4_tile.cu), and how it cuts a product.

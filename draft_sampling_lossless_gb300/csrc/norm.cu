@@ -175,7 +175,7 @@ __global__ void __maxnreg__(V == 1 ? 64 : V == 2 ? 56 : 128) norm_kernel(const N
       }
     };
     // (A second copy of the loop saves a product: 2000 rows of 2560 7.45 us for 7.6.  With eight
-    // pieces it costs registers: 1000 rows of 32768, fp32 stream, 107 us for 103, bf16 77.6 for 78.3.)
+    // pieces it costs registers: 1000 rows of 32768, fp32 stream, 107 us for 103, bf16 78 us both.)
     if (V < 8 && r.s == 1.f) add(std::false_type());
     else add(std::true_type());
   }

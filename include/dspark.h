@@ -632,7 +632,8 @@ int dspark_linear4(const dspark_weights4* w, int T, const void* x, int64_t x_str
  *   gate, up   two matrices of one shape [N][K]
  *   act        DSPARK_ACT_SILU: a / (1 + exp(-a));  DSPARK_ACT_GELU:
  *              0.5 a (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3)))
- *   the rest as in dspark_linear4; neither product is rounded before act
+ *   the rest as in dspark_linear4; neither product is rounded before act; act is
+ *   fp32 down to the smallest subnormals
  */
 int dspark_gated4(const dspark_weights4* gate, const dspark_weights4* up, int act, int T,
                   const void* x, int64_t x_stride, void* out, int64_t out_stride, void* ws,
