@@ -216,8 +216,10 @@ class Decoder:
             raise RuntimeError(f"device status {a.status(ws):#x}")
 
     def check(self):
-        words = [self.step_.status(), self.t.status()]
-        for word in words + [self.caches[0].status(w) for w in self.ws.values()]:
+        words = [self.step_.status()] + [self.caches[0].status(w) for w in self.ws.values()]
+        if hasattr(self.t, "status"):  # (a target needs none)
+            words.append(self.t.status())
+        for word in words:
             if word != 0:
                 raise RuntimeError(f"device status {word:#x}")
 
