@@ -88,34 +88,43 @@ class Target4(Target):
         self.down4 = [w(d, F, 0.7 / math.sqrt(F)) for _ in range(layers)]
         self.unemb4 = layer.Weights4.quantize(self.unemb)
         self.ones = torch.ones(d, device=device)
-        self.ws = None
+        self.rows, self.ws = 0, []  # workspaces, the last one for up to so many rows
 
     def forward(self, tokens, attention):
         T, dev = len(tokens), self.emb.device
         widest = max(self.d, self.Hq * self.D, self.F)
-        if self.ws is None or self.ws.numel() < layer.workspace_bytes(T, widest):
-            self.ws = layer.workspace(T, widest, dev)
+        if not self.ws or self.rows < T:
+            # the smaller ones stay: their status words are read later, a captured pass may use
+            # them; each at least twice the last, so that they add up to no more than the last
+            self.rows = max(T, min(2 * self.rows, 1 << 24))
+            self.ws.append(layer.workspace(self.rows, widest, dev))
+        ws = self.ws[-1]
 
         def rows(n):
             return torch.empty((T, n), dtype=torch.bfloat16, device=dev)
 
         x, h, y = self.emb[tokens], rows(self.d), rows(self.d)
+        heads = self.Hq + 2 * self.Hkv
         layer.norm(x, h, self.ones)
         for i, (gate, up, down) in enumerate(zip(self.gate4, self.up4, self.down4)):
-            qkv, m = rows((self.Hq + 2 * self.Hkv) * self.D), rows(self.F)
-            layer.linear4(h, self.qkv4[i], qkv, self.ws)
-            o = attention(i, *qkv.view(T, -1, self.D).split([self.Hq, self.Hkv, self.Hkv], dim=1))
-            layer.linear4(o.reshape(T, -1), self.wo4[i], y, self.ws)
+            qkv, m = rows(heads * self.D), rows(self.F)
+            layer.linear4(h, self.qkv4[i], qkv, ws)
+            qkv = qkv.view(T, heads, self.D).split([self.Hq, self.Hkv, self.Hkv], dim=1)
+            o = attention(i, *qkv).reshape(T, self.Hq * self.D)
+            layer.linear4(o, self.wo4[i], y, ws)
             layer.norm(x, h, self.ones, y=y, x_out=x)
-            layer.gated4(h, gate, up, m, self.ws)
-            layer.linear4(m, down, y, self.ws)
+            layer.gated4(h, gate, up, m, ws)
+            layer.linear4(m, down, y, ws)
             layer.norm(x, h, self.ones, y=y, x_out=x)
         logits = rows(self.V)
-        layer.linear4(h, self.unemb4, logits, self.ws)
+        layer.linear4(h, self.unemb4, logits, ws)
         return logits.float()
 
     def status(self) -> int:
-        return 0 if self.ws is None else layer.status(self.ws)
+        word = 0
+        for ws in self.ws:
+            word |= layer.status(ws)
+        return word
 
 
 class Decoder:
@@ -141,6 +150,7 @@ class Decoder:
         flat = torch.tensor([t for p in prompts for t in p[:-1]], dtype=torch.int64, device=dev)
         if len(flat):
             self._forward(flat, row_off, max(lens))
+            self.check()
         self.ctx += torch.tensor(lens, dtype=torch.int32, device=dev)
         self.anchor = torch.tensor([p[-1] for p in prompts], dtype=torch.int32, device=dev)
         self.tokens = [list(p) for p in prompts]
