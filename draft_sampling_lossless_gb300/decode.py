@@ -88,14 +88,14 @@ class Target4(Target):
         self.down4 = [w(d, F, 0.7 / math.sqrt(F)) for _ in range(layers)]
         self.unemb4 = layer.Weights4.quantize(self.unemb)
         self.ones = torch.ones(d, device=device)
-        self.rows, self.ws = 0, []  # workspaces, the last one for up to so many rows
+        self.rows, self.ws = 0, []  # workspaces, the last one made for so many rows
 
     def forward(self, tokens, attention):
         T, dev = len(tokens), self.emb.device
         widest = max(self.d, self.Hq * self.D, self.F)
-        if not self.ws or self.rows < T:
+        if not self.ws or self.ws[-1].numel() < layer.workspace_bytes(T, widest):
             # the smaller ones stay: their status words are read later, a captured pass may use
-            # them; each at least twice the last, so that they add up to no more than the last
+            # them; each is for twice the last one's rows, so that there are few
             self.rows = max(T, min(2 * self.rows, 1 << 24))
             self.ws.append(layer.workspace(self.rows, widest, dev))
         ws = self.ws[-1]
