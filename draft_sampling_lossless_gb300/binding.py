@@ -571,17 +571,21 @@ def _products(x, out, ws, N, K, stream, devices):
 
 
 def dspark_linear4(w, N, K, x, out, ws, stream=None, devices=()):
-    """devices: that of the weights' store."""
-    code = lib().dspark_linear4(w, *_products(x, out, ws, N, K, stream, devices))
+    """devices: that of the weights' store.  Returns the handle of the stream it runs on."""
+    args = _products(x, out, ws, N, K, stream, devices)
+    code = lib().dspark_linear4(w, *args)
     if code:
         _check("dspark_linear4", code)
+    return args[-1]
 
 
 def dspark_gated4(gate, up, N, K, act, x, out, ws, stream=None, devices=()):
-    """devices: those of the weights' stores."""
-    code = lib().dspark_gated4(gate, up, act, *_products(x, out, ws, N, K, stream, devices))
+    """devices: those of the weights' stores.  Returns as dspark_linear4."""
+    args = _products(x, out, ws, N, K, stream, devices)
+    code = lib().dspark_gated4(gate, up, act, *args)
     if code:
         _check("dspark_gated4", code)
+    return args[-1]
 
 
 def dspark_norm(x, y, post, gate, alpha, pre, eps, x_out, h, stream=None):

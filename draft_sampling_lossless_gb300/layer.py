@@ -3,7 +3,10 @@ gated product of a feed-forward block, the norms between blocks (libdspark's
 dspark_linear4, dspark_gated4, dspark_norm), enqueued on one stream.  Marshalling
 only -- every operator runs in the CUDA library.
 
-Tensors are on the current device; rows may lie apart (slices of wider tensors)."""
+Tensors are on the current device; rows may lie apart (slices of wider tensors).  A
+call given a stream runs there: its tensors have to be ready on that stream, and their
+memory must not be reused before it has passed the call (as for any use of a tensor on
+another stream; Tensor.record_stream says so to torch).  Weights see to that themselves."""
 
 from __future__ import annotations
 
@@ -27,6 +30,13 @@ class Weights4:
         self.desc = B.weights4_init(N, K, self.store)
         self._ref = ctypes.byref(self.desc)
         self._on = (self.store.get_device(),)
+        # the handles of the streams that torch knows the store to be in use on
+        self._streams = {torch._C._cuda_getCurrentRawStream(self._on[0])}
+
+    def _used_on(self, handle, stream):
+        """The store's memory is reused only after what `stream` does with it."""
+        self.store.record_stream(torch.cuda.current_stream() if stream is None else stream)
+        self._streams.add(handle)
 
     @classmethod
     def load(cls, codes, scales, stream=None):
@@ -35,6 +45,9 @@ class Weights4:
         with torch.cuda.stream(stream):  # the store's memory is that stream's
             w = cls(codes.shape[0], 2 * codes.shape[1], codes.device)
         B.dspark_weights4_load(w._ref, w.N, w.K, codes, scales, stream)
+        if stream is not None:
+            codes.record_stream(stream)
+            scales.record_stream(stream)
         return w
 
     @classmethod
@@ -44,6 +57,8 @@ class Weights4:
         with torch.cuda.stream(stream):
             w = cls(src.shape[0], src.shape[1], src.device)
         B.dspark_weights4_quantize(w._ref, w.N, w.K, src, stream)
+        if stream is not None:
+            src.record_stream(stream)
         return w
 
 
@@ -55,15 +70,20 @@ def workspace_bytes(T, K) -> int:
     return n
 
 
-def workspace(T, K, device="cuda"):
+def workspace(T, K, device="cuda", stream=None):
     """A zeroed workspace (uint8) for products of up to T rows of up to K columns;
-    calls in flight at the same time need one each."""
-    return torch.zeros(workspace_bytes(T, K), dtype=torch.uint8, device=device)
+    calls in flight at the same time need one each.  It is zeroed on `stream`, which
+    its memory belongs to; calls on another one have to wait for that."""
+    n = workspace_bytes(T, K)
+    with torch.cuda.stream(stream):
+        return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
 def linear4(x, w, out, ws, stream=None):
     """out = x w^T: x [T, K], out [T, N] bf16."""
-    B.dspark_linear4(w._ref, w.N, w.K, x, out, ws, stream, w._on)
+    h = B.dspark_linear4(w._ref, w.N, w.K, x, out, ws, stream, w._on)
+    if h not in w._streams:
+        w._used_on(h, stream)
 
 
 def gated4(x, gate, up, out, ws, act="silu", stream=None):
@@ -73,8 +93,11 @@ def gated4(x, gate, up, out, ws, act="silu", stream=None):
         raise ValueError(f"act must be one of {sorted(B.ACTIVATIONS)}, got {act!r}")
     if (up.N, up.K) != (gate.N, gate.K):
         raise ValueError("gate and up differ in shape")
-    B.dspark_gated4(gate._ref, up._ref, gate.N, gate.K, B.ACTIVATIONS[act], x, out, ws, stream,
-                    (*gate._on, *up._on))
+    h = B.dspark_gated4(gate._ref, up._ref, gate.N, gate.K, B.ACTIVATIONS[act], x, out, ws,
+                        stream, (*gate._on, *up._on))
+    for w in (gate, up):
+        if h not in w._streams:
+            w._used_on(h, stream)
 
 
 def norm(x, h=None, pre=None, y=None, x_out=None, post=None, gate=None, alpha=1.0, eps=1e-6,
