@@ -23,6 +23,26 @@ __device__ __forceinline__ float activation(int act, float a) {
   return a * (g * r);
 }
 
+// Codes p and p + 4 of a word as two bf16, 2^-126 of their values (0.5 is a subnormal).
+template <int P>
+__device__ __forceinline__ uint32_t pair_bits(uint32_t w) {
+  const uint32_t u = P == 3 ? w : w << (12 - 4 * P);
+  return (u & 0x80008000u) | ((u >> 6) & 0x01c001c0u);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 c = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&c);
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 // The kernel on the tensor cores (linear4_tile.cu), and how it cuts a product.
 struct TileCut {
   int mats;      // row tiles of 128 (of W, or one each of two matrices) that share a block's x

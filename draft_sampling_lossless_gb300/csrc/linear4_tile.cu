@@ -9,7 +9,8 @@
 //
 // but for what lies below 2^-22 of a group's largest (lo ends at 2^-9 of its scale), so
 // each step of K runs two MMAs, on hi and on lo, into one accumulator.  That is the rate of
-// bf16 MMAs, for a quarter of the weights' bytes and no conversions.
+// bf16 MMAs, for a quarter of the weights' bytes and no conversions.  Rows where that is more than
+// a few small values among larger ones are found as x is split and computed again from x itself.
 //
 // A first kernel writes hi, lo and their exponents in tiles that one bulk copy brings in,
 // swizzled as the MMA reads them; the second starts under it and already loads weights.  Blocks
@@ -52,6 +53,13 @@ __host__ __device__ constexpr uint32_t exp_blocks(int tokens, int wide) {
 }
 __host__ __device__ constexpr uint32_t tile_bytes(int tokens, int wide) {
   return (uint32_t)tokens * 256 + exp_blocks(tokens, wide) * 512;
+}
+
+// A workspace: the status word; a byte for 512 columns of a row, whether they lost bits,
+// [ceil(Kp / 512)][T rounded up to 8]; tiles of x.
+__host__ __device__ constexpr int lossy_stride(int T) { return (T + 7) & ~7; }
+__host__ __device__ constexpr size_t lossy_bytes(int T, int Kp) {
+  return ((size_t)lossy_stride(T) * ((Kp + 511) / 512) + 255) & ~(size_t)255;
 }
 
 // ---------------------------------------------------------------- x in two terms
@@ -109,6 +117,38 @@ __device__ __forceinline__ void codes_of8(const float (&v)[8], float f, uint2& h
   hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
   lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
+// The two terms hold all 8 bits of values from 2^-6 of the scale up (2^-14 of a group's largest);
+// below, bits go.  A group counts as lossy where half of its nonzero values lie there: beside one
+// channel far above its neighbours, whose weight may be zero (with the neighbours at 2^-14 of it
+// the group's sum is then off by 2^-9 of itself, at 2^-16 by 2^-7).  Rows with such a group are
+// computed again by exact_rows below.  In normal and gated activations a value or two of a group
+// are that small, beside a channel of 2^10 a few, of 2^12 a fifth: what those lose is below
+// 2^-22 of the largest, and most of the others are there at full length.
+//
+// The bits 7 of four codes of hi that are above 2^-6: no more than the whole values among them,
+// so that the counting is left out for nearly all.
+__device__ __forceinline__ uint32_t whole_codes(uint32_t hi) {
+  return ((hi & 0x7f7f7f7fu) + 0x77777777u) & 0x80808080u;
+}
+// How many of eight nonzero values are below 2^-6 of exponent e's scale, and in the second byte how
+// many are not zero.
+__device__ __forceinline__ uint32_t small_of8(uint4 raw, int e) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  const uint32_t add = (0x8000u - ((uint32_t)(e + 121) << 7)) * 0x00010001u;
+  uint32_t nonzero = 0, big = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // (no sum of two halves passes 0xffff)
+    const uint32_t m = w[j] & 0x7fff7fffu;
+    nonzero = nonzero >> 1 | ((m + 0x7fff7fffu) & 0x80008000u);
+    big = big >> 1 | ((m + add) & 0x80008000u);
+  }
+  return (uint32_t)(__popc(nonzero) - __popc(big)) | (uint32_t)__popc(nonzero) << 8;
+}
+__device__ __forceinline__ bool lossy_group(uint32_t counts) {
+  const uint32_t small = counts & 0xffu, nonzero = counts >> 8;
+  return small > 0 && 2 * small >= nonzero;
+}
+
 // A row's exponents go to the place of its MMA column n: lane n % 32 of tensor memory, column
 // n / 32; hi's and lo's (`term` 0 and 1).
 __device__ __forceinline__ void put_exps(uint8_t* dst, int tokens, int wide, int r, int term,
@@ -118,14 +158,16 @@ __device__ __forceinline__ void put_exps(uint8_t* dst, int tokens, int wide, int
                                ((n >> 5) & 3) * 4) = exps - term * 0x04040404u;
 }
 
-// Eight values of a row's 128 columns by each of 16 lanes, into row r of the tile at `dst`.
-__device__ __forceinline__ void split8(uint4 raw, uint8_t* dst, int tokens, int wide, int r) {
+// Eight values of a row's 128 columns by each of 16 lanes, into row r of the tile at `dst`; e:
+// the group's exponent; whether to count its small values.
+__device__ __forceinline__ bool split8(uint4 raw, uint8_t* dst, int tokens, int wide, int r,
+                                       int& e) {
   const int lane = threadIdx.x & 15;
   float v[8];
   uint32_t top = top_of8(raw, v);
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const int e = group_exponent(__uint_as_float(top << 16));
+  e = group_exponent(__uint_as_float(top << 16));
   uint2 hi, lo;
   codes_of8(v, __uint_as_float((uint32_t)(127 - e) << 23), hi, lo);
   uint32_t exps = 0;
@@ -136,20 +178,25 @@ __device__ __forceinline__ void split8(uint4 raw, uint8_t* dst, int tokens, int 
   *reinterpret_cast<uint2*>(dst + at) = hi;
   *reinterpret_cast<uint2*>(dst + tokens * 128 + at) = lo;
   if (lane < 2) put_exps(dst, tokens, wide, r, lane, exps);
+  return top != 0 && (whole_codes(hi.x) & whole_codes(hi.y)) != 0x80808080u;
 }
 
 // A warp a row's four tiles of 128 columns, 16 values a lane.  Rows past T stay as they are:
 // they reach only columns of the product that are not stored.
 constexpr int kSplitWarps = 8;
 
-__global__ void __launch_bounds__(kSplitWarps * 32)
+__global__ void __launch_bounds__(kSplitWarps * 32, 8)
     split_kernel(const __nv_bfloat16* __restrict__ x, int64_t x_stride, int T, int K, int KB,
-                 int tokens, int wide, uint8_t* __restrict__ out) {
+                 int tokens, int wide, uint8_t* __restrict__ out, uint8_t* __restrict__ lossy) {
   grid_dependency_wait();
   asm volatile("griddepcontrol.launch_dependents;");
   const int t = blockIdx.x * kSplitWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int kb = blockIdx.y * 4 + (lane >> 3), l8 = lane & 7, col = kb * 128 + l8 * 16;
-  if (t >= T) return;  // (whole warps)
+  if (t >= T) {  // (whole warps)
+    if (lane == 0) lossy[(size_t)blockIdx.y * lossy_stride(T) + t] = 0;
+    return;
+  }
+  const int tile = t / tokens, r = t - tile * tokens;
   uint4 raw[2] = {};
   if (col < K) {  // K is a multiple of 32
     const uint4* p = reinterpret_cast<const uint4*>(x + t * x_stride + col);
@@ -164,12 +211,25 @@ __global__ void __launch_bounds__(kSplitWarps * 32)
   uint2 hi[2], lo[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) codes_of8(v[i], f, hi[i], lo[i]);
-  uint32_t exps = 0;
-#pragma unroll
-  for (int g = 0; g < 4; ++g)
-    exps |= (uint32_t)(__shfl_sync(0xffffffffu, e, (lane & 24) + g * 2) + 127) << (8 * g);
+  uint32_t exps = (uint32_t)(e + 127) << (4 * (l8 & 6));  // of the lane's group, then of four
+  exps |= __shfl_xor_sync(0xffffffffu, exps, 2);
+  exps |= __shfl_xor_sync(0xffffffffu, exps, 4);
+  uint32_t any = 0;
+  int whole = __popc(whole_codes(hi[0].x) | whole_codes(hi[0].y) >> 1 | whole_codes(hi[1].x) >> 2 |
+                     whole_codes(hi[1].y) >> 3);
+  whole += __shfl_xor_sync(0xffffffffu, whole, 1);
+  // (with more than 16 whole ones the small ones are fewer than half)
+  if (__builtin_expect(__any_sync(0xffffffffu, top != 0 && whole <= 16), 0)) {
+    uint32_t counts = 0;
+    if (col < K) {  // (read again: kept, the values cost registers)
+      const uint4* p = reinterpret_cast<const uint4*>(x + t * x_stride + col);
+      counts = small_of8(__ldg(p), e) + small_of8(__ldg(p + 1), e);
+    }
+    counts += __shfl_xor_sync(0xffffffffu, counts, 1);
+    any = __any_sync(0xffffffffu, lossy_group(counts));
+  }
+  if (lane == 0) lossy[(size_t)blockIdx.y * lossy_stride(T) + t] = any ? 1 : 0;
   if (kb >= KB) return;
-  const int tile = t / tokens, r = t - tile * tokens;
   uint8_t* dst = out + ((size_t)tile * KB + kb) * tile_bytes(tokens, wide);
   const uint32_t at = r * 128 + ((l8 ^ (r & 7)) << 4);
   *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0].x, hi[0].y, hi[1].x, hi[1].y);
@@ -183,6 +243,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32)
 struct Params {
   const uint8_t *w, *u;    // the matrices' tiles
   const uint8_t* xq;       // tiles of x, or null: the blocks make their own
+  const uint8_t* lossy;    // with xq: which rows lost bits
   const __nv_bfloat16* x;
   int64_t x_stride;
   int N, T, K, KB, row_blocks, tokens, wide, feature_tiles, tiles, split, stages, slots, act;
@@ -194,6 +255,8 @@ struct Params {
 
 struct Small {  // at the end of shared memory
   uint64_t full[12], empty[12], acc_full[kMaxSlots], acc_empty[kMaxSlots], drain;
+  uint32_t lossy[kMaxSplit][kMaxTokens / 32];  // rows that the blocks split and that lost bits
+  int again;  // there are rows for exact_rows
   uint32_t tmem;
   int abort_flag, issued;
 };
@@ -248,6 +311,27 @@ __device__ __forceinline__ void store_cluster(uint32_t addr, int rank, const flo
       "mapa.shared::cluster.u32 a, %0, %1;\n\t"
       "st.shared::cluster.v4.f32 [a], {%2, %3, %4, %5};\n\t}" ::"r"(addr),
       "r"(rank), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+      : "memory");
+}
+
+// What the kernel before wrote of rows t .. t + 7 and 512 columns.
+__device__ __forceinline__ uint64_t lossy_bytes8(const Params& p, int i, int t) {
+  return *reinterpret_cast<const uint64_t*>(p.lossy + (size_t)i * lossy_stride(p.T) + t);
+}
+// Which of these rows lost bits.
+__device__ __forceinline__ uint32_t lossy_rows(const Params& p, int t) {
+  uint64_t any = 0;
+  for (int i = threadIdx.x & 31; i < (p.KB + 3) >> 2; i += 32) any |= lossy_bytes8(p, i, t);
+  const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)any);
+  const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(any >> 32));
+  return (lo * 0x10204080u >> 28) | (hi * 0x10204080u >> 28) << 4;  // (bytes of 0 or 1 to bits)
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, int rank, uint32_t v) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "st.shared::cluster.u32 [a], %2;\n\t}" ::"r"(addr),
+      "r"(rank), "r"(v)
       : "memory");
 }
 
@@ -321,6 +405,95 @@ __device__ __forceinline__ void store_rows(const uint32_t* v, const Params& p,
   }
 }
 
+// The rows of a tile (of r0 .. r0 + n - 1) that lost bits, computed again from x itself: bf16 MMAs
+// of 16 features by 8 rows, the codes as they are loaded, as in linear4_rows.cu.  A warp has 16 of
+// the block's features and all of K (half of it with one row tile).  This runs after everything
+// else in the block: calls without such rows take 0 to 0.4 us more than without all of this (122
+// rows by 2560 x 4096 10.98 us for 10.7, 4100 by 6144 x 2560 83.7 for 83.1).  A few rows take some
+// 16 us, all of 4100 some twenty times as long as the rest (1.6 ms for 84 us).
+template <int MATS, bool GATED>
+__device__ __forceinline__ void exact_rows(const Params& p, Small* ms, uint8_t* smem, int tile,
+                                           int r0, int n) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  float4(*red)[32] = reinterpret_cast<float4(*)[32]>(smem);  // [16 warps][32]
+  int* count = reinterpret_cast<int*>(smem + 8192);
+  int* list = count + 1;
+  const int tt = tile / p.feature_tiles, ft = tile - tt * p.feature_tiles;
+  const int t0 = tt * p.tokens, end = min(r0 + n, p.T - t0);
+  __syncthreads();  // (the last tile's results have been read)
+  if (tid == 0) *count = 0;
+  __syncthreads();
+  for (int c = (r0 & ~7) + warp * 8; c < end; c += kThreads / 4) {
+    uint32_t mask = 0;
+    if (p.xq) {
+      mask = lossy_rows(p, t0 + c);
+    } else {
+      for (int i = 0; i < p.split; ++i) mask |= ms->lossy[i][c >> 5] >> (c & 31);
+    }
+    const int r = c + lane;
+    if (lane < 8 && (mask >> lane & 1) && r >= r0 && r < end) list[atomicAdd(count, 1)] = r;
+  }
+  __syncthreads();
+  const int rows = *count;
+  for (int b = 0; b < rows; b += 8) {
+    if (warp < 16) {
+      const int m = MATS == 2 ? warp >> 3 : 0, half = MATS == 2 ? 0 : warp >> 3;
+      const int f = (warp & 7) * 16 + g;
+      const int k0 = MATS == 2 ? 0 : p.KB * half / 2, k1 = MATS == 2 || half ? p.KB : p.KB / 2;
+      const int block = min(GATED || MATS == 1 ? ft : ft * 2 + m, p.row_blocks - 1);
+      const uint8_t* w = (GATED && m ? p.u : p.w) + (size_t)block * p.KB * kTileBytes;
+      const int row = t0 + list[min(b + g, rows - 1)];
+      const __nv_bfloat16* x = p.x + (int64_t)row * p.x_stride + t * 32;
+      float d[4] = {};
+#pragma unroll 2
+      for (int k = k0; k < k1; ++k) {
+        const uint8_t* at = w + (size_t)k * kTileBytes;
+        const uint4 c0 = __ldg(reinterpret_cast<const uint4*>(at + code_in_tile(f, t)));
+        const uint4 c1 = __ldg(reinterpret_cast<const uint4*>(at + code_in_tile(f + 8, t)));
+        const uint32_t s0 = __ldg(at + scale_in_tile(f, t));
+        const uint32_t s1 = __ldg(at + scale_in_tile(f + 8, t));
+        // a group's power of two, times 2^126 for the codes' bits, in two factors
+        const uint32_t f0 = min(s0 + 126u, 254u) * 0x00800080u;
+        const uint32_t f1 = min(s1 + 126u, 254u) * 0x00800080u;
+        const uint32_t h0 = (max(s0, 128u) - 1u) * 0x00800080u;
+        const uint32_t h1 = (max(s1, 128u) - 1u) * 0x00800080u;
+        const bool in = k * 128 + t * 32 < p.K;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (in) v = __ldg(reinterpret_cast<const uint4*>(x + k * 128) + i);
+          const uint32_t w0 = i == 0 ? c0.x : i == 1 ? c0.y : i == 2 ? c0.z : c0.w;
+          const uint32_t w1 = i == 0 ? c1.x : i == 1 ? c1.y : i == 2 ? c1.z : c1.w;
+          auto value = [](uint32_t bits, uint32_t f, uint32_t h) {
+            return mul_bf16x2(mul_bf16x2(bits, f), h);
+          };
+          const uint32_t lo[4] = {value(pair_bits<0>(w0), f0, h0), value(pair_bits<0>(w1), f1, h1),
+                                  value(pair_bits<1>(w0), f0, h0), value(pair_bits<1>(w1), f1, h1)};
+          const uint32_t hi[4] = {value(pair_bits<2>(w0), f0, h0), value(pair_bits<2>(w1), f1, h1),
+                                  value(pair_bits<3>(w0), f0, h0), value(pair_bits<3>(w1), f1, h1)};
+          mma_16816(d, lo, __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
+          mma_16816(d, hi, __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+        }
+      }
+      red[warp][lane] = make_float4(d[0], d[1], d[2], d[3]);
+    }
+    __syncthreads();
+    for (int i = tid; i < (GATED ? 1 : MATS) * 1024; i += kThreads) {
+      const int c = i & 127, j = i >> 7 & 7, m = i >> 10;  // feature, row, row tile
+      const int l = (c & 7) * 4 + (j >> 1), e = (c >> 3 & 1) * 2 + (j & 1);
+      float o = reinterpret_cast<const float*>(&red[m * 8 + (c >> 4)][l])[e];
+      if (MATS == 1 || GATED) {
+        const float o1 = reinterpret_cast<const float*>(&red[8 + (c >> 4)][l])[e];
+        o = GATED ? activation(p.act, o) * o1 : o + o1;
+      }
+      const int feature = (GATED ? ft : ft * MATS + m) * 128 + c;
+      if (b + j < rows && feature < p.N)
+        p.out[(int64_t)(t0 + list[b + j]) * p.out_stride + feature] = __float2bfloat16(o);
+    }
+    __syncthreads();
+  }
+}
+
 // MATS row tiles of 128 share a block's x: two of one matrix, or (GATED) one of each.
 template <int MATS, bool GATED>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -340,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t b_drain = smem_u32(&ms->drain);
   volatile int* s_abort = &ms->abort_flag;
 
+  if (tid >= 64 && tid < 64 + kMaxSplit * (kMaxTokens / 32)) ms->lossy[0][tid - 64] = 0;
   if (warp == 1) {
     tmem_alloc(smem_u32(&ms->tmem), 512);
     tmem_relinquish();
@@ -359,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     ms->abort_flag = 0;
     ms->issued = 0;
+    ms->again = 0;
     tma_prefetch(&tm_w);
     if (GATED) tma_prefetch(&tm_u);
   }
@@ -564,12 +739,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         uint8_t* dst = smem + (size_t)s_now * stage_bytes + MATS * 16384;
+        bool small = false;
+        int e[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)  // (the tile has a multiple of 16 rows)
-          split8(now[i], dst, p.tokens, p.wide, q_now * 4 + i * 2 + (lane >> 4));
+          small |= split8(now[i], dst, p.tokens, p.wide, q_now * 4 + i * 2 + (lane >> 4), e[i]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_full + 8 * s_now);
+        if (__any_sync(0xffffffffu, small)) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = q_now * 4 + i * 2 + (lane >> 4);
+            uint32_t counts = small_of8(now[i], e[i]);
+            counts += __shfl_xor_sync(0xffffffffu, counts, 1);
+            counts += __shfl_xor_sync(0xffffffffu, counts, 2);
+            if (lossy_group(counts)) {
+              atomicOr(&ms->lossy[rank][r >> 5], 1u << (r & 31));
+              ms->again = 1;
+            }
+          }
+        }
       }
     }
     auto wait_slot = [&]() {
@@ -591,6 +781,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tt = tile / p.feature_tiles, ft = tile - tt * p.feature_tiles;
       const int t0 = tt * p.tokens, rows = min(p.tokens, p.T - t0);
       const int f0 = ft * (GATED ? 128 : 128 * MATS) + quad * 32;
+      if (p.xq) {  // rows that lost bits?  (512 columns and 8 rows a lane)
+        uint64_t lossy = 0;
+        for (int c = ((lane >> 3) * kTurns + turn) * 8; c < rows; c += 4 * kTurns * 8)
+          for (int i = lane & 7; i < (p.KB + 3) >> 2; i += 8) lossy |= lossy_bytes8(p, i, t0 + c);
+        if (lossy != 0) ms->again = 1;
+      }
       // The sums leave tensor memory before the activation and the stores (which go out at some 2
       // TB/s where all blocks store at once): the first matrix's in fp32 where the second
       // belongs to it, else rounded.
@@ -654,6 +850,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync_all();
     const int cols = p.tokens / p.split;  // a multiple of 4
     float4* part = reinterpret_cast<float4*>(smem);  // [split][MATS][cols / 4][128]
+    constexpr int kWords = kMaxTokens / 32;
+    if (!p.xq && tid < p.split * kWords) {  // the rows that lost bits in this block's range, to all
+      const uint32_t mask = ms->lossy[rank][tid % kWords];
+      if (mask != 0) {
+        store_cluster(smem_u32(&ms->lossy[rank][tid % kWords]), tid / kWords, mask);
+        store_cluster(smem_u32(&ms->again), tid / kWords, 1u);
+      }
+    }
     if (warp >= 2) {
       tc_fence_after();
       const int quad = warp & 3, turn = (warp - 2) >> 2, f = quad * 32 + lane;
@@ -716,6 +920,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (__builtin_expect(ms->again && !*s_abort, 0)) {
+    const int per = p.tokens / p.split;
+    for (int tile = first; tile < p.tiles; tile += step)
+      exact_rows<MATS, GATED>(p, ms, smem, tile, rank * per, per);
+  }
   if (tid == 0 && *s_abort) {
     set_flag(p.status, kFlagWaitTimeout);
     // the copies in flight land before the block's shared memory goes
@@ -813,7 +1022,8 @@ cudaError_t launch(const Linear4Args& a, const Cut& cut, cudaStream_t st) {
   Params p;
   p.w = a.w->store;
   p.u = a.up ? a.up->store : nullptr;
-  p.xq = cut.own ? nullptr : static_cast<const uint8_t*>(a.ws) + kStatusBytes;
+  p.lossy = static_cast<const uint8_t*>(a.ws) + kStatusBytes;
+  p.xq = cut.own ? nullptr : p.lossy + lossy_bytes(a.T, a.w->Kp);
   p.x = a.x;
   p.x_stride = a.x_stride;
   p.K = a.w->K;
@@ -862,11 +1072,12 @@ size_t linear4_tile_workspace_bytes(int T, int K) {
       const size_t n = (size_t)((T + tokens - 1) / tokens) * tile_bytes(tokens, wide);
       if (n > most) most = n;
     }
-  return kStatusBytes + most * (padded_k(K) / 128);
+  return kStatusBytes + lossy_bytes(T, padded_k(K)) + most * (padded_k(K) / 128);
 }
 
 cudaError_t launch_linear4_tile(const Linear4Args& a, const TileCut& cut, cudaStream_t st) {
   const int KB = a.w->Kp / 128;
+  uint8_t* lossy = static_cast<uint8_t*>(a.ws) + kStatusBytes;
   cudaError_t e;
   if (!cut.own) {
     DSPARK_LAUNCH(kKindLinear4, st,
@@ -874,7 +1085,7 @@ cudaError_t launch_linear4_tile(const Linear4Args& a, const TileCut& cut, cudaSt
                                  dim3((a.T + kSplitWarps - 1) / kSplitWarps, (KB + 3) / 4),
                                  dim3(kSplitWarps * 32), 0, st, a.x, a.x_stride, a.T, a.w->K, KB,
                                  cut.tokens, cut.wide,
-                                 static_cast<uint8_t*>(a.ws) + kStatusBytes));
+                                 lossy + lossy_bytes(a.T, a.w->Kp), lossy));
     if (e != cudaSuccess) return e;
   }
   return a.up            ? launch<2, true>(a, cut, st)

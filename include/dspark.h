@@ -616,9 +616,10 @@ size_t dspark_linear4_workspace_bytes(int T, int K);
  *         K), 16-byte aligned
  *   out   [T][N] bf16, rows out_stride elements apart (at least N)
  * What lies between the rows of out is left as it is.  out must not overlap x.
- * Products are exact but for what a row's values have below 2^-21 of the largest
- * of their 32 columns (which may be rounded away, as may values below 2^-118);
- * sums are fp32, the result is rounded once.  A row of x with a NaN or an
+ * Products are exact, but where more than half of the nonzero values of 32 columns
+ * of a row are above 2^-14 of the largest of them (and above 2^-124): there the
+ * others may lose what they have below 2^-21 of the largest (below 2^-131).
+ * Sums are fp32, the result is rounded once.  A row of x with a NaN or an
  * infinity gives NaN or infinities in its own row of out, and only there.
  * Results are bit-reproducible (for the same T, N and K).
  */
