@@ -11,7 +11,7 @@ namespace dspark {
 // What the opaque words of a dspark_weights4 hold.  The store: tiles of 128 rows by 128 columns,
 // [ceil(N / 128)][Kp / 128], Kp = K rounded up to 128, each its codes [128][64 bytes] and then
 // its scales, one run of 8704 bytes.  (With codes in rows of K, 4100 rows of
-// x gated by 2 x 10240 x 2560 took 235 us for 231, one by 6144 x 2560 5.6 us for 5.45.)
+// x gated by 2 x 10240 x 2560 took 2% longer, one by 6144 x 2560 3%.)
 struct Weights4Desc {
   uint64_t magic;
   int N, K, Kp, pad;

@@ -14,9 +14,10 @@
 // order, 16 bytes a lane and two MMAs.
 //
 // What bounds it: for small matrices latency (one row by 1000 x 1024 3.0 us among calls in a
-// graph, by 6144 x 2560 5.5 us: a launch, one round trip to memory, the sums of a tile's
-// warps); past that the conversions, 21 values a cycle an SM (4.8 instructions a value with
-// everything), so larger matrices go to the tensor cores' kernel.  Conversions by e2m1x2 to
+// graph: a launch, one round trip to memory, the sums of a tile's warps); past that the
+// conversions, 21 values a cycle an SM (4.8 instructions a value with everything; one row by 6144 x
+// 2560 5.5 us, half of it the three row tiles of the busiest SM), so larger matrices go to
+// the tensor cores' kernel.  Conversions by e2m1x2 to
 // f16x2, with x in f16 and scales after the MMAs, were no faster (one row 5.4 us, eight 6.6 for
 // 6.3, 151936 x 2560 68 for 63).
 #include "linear4.cuh"

@@ -18,12 +18,13 @@
 //
 // What bounds it: with many rows the MMAs (an A of 128 x 32 takes 62 cycles from shared memory,
 // so N = 160 to 192 columns run at 90 to 95% of their rate and 64 at half of it); with a few
-// the same 62 cycles, on as many SMs as there are tiles; with a large vocabulary HBM.  Measured
-// among calls in a graph: 4100 rows gated by 2 x 10240 x 2560 235 us, 1.83 PFLOP/s (95% of
-// cuBLAS's measured bf16 rate), tensor pipe 76% busy at 2100 rows; 4100 rows by 6144 x 2560 83
-// us, 1.55 PFLOP/s, 10 of them the first kernel; 64 rows by 151936 x 2560 47.2 us, 4.8 TB/s; 122
-// rows by 2560 x 4096 10.7 us, gated by 2 x 10240 x 2560 18.8 us (80 tiles on 152 SMs, or 240 in
-// two rounds); one row gated by the same 10.3 us.
+// the issuing thread, 390 to 500 cycles a step of 128 columns (waits, copies of scales and
+// commits 210, an MMA 45) where A's reads take some 300, on as many SMs as there are tiles;
+// with a large vocabulary HBM beside the MMAs.  Measured among calls in a graph: 4100 rows gated by 2 x
+// 10240 x 2560 237 us, 1.81 PFLOP/s (97% of cuBLAS's measured bf16 rate), tensor pipe 78%
+// busy at 2100 rows; 4100 rows by 6144 x 2560 84 us, 1.54 PFLOP/s, 10 of them the first kernel; 64
+// rows by 151936 x 2560 47.3 us, 4.8 TB/s; 122 rows by 2560 x 4096 11.0 us, gated by 2 x 10240 x
+// 2560 19.4 us (80 tiles on 152 SMs, or 240 in two rounds); one row gated by the same 10.5 us.
 #include "linear4.cuh"
 #include "sm100.cuh"
 

@@ -80,7 +80,8 @@ def workspace(T, K, device="cuda", stream=None):
 
 
 def linear4(x, w, out, ws, stream=None):
-    """out = x w^T: x [T, K], out [T, N] bf16."""
+    """out = x w^T: x [T, K], out [T, N] bf16.  (dspark.h says what small values of x
+    among larger ones may lose.)"""
     h = B.dspark_linear4(w._ref, w.N, w.K, x, out, ws, stream, w._on)
     if h not in w._streams:
         w._used_on(h, stream)
