@@ -16,7 +16,7 @@ def norm_error(d):
     return (d / 8 + 16) * 2.0 ** -24 + 8 * 2.0 ** -24
 
 
-@pytest.mark.parametrize("d", (64, 2560, 12000))
+@pytest.mark.parametrize("d", (64, 2560, 12000, 20000))
 def test_norm_of_a_blocks_largest_output(d):
     """y near bf16's largest, a post (and gate) above 1: rms(y) * post is of ordinary size."""
     for T in (2, 200):
@@ -44,7 +44,7 @@ def test_norm_with_a_gate_and_a_small_alpha():
     assert ((xo.double() - want).abs() <= 3 * 2.0 ** -24 * want.abs()).all()
 
 
-@pytest.mark.parametrize("d", (64, 2560, 12000))
+@pytest.mark.parametrize("d", (64, 2560, 12000, 20000))
 @pytest.mark.parametrize("size", (2.0 ** -126, 2.0 ** -130, 2.0 ** -140, 2.0 ** -148))
 def test_norm_of_the_smallest_rows(d, size):
     """eps = 0 and rows below fp32's smallest normal number: each value is what fp32 (and, for y,
